@@ -15,6 +15,8 @@
  *   offset s % B.  PA_LAYOUT_SPLIT is the vLLM layout (see pa_layout_t).
  * - Element types: PA_F32 (IEEE fp32) or PA_BF16 (bfloat16).  q, k, v, out
  *   and both caches share the cache's element type.  Arithmetic is fp32.
+ *   PA_FP8_E4M3 is the element type of an 8-bit cache (the calls named _fp8
+ *   only; see "8-bit cache").
  * - Pointers named "device" must be CUDA device memory (or managed memory)
  *   of the current device; "host" pointers are ordinary host memory.  The
  *   caller owns every buffer.  The library never allocates device memory and
@@ -56,7 +58,7 @@ typedef enum pa_status {
     PA_ERR_HOST_MEMORY = -9     /* a host allocation failed (no C++ exception ever leaves a call) */
 } pa_status_t;
 
-typedef enum pa_dtype { PA_F32 = 0, PA_BF16 = 1 } pa_dtype_t;
+typedef enum pa_dtype { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2 } pa_dtype_t;
 
 /* Cache layouts.  Both keep each physical block contiguous (B * Hk * D
  * elements per tensor), so block copies and the block-table walk are the same.
@@ -329,6 +331,112 @@ int32_t pa_decode_launch_count(const pa_cache_desc_t *cache, int32_t num_seqs, i
 void pa_split_range(int64_t total_blocks, int32_t num_splits, int32_t c, int64_t *begin,
                     int64_t *end);
 int32_t pa_split_owner(int64_t total_blocks, int32_t num_splits, int64_t x);
+
+/* ------------------------------------------------------------------------
+ * pa_prefill - attention of a chunk of new tokens over the paged cache.
+ *
+ * Sequence i has n_i = cu_q_lens[i + 1] - cu_q_lens[i] new tokens, the rows
+ * cu_q_lens[i] .. of q and out, whose K and V are already in the cache
+ * (pa_reshape_and_cache first).  seq_lens[i] = L_i counts every position, the
+ * new ones included, so new token r stands at position p = L_i - n_i + r and
+ * sees the positions up to its own:
+ *     out[cu_q_lens[i] + r, h, :] = sum_j softmax_j(scale * q . K_j) V_j, j <= p,
+ * with K_j, V_j as in pa_decode (kv head h / (H / Hk), slot
+ * block_tables[i, j / B] * B + j % B).  A whole prompt (L_i = n_i), a chunk of
+ * one behind a cached prefix, and drafted tokens being checked are the same
+ * call; n_i = 0 is allowed.  A row at a negative position (n_i > L_i) sees
+ * nothing and is zero.  Rows of out outside [cu_q_lens[0], cu_q_lens[N]) are
+ * left as they were.
+ *
+ * The new tokens of a sequence are cut into tiles of query rows (the G = H / Hk
+ * heads of a KV head side by side), and the list of (KV head, tile, unit of
+ * keys) is split evenly over persistent CTAs; a tile cut between CTAs is
+ * merged by a second kernel.  The split depends only on the lengths and the
+ * split count, so the same call gives the same bits every time.  Each call
+ * launches 3 kernels on `stream` (work list, attention, merge).
+ *
+ * out, q        device [num_tokens, H, D], the cache's element type.
+ * cu_q_lens     device int32 [num_seqs + 1], not decreasing, within
+ *               [0, num_tokens].  Offsets that are not are recorded as
+ *               PA_ERR_DEVICE_BOUNDS and the call writes nothing.
+ * block_tables, seq_lens, scale, workspace, stream: as for pa_decode (a length
+ *               outside the table's reach counts as 0 and is recorded; an entry
+ *               outside the pool reads zeros and is recorded).
+ * K and V at positions past L_i are never used, whatever they hold; a K or V
+ * that is not finite at a position that a row does not see does not reach
+ * that row.
+ * Requirements: H % Hk == 0, H / Hk <= 64, D in {64, 128, 256}, fp32 or bf16,
+ *               either layout; q and out aligned to 2 elements, the caches to
+ *               16 bytes.  The tensor-core kernel (tcgen05) takes bf16, D 64 or
+ *               128, the row layout, block sizes that are multiples of 8, scale
+ *               > 0 and 16-byte aligned q and out; CUDA cores take the rest.
+ * ---------------------------------------------------------------------- */
+typedef struct pa_prefill_opts {
+    int32_t num_splits; /* persistent CTAs sharing the work; 0 = one wave on this device */
+    int32_t kernel;     /* pa_kernel_t; PA_KERNEL_MMA: the tcgen05 kernel or PA_ERR_UNSUPPORTED */
+} pa_prefill_opts_t;
+
+size_t pa_prefill_workspace_bytes(const pa_cache_desc_t *cache, int32_t num_seqs, int32_t num_tokens,
+                                  int32_t num_heads, const pa_prefill_opts_t *opts);
+
+pa_status_t pa_prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
+                       const pa_cache_desc_t *cache, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                       const int32_t *seq_lens, const int32_t *cu_q_lens, int32_t num_seqs, int32_t num_tokens,
+                       int32_t num_heads, float scale, void *workspace, size_t workspace_bytes,
+                       const pa_prefill_opts_t *opts, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit cache (PA_FP8_E4M3, PA_LAYOUT_ROW): e4m3 codes [NB, B, Hk, D] for K and
+ * for V, and one scale byte per token and KV head in k_scale, v_scale
+ * [NB, B, Hk].  Byte b stands for 2^(b - 127) (E8M0); an element's value is
+ * code * 2^(b - 127).
+ *
+ * Rule of the write: over the D values x of one token's one KV head, e is the
+ * smallest integer in [-126, 120] with |x| <= 448 * 2^e for every finite x;
+ * the byte is e + 127 and a code is x * 2^-e rounded to the nearest e4m3 (ties
+ * to even).  Infinities become +-448 * 2^e, NaN stays NaN, a row of zeros has
+ * byte 1.  The product with 2^-e is exact, so a code is one rounding of x.
+ *
+ * pa_reshape_and_cache_fp8  the write of pa_reshape_and_cache: k, v
+ *     [num_tokens, Hk, D] of element type dtype (PA_F32 or PA_BF16) into the
+ *     slots; a negative slot is padding and skipped, a slot past the pool is
+ *     skipped and recorded.  Slots must be distinct.
+ * pa_gather_cache_fp8  the way back: k, v [num_tokens, Hk, D] of type dtype
+ *     receive the values at the slots, rounded once (exact in fp32).  The rows
+ *     of negative slots and of slots past the pool (recorded) are zero.  The
+ *     result is also a pool of its own: pa_prefill and pa_decode read it with
+ *     consecutive blocks.
+ * pa_copy_blocks_fp8  pa_copy_blocks for codes and scale bytes.
+ * pa_decode_fp8  pa_decode over the 8-bit cache: q and out are bf16, K_j and
+ *     V_j the values, arithmetic in fp32 (the tensor-core kernel multiplies
+ *     the codes as fp16, which holds them exactly, rounds q scaled by a power
+ *     of two per row and the probabilities to fp16, and sums in fp32).
+ *     Requirements as pa_decode (H / Hk <= 8, D in {64, 128, 256}); q and out
+ *     aligned to 4 bytes, the caches to 16.  The tensor-core kernel takes D 64
+ *     or 128 and block sizes that are multiples of 8; CUDA cores take the
+ *     rest.  opts: num_splits and kernel.
+ * Any D >= 1 and alignment can be written, read back and copied.
+ * ---------------------------------------------------------------------- */
+pa_status_t pa_reshape_and_cache_fp8(const void *k, const void *v, int32_t dtype, const int32_t *slot_mapping,
+                                     int32_t num_tokens, void *k_cache, void *v_cache, uint8_t *k_scale,
+                                     uint8_t *v_scale, const pa_cache_desc_t *cache, pa_stream_t stream);
+
+pa_status_t pa_gather_cache_fp8(void *k, void *v, int32_t dtype, const int32_t *slot_mapping, int32_t num_tokens,
+                                const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+                                const uint8_t *v_scale, const pa_cache_desc_t *cache, pa_stream_t stream);
+
+pa_status_t pa_copy_blocks_fp8(void *k_cache, void *v_cache, uint8_t *k_scale, uint8_t *v_scale,
+                               const pa_cache_desc_t *cache, const int32_t *src_dst_pairs, int32_t num_pairs,
+                               pa_stream_t stream);
+
+size_t pa_decode_fp8_workspace_bytes(const pa_cache_desc_t *cache, int32_t num_seqs, int32_t num_heads,
+                                     const pa_prefill_opts_t *opts);
+
+pa_status_t pa_decode_fp8(void *out, const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+                          const uint8_t *v_scale, const pa_cache_desc_t *cache, const int32_t *block_tables,
+                          int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t num_seqs, int32_t num_heads,
+                          float scale, void *workspace, size_t workspace_bytes, const pa_prefill_opts_t *opts,
+                          pa_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * pa_get_device_error - synchronise `stream`, then read and clear the error

@@ -10,6 +10,10 @@ Calls (same names as the C ABI):
   pa_reshape_and_cache(k, v, slot_mapping, k_cache, v_cache)
   pa_copy_blocks(k_cache, v_cache, src_dst_pairs)
   pa_decode(q, k_cache, v_cache, block_tables, seq_lens, scale, ...)
+  pa_prefill(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, scale, ...)
+  pa_reshape_and_cache_fp8, pa_gather_cache_fp8, pa_copy_blocks_fp8,
+  pa_decode_fp8: the same over an 8-bit cache (float8_e4m3fn codes and one
+  power-of-two scale byte per token and KV head)
   pa_get_device_error()
   BlockManager: the host block manager (free list, refcounts, fork,
   copy-on-write, slot mapping).
@@ -245,6 +249,199 @@ def pa_decode(q, k_cache, v_cache, block_tables, seq_lens, scale, out=None, work
                        _dev(seq_lens, "seq_lens", torch.int32, d), N, H, float(scale),
                        _dev(workspace, "workspace", device=d), workspace.numel(), ctypes.byref(o), _stream())
     _lib.check("pa_decode", st)
+    return out
+
+
+def _prefill_opts(num_splits, kernel):
+    return _lib.PrefillOpts(int(num_splits), _KERNELS[kernel])
+
+
+def pa_prefill_workspace_bytes(k_cache, num_tokens, num_seqs, num_heads, num_splits=0, kernel="auto"):
+    """Workspace bytes of pa_prefill for a batch of num_tokens new tokens."""
+    desc = _cache_desc_from_k(k_cache)
+    o = _prefill_opts(num_splits, kernel)
+    n = _lib.load().pa_prefill_workspace_bytes(ctypes.byref(desc), int(num_seqs), int(num_tokens), int(num_heads),
+                                               ctypes.byref(o))
+    if n == 0:
+        raise PagedAttentionError("pa_prefill_workspace_bytes", _lib.PA_ERR_UNSUPPORTED)
+    return int(n)
+
+
+def pa_prefill(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, scale, out=None, workspace=None,
+               num_splits=0, kernel="auto"):
+    """Attention of a chunk of new tokens over the paged cache; returns ``out``
+    [T, H, D].
+
+    Rows cu_q_lens[i] .. cu_q_lens[i + 1] - 1 of ``q`` are the new tokens of
+    sequence i, the last ones of its seq_lens[i] positions; their K and V are
+    in the cache already.  Each sees the positions up to its own.  Rows that
+    belong to no sequence are left as they were (in a fresh ``out``:
+    unspecified)."""
+    torch = _torch()
+    desc = _cache_desc(k_cache, v_cache)
+    T, H, D = q.shape
+    N = seq_lens.shape[0]
+    if D != desc.head_dim or q.dtype != k_cache.dtype:
+        raise ValueError("q must be [num_tokens, num_heads, head_dim] in the cache's element type")
+    if block_tables.dim() != 2 or block_tables.shape[0] != N or seq_lens.shape != (N,):
+        raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
+    if cu_q_lens.shape != (N + 1,):
+        raise ValueError("cu_q_lens must be [num_seqs + 1]")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must match q")
+    d = _current_device()
+    o = _prefill_opts(num_splits, kernel)
+    lib = _lib.load()
+    if workspace is None:
+        need = lib.pa_prefill_workspace_bytes(ctypes.byref(desc), N, T, H, ctypes.byref(o))
+        if need == 0:
+            raise PagedAttentionError("pa_prefill_workspace_bytes", _lib.PA_ERR_UNSUPPORTED)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    st = lib.pa_prefill(_dev(out, "out", device=d), _dev(q, "q", device=d), _dev(k_cache, "k_cache", device=d),
+                        _dev(v_cache, "v_cache", device=d), ctypes.byref(desc),
+                        _dev(block_tables, "block_tables", torch.int32, d), block_tables.shape[1],
+                        _dev(seq_lens, "seq_lens", torch.int32, d), _dev(cu_q_lens, "cu_q_lens", torch.int32, d), N, T,
+                        H, float(scale), _dev(workspace, "workspace", device=d),
+                        workspace.numel() * workspace.element_size(), ctypes.byref(o), _stream())
+    _lib.check("pa_prefill", st)
+    return out
+
+
+def _cache_desc_fp8(k_cache, v_cache=None, k_scale=None, v_scale=None):
+    """Descriptor of an 8-bit cache: codes float8_e4m3fn [NB, B, Hk, D], scale
+    bytes uint8 [NB, B, Hk]."""
+    torch = _torch()
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t is None:
+            continue
+        if t.dtype != torch.float8_e4m3fn:
+            raise TypeError("%s must be float8_e4m3fn, got %s" % (name, t.dtype))
+        if t.dim() != 4 or t.shape != k_cache.shape:
+            raise ValueError("caches must be K, V [num_blocks, block_size, num_kv_heads, head_dim]")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is None:
+            continue
+        if t.dtype != torch.uint8:
+            raise TypeError("%s must be uint8, got %s" % (name, t.dtype))
+        if t.shape != k_cache.shape[:3]:
+            raise ValueError("%s must be [num_blocks, block_size, num_kv_heads]" % name)
+    nb, bs, hk, d = k_cache.shape
+    return _lib.CacheDesc(nb, bs, hk, d, _lib.PA_FP8_E4M3, _lib.PA_LAYOUT_ROW)
+
+
+def _check_rows(k, v, slot_mapping, desc):
+    T = slot_mapping.shape[0]
+    for t in (k, v):
+        if tuple(t.shape) != (T, desc.num_kv_heads, desc.head_dim):
+            raise ValueError("k, v must be [num_tokens, num_kv_heads, head_dim] matching the cache and slot_mapping "
+                             "[num_tokens]")
+    if k.dtype != v.dtype:
+        raise TypeError("k and v element types differ")
+    return T, _dtype_code(k)
+
+
+def pa_reshape_and_cache_fp8(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale):
+    """Quantise new tokens' K/V rows (fp32 or bf16) into the 8-bit caches at
+    their slots: e4m3 codes and one power-of-two scale byte (2^(b - 127)) per
+    token and KV head."""
+    torch = _torch()
+    desc = _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale)
+    if slot_mapping.dim() != 1:
+        raise ValueError("slot_mapping must be [num_tokens]")
+    T, dt = _check_rows(k, v, slot_mapping, desc)
+    d = _current_device()
+    st = _lib.load().pa_reshape_and_cache_fp8(
+        _dev(k, "k", device=d), _dev(v, "v", device=d), dt, _dev(slot_mapping, "slot_mapping", torch.int32, d), T,
+        _dev(k_cache, "k_cache", device=d), _dev(v_cache, "v_cache", device=d), _dev(k_scale, "k_scale", device=d),
+        _dev(v_scale, "v_scale", device=d), ctypes.byref(desc), _stream())
+    _lib.check("pa_reshape_and_cache_fp8", st)
+
+
+def pa_gather_cache_fp8(k_cache, v_cache, k_scale, v_scale, slot_mapping, k=None, v=None, dtype=None):
+    """Read rows of the 8-bit caches back: (k, v) [num_tokens, Hk, D] with the
+    values at the slots (zeros for negative slots), in ``k`` and ``v`` or in new
+    tensors of ``dtype`` (default bfloat16)."""
+    torch = _torch()
+    desc = _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale)
+    if slot_mapping.dim() != 1:
+        raise ValueError("slot_mapping must be [num_tokens]")
+    if (k is None) != (v is None):
+        raise ValueError("give both k and v or neither")
+    if k is None:
+        shape = (slot_mapping.shape[0], desc.num_kv_heads, desc.head_dim)
+        k = torch.empty(shape, dtype=dtype or torch.bfloat16, device=k_cache.device)
+        v = torch.empty_like(k)
+    elif dtype is not None and k.dtype != dtype:
+        raise TypeError("k is %s, not %s" % (k.dtype, dtype))
+    T, dt = _check_rows(k, v, slot_mapping, desc)
+    d = _current_device()
+    st = _lib.load().pa_gather_cache_fp8(
+        _dev(k, "k", device=d), _dev(v, "v", device=d), dt, _dev(slot_mapping, "slot_mapping", torch.int32, d), T,
+        _dev(k_cache, "k_cache", device=d), _dev(v_cache, "v_cache", device=d), _dev(k_scale, "k_scale", device=d),
+        _dev(v_scale, "v_scale", device=d), ctypes.byref(desc), _stream())
+    _lib.check("pa_gather_cache_fp8", st)
+    return k, v
+
+
+def pa_copy_blocks_fp8(k_cache, v_cache, k_scale, v_scale, src_dst_pairs):
+    """pa_copy_blocks for an 8-bit cache: codes and scale bytes."""
+    torch = _torch()
+    desc = _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale)
+    if src_dst_pairs.numel() == 0:
+        return
+    pairs = src_dst_pairs.reshape(-1, 2)
+    d = _current_device()
+    st = _lib.load().pa_copy_blocks_fp8(
+        _dev(k_cache, "k_cache", device=d), _dev(v_cache, "v_cache", device=d), _dev(k_scale, "k_scale", device=d),
+        _dev(v_scale, "v_scale", device=d), ctypes.byref(desc), _dev(pairs, "src_dst_pairs", torch.int32, d),
+        pairs.shape[0], _stream())
+    _lib.check("pa_copy_blocks_fp8", st)
+
+
+def pa_decode_fp8_workspace_bytes(k_cache, num_seqs, num_heads, num_splits=0, kernel="auto"):
+    """Workspace bytes of pa_decode_fp8."""
+    desc = _cache_desc_fp8(k_cache)
+    o = _prefill_opts(num_splits, kernel)
+    n = _lib.load().pa_decode_fp8_workspace_bytes(ctypes.byref(desc), int(num_seqs), int(num_heads), ctypes.byref(o))
+    if n == 0:
+        raise PagedAttentionError("pa_decode_fp8_workspace_bytes", _lib.PA_ERR_UNSUPPORTED)
+    return int(n)
+
+
+def pa_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, scale, out=None, workspace=None,
+                  num_splits=0, kernel="auto"):
+    """Decode attention over an 8-bit cache through block tables; q and the
+    returned ``out`` are bfloat16 [N, H, D]."""
+    torch = _torch()
+    desc = _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale)
+    N, H, D = q.shape
+    if D != desc.head_dim:
+        raise ValueError("q must be [num_seqs, num_heads, head_dim] matching the cache")
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16, got %s" % q.dtype)
+    if block_tables.dim() != 2 or block_tables.shape[0] != N or seq_lens.shape != (N,):
+        raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must match q")
+    d = _current_device()
+    o = _prefill_opts(num_splits, kernel)
+    lib = _lib.load()
+    if workspace is None:
+        need = lib.pa_decode_fp8_workspace_bytes(ctypes.byref(desc), N, H, ctypes.byref(o))
+        if need == 0:
+            raise PagedAttentionError("pa_decode_fp8_workspace_bytes", _lib.PA_ERR_UNSUPPORTED)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    st = lib.pa_decode_fp8(
+        _dev(out, "out", device=d), _dev(q, "q", device=d), _dev(k_cache, "k_cache", device=d),
+        _dev(v_cache, "v_cache", device=d), _dev(k_scale, "k_scale", device=d), _dev(v_scale, "v_scale", device=d),
+        ctypes.byref(desc), _dev(block_tables, "block_tables", torch.int32, d), block_tables.shape[1],
+        _dev(seq_lens, "seq_lens", torch.int32, d), N, H, float(scale), _dev(workspace, "workspace", device=d),
+        workspace.numel() * workspace.element_size(), ctypes.byref(o), _stream())
+    _lib.check("pa_decode_fp8", st)
     return out
 
 
@@ -541,6 +738,9 @@ def version():
 __all__ = [
     "pa_reshape_and_cache", "pa_copy_blocks", "pa_decode", "pa_decode_workspace_bytes", "pa_decode_no_alloc",
     "pa_decode_default_splits", "pa_decode_shared_tc", "pa_decode_launch_count", "pa_get_device_error", "pa_selftest_wait_timeout",
+    "pa_prefill", "pa_prefill_workspace_bytes",
+    "pa_reshape_and_cache_fp8", "pa_gather_cache_fp8", "pa_copy_blocks_fp8", "pa_decode_fp8",
+    "pa_decode_fp8_workspace_bytes",
     "pa_split_range", "pa_split_owner",
     "BlockManager", "PagedAttentionError", "sampling_memory", "simulate", "version",
 ]

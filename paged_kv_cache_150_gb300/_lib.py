@@ -21,6 +21,7 @@ PA_ERR_HOST_MEMORY = -9
 
 PA_F32 = 0
 PA_BF16 = 1
+PA_FP8_E4M3 = 2
 
 PA_NO_ALLOC_SCRATCH_BYTES = 16 << 20  # include/pa.h
 
@@ -57,6 +58,10 @@ class DecodeOpts(ctypes.Structure):
                 ("shared_plan", ctypes.c_void_p), ("host_seq_lens", ctypes.c_void_p)]
 
 
+class PrefillOpts(ctypes.Structure):
+    _fields_ = [("num_splits", ctypes.c_int32), ("kernel", ctypes.c_int32)]
+
+
 class SharedPlanInfo(ctypes.Structure):
     _fields_ = [("num_groups", ctypes.c_int32), ("num_members", ctypes.c_int32),
                 ("shared_blocks", ctypes.c_int64), ("saved_blocks", ctypes.c_int64)]
@@ -70,6 +75,7 @@ _PI32 = ctypes.POINTER(ctypes.c_int32)
 _PI64 = ctypes.POINTER(ctypes.c_int64)
 _DESC = ctypes.POINTER(CacheDesc)
 _OPTS = ctypes.POINTER(DecodeOpts)
+_POPTS = ctypes.POINTER(PrefillOpts)
 
 SIGNATURES = {
     "pa_status_string": (ctypes.c_char_p, [_I32]),
@@ -86,6 +92,15 @@ SIGNATURES = {
     "pa_decode_shared_tc": (_I32, [_DESC, _I32, _I32, _OPTS]),
     "pa_decode_launch_count": (_I32, [_DESC, _I32, _I32, _I32, _OPTS]),
     "pa_decode_no_alloc": (_I32, [_P, _P, _P, _P, _DESC, _P, _I32, _P, _I32, _I32, ctypes.c_float, _OPTS, _P]),
+    "pa_prefill_workspace_bytes": (ctypes.c_size_t, [_DESC, _I32, _I32, _I32, _POPTS]),
+    "pa_prefill": (_I32, [_P, _P, _P, _P, _DESC, _P, _I32, _P, _P, _I32, _I32, _I32, ctypes.c_float, _P,
+                          ctypes.c_size_t, _POPTS, _P]),
+    "pa_reshape_and_cache_fp8": (_I32, [_P, _P, _I32, _P, _I32, _P, _P, _P, _P, _DESC, _P]),
+    "pa_gather_cache_fp8": (_I32, [_P, _P, _I32, _P, _I32, _P, _P, _P, _P, _DESC, _P]),
+    "pa_copy_blocks_fp8": (_I32, [_P, _P, _P, _P, _DESC, _P, _I32, _P]),
+    "pa_decode_fp8_workspace_bytes": (ctypes.c_size_t, [_DESC, _I32, _I32, _POPTS]),
+    "pa_decode_fp8": (_I32, [_P, _P, _P, _P, _P, _P, _DESC, _P, _I32, _P, _I32, _I32, ctypes.c_float, _P,
+                             ctypes.c_size_t, _POPTS, _P]),
     "pa_split_range": (None, [_I64, _I32, _I32, _PI64, _PI64]),
     "pa_split_owner": (_I32, [_I64, _I32, _I64]),
     "pa_get_device_error": (_I32, [_P]),

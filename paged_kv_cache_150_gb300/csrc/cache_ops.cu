@@ -164,7 +164,41 @@ static int vec_bytes_for(int64_t row_bytes, const void *a, const void *b, const 
     if (row_bytes % 16 == 0 && any % 16 == 0) return 16;
     if (row_bytes % 8 == 0 && any % 8 == 0) return 8;
     if (row_bytes % 4 == 0 && any % 4 == 0) return 4;
-    return 2;
+    return row_bytes % 2 == 0 && any % 2 == 0 ? 2 : 1;  // 1: the 8-bit cache's codes and scale bytes
+}
+
+void launch_copy_blocks(void *k_cache, void *v_cache, int64_t block_bytes, int32_t num_blocks,
+                        const int32_t *src_dst_pairs, int32_t num_pairs, unsigned int *err, cudaStream_t s) {
+    const int vb = vec_bytes_for(block_bytes, k_cache, v_cache, k_cache, v_cache);
+    const int64_t block_vecs = block_bytes / vb;
+    const int threads = 256;
+    // 16 KiB of each tensor per CTA (8 warps x 32 lanes x kUnroll 16-byte
+    // vectors: one round trip), at least one CTA per pair
+    int32_t chunks = (int32_t)std::max<int64_t>(1, (block_vecs * vb + 16383) / 16384);
+    if ((int64_t)num_pairs * chunks > INT32_MAX) chunks = INT32_MAX / num_pairs;
+    const int grid = num_pairs * chunks;
+    switch (vb) {
+        case 16:
+            launch_pdl(copy_blocks_kernel<uint4>, grid, threads, s, (uint4 *)k_cache, (uint4 *)v_cache,
+                       src_dst_pairs, num_pairs, num_blocks, block_vecs, chunks, err);
+            break;
+        case 8:
+            launch_pdl(copy_blocks_kernel<uint2>, grid, threads, s, (uint2 *)k_cache, (uint2 *)v_cache,
+                       src_dst_pairs, num_pairs, num_blocks, block_vecs, chunks, err);
+            break;
+        case 4:
+            launch_pdl(copy_blocks_kernel<uint32_t>, grid, threads, s, (uint32_t *)k_cache, (uint32_t *)v_cache,
+                       src_dst_pairs, num_pairs, num_blocks, block_vecs, chunks, err);
+            break;
+        case 2:
+            launch_pdl(copy_blocks_kernel<uint16_t>, grid, threads, s, (uint16_t *)k_cache, (uint16_t *)v_cache,
+                       src_dst_pairs, num_pairs, num_blocks, block_vecs, chunks, err);
+            break;
+        default:
+            launch_pdl(copy_blocks_kernel<uint8_t>, grid, threads, s, (uint8_t *)k_cache, (uint8_t *)v_cache,
+                       src_dst_pairs, num_pairs, num_blocks, block_vecs, chunks, err);
+            break;
+    }
 }
 
 }  // namespace pa
@@ -200,7 +234,7 @@ extern "C" pa_status_t pa_reshape_and_cache(const void *k, const void *v, const 
         return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }
     const int64_t row_bytes = (int64_t)cache->num_kv_heads * cache->head_dim * dtype_bytes(cache->dtype);
-    const int vb = vec_bytes_for(row_bytes, k, v, k_cache, v_cache);
+    const int vb = std::max(2, vec_bytes_for(row_bytes, k, v, k_cache, v_cache));
     const int32_t row_vecs = (int32_t)(row_bytes / vb);
     // One warp per (token, row chunk) up to 32 warps (4 resident CTAs of 256
     // threads) per SM.
@@ -242,32 +276,7 @@ extern "C" pa_status_t pa_copy_blocks(void *k_cache, void *v_cache, const pa_cac
     if (!err) return PA_ERR_CUDA;
     const int64_t block_bytes = (int64_t)cache->block_size * cache->num_kv_heads * cache->head_dim *
                                 dtype_bytes(cache->dtype);
-    const int vb = vec_bytes_for(block_bytes, k_cache, v_cache, k_cache, v_cache);
-    const int64_t block_vecs = block_bytes / vb;
-    const int threads = 256;
-    // 16 KiB of each tensor per CTA (8 warps x 32 lanes x kUnroll 16-byte
-    // vectors: one round trip), at least one CTA per pair
-    int32_t chunks = (int32_t)std::max<int64_t>(1, (block_vecs * vb + 16383) / 16384);
-    if ((int64_t)num_pairs * chunks > INT32_MAX) chunks = INT32_MAX / num_pairs;
-    const int grid = num_pairs * chunks;
-    cudaStream_t s = (cudaStream_t)stream;
-    switch (vb) {
-        case 16:
-            launch_pdl(copy_blocks_kernel<uint4>, grid, threads, s, (uint4 *)k_cache, (uint4 *)v_cache,
-                       src_dst_pairs, num_pairs, cache->num_blocks, block_vecs, chunks, err);
-            break;
-        case 8:
-            launch_pdl(copy_blocks_kernel<uint2>, grid, threads, s, (uint2 *)k_cache, (uint2 *)v_cache,
-                       src_dst_pairs, num_pairs, cache->num_blocks, block_vecs, chunks, err);
-            break;
-        case 4:
-            launch_pdl(copy_blocks_kernel<uint32_t>, grid, threads, s, (uint32_t *)k_cache, (uint32_t *)v_cache,
-                       src_dst_pairs, num_pairs, cache->num_blocks, block_vecs, chunks, err);
-            break;
-        default:
-            launch_pdl(copy_blocks_kernel<uint16_t>, grid, threads, s, (uint16_t *)k_cache, (uint16_t *)v_cache,
-                       src_dst_pairs, num_pairs, cache->num_blocks, block_vecs, chunks, err);
-            break;
-    }
+    launch_copy_blocks(k_cache, v_cache, block_bytes, cache->num_blocks, src_dst_pairs, num_pairs, err,
+                       (cudaStream_t)stream);
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

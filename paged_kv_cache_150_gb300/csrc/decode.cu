@@ -47,8 +47,6 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include <mutex>
-
 #include "pa_internal.h"
 
 #include "decode_kernels.h"
@@ -196,44 +194,6 @@ const void *mma_kernel_ptr(int D, int B, int layout, bool shared) {
     return shared ? mma_kernel_ptr_shared(D, B, layout) : mma_kernel_ptr_plain(D, B, layout);
 }
 
-// Occupancy-based default split count: one full wave of resident CTAs.  The
-// answer is fixed per (device, kernel, threads, shared memory) and kept in a
-// fixed table: the occupancy query costs about a microsecond of host time per
-// call.  -1 on failure.
-int default_ctas(const void *fn, int threads, size_t smem) {
-    struct Entry {
-        int dev;
-        const void *fn;
-        int threads;
-        size_t smem;
-        int ctas;
-    };
-    constexpr int kEntries = 256;  // distinct (device, kernel, shape) answers kept; later ones are not cached
-    static std::mutex mu;
-    static Entry cache[kEntries];
-    static int used = 0;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return -1;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        for (int i = 0; i < used; ++i) {
-            const Entry &e = cache[i];
-            if (e.dev == dev && e.fn == fn && e.threads == threads && e.smem == smem) return e.ctas;
-        }
-    }
-    const int sms = num_sms();
-    if (sms <= 0) return -1;
-    int per_sm = 0;
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return -1;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, threads, smem) != cudaSuccess) return -1;
-    const int ctas = sms * std::max(per_sm, 1);
-    std::lock_guard<std::mutex> lock(mu);
-    if (used < kEntries) cache[used++] = Entry{dev, fn, threads, smem, ctas};
-    return ctas;
-}
-
 pa_status_t make_plan(const pa_cache_desc_t *c, int32_t N, int32_t H, const pa_decode_opts_t *opts,
                       bool need_default_splits, DecodePlan *p) {
     pa_status_t st = validate_cache_desc(c);
@@ -348,37 +308,6 @@ pa_status_t make_plan(const pa_cache_desc_t *c, int32_t N, int32_t H, const pa_d
     }
     p->total = off;
     return PA_OK;
-}
-
-// Launch with programmatic stream serialization: the grid may be scheduled
-// while the previous kernel on the stream finishes; the kernel itself calls
-// griddepcontrol.wait before touching anything that kernel produced.
-cudaError_t launch_pdl(const void *fn, dim3 grid, dim3 block, void **args, size_t smem, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelExC(&cfg, fn, args);
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = (PFN_cuTensorMapEncodeTiled_v12000)ptr;
-    });
-    return fn;
 }
 
 // 4-D maps over one cache (128-byte rows: 64 bf16 or 32 fp32 elements); NH

@@ -1,6 +1,9 @@
 // Host-side helpers shared by the translation units of libpa.so.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
@@ -11,7 +14,7 @@
 
 namespace pa {
 
-inline int dtype_bytes(int32_t dtype) { return dtype == PA_F32 ? 4 : 2; }
+inline int dtype_bytes(int32_t dtype) { return dtype == PA_F32 ? 4 : dtype == PA_FP8_E4M3 ? 1 : 2; }
 
 inline pa_status_t validate_cache_desc(const pa_cache_desc_t *c) {
     if (!c) return PA_ERR_INVALID_ARG;
@@ -57,5 +60,21 @@ void *symbol_address(SymbolCache *cache, const void *symbol);
 
 // Streaming multiprocessors of the current device (0 on failure).
 int num_sms();
+
+// One full wave of resident CTAs of a kernel on the current device (cached);
+// -1 on failure.
+int default_ctas(const void *fn, int threads, size_t smem);
+
+// Launch with programmatic stream serialization (see the definition).
+cudaError_t launch_pdl(const void *fn, dim3 grid, dim3 block, void **args, size_t smem, cudaStream_t s);
+
+// Copy-on-write copies of blocks of block_bytes in two arrays (errors are left
+// to cudaGetLastError).
+void launch_copy_blocks(void *k_cache, void *v_cache, int64_t block_bytes, int32_t num_blocks,
+                        const int32_t *src_dst_pairs, int32_t num_pairs, unsigned int *err, cudaStream_t s);
+
+// The driver's cuTensorMapEncodeTiled (nullptr when the driver lacks it).
+using TensorMapEncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
+TensorMapEncodeFn encode_fn();
 
 }  // namespace pa

@@ -1,0 +1,169 @@
+// Chunk attention over the paged cache (pa_prefill): host side and the work
+// list and merge kernels.  The attention kernels are prefill_tc.cuh (tcgen05)
+// and prefill_simt.cuh (CUDA cores); prefill_plan.cuh describes the split.
+#include "prefill_kernels.h"
+
+namespace pa {
+
+namespace {
+
+inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+bool tc_supported(const pa_cache_desc_t *c, int G) {
+    return false && c->dtype == PA_BF16 && c->layout == PA_LAYOUT_ROW && (c->head_dim == 64 || c->head_dim == 128) &&
+           c->block_size % 8 == 0 && G <= 64;
+}
+
+}  // namespace
+
+pa_status_t prefill_layout(bool tc, const pa_cache_desc_t *c, int32_t N, int32_t T, int32_t H, int32_t num_splits,
+                           PrefillPlan *p) {
+    const int32_t G = H / c->num_kv_heads;
+    const void *fn = prefill_simt_ptr(c->dtype, c->head_dim, c->layout, &p->smem);
+    if (!fn) return PA_ERR_UNSUPPORTED;
+    p->tc = tc;
+    p->rows = 64;
+    p->nrt = 1;
+    p->kt = 64;
+    const int threads = 256;
+    p->tq1 = p->rows / G;
+    const int64_t tq = (int64_t)p->tq1 * p->nrt;
+    const int64_t tiles = (int64_t)N + T / tq;  // sum of ceil(n_i / tq)
+    if (tiles >= ((int64_t)1 << 30)) return PA_ERR_UNSUPPORTED;
+    p->max_tiles = (int32_t)tiles;
+    p->C = num_splits;
+    if (p->C == 0) p->C = default_ctas(fn, threads, p->smem);
+    if (p->C <= 0) return PA_ERR_CUDA;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = align256(off + bytes);
+        return at;
+    };
+    p->off_ctl = take(256);
+    p->off_tile0 = take(sizeof(int32_t) * ((size_t)N + 1));
+    p->off_cu = take(sizeof(int32_t) * ((size_t)tiles + 1));
+    p->off_tiles = take(sizeof(PrefillTile) * std::max<size_t>((size_t)tiles, 1));
+    p->off_start = take(sizeof(int32_t) * (size_t)p->C);
+    const size_t slot_rows = 2 * (size_t)p->C * p->nrt * p->rows;
+    p->off_ml = take(sizeof(float2) * slot_rows);
+    p->off_acc = take(sizeof(float) * slot_rows * c->head_dim);
+    p->total = off;
+    return PA_OK;
+}
+
+pa_status_t prefill_launch(const PrefillPlan &p, const pa_cache_desc_t *c, PrefillArgs a, void *workspace,
+                           cudaStream_t s) {
+    uint8_t *ws = (uint8_t *)workspace;
+    a.Hk = c->num_kv_heads;
+    a.G = a.H / a.Hk;
+    a.NB = c->num_blocks;
+    a.B = c->block_size;
+    a.tq1 = p.tq1;
+    a.rows = p.rows;
+    a.nrt = p.nrt;
+    a.kt = p.kt;
+    a.C = p.C;
+    a.max_tiles = p.max_tiles;
+    a.ctl = (int32_t *)(ws + p.off_ctl);
+    a.seq_tile0 = (int32_t *)(ws + p.off_tile0);
+    a.cu = (int32_t *)(ws + p.off_cu);
+    a.tiles = (PrefillTile *)(ws + p.off_tiles);
+    a.start_tile = (int32_t *)(ws + p.off_start);
+    a.ml = (float2 *)(ws + p.off_ml);
+    a.acc = (float *)(ws + p.off_acc);
+    a.err = device_error_word();
+    if (!a.err) return PA_ERR_CUDA;
+    cudaGetLastError();  // clear a stale launch error so the checks below are ours
+    void *args[] = {&a};
+    if (launch_pdl((const void *)prefill_plan_kernel, dim3(1), dim3(1024), args, 0, s) != cudaSuccess) return PA_ERR_CUDA;
+    size_t smem;
+    const void *fn = prefill_simt_ptr(c->dtype, c->head_dim, c->layout, &smem);
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return PA_ERR_CUDA;
+    if (launch_pdl(fn, dim3(p.C), dim3(256), args, smem, s) != cudaSuccess) return PA_ERR_CUDA;
+    if (p.C > 1) {  // a single CTA cuts no tile
+        const bool f32 = c->dtype == PA_F32;
+        const void *mfn =
+            c->head_dim == 64    ? (f32 ? (const void *)prefill_merge_kernel<float, 64>
+                                        : (const void *)prefill_merge_kernel<__nv_bfloat16, 64>)
+            : c->head_dim == 128 ? (f32 ? (const void *)prefill_merge_kernel<float, 128>
+                                        : (const void *)prefill_merge_kernel<__nv_bfloat16, 128>)
+                                 : (f32 ? (const void *)prefill_merge_kernel<float, 256>
+                                        : (const void *)prefill_merge_kernel<__nv_bfloat16, 256>);
+        // 4 CTAs of 8 warps share the rows of a cut tile
+        if (launch_pdl(mfn, dim3(p.C - 1, 4), dim3(256), args, 0, s) != cudaSuccess) return PA_ERR_CUDA;
+    }
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+static pa_status_t prefill_plan_of(const pa_cache_desc_t *c, int32_t N, int32_t T, int32_t H,
+                                   const pa_prefill_opts_t *opts, bool scale_ok, PrefillPlan *p) {
+    const pa_status_t st = validate_cache_desc(c);
+    if (st != PA_OK) return st;
+    if (N < 0 || T < 0 || H <= 0 || H % c->num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+    const int want = opts ? opts->kernel : PA_KERNEL_AUTO;
+    if (want != PA_KERNEL_AUTO && want != PA_KERNEL_SIMT && want != PA_KERNEL_MMA) return PA_ERR_INVALID_ARG;
+    if (opts && opts->num_splits < 0) return PA_ERR_INVALID_ARG;
+    const int32_t G = H / c->num_kv_heads;
+    if (G > 64) return PA_ERR_UNSUPPORTED;
+    const bool tc = want != PA_KERNEL_SIMT && scale_ok && tc_supported(c, G);
+    if (want == PA_KERNEL_MMA && !tc) return PA_ERR_UNSUPPORTED;
+    return prefill_layout(tc, c, N, T, H, opts ? opts->num_splits : 0, p);
+}
+
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" size_t pa_prefill_workspace_bytes(const pa_cache_desc_t *cache, int32_t num_seqs, int32_t num_tokens,
+                                             int32_t num_heads, const pa_prefill_opts_t *opts) try {
+    PrefillPlan p;
+    if (prefill_plan_of(cache, num_seqs, num_tokens, num_heads, opts, true, &p) != PA_OK) return 0;
+    return p.total;
+} catch (...) {
+    return 0;
+}
+
+extern "C" pa_status_t pa_prefill(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                  const pa_cache_desc_t *cache, const int32_t *block_tables,
+                                  int32_t max_blocks_per_seq, const int32_t *seq_lens, const int32_t *cu_q_lens,
+                                  int32_t num_seqs, int32_t num_tokens, int32_t num_heads, float scale,
+                                  void *workspace, size_t workspace_bytes, const pa_prefill_opts_t *opts,
+                                  pa_stream_t stream) try {
+    PrefillPlan p;
+    pa_status_t st = prefill_plan_of(cache, num_seqs, num_tokens, num_heads, opts, true, &p);
+    if (st != PA_OK) return st;
+    if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens || !cu_q_lens || !workspace)
+        return PA_ERR_INVALID_ARG;
+    if (max_blocks_per_seq <= 0 || (int64_t)num_seqs * max_blocks_per_seq >= ((int64_t)1 << 31) ||
+        (int64_t)max_blocks_per_seq * cache->block_size >= ((int64_t)1 << 31))
+        return PA_ERR_INVALID_ARG;
+    // the units of a KV head are counted in 32 bits
+    if ((int64_t)p.max_tiles * ((int64_t)max_blocks_per_seq * cache->block_size / p.kt + 1) >= ((int64_t)1 << 31))
+        return PA_ERR_UNSUPPORTED;
+    if (!(scale == scale)) return PA_ERR_INVALID_ARG;
+    if (((uintptr_t)workspace & 255) != 0) return PA_ERR_INVALID_ARG;
+    if (workspace_bytes < p.total) return PA_ERR_WORKSPACE;
+    const int eb = dtype_bytes(cache->dtype);
+    if (((uintptr_t)q | (uintptr_t)out) % (size_t)(eb * 2) != 0) return PA_ERR_INVALID_ARG;
+    if (((uintptr_t)k_cache | (uintptr_t)v_cache) % 16 != 0) return PA_ERR_INVALID_ARG;
+    PrefillArgs a{};
+    a.q = q;
+    a.out = out;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.tables = block_tables;
+    a.seq_lens = seq_lens;
+    a.cu_q = cu_q_lens;
+    a.max_blocks = max_blocks_per_seq;
+    a.N = num_seqs;
+    a.T = num_tokens;
+    a.H = num_heads;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    return prefill_launch(p, cache, a, workspace, (cudaStream_t)stream);
+} catch (...) {
+    return host_failure();
+}

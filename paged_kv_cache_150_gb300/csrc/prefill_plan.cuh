@@ -1,0 +1,316 @@
+// Work list, pieces and merge of chunk attention (pa_prefill).
+//
+// The chunk's new tokens are cut into tiles of tq tokens x the G query heads
+// of one KV head; a tile attends to keys 0 .. p0 + ntok - 1 of its sequence
+// in units of kt keys.  The flattened list of (KV head, tile, unit) is cut
+// evenly over C persistent CTAs (split_begin), so that long and short
+// chunks, and one long context as well as many short ones, load every CTA
+// alike.  A CTA's range is a run of segments (one tile's units); a segment
+// that holds all of its tile's units writes `out`, any other one (at most the
+// first and the last of a range) writes a piece: the unnormalised
+// accumulator with its running maximum (log2 units) and sum.
+// prefill_merge_kernel folds the pieces of every cut tile in CTA order, so
+// the same call gives the same bits every time.
+#pragma once
+
+#include "decode_merge.cuh"  // store_out
+#include "pa_internal.h"
+
+namespace pa {
+
+// One tile of the list.
+struct PrefillTile {
+    int32_t seq;   // sequence (block-table row)
+    int32_t row0;  // row of q / out of its first token
+    int32_t ntok;  // tokens in this tile
+    int32_t p0;    // position of its first token (negative: before the sequence's first key)
+};
+
+// The call, as its kernels see it (one struct, passed by value).
+struct PrefillArgs {
+    const void *q;
+    void *out;
+    const void *k_cache, *v_cache;
+    const uint8_t *k_scale, *v_scale;  // 8-bit caches: biased scale exponents [NB, B, Hk]
+    const int32_t *tables, *seq_lens;
+    const int32_t *cu_q;  // nullptr: one new token per sequence
+    int32_t max_blocks, N, T, H, Hk, G, NB, B;
+    int32_t tq1;          // tokens per row tile of the kernel (rows / G)
+    int32_t rows;         // query rows of one row tile
+    int32_t nrt;          // row tiles per tile (tq = tq1 * nrt)
+    int32_t kt;           // keys per unit
+    int32_t C;            // persistent CTAs
+    int32_t max_tiles;    // capacity of tiles[] and cu[]
+    float scale_log2;
+    int32_t *ctl;         // ctl[0]: tiles of the list
+    int32_t *seq_tile0;   // [N + 1] first tile of each sequence
+    int32_t *cu;          // [max_tiles + 1] exclusive prefix sums of the tiles' units
+    PrefillTile *tiles;   // [max_tiles]
+    int32_t *start_tile;  // [C] tile holding the first unit of each CTA's range
+    float2 *ml;           // [2 C][nrt * rows]
+    float *acc;           // [2 C][nrt * rows][D]
+    unsigned int *err;
+};
+
+__device__ __forceinline__ int32_t prefill_units(const PrefillTile &t, int32_t kt) {
+    const int32_t keys = t.p0 + t.ntok;
+    return keys <= kt ? 1 : (int32_t)(((int64_t)keys + kt - 1) / kt);  // no key: one unit that writes zeros
+}
+
+// Inclusive block-wide scan of x over 1024 threads plus carry; returns this
+// thread's inclusive sum, *total the sum with the carry.
+__device__ __forceinline__ int32_t block_scan_1024(int32_t x, int32_t carry, int32_t *warp_incl, int32_t *total) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();  // the previous scan's reads of warp_incl
+    if (lane == 31) warp_incl[w] = x;
+    __syncthreads();
+    if (w == 0) {
+        int32_t s = warp_incl[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        warp_incl[lane] = s;
+    }
+    __syncthreads();
+    *total = carry + warp_incl[31];
+    return carry + x + (w > 0 ? warp_incl[w - 1] : 0);
+}
+
+// One CTA: the tiles of every sequence, the prefix sums of their units, and
+// the tile in which each CTA's range starts.  Row offsets that are not
+// increasing within [0, T] void the whole call (no tile: out stays as it
+// was), a length outside the table's reach counts as 0; both are recorded.
+static __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillArgs a) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    constexpr int32_t kSmemCu = 8192;
+    __shared__ int32_t warp_incl[32];
+    __shared__ int32_t cu_s[kSmemCu];
+    const int tid = threadIdx.x;
+    const int64_t max_len = (int64_t)a.max_blocks * a.B;
+    const int32_t tq = a.tq1 * a.nrt;
+    bool ok = true;
+    if (a.cu_q) {
+        for (int32_t i = tid; i <= a.N; i += 1024) {
+            const int32_t x = a.cu_q[i];
+            ok = ok && x >= 0 && x <= a.T && (i == 0 || a.cu_q[i - 1] <= x);
+        }
+    }
+    ok = __syncthreads_and(ok) != 0;
+    if (!ok) {
+        if (tid == 0) {
+            atomicOr(a.err, kErrBounds);
+            a.ctl[0] = 0;
+            a.cu[0] = 0;
+        }
+        return;
+    }
+    int32_t tiles = 0;
+    for (int32_t base = 0; base < a.N; base += 1024) {
+        const int32_t i = base + tid;
+        int32_t nt = 0;
+        if (i < a.N) {
+            const int32_t n = a.cu_q ? a.cu_q[i + 1] - a.cu_q[i] : 1;
+            nt = (int32_t)(((int64_t)n + tq - 1) / tq);
+            const int32_t L = a.seq_lens[i];
+            if (L < 0 || L > max_len) atomicOr(a.err, kErrLength);
+        }
+        int32_t total;
+        const int32_t incl = block_scan_1024(nt, tiles, warp_incl, &total);
+        if (i < a.N) a.seq_tile0[i] = incl - nt;
+        tiles = total;
+    }
+    if (tid == 0) a.seq_tile0[a.N] = tiles;
+    __syncthreads();  // seq_tile0 (global memory) is read by this CTA's other threads
+    const bool in_smem = tiles + 1 <= kSmemCu;
+    int32_t units = 0;
+    for (int32_t base = 0; base < tiles; base += 1024) {
+        const int32_t k = base + tid;
+        int32_t u = 0;
+        if (k < tiles) {
+            int32_t lo = 0, hi = a.N - 1;  // largest sequence with seq_tile0 <= k (it has tiles)
+            while (lo < hi) {
+                const int32_t mid = (lo + hi + 1) >> 1;
+                if (a.seq_tile0[mid] <= k)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const int32_t r0 = a.cu_q ? a.cu_q[lo] : lo, n = a.cu_q ? a.cu_q[lo + 1] - r0 : 1;
+            const int32_t t0 = (k - a.seq_tile0[lo]) * tq;
+            int32_t L = a.seq_lens[lo];
+            if (L < 0 || L > max_len) L = 0;
+            PrefillTile t;
+            t.seq = lo;
+            t.row0 = r0 + t0;
+            t.ntok = min(tq, n - t0);
+            t.p0 = L - n + t0;
+            a.tiles[k] = t;
+            u = prefill_units(t, a.kt);
+        }
+        int32_t total;
+        const int32_t incl = block_scan_1024(u, units, warp_incl, &total);
+        if (k < tiles) {
+            a.cu[k] = incl - u;
+            if (in_smem) cu_s[k] = incl - u;
+        }
+        units = total;
+    }
+    if (tid == 0) {
+        a.cu[tiles] = units;
+        a.ctl[0] = tiles;
+    }
+    __syncthreads();
+    const int32_t *cu = in_smem ? cu_s : a.cu;
+    const int64_t W = (int64_t)a.Hk * units;
+    const int32_t Ce = (int32_t)min(W, (int64_t)a.C);
+    for (int32_t c = tid; c < Ce; c += 1024) {
+        const int32_t r = (int32_t)(split_begin(c, W, Ce) % units);
+        int32_t lo = 0, hi = tiles - 1;
+        while (lo < hi) {
+            const int32_t mid = (lo + hi + 1) >> 1;
+            if (cu[mid] <= r)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        a.start_tile[c] = lo;
+    }
+}
+
+// A CTA's walk over its range: segments of consecutive units of one tile.
+struct PrefillCursor {
+    int64_t x, hi;     // next flattened unit, end of the range
+    int32_t kvh, k;    // KV head and tile of the current segment
+    int32_t j0, j1;    // its units [j0, j1)
+    int32_t nu;        // units of its tile
+    int32_t tiles, U;
+    bool first;        // the range's first segment
+
+    // False when the CTA has no work.
+    __device__ __forceinline__ bool init(const PrefillArgs &a, int32_t c) {
+        tiles = a.ctl[0];
+        U = a.cu[tiles];
+        const int64_t W = (int64_t)a.Hk * U;
+        const int32_t Ce = (int32_t)min(W, (int64_t)a.C);
+        if (c >= Ce) return false;
+        x = split_begin(c, W, Ce);
+        hi = split_begin((int64_t)c + 1, W, Ce);
+        kvh = (int32_t)(x / U);
+        k = a.start_tile[c];
+        first = true;
+        j0 = (int32_t)(x - (int64_t)kvh * U) - a.cu[k];
+        set_end(a);
+        return true;
+    }
+    __device__ __forceinline__ void set_end(const PrefillArgs &a) {
+        nu = a.cu[k + 1] - a.cu[k];
+        j1 = (int32_t)min((int64_t)nu, j0 + (hi - x));
+    }
+    // Moves to the next segment; false at the range's end.
+    __device__ __forceinline__ bool next(const PrefillArgs &a) {
+        x += j1 - j0;
+        first = false;
+        if (x >= hi) return false;
+        j0 = 0;
+        if (++k == tiles) {
+            k = 0;
+            ++kvh;
+        }
+        set_end(a);
+        return true;
+    }
+    __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == nu; }
+    // Slot of this segment's piece: a range has at most two, its first segment's and its last one's.
+    __device__ __forceinline__ int64_t slot(int32_t c) const { return 2 * (int64_t)c + (first ? 0 : 1); }
+};
+
+// Merge of the cut tiles: block (c - 1, y) folds the tile that the start of
+// CTA c's range cuts, if CTA c - 1 holds that tile's first unit (so each cut
+// tile has one c).  One warp per query row; pieces in CTA order.
+template <typename T, int D>
+static __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs a) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int32_t c = blockIdx.x + 1;
+    const int32_t tiles = a.ctl[0], U = a.cu[tiles];
+    const int64_t W = (int64_t)a.Hk * U;
+    const int32_t Ce = (int32_t)min(W, (int64_t)a.C);
+    if (c >= Ce) return;
+    const int64_t x = split_begin(c, W, Ce);
+    const int32_t kvh = (int32_t)(x / U), k = a.start_tile[c];
+    const int64_t x0 = (int64_t)kvh * U + a.cu[k];
+    if (x0 == x) return;  // the range starts with its tile
+    const int32_t c0 = split_owner(x0, W, Ce);
+    if (c0 != c - 1) return;  // an earlier block's tile
+    const int32_t c1 = split_owner((int64_t)kvh * U + a.cu[k + 1] - 1, W, Ce);
+    const PrefillTile t = a.tiles[k];
+    const int lane = threadIdx.x & 31;
+    const int32_t wid = blockIdx.y * 8 + (threadIdx.x >> 5), nw = gridDim.y * 8;
+    const int64_t slot_rows = (int64_t)a.nrt * a.rows;
+    const int64_t first_slot = 2 * (int64_t)c0 + (split_begin(c0, W, Ce) == x0 ? 0 : 1);
+    constexpr int E = D / 32;  // accumulator elements of a lane
+    for (int32_t i = wid; i < t.ntok * a.G; i += nw) {
+        const int32_t tok = i / a.G, g = i - tok * a.G;
+        const int64_t row = (int64_t)(tok / a.tq1) * a.rows + (tok % a.tq1) * a.G + g;
+        float M = -INFINITY, Ls = 0.f, o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = 0.f;
+        for (int32_t p0 = c0; p0 <= c1; p0 += 32) {
+            // 32 pieces' statistics at a time, one per lane
+            const int32_t p = p0 + lane;
+            const int64_t idx = ((p == c0 ? first_slot : 2 * (int64_t)p) * slot_rows + row);
+            float2 v = make_float2(-INFINITY, 0.f);
+            if (p <= c1) v = __ldcg(&a.ml[idx]);
+            float mb = v.x;
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, s));
+            const float Mn = fmaxf(M, mb);
+            if (Mn == -INFINITY && !__any_sync(0xffffffffu, v.y != 0.f)) continue;  // no key seen so far
+            const float mref = Mn == -INFINITY ? 0.f : Mn;
+            const float sc = ex2_approx(M - mref);
+            const float wgt = ex2_approx(v.x - mref);
+            float lw = wgt * v.y;
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, s);
+            Ls = Ls * sc + lw;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] *= sc;
+            const int32_t np = min(32, c1 - p0 + 1);
+#pragma unroll 4
+            for (int32_t j = 0; j < np; ++j) {
+                const float wj = __shfl_sync(0xffffffffu, wgt, j);
+                const int64_t ij = ((p0 + j == c0 ? first_slot : 2 * (int64_t)(p0 + j)) * slot_rows + row);
+                const float *ap = a.acc + ij * D + lane * E;
+                if constexpr (E % 4 == 0) {
+#pragma unroll
+                    for (int e = 0; e < E; e += 4) {
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(ap + e));
+                        o[e] = fmaf(wj, y.x, o[e]);
+                        o[e + 1] = fmaf(wj, y.y, o[e + 1]);
+                        o[e + 2] = fmaf(wj, y.z, o[e + 2]);
+                        o[e + 3] = fmaf(wj, y.w, o[e + 3]);
+                    }
+                } else {
+                    const float2 y = __ldcg(reinterpret_cast<const float2 *>(ap));
+                    o[0] = fmaf(wj, y.x, o[0]);
+                    o[1] = fmaf(wj, y.y, o[1]);
+                }
+            }
+            M = Mn;
+        }
+        const float inv = Ls == 0.f ? 0.f : 1.f / Ls;  // a row without keys is zero
+        T *op = (T *)a.out + ((int64_t)(t.row0 + tok) * a.H + (int64_t)kvh * a.G + g) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) store_out(op + e, o[e] * inv);
+    }
+}
+
+}  // namespace pa

@@ -1,0 +1,320 @@
+"""The 8-bit cache: write, read-back and block copy bit by bit against the rule
+worked out in fp64, and decode attention over it against fp64."""
+import math
+
+import pytest
+import torch
+
+import paged_kv_cache_150_gb300 as pa
+from _chunks import attention, make_tables, slots_of, tolerance, used_rows
+
+pytestmark = pytest.mark.gpu
+BF, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+
+def code_values():
+    """Values of the 256 e4m3 codes, from the format's definition."""
+    vals = []
+    for c in range(256):
+        e, m = (c >> 3) & 15, c & 7
+        x = math.nan if (c & 127) == 127 else (m / 8 * 2.0 ** -6 if e == 0 else (1 + m / 8) * 2.0 ** (e - 7))
+        vals.append(-x if c > 127 else x)
+    return torch.tensor(vals, dtype=torch.float64)
+
+
+def rule(x):
+    """(values of the codes, scale bytes) of rows x [t, hk, d], in fp64 on the CPU."""
+    x = x.double()
+    fin = torch.where(torch.isfinite(x), x.abs(), 0.0)
+    top = fin.amax(-1)
+    e = torch.full_like(top, -126.0)
+    for step in range(-126, 120):  # raise e while the row does not fit
+        e = torch.where(top > 448.0 * 2.0 ** step, torch.full_like(e, step + 1.0), e)
+    y = x / torch.exp2(e).unsqueeze(-1)
+    mag = y.abs()
+    octave = torch.floor(torch.log2(mag.clamp(min=2.0 ** -12, max=448.0))).clamp(min=-6)
+    unit = torch.exp2(octave - 3)
+    r = torch.round(mag / unit) * unit  # half to even
+    r = torch.where(torch.isinf(mag), torch.full_like(r, 448.0), r)
+    return torch.where(torch.isnan(x), x, torch.copysign(r, y)), (e + 127).to(torch.uint8)
+
+
+def pools(nb, bs, hk, d, fill=0x2b):
+    codes = [torch.full((nb, bs, hk, d), fill, dtype=torch.uint8, device="cuda").view(E4M3) for _ in range(2)]
+    scales = [torch.full((nb, bs, hk), 99, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    return codes + scales
+
+
+def rows(shape, dtype, seed, special=True):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(shape, generator=g) * torch.exp2(torch.randint(-40, 40, shape[:2], generator=g).float()).unsqueeze(-1)
+    x = x.to(dtype)
+    if special and x.numel() > 40:
+        f = x.view(-1)
+        f[1], f[5], f[7], f[11] = math.inf, -math.inf, math.nan, 0.0
+        x[0, -1] = 0
+        x[-1, 0] = torch.finfo(dtype).tiny  # clamps the exponent
+        x[-1, -1, 0] = torch.finfo(dtype).max
+    return x
+
+
+SHAPES = [(7, 2, 64), (33, 8, 128), (5, 1, 256), (9, 3, 8), (6, 2, 96), (4, 2, 7), (3, 1, 1), (5, 2, 33), (3, 2, 1024),
+          (200, 4, 128)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("t,hk,d", SHAPES)
+def test_write_and_read_back_bit_by_bit(t, hk, d, dtype):
+    bs = 4
+    nb = t // bs + 3
+    k, v = rows((t, hk, d), dtype, t), rows((t, hk, d), dtype, t + 1)
+    g = torch.Generator().manual_seed(t + 2)
+    slots = torch.randperm(nb * bs, generator=g)[:t].to(torch.int32)
+    slots[t // 2] = -1
+    kc, vc, ks, vs = pools(nb, bs, hk, d)
+    pa.pa_reshape_and_cache_fp8(k.cuda(), v.cuda(), slots.cuda(), kc, vc, ks, vs)
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
+    keep = slots >= 0
+    at = slots[keep].long()
+    vals = code_values()
+    for x, codes, scales in ((k, kc, ks), (v, vc, vs)):
+        want, byte = rule(x[keep])
+        got = vals[codes.view(torch.uint8).cpu().view(-1, hk, d)[at].long()]
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(got.nan_to_num(), want.nan_to_num())
+        assert torch.equal(scales.cpu().view(-1, hk)[at], byte)
+        rest = torch.ones(nb * bs, dtype=torch.bool)
+        rest[at] = False  # every other slot as it was
+        assert bool((codes.view(torch.uint8).cpu().view(-1, hk, d)[rest] == 0x2b).all())
+        assert bool((scales.cpu().view(-1, hk)[rest] == 99).all())
+    for out_dt in (BF, F32):
+        gk, gv = pa.pa_gather_cache_fp8(kc, vc, ks, vs, slots.cuda(), dtype=out_dt)
+        assert pa.pa_get_device_error(raise_on_error=False) == 0
+        for x, got in ((k, gk), (v, gv)):
+            want, byte = rule(x[keep])
+            want = (want * torch.exp2(byte.double() - 127).unsqueeze(-1)).to(out_dt)
+            full = torch.zeros(t, hk, d, dtype=out_dt)
+            full[keep] = want
+            got = got.cpu()
+            assert torch.equal(torch.isnan(got), torch.isnan(full))
+            assert torch.equal(got.nan_to_num(), full.nan_to_num())
+
+
+def test_every_code_and_scale_byte_reads_back():
+    hk, d, bs = 1, 256, 1
+    kc, vc, ks, vs = pools(254, bs, hk, d)
+    allc = torch.arange(256, dtype=torch.uint8).view(1, 1, 1, 256).expand(254, bs, hk, d).contiguous()
+    kc.view(torch.uint8).copy_(allc)
+    ks.copy_(torch.arange(1, 255, dtype=torch.uint8).view(254, 1, 1))
+    slots = torch.arange(254, dtype=torch.int32, device="cuda")
+    got = pa.pa_gather_cache_fp8(kc, vc, ks, vs, slots, dtype=F32)[0].cpu().view(254, 256)
+    want = (code_values()[None] * torch.exp2(torch.arange(1, 255).double() - 127)[:, None]).float()
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got.nan_to_num(posinf=3e38), want.nan_to_num(posinf=3e38))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_unaligned_rows(dtype):
+    """k, v and the outputs start one element past a 16-byte boundary."""
+    t, hk, d, bs = 9, 2, 64, 4
+    k, v = rows((t, hk, d), dtype, 31), rows((t, hk, d), dtype, 32)
+    kc, vc, ks, vs = pools(4, bs, hk, d)
+    kd, vd = (torch.empty(t * hk * d + 1, dtype=dtype, device="cuda")[1:].view(t, hk, d) for _ in range(2))
+    kd.copy_(k)
+    vd.copy_(v)
+    slots = torch.arange(t, dtype=torch.int32, device="cuda")
+    pa.pa_reshape_and_cache_fp8(kd, vd, slots, kc, vc, ks, vs)
+    ref = pools(4, bs, hk, d)
+    pa.pa_reshape_and_cache_fp8(k.cuda(), v.cuda(), slots, *ref)
+    for a, b in zip((kc, vc, ks, vs), ref):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    pa.pa_gather_cache_fp8(kc, vc, ks, vs, slots, k=kd, v=vd)
+    gk, gv = pa.pa_gather_cache_fp8(kc, vc, ks, vs, slots, dtype=dtype)
+    assert torch.equal(kd.nan_to_num(), gk.nan_to_num()) and torch.equal(vd.nan_to_num(), gv.nan_to_num())
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
+
+
+@pytest.mark.parametrize("d", [128, 33])
+def test_slots_past_the_pool(d):
+    hk, bs, nb = 2, 4, 3
+    kc, vc, ks, vs = pools(nb, bs, hk, d)
+    k = torch.ones(3, hk, d, dtype=BF, device="cuda")
+    slots = torch.tensor([nb * bs, 5, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    pa.pa_reshape_and_cache_fp8(k, k, slots, kc, vc, ks, vs)
+    assert pa.pa_get_device_error(raise_on_error=False) == pa._lib.PA_ERR_DEVICE_BOUNDS
+    assert int((ks != 99).sum()) == hk
+    gk, gv = pa.pa_gather_cache_fp8(kc, vc, ks, vs, slots)
+    assert pa.pa_get_device_error(raise_on_error=False) == pa._lib.PA_ERR_DEVICE_BOUNDS
+    assert torch.count_nonzero(gk[0]) == 0 and torch.count_nonzero(gk[2]) == 0 and torch.equal(gk[1], k[1])
+
+
+def test_write_and_read_rows_past_32_bits():
+    """More than 2^31 codes in the pool and more than 2^31 elements in k and v."""
+    hk, d, bs = 8, 128, 16
+    t = (2 ** 31) // (hk * d) + 1000
+    nb = -(-t // bs) + 1
+    kc, vc, ks, vs = pools(nb, bs, hk, d)
+    k = torch.zeros(t, hk, d, dtype=BF, device="cuda")
+    k[-1000:] = torch.randn(1000, hk, d, device="cuda").to(BF)
+    slots = torch.arange(t, dtype=torch.int32, device="cuda") + bs
+    pa.pa_reshape_and_cache_fp8(k, k, slots, kc, vc, ks, vs)
+    gk, gv = pa.pa_gather_cache_fp8(kc, vc, ks, vs, slots)
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
+    want, byte = rule(k[-1000:].cpu())
+    want = (want * torch.exp2(byte.double() - 127).unsqueeze(-1)).to(BF)
+    assert torch.equal(gk[-1000:].cpu(), want) and torch.equal(gv[-1000:].cpu(), want)
+    assert torch.count_nonzero(gk[:-1000]) == 0
+
+
+@pytest.mark.parametrize("nb,bs,hk,d", [(12, 16, 8, 128), (9, 4, 2, 64), (8, 1, 1, 7), (8, 3, 1, 1)])
+def test_copy_blocks(nb, bs, hk, d):
+    g = torch.Generator().manual_seed(nb)
+    kc, vc = (torch.randint(0, 256, (nb, bs, hk, d), generator=g).to(torch.uint8).cuda().view(E4M3) for _ in range(2))
+    ks, vs = (torch.randint(1, 240, (nb, bs, hk), generator=g).to(torch.uint8).cuda() for _ in range(2))
+    want = [x.view(torch.uint8).clone() for x in (kc, vc, ks, vs)]
+    pairs = torch.tensor([[0, 5], [1, 6], [0, 7]], dtype=torch.int32)
+    for w in want:
+        w[pairs[:, 1].long()] = w[pairs[:, 0].long()]
+    pa.pa_copy_blocks_fp8(kc, vc, ks, vs, pairs.cuda())
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
+    for w, x in zip(want, (kc, vc, ks, vs)):
+        assert torch.equal(w, x.view(torch.uint8))
+    pa.pa_copy_blocks_fp8(kc, vc, ks, vs, torch.zeros(0, 2, dtype=torch.int32, device="cuda"))
+
+
+class Batch:
+    """A pa_decode_fp8 call; stale slots hold NaN codes and the NaN scale byte."""
+
+    def __init__(self, lens, H, Hk, D, block, seed, spread=6):
+        g = torch.Generator().manual_seed(seed)
+        self.lens, self.block, self.scale = lens, block, 1.0 / math.sqrt(D)
+        self.tables, pool = make_tables(lens, block, g)
+        stale = ~used_rows(self.tables, lens, block, pool)
+        self.vals, self.dev = [], {}
+        for name in ("k", "v"):
+            x = torch.randn(pool * block, Hk, D, generator=g)
+            x *= torch.exp2(torch.randint(-spread, 3, (pool * block, Hk), generator=g).float()).unsqueeze(-1)
+            cache, byte = x.to(BF), None
+            c = torch.empty(pool, block, Hk, D, dtype=torch.uint8, device="cuda").view(E4M3)
+            s = torch.empty(pool, block, Hk, dtype=torch.uint8, device="cuda")
+            slots = torch.arange(pool * block, dtype=torch.int32, device="cuda")
+            pa.pa_reshape_and_cache_fp8(cache.cuda(), cache.cuda(), slots, c, c.clone(), s, s.clone())
+            c.view(torch.uint8).view(-1, Hk, D)[stale.cuda()] = 0x7f
+            s.view(-1, Hk)[stale.cuda()] = 255
+            codes = code_values()[c.view(torch.uint8).cpu().view(-1, Hk, D).long()]
+            self.vals.append(codes * torch.exp2(s.cpu().view(-1, Hk).double() - 127).unsqueeze(-1))
+            self.dev[name + "_cache"], self.dev[name + "_scale"] = c, s
+        self.q = torch.randn(len(lens), H, D, generator=g).to(BF)
+        self.dev.update(q=self.q.cuda(), block_tables=self.tables.cuda(), scale=self.scale,
+                        seq_lens=torch.tensor(lens, dtype=torch.int32).cuda())
+
+    def check(self, out):
+        # probabilities in fp16: 2^-11 each, or 2^-25 absolute of a weight of at least 1 (the largest score's)
+        p_eps = 2.0 ** -11
+        for i, L in enumerate(self.lens):
+            r = slots_of(self.tables[i], L, self.block)
+            k, v = self.vals[0][r].cuda(), self.vals[1][r].cuda()
+            ref, amount, dots, top = attention(self.q[i:i + 1].cuda(), k, v, L - 1, self.scale)
+            big = float(v.abs().max()) if L else 0.0
+            tol = tolerance(BF, ref, amount, dots, top, L, ref.shape[-1], p_eps) + L * 2.0 ** -25 * big
+            got = out[i:i + 1].double()
+            assert torch.isfinite(got).all()
+            assert float(((got - ref).abs() / tol).max()) <= 1.0, (i, L)
+
+
+DECODE = [(32, 8, 128, 16), (8, 8, 128, 16), (16, 2, 64, 32), (12, 4, 128, 16), (8, 1, 128, 64), (7, 1, 64, 8),
+          (8, 4, 128, 128), (6, 6, 128, 48), (8, 2, 128, 5), (8, 2, 256, 16), (4, 4, 64, 4), (4, 2, 64, 256)]
+
+
+@pytest.mark.parametrize("kernel", ["auto", "simt"])
+@pytest.mark.parametrize("H,Hk,D,block", DECODE)
+def test_decode(H, Hk, D, block, kernel):
+    b = Batch([1, 0, 15, 16, 17, 31, 33, 64, 65, 700, 129], H, Hk, D, block, seed=H + D + block)
+    out = pa.pa_decode_fp8(**b.dev, kernel=kernel)
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
+    b.check(out)
+    assert torch.count_nonzero(out[1]) == 0
+    assert torch.equal(out, pa.pa_decode_fp8(**b.dev, kernel=kernel))
+
+
+@pytest.mark.parametrize("kernel", ["auto", "simt"])
+@pytest.mark.parametrize("splits", [1, 2, 5, 37, 900])
+def test_decode_any_split_count(kernel, splits):
+    b = Batch([3000, 1, 900, 50], 32, 8, 128, 16, seed=40)
+    b.check(pa.pa_decode_fp8(**b.dev, num_splits=splits, kernel=kernel))
+
+
+@pytest.mark.parametrize("kernel", ["auto", "simt"])
+def test_decode_over_rows_of_very_different_size(kernel):
+    b = Batch([700, 300, 2000], 32, 8, 128, 16, seed=41, spread=40)
+    b.check(pa.pa_decode_fp8(**b.dev, kernel=kernel))
+
+
+@pytest.mark.parametrize("kernel", ["auto", "simt"])
+def test_decode_bad_pages_and_lengths(kernel):
+    b = Batch([200, 60], 8, 2, 128, 16, seed=42)
+    tables = b.tables.clone()
+    tables[0, 3], tables[1, 0] = b.dev["k_cache"].shape[0], -7
+    for i, blk in ((0, 3), (1, 0)):
+        r = slots_of(b.tables[i], b.lens[i], 16)[blk * 16:(blk + 1) * 16]
+        for x in b.vals:
+            x[r] = 0
+    out = pa.pa_decode_fp8(**dict(b.dev, block_tables=tables.cuda()), kernel=kernel)
+    assert pa.pa_get_device_error(raise_on_error=False) == pa._lib.PA_ERR_DEVICE_BOUNDS
+    b.check(out)
+    out = pa.pa_decode_fp8(**dict(b.dev, seq_lens=torch.tensor([200, 10 ** 6], dtype=torch.int32).cuda()), kernel=kernel)
+    assert pa.pa_get_device_error(raise_on_error=False) == pa._lib.PA_ERR_DEVICE_BOUNDS
+    assert torch.count_nonzero(out[1]) == 0
+
+
+def test_decode_side_stream_and_graphs_that_share_a_workspace():
+    a, b = Batch([200, 60, 3000], 32, 8, 128, 16, seed=43), Batch([7, 64], 32, 8, 128, 16, seed=44)
+    need = max(pa.pa_decode_fp8_workspace_bytes(x.dev["k_cache"], len(x.lens), 32) for x in (a, b))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros_like(x.dev["q"]) for x in (a, b)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for x, o in zip((a, b), outs):
+            pa.pa_decode_fp8(**x.dev, out=o, workspace=ws)
+    torch.cuda.current_stream().wait_stream(s)
+    want = [o.clone() for o in outs]
+    a.check(want[0])
+    b.check(want[1])
+    graphs = []
+    for x, o in zip((a, b), outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pa.pa_decode_fp8(**x.dev, out=o, workspace=ws)
+        graphs.append(g)
+    for order in ((0, 1), (1, 0), (0, 0, 1)):
+        for o in outs:
+            o.zero_()
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in set(order):
+            assert torch.equal(outs[i], want[i])
+
+
+def test_python_refusals():
+    b = Batch([20, 6], 8, 2, 128, 16, seed=45)
+    d = b.dev
+    with pytest.raises(TypeError):
+        pa.pa_decode_fp8(**dict(d, q=d["q"].float()))
+    with pytest.raises(TypeError):
+        pa.pa_decode_fp8(**dict(d, k_cache=d["k_cache"].view(torch.uint8)))
+    with pytest.raises(ValueError):
+        pa.pa_decode_fp8(**dict(d, k_scale=d["k_scale"][:, :, :1]))
+    with pytest.raises(pa.PagedAttentionError):
+        pa.pa_decode_fp8(**dict(d, q=torch.zeros(2, 32, 128, dtype=BF, device="cuda")))  # 16 heads per KV head
+    with pytest.raises(pa.PagedAttentionError):
+        pa.pa_decode_fp8(**d, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    k = torch.zeros(2, 2, 128, dtype=torch.float16, device="cuda")
+    slots = torch.zeros(2, dtype=torch.int32, device="cuda")
+    with pytest.raises(TypeError):
+        pa.pa_reshape_and_cache_fp8(k, k, slots, d["k_cache"], d["v_cache"], d["k_scale"], d["v_scale"])
+    with pytest.raises(ValueError):
+        pa.pa_gather_cache_fp8(d["k_cache"], d["v_cache"], d["k_scale"], d["v_scale"], slots, k=k)
+    with pytest.raises(ValueError):
+        pa.pa_reshape_and_cache_fp8(k[:, :1].bfloat16(), k[:, :1].bfloat16(), slots, d["k_cache"], d["v_cache"],
+                                    d["k_scale"], d["v_scale"])
