@@ -1,7 +1,11 @@
 // Chunk attention over the paged cache (pa_prefill): host side and the work
 // list and merge kernels.  The attention kernels are prefill_tc.cuh (tcgen05)
 // and prefill_simt.cuh (CUDA cores); prefill_plan.cuh describes the split.
+#include <cmath>
+
 #include "prefill_kernels.h"
+#include "prefill_simt.cuh"
+#include "prefill_tc.cuh"
 
 namespace pa {
 
@@ -10,8 +14,35 @@ namespace {
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 bool tc_supported(const pa_cache_desc_t *c, int G) {
-    return false && c->dtype == PA_BF16 && c->layout == PA_LAYOUT_ROW && (c->head_dim == 64 || c->head_dim == 128) &&
+    return c->dtype == PA_BF16 && c->layout == PA_LAYOUT_ROW && (c->head_dim == 64 || c->head_dim == 128) &&
            c->block_size % 8 == 0 && G <= 64;
+}
+
+int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
+
+// Maps of the tcgen05 kernel: K and V as {64 elements, NB * B rows, D / 64
+// panels, Hk heads} in boxes of gran rows of one panel and head; q as {64, D / 64
+// panels, H, T} in boxes of tq1 tokens x G heads of one panel.  All boxes land
+// as 128-byte lines with the 128-byte swizzle.
+bool encode_tc_maps(CUtensorMap *q, CUtensorMap *k, CUtensorMap *v, const PrefillArgs &a, const pa_cache_desc_t *c,
+                    int gran) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t D = c->head_dim, Hk = c->num_kv_heads;
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    auto enc = [&](CUtensorMap *m, const void *base, const cuuint64_t *dims, const cuuint64_t *strides,
+                   const cuuint32_t *box) {
+        return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    const cuuint64_t kd[4] = {64, (cuuint64_t)c->num_blocks * c->block_size, D / 64, Hk};
+    const cuuint64_t ks[3] = {Hk * D * 2, 128, D * 2};
+    const cuuint32_t kb[4] = {64, (cuuint32_t)gran, 1, 1};
+    const cuuint64_t qd[4] = {64, D / 64, (cuuint64_t)a.H, (cuuint64_t)a.T};
+    const cuuint64_t qs[3] = {128, D * 2, (cuuint64_t)a.H * D * 2};
+    const cuuint32_t qb[4] = {64, 1, (cuuint32_t)a.G, (cuuint32_t)a.tq1};
+    return enc(k, a.k_cache, kd, ks, kb) && enc(v, a.v_cache, kd, ks, kb) && enc(q, a.q, qd, qs, qb);
 }
 
 }  // namespace
@@ -19,20 +50,21 @@ bool tc_supported(const pa_cache_desc_t *c, int G) {
 pa_status_t prefill_layout(bool tc, const pa_cache_desc_t *c, int32_t N, int32_t T, int32_t H, int32_t num_splits,
                            PrefillPlan *p) {
     const int32_t G = H / c->num_kv_heads;
-    const void *fn = prefill_simt_ptr(c->dtype, c->head_dim, c->layout, &p->smem);
+    const void *fn = tc ? prefill_tc_ptr(c->head_dim, &p->smem)
+                        : prefill_simt_ptr(c->dtype, c->head_dim, c->layout, &p->smem);
     if (!fn) return PA_ERR_UNSUPPORTED;
     p->tc = tc;
-    p->rows = 64;
-    p->nrt = 1;
-    p->kt = 64;
-    const int threads = 256;
+    p->rows = tc ? kTcRows : kSimtRows;
+    p->nrt = tc ? 2 : 1;
+    p->kt = tc ? kTcKeys : kSimtKeys;
+    p->threads = tc ? kTcThreads : kSimtThreads;
     p->tq1 = p->rows / G;
     const int64_t tq = (int64_t)p->tq1 * p->nrt;
     const int64_t tiles = (int64_t)N + T / tq;  // sum of ceil(n_i / tq)
     if (tiles >= ((int64_t)1 << 30)) return PA_ERR_UNSUPPORTED;
     p->max_tiles = (int32_t)tiles;
     p->C = num_splits;
-    if (p->C == 0) p->C = default_ctas(fn, threads, p->smem);
+    if (p->C == 0) p->C = default_ctas(fn, p->threads, p->smem);
     if (p->C <= 0) return PA_ERR_CUDA;
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -78,11 +110,20 @@ pa_status_t prefill_launch(const PrefillPlan &p, const pa_cache_desc_t *c, Prefi
     void *args[] = {&a};
     if (launch_pdl((const void *)prefill_plan_kernel, dim3(1), dim3(1024), args, 0, s) != cudaSuccess) return PA_ERR_CUDA;
     size_t smem;
-    const void *fn = prefill_simt_ptr(c->dtype, c->head_dim, c->layout, &smem);
+    const void *fn = p.tc ? prefill_tc_ptr(c->head_dim, &smem)
+                          : prefill_simt_ptr(c->dtype, c->head_dim, c->layout, &smem);
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return PA_ERR_CUDA;
-    if (launch_pdl(fn, dim3(p.C), dim3(256), args, smem, s) != cudaSuccess) return PA_ERR_CUDA;
+    if (p.tc) {
+        CUtensorMap tmq, tmk, tmv;
+        int32_t gran = gcd(c->block_size, kTcKeys);
+        if (!encode_tc_maps(&tmq, &tmk, &tmv, a, c, gran)) return PA_ERR_CUDA;
+        void *targs[] = {&tmq, &tmk, &tmv, &a, &gran};
+        if (launch_pdl(fn, dim3(p.C), dim3(p.threads), targs, smem, s) != cudaSuccess) return PA_ERR_CUDA;
+    } else if (launch_pdl(fn, dim3(p.C), dim3(p.threads), args, smem, s) != cudaSuccess) {
+        return PA_ERR_CUDA;
+    }
     if (p.C > 1) {  // a single CTA cuts no tile
         const bool f32 = c->dtype == PA_F32;
         const void *mfn =
@@ -98,8 +139,9 @@ pa_status_t prefill_launch(const PrefillPlan &p, const pa_cache_desc_t *c, Prefi
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+// The call's plan; fits: its scale and alignment suit the tcgen05 kernel.
 static pa_status_t prefill_plan_of(const pa_cache_desc_t *c, int32_t N, int32_t T, int32_t H,
-                                   const pa_prefill_opts_t *opts, bool scale_ok, PrefillPlan *p) {
+                                   const pa_prefill_opts_t *opts, bool fits, PrefillPlan *p) {
     const pa_status_t st = validate_cache_desc(c);
     if (st != PA_OK) return st;
     if (N < 0 || T < 0 || H <= 0 || H % c->num_kv_heads != 0) return PA_ERR_INVALID_ARG;
@@ -108,7 +150,7 @@ static pa_status_t prefill_plan_of(const pa_cache_desc_t *c, int32_t N, int32_t 
     if (opts && opts->num_splits < 0) return PA_ERR_INVALID_ARG;
     const int32_t G = H / c->num_kv_heads;
     if (G > 64) return PA_ERR_UNSUPPORTED;
-    const bool tc = want != PA_KERNEL_SIMT && scale_ok && tc_supported(c, G);
+    const bool tc = want != PA_KERNEL_SIMT && fits && tc_supported(c, G);
     if (want == PA_KERNEL_MMA && !tc) return PA_ERR_UNSUPPORTED;
     return prefill_layout(tc, c, N, T, H, opts ? opts->num_splits : 0, p);
 }
@@ -121,7 +163,11 @@ extern "C" size_t pa_prefill_workspace_bytes(const pa_cache_desc_t *cache, int32
                                              int32_t num_heads, const pa_prefill_opts_t *opts) try {
     PrefillPlan p;
     if (prefill_plan_of(cache, num_seqs, num_tokens, num_heads, opts, true, &p) != PA_OK) return 0;
-    return p.total;
+    const size_t need = p.total;
+    if (!p.tc || (opts && opts->kernel == PA_KERNEL_MMA)) return need;
+    // a call whose scale or alignment keeps it from the tcgen05 kernel needs the other layout
+    if (prefill_plan_of(cache, num_seqs, num_tokens, num_heads, opts, false, &p) != PA_OK) return 0;
+    return std::max(need, p.total);
 } catch (...) {
     return 0;
 }
@@ -133,7 +179,8 @@ extern "C" pa_status_t pa_prefill(void *out, const void *q, const void *k_cache,
                                   void *workspace, size_t workspace_bytes, const pa_prefill_opts_t *opts,
                                   pa_stream_t stream) try {
     PrefillPlan p;
-    pa_status_t st = prefill_plan_of(cache, num_seqs, num_tokens, num_heads, opts, true, &p);
+    const bool fits = scale > 0.f && scale < INFINITY && ((uintptr_t)q | (uintptr_t)out) % 16 == 0;
+    const pa_status_t st = prefill_plan_of(cache, num_seqs, num_tokens, num_heads, opts, fits, &p);
     if (st != PA_OK) return st;
     if (num_seqs == 0 || num_tokens == 0) return PA_OK;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens || !cu_q_lens || !workspace)

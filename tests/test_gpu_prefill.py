@@ -252,3 +252,15 @@ def test_python_refusals():
         pa.pa_prefill(**d, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(pa.PagedAttentionError):
         pa.pa_prefill(**dict(d, q=torch.zeros(38, 7, 128, dtype=BF, device="cuda")))
+
+
+@pytest.mark.parametrize("splits", [1, 3, 0])
+def test_many_segments_per_cta_with_row_tiles_that_end_apart(splits):
+    """Tiles whose first row tile needs a unit less than the second one (and
+    finishes early), many in a row on every CTA."""
+    lens = [64 + 37 * (i % 5) for i in range(40)]
+    ctx = [90 + 61 * (i % 7) for i in range(40)]
+    c = Chunk(lens, [a + b for a, b in zip(lens, ctx)], 32, 8, 128, 16, BF, seed=23)
+    for _ in range(3):
+        out = run(c, num_splits=splits)
+    c.check(out, P_EPS[BF])
