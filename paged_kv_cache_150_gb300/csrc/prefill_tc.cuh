@@ -8,8 +8,8 @@
 //   P = 2^(scale S - m)         one thread per row, P as bf16 over S's columns,
 //   O[128][D] += P V            8 MMAs, P from tensor memory, V from shared.
 // One CTA per SM, twelve warps: 0-3 and 4-7 are the softmax of the two row tiles
-// (a thread owns one row: no shuffles), 8 issues the MMAs, 9 the TMA copies
-// (10 and 11 fill up the third warpgroup).
+// (a thread owns one row: no shuffles), 8 issues the MMAs, 9 and 10 the
+// TMA copies, 11 guards V's masked rows.
 // The two row tiles take turns on the tensor pipe: while one's S is turned
 // into P, the other's O += P V and next S run.  Tensor memory holds S (128
 // columns) and O (D columns) of both, 512 columns at head_dim 128.
@@ -49,7 +49,7 @@ struct TcPrefill {
 
 // Barriers of a CTA, in shared memory.
 struct TcBars {
-    uint32_t q_full, q_free, kv_full, kv_free, s_full, p_full, o_full, o_free;  // addresses; arrays 8 bytes apart
+    uint32_t q_full, q_free, v_go, v_ok, kv_full, kv_free, s_full, p_full, o_full, o_free;  // addresses; arrays 8 bytes apart
     __device__ __forceinline__ TcBars(uint32_t base, int stages) {
         q_full = base;
         q_free = base + 8;
@@ -57,7 +57,9 @@ struct TcBars {
         p_full = base + 32;
         o_full = base + 48;
         o_free = base + 64;
-        kv_full = base + 80;
+        v_go = base + 80;
+        v_ok = base + 88;
+        kv_full = base + 96;
         kv_free = kv_full + 8 * (uint32_t)stages;
     }
 };
@@ -91,244 +93,290 @@ struct TcSegment {
     }
 };
 
-// ------------------------------------------------------------ TMA producer
-// One warp.  Per segment the Q rows (one box of tq1 tokens x G heads per row
-// tile and 64-element panel), then K and V units through the ring, K first.
-// A unit is 128 / gran boxes per panel, gran = gcd(block size, 128) keys, one
-// box per lane; the block-table entries of a unit are read one unit ahead.
-template <int D>
+// ----------------------------------------------------------- TMA producers
+// One warp for K (and the Q rows), one for V.  Entry n of the ring is K of a
+// unit for even n, V for odd n.  A unit is 128 / gran boxes per panel, gran =
+// gcd(block size, 128) keys, one box per lane; the block-table entry of a
+// lane's next box is read a unit ahead and looked at when its unit comes, so
+// no load is waited for.  Q: one box of tq1 tokens x G heads per row tile and
+// 64-element panel.
+template <int D, bool kIsV>
 __device__ __forceinline__ void tc_producer(const PrefillArgs &a, uint8_t *smem, const TcBars &bar,
-                                            const CUtensorMap *tmq, const CUtensorMap *tmk, const CUtensorMap *tmv,
-                                            int32_t gran, PrefillCursor cur, int lane) {
+                                            const CUtensorMap *tmq, const CUtensorMap *tm, int32_t gran,
+                                            PrefillCursor cur, int lane) {
     using L = TcPrefill<D>;
     if (lane == 0) {
-        prefetch_tmap(tmq);
-        prefetch_tmap(tmk);
-        prefetch_tmap(tmv);
+        if (!kIsV) prefetch_tmap(tmq);
+        prefetch_tmap(tm);
     }
     const uint32_t q_dst = smem_u32(smem), ring = q_dst + L::kRing;
     const int32_t nbm = kTcKeys / gran;  // boxes of a unit per panel (at most 16)
     const int32_t bi = lane % nbm, panel = lane / nbm;
     const bool has_box = panel < L::kPanels;
     const uint32_t box_off = (uint32_t)panel * L::kPanel + (uint32_t)(bi * gran) * 128u;
-    uint32_t n = 0, segs = 0;  // ring entries and Q loads issued
+    uint32_t n = kIsV ? 1 : 0, segs = 0;  // next ring entry, segments with units
     bool abort = false;
     do {
         const TcSegment sg(a, cur);
         if (sg.jend <= cur.j0) continue;
         const int32_t *row = a.tables + (int64_t)sg.t.seq * a.max_blocks;
-        auto entry = [&](int32_t j) -> int32_t {  // pool row of this lane's box of unit j, -1: no box
-            const int64_t pos = (int64_t)j * kTcKeys + bi * gran;
-            if (!has_box || pos >= sg.keys) return -1;
-            const int32_t p = (int32_t)pos, blk = p / a.B, phys = row[blk];
-            if (phys < 0 || phys >= a.NB) {  // reads zeros: the box lies past the pool
-                atomicOr(a.err, kErrBounds);
-                return a.NB * a.B;
+        auto has_key = [&](int32_t j) { return has_box && (int64_t)j * kTcKeys + bi * gran < sg.keys; };
+        auto entry = [&](int32_t j) { return has_key(j) ? row[(j * kTcKeys + bi * gran) / a.B] : 0; };
+        int32_t phys = entry(cur.j0);
+        if (!kIsV) {
+            if (segs > 0) tc_wait(bar.q_free, (segs - 1) & 1, abort, a.err);
+            if (__any_sync(0xffffffffu, abort)) break;
+            if (lane == 0) {
+                const int32_t nrt = sg.t.ntok > a.tq1 ? 2 : 1;
+                mbar_arrive_expect_tx(bar.q_full, (uint32_t)(nrt * L::kPanels * a.tq1 * a.G) * 128u);
+                for (int32_t i = 0; i < nrt; ++i)
+                    for (int32_t p = 0; p < L::kPanels; ++p)
+                        tma_load_4d(q_dst + i * L::kTile + p * L::kPanel, tmq, bar.q_full, 0, p, cur.kvh * a.G,
+                                    sg.t.row0 + i * a.tq1);
             }
-            return phys * a.B + (p - blk * a.B);
-        };
-        int32_t next = entry(cur.j0);
-        if (segs > 0) tc_wait(bar.q_free, (segs - 1) & 1, abort, a.err);
-        if (__any_sync(0xffffffffu, abort)) break;
-        if (lane == 0) {
-            const int32_t nrt = sg.t.ntok > a.tq1 ? 2 : 1;
-            mbar_arrive_expect_tx(bar.q_full, (uint32_t)(nrt * L::kPanels * a.tq1 * a.G) * 128u);
-            for (int32_t i = 0; i < nrt; ++i)
-                for (int32_t p = 0; p < L::kPanels; ++p)
-                    tma_load_4d(q_dst + i * L::kTile + p * L::kPanel, tmq, bar.q_full, 0, p, cur.kvh * a.G,
-                                sg.t.row0 + i * a.tq1);
         }
         ++segs;
-        for (int32_t j = cur.j0; j < sg.jend; ++j) {
-            const int32_t at = next;
-            if (j + 1 < sg.jend) next = entry(j + 1);
-            const uint32_t bytes =
-                (uint32_t)__popc(__ballot_sync(0xffffffffu, at >= 0)) * (uint32_t)gran * 128u;  // of K, and of V
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv, ++n) {
-                const uint32_t st = n % L::kStages;
-                if (n >= L::kStages) tc_wait(bar.kv_free + 8 * st, (n / L::kStages + 1) & 1, abort, a.err);
-                if (__any_sync(0xffffffffu, abort)) break;
-                if (lane == 0) mbar_arrive_expect_tx(bar.kv_full + 8 * st, bytes);
-                __syncwarp();
-                if (at >= 0)
-                    tma_load_4d(ring + st * L::kTile + box_off, kv == 0 ? tmk : tmv, bar.kv_full + 8 * st, 0, at, panel,
-                                cur.kvh);
-            }
+        for (int32_t j = cur.j0; j < sg.jend; ++j, n += 2) {
+            const int32_t p = j * kTcKeys + bi * gran;
+            const bool box = has_key(j);
+            int32_t at = a.NB * a.B;  // a bad entry reads zeros: the box lies past the pool
+            if (phys >= 0 && phys < a.NB)
+                at = phys * a.B + p % a.B;
+            else if (box)
+                atomicOr(a.err, kErrBounds);
+            if (j + 1 < sg.jend) phys = entry(j + 1);
+            const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, box)) * (uint32_t)gran * 128u;
+            const uint32_t st = n % L::kStages;
+            if (n >= L::kStages) tc_wait(bar.kv_free + 8 * st, (n / L::kStages + 1) & 1, abort, a.err);
             if (__any_sync(0xffffffffu, abort)) break;
+            if (lane == 0) mbar_arrive_expect_tx(bar.kv_full + 8 * st, bytes);
+            __syncwarp();
+            if (box)
+                tma_load_4d(ring + st * L::kTile + box_off, tm, bar.kv_full + 8 * st, 0, at, panel, cur.kvh);
         }
         if (__any_sync(0xffffffffu, abort)) break;
     } while (cur.next(a));
-    // Copies in flight, and the issuer's last arrivals on the free barriers,
-    // land before the CTA may exit.
+    // This warp's copies in flight, and the issuer's last arrivals on the free
+    // barriers, land before the CTA may exit.
     bool late = false;
-    for (uint32_t k = n > (uint32_t)L::kStages ? n - L::kStages : 0; k < n; ++k) {
+    const uint32_t total = n - (kIsV ? 1u : 0u);  // ring entries of the CTA; the last kStages are not reused
+    uint32_t k = total > (uint32_t)L::kStages ? total - L::kStages : 0;
+    if ((k & 1u) != (kIsV ? 1u : 0u)) ++k;
+    for (; k < total; k += 2) {
         tc_wait(bar.kv_full + 8 * (k % L::kStages), (k / L::kStages) & 1, late, a.err);
         tc_wait(bar.kv_free + 8 * (k % L::kStages), (k / L::kStages) & 1, late, a.err);
     }
-    if (segs > 0) {
+    if (!kIsV && segs > 0) {
         tc_wait(bar.q_full, (segs - 1) & 1, late, a.err);
         tc_wait(bar.q_free, (segs - 1) & 1, late, a.err);
     }
 }
 
-// Columns of V with values that are not finite at keys that only some rows of
-// a tile see (the tile's own tokens): 0 x V is not 0 there, so such a value is
-// replaced by 0 before the products, and each column keeps the first
-// position that holds +inf, -inf and NaN; rows that see it add it at the end.
+// --------------------------------------------------------------- V's guard
+// 0 x V is not 0 where V is not finite, and the products run over whole units:
+// keys that only some rows of a tile see (its own tokens, from position
+// p0 + 1 on) and the rest of the last 16 keys.  One warp looks at those rows
+// of V before their products: rows past the tile's keys become zeros, and a
+// value that is not finite is replaced by 0 while its column keeps the first
+// position that holds +inf, -inf and NaN; the rows that see it add it at the
+// end.  odd.segment names the segment the columns belong to.
 struct OddColumns {
-    int32_t *first;  // [3][D]: +inf, -inf, NaN; kNone without one
+    int32_t *first;    // [3][D]: +inf, -inf, NaN; kNone without one
+    int32_t *segment;  // 1-based count of segments with units; 0: none so far
     static constexpr int32_t kNone = 0x7fffffff;
 };
 
-// Rows [r0, r1) of a staged V unit: values that are not finite to
-// odd.first, zeros in their place; rows [r1, r2) all zeros.  One warp.
-// Returns whether any was found.
+// First unit of a segment that holds keys for the guard.
+__device__ __forceinline__ int32_t guard_from(const TcSegment &sg) { return max(sg.t.p0 + 1, 0) / kTcKeys; }
+
 template <int D>
-__device__ __forceinline__ bool tc_clean_v(uint32_t vbase, int r0, int r1, int r2, int32_t pos0, const OddColumns &odd,
-                                           int lane) {
+__device__ __forceinline__ uint32_t v_chunk(uint32_t vbase, int e) {  // address of 16-byte chunk e % (D / 8) of row e / (D / 8)
+    constexpr int kChunks = D / 8;
+    const int r = e / kChunks, ch = e % kChunks;
+    return vbase + (uint32_t)(ch >> 3) * TcPrefill<D>::kPanel + (uint32_t)r * 128u +
+           (uint32_t)(((ch & 7) ^ (r & 7)) << 4);
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, const uint4 &v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// Sign bits of the halves whose exponent is all ones (bf16 infinities and NaN).
+__device__ __forceinline__ uint32_t odd_bits(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
+template <int D>
+__device__ __forceinline__ void tc_guard(const PrefillArgs &a, uint8_t *smem, const TcBars &bar, const OddColumns &odd,
+                                         PrefillCursor cur, int lane) {
     using L = TcPrefill<D>;
-    bool found = false;
-    constexpr int kChunks = D / 8;  // 16-byte chunks of a row
-    for (int e = r0 * kChunks + lane; e < r2 * kChunks; e += 32) {
-        const int r = e / kChunks, ch = e % kChunks;
-        const uint32_t addr =
-            vbase + (uint32_t)(ch >> 3) * L::kPanel + (uint32_t)r * 128u + (uint32_t)(((ch & 7) ^ (r & 7)) << 4);
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
-        bool store = r >= r1;
-        if (!store) {
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(addr));
+    constexpr int kChunks = D / 8;
+    const uint32_t ring = smem_u32(smem) + L::kRing;
+    uint32_t n = 1, segs = 0, units = 0;  // ring entry of V, segments, guarded units
+    uint32_t no[2] = {0, 0};              // earlier segments with units per row tile
+    bool abort = false, dirty = false;
+    do {
+        const TcSegment sg(a, cur);
+        if (sg.jend <= cur.j0) continue;
+        ++segs;
+        for (int32_t j = max(cur.j0, guard_from(sg)); j < sg.jend; ++j, ++units) {
+            tc_wait(bar.v_go, units & 1, abort, a.err);  // the issuer has seen V arrive
+            const uint32_t vbase = ring + ((n + 2 * (uint32_t)(j - cur.j0)) % L::kStages) * L::kTile;
+            const int32_t pos0 = j * kTcKeys;
+            const int nk = min(kTcKeys, sg.keys - pos0), nk16 = (nk + 15) & ~15;
+            const int r0 = min(nk, max(0, sg.t.p0 + 1 - pos0));
+            for (int e = nk * kChunks + lane; e < nk16 * kChunks; e += 32)
+                sts128(v_chunk<D>(vbase, e), make_uint4(0u, 0u, 0u, 0u));
+            uint32_t any = 0;
+            int e = r0 * kChunks + lane;
+            for (; e + 96 < nk * kChunks; e += 128) {  // four loads in flight
+                uint4 v[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t h = (w[k >> 1] >> (16 * (k & 1))) & 0xffffu;
-                if ((h & 0x7f80u) == 0x7f80u) {
-                    const int kind = (h & 0x7fu) ? 2 : (h >> 15);
-                    atomicMin(&odd.first[kind * D + ch * 8 + k], pos0 + r);
-                    w[k >> 1] &= k & 1 ? 0x0000ffffu : 0xffff0000u;
-                    store = found = true;
-                }
+                for (int u = 0; u < 4; ++u) v[u] = lds128(v_chunk<D>(vbase, e + 32 * u));
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    any |= odd_bits(v[u].x) | odd_bits(v[u].y) | odd_bits(v[u].z) | odd_bits(v[u].w);
             }
+            for (; e < nk * kChunks; e += 32) {
+                const uint4 v = lds128(v_chunk<D>(vbase, e));
+                any |= odd_bits(v.x) | odd_bits(v.y) | odd_bits(v.z) | odd_bits(v.w);
+            }
+            if (__any_sync(0xffffffffu, any != 0)) {
+                // The columns are read by the rows of the segment before: wait
+                // until they are through.  A row tile that began its units at
+                // j0 has been waited for there (its barrier may be a phase on).
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (no[i] > 0 && (j == cur.j0 || sg.je[i] <= cur.j0))
+                        tc_wait(bar.o_free + 8 * i, (no[i] - 1) & 1, abort, a.err);
+                if (dirty && *odd.segment != (int32_t)segs)
+                    for (int x = lane; x < 3 * D; x += 32) odd.first[x] = OddColumns::kNone;
+                __syncwarp();
+                for (e = r0 * kChunks + lane; e < nk * kChunks; e += 32) {
+                    const uint32_t addr = v_chunk<D>(vbase, e);
+                    const uint4 v = lds128(addr);
+                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    if (!(odd_bits(v.x) | odd_bits(v.y) | odd_bits(v.z) | odd_bits(v.w))) continue;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t h = (w[k >> 1] >> (16 * (k & 1))) & 0xffffu;
+                        if ((h & 0x7f80u) == 0x7f80u) {
+                            const int kind = (h & 0x7fu) ? 2 : (int)(h >> 15);
+                            atomicMin(&odd.first[kind * D + (e % kChunks) * 8 + k], pos0 + e / kChunks);
+                            w[k >> 1] &= k & 1 ? 0x0000ffffu : 0xffff0000u;
+                        }
+                    }
+                    sts128(addr, make_uint4(w[0], w[1], w[2], w[3]));
+                }
+                dirty = true;
+                __syncwarp();
+                if (lane == 0) *odd.segment = (int32_t)segs;
+            }
+            fence_proxy_async_smem();  // the MMAs read these rows through the async proxy
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar.v_ok);
         }
-        if (store)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                         : "memory");
-    }
-    fence_proxy_async_smem();  // the MMAs read these rows through the async proxy
-    return __any_sync(0xffffffffu, found);
+        n += 2 * (uint32_t)(sg.jend - cur.j0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) no[i] += cur.j0 < sg.je[i] ? 1 : 0;
+    } while (cur.next(a));
 }
 
 // -------------------------------------------------------------- MMA issuer
-// One warp; lane 0 issues.  MMAs of one thread complete in order, so S of a
+// One warp; one elected lane issues.  MMAs of one thread complete in order, so S of a
 // unit may be computed over the P of the one before (its O += P V was issued
 // earlier), and a row tile's S being complete says that its earlier O is too.
 template <int D>
 __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, const TcBars &bar, uint32_t tmem,
-                                          const OddColumns &odd, int32_t *odd_flag, PrefillCursor cur, int lane) {
+                                          PrefillCursor cur, int lane) {
     using L = TcPrefill<D>;
     constexpr uint32_t IDESC_S = tc_idesc_bf16(128, kTcKeys, false, false);
     constexpr uint32_t IDESC_O = tc_idesc_bf16(128, D, false, true);
-    const uint32_t q_base = smem_u32(smem), ring = q_base + L::kRing;
-    uint32_t n = 0, segs = 0;        // ring entries consumed, segments
-    uint32_t np[2] = {0, 0};         // P tiles taken per row tile
-    uint32_t no[2] = {0, 0};         // segments with units per row tile
-    bool abort = false, odd_dirty = false;
+    const uint32_t ring = smem_u32(smem) + L::kRing;
+    // Descriptors of the first Q row tile and ring entry; the others' start
+    // addresses (in 16-byte units, the low bits of a descriptor) are added.
+    const uint64_t q_desc = smem_desc_sw128(smem_u32(smem), 16, 1024), k_desc = smem_desc_sw128(ring, 16, 1024),
+                   v_desc = smem_desc_sw128(ring, L::kPanel, 1024);
+    const uint32_t one = elect_one();
+    uint32_t n = 0, segs = 0, units = 0;  // ring entries consumed, segments, guarded units
+    uint32_t np[2] = {0, 0};              // P tiles taken per row tile
+    uint32_t no[2] = {0, 0};              // segments with units per row tile
+    bool abort = false;
     do {
         const TcSegment sg(a, cur);
         if (sg.jend <= cur.j0) continue;
+        const int32_t jg = guard_from(sg);
         tc_wait(bar.q_full, segs & 1, abort, a.err);
         ++segs;
-        // The row tile's earlier rows have left O and the odd columns.  Waited
-        // for once per segment: a row tile may finish this segment (and
-        // complete the barrier's next phase) units before the other does.
-        bool rows_read[2] = {no[0] == 0, no[1] == 0};
-        auto wait_rows_read = [&](int i) {
-            if (!rows_read[i]) tc_wait(bar.o_free + 8 * i, (no[i] - 1) & 1, abort, a.err);
-            rows_read[i] = true;
-        };
-        auto issue_s = [&](int i, uint32_t kbase) {
+        auto issue_s = [&](int i, uint32_t slot) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (uint32_t)(k >> 2) * L::kPanel + (uint32_t)(k & 3) * 32;
-                tc_mma_bf16(tmem + L::kS + i * 128, smem_desc_sw128(q_base + i * L::kTile + off, 16, 1024),
-                            smem_desc_sw128(kbase + off, 16, 1024), IDESC_S, k > 0 ? 1u : 0u);
+                const uint32_t off = ((uint32_t)(k >> 2) * L::kPanel + (uint32_t)(k & 3) * 32) >> 4;
+                tc_mma_bf16_ss_if(one, tmem + L::kS + i * 128, q_desc + (uint32_t)(i * (L::kTile >> 4) + off),
+                                  k_desc + (slot * (L::kTile >> 4) + off), IDESC_S, k > 0 ? 1u : 0u);
             }
-            tc_commit(bar.s_full + 8 * i);
+            tc_commit_if(one, bar.s_full + 8 * i);
         };
-        uint32_t st = n % L::kStages;
+        const uint32_t st = n % L::kStages;
         tc_wait(bar.kv_full + 8 * st, (n / L::kStages) & 1, abort, a.err);
         ++n;
         tc_fence_after();
-        if (lane == 0) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (cur.j0 < sg.je[i]) issue_s(i, ring + st * L::kTile);
-            tc_commit(bar.kv_free + 8 * st);
-            if (cur.j0 + 1 == sg.jend) tc_commit(bar.q_free);
-        }
-        __syncwarp();
+        for (int i = 0; i < 2; ++i)
+            if (cur.j0 < sg.je[i]) issue_s(i, st);
+        tc_commit_if(one, bar.kv_free + 8 * st);
+        if (cur.j0 + 1 == sg.jend) tc_commit_if(one, bar.q_free);
         for (int32_t j = cur.j0; j < sg.jend; ++j) {
-            const uint32_t sv = n % L::kStages;
-            const uint32_t vbase = ring + sv * L::kTile;
-            tc_wait(bar.kv_full + 8 * sv, (n / L::kStages) & 1, abort, a.err);
-            ++n;
-            // keys of this unit that not every row sees, or that no row does
-            const int32_t pos0 = j * kTcKeys;
-            const int nk = min(kTcKeys, sg.keys - pos0), nk16 = (nk + 15) & ~15;
-            const int shared = min(nk, max(0, sg.t.p0 + 1 - pos0));
-            if (shared < nk16) {
-                wait_rows_read(0);
-                wait_rows_read(1);
-                if (odd_dirty) {  // an earlier tile's columns
-                    for (int e = lane; e < 3 * D; e += 32) odd.first[e] = OddColumns::kNone;
-                    if (lane == 0) *odd_flag = 0;
-                    odd_dirty = false;
-                    __syncwarp();
-                }
-                if (tc_clean_v<D>(vbase, shared, nk, nk16, pos0, odd, lane)) {
-                    if (lane == 0) *odd_flag = 1;
-                }
-                __syncwarp();
-            }
             const bool more = j + 1 < sg.jend;
-            const uint32_t sk = n % L::kStages;
-            const uint32_t nk_par = (n / L::kStages) & 1;
-            if (more) ++n;
+            const uint32_t nv = n, nk = n + 1;  // ring entries of this unit's V and the next one's K
+            const uint32_t sv = nv % L::kStages, sk = nk % L::kStages;
+            n += more ? 2 : 1;
+            tc_wait(bar.kv_full + 8 * sv, (nv / L::kStages) & 1, abort, a.err);
+            const bool guarded = j >= jg;
+            int ksteps = kTcKeys / 16;
+            if (guarded) {
+                ksteps = min(ksteps, (sg.keys - j * kTcKeys + 15) / 16);
+                if (one) mbar_arrive(bar.v_go);
+            }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (j < sg.je[i]) {
-                    if (j == cur.j0) {  // O is about to be overwritten
-                        wait_rows_read(i);
+                    if (j == cur.j0) {  // O is about to be overwritten: its earlier rows have been read
+                        if (no[i] > 0) tc_wait(bar.o_free + 8 * i, (no[i] - 1) & 1, abort, a.err);
                         ++no[i];
                     }
                     tc_wait(bar.p_full + 8 * i, np[i] & 1, abort, a.err);
                     ++np[i];
-                    tc_fence_after();
-                    if (lane == 0) {
-                        for (int k = 0; k < nk16 / 16; ++k)
-                            tc_mma_bf16_ta(tmem + L::kO + i * D, tmem + L::kS + i * 128 + k * 8,
-                                           smem_desc_sw128(vbase + (uint32_t)k * 2048, L::kPanel, 1024), IDESC_O,
-                                           j > cur.j0 || k > 0 ? 1u : 0u);
-                        if (j + 1 == sg.je[i]) tc_commit(bar.o_full + 8 * i);
-                    }
-                    __syncwarp();
                 }
-                if (more && i == 0) tc_wait(bar.kv_full + 8 * sk, nk_par, abort, a.err);
+                if (guarded && i == 0) tc_wait(bar.v_ok, units & 1, abort, a.err);
+                if (j < sg.je[i]) {
+                    tc_fence_after();
+                    auto issue_o = [&](int k) {
+                        tc_mma_bf16_ts_if(one, tmem + L::kO + i * D, tmem + L::kS + i * 128 + k * 8,
+                                          v_desc + (sv * (L::kTile >> 4) + (uint32_t)k * 128u), IDESC_O,
+                                          j > cur.j0 || k > 0 ? 1u : 0u);
+                    };
+                    if (ksteps == kTcKeys / 16) {
+#pragma unroll
+                        for (int k = 0; k < kTcKeys / 16; ++k) issue_o(k);
+                    } else {
+#pragma unroll 1
+                        for (int k = 0; k < ksteps; ++k) issue_o(k);
+                    }
+                    if (j + 1 == sg.je[i]) tc_commit_if(one, bar.o_full + 8 * i);
+                }
+                if (more && i == 0) tc_wait(bar.kv_full + 8 * sk, (nk / L::kStages) & 1, abort, a.err);
                 if (j + 1 < sg.je[i]) {
                     tc_fence_after();
-                    if (lane == 0) issue_s(i, ring + sk * L::kTile);
-                    __syncwarp();
+                    issue_s(i, sk);
                 }
             }
-            if (lane == 0) {
-                tc_commit(bar.kv_free + 8 * sv);
-                if (more) tc_commit(bar.kv_free + 8 * sk);
-                if (j + 2 == sg.jend) tc_commit(bar.q_free);
-            }
-            __syncwarp();
+            if (guarded) ++units;
+            tc_commit_if(one, bar.kv_free + 8 * sv);
+            if (more) tc_commit_if(one, bar.kv_free + 8 * sk);
+            if (j + 2 == sg.jend) tc_commit_if(one, bar.q_free);
         }
-        odd_dirty = *odd_flag != 0;  // written by this warp alone
     } while (cur.next(a));
     // Every MMA ends in an o_full that the softmax warps wait for; nothing of
     // this warp is in flight once they have (see the kernel's end).
@@ -338,7 +386,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
 // Four warps per row tile; a thread owns one query row (tensor-memory lane).
 template <int D>
 __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &bar, uint32_t tmem,
-                                           const OddColumns &odd, const int32_t *odd_flag, PrefillCursor cur, int32_t c,
+                                           const OddColumns &odd, PrefillCursor cur, int32_t c,
                                            int i, int warp, int lane) {
     using L = TcPrefill<D>;
     const int r = warp * 32 + lane;  // row of the row tile
@@ -347,7 +395,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
     const uint32_t s_full = bar.s_full + 8 * i, p_full = bar.p_full + 8 * i;
     const int tok_r = r / a.G, g = r - tok_r * a.G;
     const float sl = a.scale_log2;
-    uint32_t ns = 0, no = 0;
+    uint32_t ns = 0, no = 0, segs = 0;
     bool abort = false;
     do {
         const TcSegment sg(a, cur);
@@ -356,6 +404,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
         const bool warp_rows = __any_sync(0xffffffffu, valid);
         const int32_t last = sg.t.p0 + tok;
         const int32_t je = sg.je[i];
+        if (sg.jend > cur.j0) ++segs;
         float m = -INFINITY, l = 0.f;
         for (int32_t j = cur.j0; j < je; ++j) {
             tc_wait(s_full, ns & 1, abort, a.err);
@@ -430,7 +479,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
         const bool whole = cur.whole();
         const int64_t row = cur.slot(c) * (2 * kTcRows) + i * kTcRows + r;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const bool odd_tile = any && *odd_flag != 0;
+        const bool odd_tile = any && *odd.segment == (int32_t)segs;
         __nv_bfloat16 *op =
             (__nv_bfloat16 *)a.out + ((int64_t)(sg.t.row0 + tok) * a.H + (int64_t)cur.kvh * a.G + g) * D;
         if (warp_rows) {
@@ -487,13 +536,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const TcBars bar(smem_u32(smem + L::kBars), L::kStages);
     uint32_t *tmem_slot = (uint32_t *)(smem + L::kBars + 248);
-    int32_t *odd_flag = (int32_t *)(smem + L::kBars + 252);
-    OddColumns odd{(int32_t *)(smem + L::kBars + 256)};
-    static_assert(80 + 16 * L::kStages <= 248, "the barriers fit");
+    const OddColumns odd{(int32_t *)(smem + L::kBars + 256), (int32_t *)(smem + L::kBars + 252)};
+    static_assert(96 + 16 * L::kStages <= 248, "the barriers fit");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         mbar_init(bar.q_full, 1);
         mbar_init(bar.q_free, 1);
+        mbar_init(bar.v_go, 1);
+        mbar_init(bar.v_ok, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar.s_full + 8 * i, 1);
             mbar_init(bar.p_full + 8 * i, 4);
@@ -504,7 +554,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(bar.kv_full + 8 * s, 1);
             mbar_init(bar.kv_free + 8 * s, 1);
         }
-        *odd_flag = 0;
+        *odd.segment = 0;
         fence_mbarrier_init();
     }
     for (int e = tid; e < 3 * D; e += kTcThreads) odd.first[e] = OddColumns::kNone;
@@ -520,13 +570,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (cur.init(a, c)) {
         if (warp < 8) {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcSoftmaxRegs));
-            tc_softmax<D>(a, bar, tmem, odd, odd_flag, cur, c, warp >> 2, warp & 3, lane);
+            tc_softmax<D>(a, bar, tmem, odd, cur, c, warp >> 2, warp & 3, lane);
         } else {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcOtherRegs));
             if (warp == 8)
-                tc_issuer<D>(a, smem, bar, tmem, odd, odd_flag, cur, lane);
+                tc_issuer<D>(a, smem, bar, tmem, cur, lane);
             else if (warp == 9)
-                tc_producer<D>(a, smem, bar, &tmq, &tmk, &tmv, gran, cur, lane);
+                tc_producer<D, false>(a, smem, bar, &tmq, &tmk, gran, cur, lane);
+            else if (warp == 10)
+                tc_producer<D, true>(a, smem, bar, &tmq, &tmv, gran, cur, lane);
+            else
+                tc_guard<D>(a, smem, bar, odd, cur, lane);
         }
     }
     // The softmax warps have waited for the last o_full, which every MMA
