@@ -44,7 +44,7 @@ extern "C" pa_status_t pa_decode_fp8(void *out, const void *q, const void *k_cac
     if (max_blocks_per_seq <= 0 || (int64_t)num_seqs * max_blocks_per_seq >= ((int64_t)1 << 31) ||
         (int64_t)max_blocks_per_seq * cache->block_size >= ((int64_t)1 << 31))
         return PA_ERR_INVALID_ARG;
-    if ((int64_t)num_seqs * ((int64_t)max_blocks_per_seq * cache->block_size / p.kt + 1) >= ((int64_t)1 << 31))
+    if ((int64_t)num_seqs * ((int64_t)max_blocks_per_seq * cache->block_size / p.kt + 1 + p.extra) >= ((int64_t)1 << 31))
         return PA_ERR_UNSUPPORTED;
     if (!(scale == scale)) return PA_ERR_INVALID_ARG;
     if (((uintptr_t)workspace & 255) != 0) return PA_ERR_INVALID_ARG;

@@ -57,6 +57,7 @@ pa_status_t prefill_layout(bool tc, const pa_cache_desc_t *c, int32_t N, int32_t
     p->rows = tc ? kTcRows : kSimtRows;
     p->nrt = tc ? 2 : 1;
     p->kt = tc ? kTcKeys : kSimtKeys;
+    p->extra = tc ? kTcExtra : kSimtExtra;
     p->threads = tc ? kTcThreads : kSimtThreads;
     p->tq1 = p->rows / G;
     const int64_t tq = (int64_t)p->tq1 * p->nrt;
@@ -95,6 +96,7 @@ pa_status_t prefill_launch(const PrefillPlan &p, const pa_cache_desc_t *c, Prefi
     a.rows = p.rows;
     a.nrt = p.nrt;
     a.kt = p.kt;
+    a.extra = p.extra;
     a.C = p.C;
     a.max_tiles = p.max_tiles;
     a.ctl = (int32_t *)(ws + p.off_ctl);
@@ -189,7 +191,7 @@ extern "C" pa_status_t pa_prefill(void *out, const void *q, const void *k_cache,
         (int64_t)max_blocks_per_seq * cache->block_size >= ((int64_t)1 << 31))
         return PA_ERR_INVALID_ARG;
     // the units of a KV head are counted in 32 bits
-    if ((int64_t)p.max_tiles * ((int64_t)max_blocks_per_seq * cache->block_size / p.kt + 1) >= ((int64_t)1 << 31))
+    if ((int64_t)p.max_tiles * ((int64_t)max_blocks_per_seq * cache->block_size / p.kt + 1 + p.extra) >= ((int64_t)1 << 31))
         return PA_ERR_UNSUPPORTED;
     if (!(scale == scale)) return PA_ERR_INVALID_ARG;
     if (((uintptr_t)workspace & 255) != 0) return PA_ERR_INVALID_ARG;

@@ -13,6 +13,7 @@ struct PrefillPlan {
     int32_t rows, nrt; // query rows of a row tile, row tiles per tile
     int32_t tq1;       // tokens per row tile
     int32_t kt;        // keys per unit
+    int32_t extra;     // weight of a tile beside its units
     int32_t threads;   // of an attention CTA
     int32_t C, max_tiles;
     size_t smem;

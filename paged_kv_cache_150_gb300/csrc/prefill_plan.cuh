@@ -2,12 +2,14 @@
 //
 // The chunk's new tokens are cut into tiles of tq tokens x the G query heads
 // of one KV head; a tile attends to keys 0 .. p0 + ntok - 1 of its sequence
-// in units of kt keys.  The flattened list of (KV head, tile, unit) is cut
-// evenly over C persistent CTAs (split_begin), so that long and short
-// chunks, and one long context as well as many short ones, load every CTA
-// alike.  A CTA's range is a run of segments (one tile's units); a segment
-// that holds all of its tile's units writes `out`, any other one (at most the
-// first and the last of a range) writes a piece: the unnormalised
+// in units of kt keys.  A tile weighs its units plus `extra`, the cost of
+// beginning and ending one in units (Q's load, the pipeline's ramp, the
+// output), laid before its units; the flattened list of (KV head, tile,
+// weight) is cut evenly over C persistent CTAs (split_begin), so that long and
+// short chunks, and one long context as well as many short ones, load every
+// CTA alike.  A CTA's range is a run of segments (one tile's units); a
+// segment that holds all of its tile's units writes `out`, any other one (at
+// most the first and the last of a range) writes a piece: the unnormalised
 // accumulator with its running maximum (log2 units) and sum.
 // prefill_merge_kernel folds the pieces of every cut tile in CTA order, so
 // the same call gives the same bits every time.
@@ -39,12 +41,13 @@ struct PrefillArgs {
     int32_t rows;         // query rows of one row tile
     int32_t nrt;          // row tiles per tile (tq = tq1 * nrt)
     int32_t kt;           // keys per unit
+    int32_t extra;        // weight of a tile beside its units
     int32_t C;            // persistent CTAs
     int32_t max_tiles;    // capacity of tiles[] and cu[]
     float scale_log2;
     int32_t *ctl;         // ctl[0]: tiles of the list
     int32_t *seq_tile0;   // [N + 1] first tile of each sequence
-    int32_t *cu;          // [max_tiles + 1] exclusive prefix sums of the tiles' units
+    int32_t *cu;          // [max_tiles + 1] exclusive prefix sums of the tiles' weights
     PrefillTile *tiles;   // [max_tiles]
     int32_t *start_tile;  // [C] tile holding the first unit of each CTA's range
     float2 *ml;           // [2 C][nrt * rows]
@@ -153,7 +156,7 @@ static __global__ void __launch_bounds__(1024) prefill_plan_kernel(const Prefill
             t.ntok = min(tq, n - t0);
             t.p0 = L - n + t0;
             a.tiles[k] = t;
-            u = prefill_units(t, a.kt);
+            u = prefill_units(t, a.kt) + a.extra;
         }
         int32_t total;
         const int32_t incl = block_scan_1024(u, units, warp_incl, &total);
@@ -186,45 +189,61 @@ static __global__ void __launch_bounds__(1024) prefill_plan_kernel(const Prefill
 }
 
 // A CTA's walk over its range: segments of consecutive units of one tile.
+// The next tile is read a segment ahead, so that moving on waits for no load.
 struct PrefillCursor {
-    int64_t x, hi;     // next flattened unit, end of the range
+    int64_t x, hi;     // weight position of the current tile's start, end of the range
     int32_t kvh, k;    // KV head and tile of the current segment
     int32_t j0, j1;    // its units [j0, j1)
     int32_t nu;        // units of its tile
-    int32_t tiles, U;
+    int32_t tiles;
     bool first;        // the range's first segment
+    PrefillTile t;     // the tile
+    PrefillTile t_next;
+    int32_t w_next;    // weight of the next tile
 
     // False when the CTA has no work.
     __device__ __forceinline__ bool init(const PrefillArgs &a, int32_t c) {
         tiles = a.ctl[0];
-        U = a.cu[tiles];
+        const int32_t U = a.cu[tiles];
         const int64_t W = (int64_t)a.Hk * U;
         const int32_t Ce = (int32_t)min(W, (int64_t)a.C);
         if (c >= Ce) return false;
-        x = split_begin(c, W, Ce);
+        const int64_t lo = split_begin(c, W, Ce);
         hi = split_begin((int64_t)c + 1, W, Ce);
-        kvh = (int32_t)(x / U);
+        kvh = (int32_t)(lo / U);
         k = a.start_tile[c];
+        const int32_t begin = a.cu[k];
+        x = (int64_t)kvh * U + begin;
         first = true;
-        j0 = (int32_t)(x - (int64_t)kvh * U) - a.cu[k];
-        set_end(a);
-        return true;
+        t = a.tiles[k];
+        nu = a.cu[k + 1] - begin - a.extra;
+        j0 = max(0, (int32_t)(lo - x) - a.extra);
+        j1 = units_to_end(a);
+        read_next(a);
+        return j1 > j0;
     }
-    __device__ __forceinline__ void set_end(const PrefillArgs &a) {
-        nu = a.cu[k + 1] - a.cu[k];
-        j1 = (int32_t)min((int64_t)nu, j0 + (hi - x));
+    __device__ __forceinline__ int32_t units_to_end(const PrefillArgs &a) const {
+        return (int32_t)max((int64_t)0, min((int64_t)nu, hi - x - a.extra));
+    }
+    __device__ __forceinline__ void read_next(const PrefillArgs &a) {
+        const int32_t n = k + 1 == tiles ? 0 : k + 1;
+        t_next = a.tiles[n];
+        w_next = a.cu[n + 1] - a.cu[n];
     }
     // Moves to the next segment; false at the range's end.
     __device__ __forceinline__ bool next(const PrefillArgs &a) {
-        x += j1 - j0;
+        x += nu + a.extra;
         first = false;
-        if (x >= hi) return false;
-        j0 = 0;
         if (++k == tiles) {
             k = 0;
             ++kvh;
         }
-        set_end(a);
+        t = t_next;
+        nu = w_next - a.extra;
+        j0 = 0;
+        j1 = units_to_end(a);
+        if (j1 == 0) return false;
+        read_next(a);
         return true;
     }
     __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == nu; }
@@ -233,8 +252,8 @@ struct PrefillCursor {
 };
 
 // Merge of the cut tiles: block (c - 1, y) folds the tile that the start of
-// CTA c's range cuts, if CTA c - 1 holds that tile's first unit (so each cut
-// tile has one c).  One warp per query row; pieces in CTA order.
+// CTA c's range cuts between units, if CTA c - 1 holds that tile's first unit
+// (so each cut tile has one c).  One warp per query row; pieces in CTA order.
 template <typename T, int D>
 static __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs a) {
     grid_dependency_wait();
@@ -247,15 +266,15 @@ static __global__ void __launch_bounds__(256) prefill_merge_kernel(const Prefill
     const int64_t x = split_begin(c, W, Ce);
     const int32_t kvh = (int32_t)(x / U), k = a.start_tile[c];
     const int64_t x0 = (int64_t)kvh * U + a.cu[k];
-    if (x0 == x) return;  // the range starts with its tile
-    const int32_t c0 = split_owner(x0, W, Ce);
+    if (x - x0 <= a.extra) return;  // the range starts with its tile's first unit
+    const int32_t c0 = split_owner(x0 + a.extra, W, Ce);
     if (c0 != c - 1) return;  // an earlier block's tile
     const int32_t c1 = split_owner((int64_t)kvh * U + a.cu[k + 1] - 1, W, Ce);
     const PrefillTile t = a.tiles[k];
     const int lane = threadIdx.x & 31;
     const int32_t wid = blockIdx.y * 8 + (threadIdx.x >> 5), nw = gridDim.y * 8;
     const int64_t slot_rows = (int64_t)a.nrt * a.rows;
-    const int64_t first_slot = 2 * (int64_t)c0 + (split_begin(c0, W, Ce) == x0 ? 0 : 1);
+    const int64_t first_slot = 2 * (int64_t)c0 + (split_begin(c0, W, Ce) >= x0 ? 0 : 1);
     constexpr int E = D / 32;  // accumulator elements of a lane
     for (int32_t i = wid; i < t.ntok * a.G; i += nw) {
         const int32_t tok = i / a.G, g = i - tok * a.G;

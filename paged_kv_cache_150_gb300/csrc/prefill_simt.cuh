@@ -21,7 +21,7 @@ namespace pa {
 // Element kinds of a cache, as the kernels read them.
 struct CacheE4m3 {};
 
-constexpr int kSimtRows = 64, kSimtKeys = 64, kSimtThreads = 256;
+constexpr int kSimtRows = 64, kSimtKeys = 64, kSimtThreads = 256, kSimtExtra = 1;
 
 // Shared memory: Q and K tiles with rows of D + 4 floats (rows of a 16-byte
 // column fall in distinct banks), V rows of D, P rows of 64 + 4, and the
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kSimtThreads, D == 256 ? 1 : 2) prefill_simt_k
     PrefillCursor cur;
     if (!cur.init(a, c)) return;
     do {
-        const PrefillTile t = a.tiles[cur.k];
+        const PrefillTile t = cur.t;
         const int32_t nrow = t.ntok * a.G;  // rows of this tile (<= 64)
         __syncthreads();                    // the previous segment's reads of Qs
         for (int e = tid; e < kSimtRows * (D / 4); e += kSimtThreads) {

@@ -28,7 +28,7 @@
 
 namespace pa {
 
-constexpr int kTcRows = 128, kTcKeys = 128, kTcThreads = 384;
+constexpr int kTcRows = 128, kTcKeys = 128, kTcThreads = 384, kTcExtra = 4;
 // Registers: 384 threads x 168 at launch; the two softmax warpgroups take 208
 // each (a row's 128 scores stay in registers), the third one keeps 88:
 // 256 x 208 + 128 x 88 = 384 x 168.
@@ -81,7 +81,7 @@ struct TcSegment {
     int32_t keys;   // keys the tile sees
     int32_t je[2], jend;
     __device__ __forceinline__ TcSegment(const PrefillArgs &a, const PrefillCursor &cur) {
-        t = a.tiles[cur.k];
+        t = cur.t;
         keys = t.p0 + t.ntok;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -283,6 +283,11 @@ __device__ __forceinline__ void tc_guard(const PrefillArgs &a, uint8_t *smem, co
     } while (cur.next(a));
 }
 
+// A value that is the same in every lane, as the compiler can see: loops and
+// branches on it keep the warp converged and its descriptors in uniform
+// registers.
+__device__ __forceinline__ int32_t uniform(int32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // -------------------------------------------------------------- MMA issuer
 // One warp; one elected lane issues.  MMAs of one thread complete in order, so S of a
 // unit may be computed over the P of the one before (its O += P V was issued
@@ -305,8 +310,10 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
     bool abort = false;
     do {
         const TcSegment sg(a, cur);
-        if (sg.jend <= cur.j0) continue;
-        const int32_t jg = guard_from(sg);
+        const int32_t j0 = uniform(cur.j0), jend = uniform(sg.jend), jg = uniform(guard_from(sg)),
+                      keys = uniform(sg.keys);
+        const int32_t je[2] = {uniform(sg.je[0]), uniform(sg.je[1])};
+        if (jend <= j0) continue;
         tc_wait(bar.q_full, segs & 1, abort, a.err);
         ++segs;
         auto issue_s = [&](int i, uint32_t slot) {
@@ -324,11 +331,11 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
         tc_fence_after();
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            if (cur.j0 < sg.je[i]) issue_s(i, st);
+            if (j0 < je[i]) issue_s(i, st);
         tc_commit_if(one, bar.kv_free + 8 * st);
-        if (cur.j0 + 1 == sg.jend) tc_commit_if(one, bar.q_free);
-        for (int32_t j = cur.j0; j < sg.jend; ++j) {
-            const bool more = j + 1 < sg.jend;
+        if (j0 + 1 == jend) tc_commit_if(one, bar.q_free);
+        for (int32_t j = j0; j < jend; ++j) {
+            const bool more = j + 1 < jend;
             const uint32_t nv = n, nk = n + 1;  // ring entries of this unit's V and the next one's K
             const uint32_t sv = nv % L::kStages, sk = nk % L::kStages;
             n += more ? 2 : 1;
@@ -336,13 +343,13 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
             const bool guarded = j >= jg;
             int ksteps = kTcKeys / 16;
             if (guarded) {
-                ksteps = min(ksteps, (sg.keys - j * kTcKeys + 15) / 16);
+                ksteps = min(ksteps, (keys - j * kTcKeys + 15) / 16);
                 if (one) mbar_arrive(bar.v_go);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if (j < sg.je[i]) {
-                    if (j == cur.j0) {  // O is about to be overwritten: its earlier rows have been read
+                if (j < je[i]) {
+                    if (j == j0) {  // O is about to be overwritten: its earlier rows have been read
                         if (no[i] > 0) tc_wait(bar.o_free + 8 * i, (no[i] - 1) & 1, abort, a.err);
                         ++no[i];
                     }
@@ -350,12 +357,12 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
                     ++np[i];
                 }
                 if (guarded && i == 0) tc_wait(bar.v_ok, units & 1, abort, a.err);
-                if (j < sg.je[i]) {
+                if (j < je[i]) {
                     tc_fence_after();
                     auto issue_o = [&](int k) {
                         tc_mma_bf16_ts_if(one, tmem + L::kO + i * D, tmem + L::kS + i * 128 + k * 8,
                                           v_desc + (sv * (L::kTile >> 4) + (uint32_t)k * 128u), IDESC_O,
-                                          j > cur.j0 || k > 0 ? 1u : 0u);
+                                          j > j0 || k > 0 ? 1u : 0u);
                     };
                     if (ksteps == kTcKeys / 16) {
 #pragma unroll
@@ -364,10 +371,10 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
 #pragma unroll 1
                         for (int k = 0; k < ksteps; ++k) issue_o(k);
                     }
-                    if (j + 1 == sg.je[i]) tc_commit_if(one, bar.o_full + 8 * i);
+                    if (j + 1 == je[i]) tc_commit_if(one, bar.o_full + 8 * i);
                 }
                 if (more && i == 0) tc_wait(bar.kv_full + 8 * sk, (nk / L::kStages) & 1, abort, a.err);
-                if (j + 1 < sg.je[i]) {
+                if (j + 1 < je[i]) {
                     tc_fence_after();
                     issue_s(i, sk);
                 }
@@ -375,9 +382,9 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
             if (guarded) ++units;
             tc_commit_if(one, bar.kv_free + 8 * sv);
             if (more) tc_commit_if(one, bar.kv_free + 8 * sk);
-            if (j + 2 == sg.jend) tc_commit_if(one, bar.q_free);
+            if (j + 2 == jend) tc_commit_if(one, bar.q_free);
         }
-    } while (cur.next(a));
+    } while (uniform(cur.next(a)));
     // Every MMA ends in an o_full that the softmax warps wait for; nothing of
     // this warp is in flight once they have (see the kernel's end).
 }
@@ -412,7 +419,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
             tc_fence_after();
             if (warp_rows) {
                 float x[128];
-                tmem_ld128(tS, x);
+                tmem_ld_cols(tS, x);
                 const int32_t nvis = last - j * kTcKeys + 1;
                 if (__any_sync(0xffffffffu, valid && nvis < kTcKeys)) {
 #pragma unroll
@@ -459,7 +466,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
                         sum[k & 1] = add_f32x2(sum[k & 1], f32x2(p0, p1));
                         w[k] = pack_bf16x2(p0, p1);
                     }
-                    tmem_st32_async(tS + 32 * h, w);
+                    { uint32_t w0[16],w1[16]; for(int q=0;q<16;++q){w0[q]=w[q];w1[q]=w[16+q];} tmem_st16_async(tS+32*h,w0); tmem_st16_async(tS+32*h+16,w1);}
                 }
                 float s0, s1;
                 f32x2_get(add_f32x2(sum[0], sum[1]), s0, s1);
@@ -562,7 +569,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     grid_dependency_wait();
     grid_launch_dependents();
     const int32_t c = blockIdx.x;
