@@ -19,7 +19,7 @@ SOURCES = ["decode_mma_shared.cu", "decode_mma_plain.cu", "decode_fma.cu", "deco
            "prefill_tc.cu", "prefill_simt.cu", "prefill.cu", "decode_fp8.cu", "cache_fp8.cu", "cache_ops.cu", "block_manager.cpp", "simulator.cpp", "shared_plan.cpp"]
 HEADERS = ["pa_common.cuh", "pa_internal.h", "decode_kernels.h", "decode_merge.cuh", "decode_plan.cuh", "decode_simt.cuh",
            "decode_mma.cuh", "decode_tc.cuh", "decode_fma.cuh", "fp8_codec.cuh", "prefill_kernels.h", "prefill_plan.cuh",
-           "prefill_simt.cuh", "prefill_tc.cuh", "tc_ptx.cuh"]
+           "prefill_simt.cuh", "prefill_tc.cuh", "tc_ptx.cuh", "decode_fp8.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -67,50 +67,79 @@ pa_status_t prefill_layout(bool tc, const pa_cache_desc_t *c, int32_t N, int32_t
     p->C = num_splits;
     if (p->C == 0) p->C = default_ctas(fn, p->threads, p->smem);
     if (p->C <= 0) return PA_ERR_CUDA;
+    prefill_workspace(p, N, c->head_dim);
+    return PA_OK;
+}
+
+void prefill_workspace(PrefillPlan *p, int32_t N, int32_t head_dim) {
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
         off = align256(off + bytes);
         return at;
     };
+    const size_t tiles = (size_t)p->max_tiles;
     p->off_ctl = take(256);
     p->off_tile0 = take(sizeof(int32_t) * ((size_t)N + 1));
-    p->off_cu = take(sizeof(int32_t) * ((size_t)tiles + 1));
-    p->off_tiles = take(sizeof(PrefillTile) * std::max<size_t>((size_t)tiles, 1));
+    p->off_cu = take(sizeof(int32_t) * (tiles + 1));
+    p->off_tiles = take(sizeof(PrefillTile) * std::max<size_t>(tiles, 1));
     p->off_start = take(sizeof(int32_t) * (size_t)p->C);
     const size_t slot_rows = 2 * (size_t)p->C * p->nrt * p->rows;
     p->off_ml = take(sizeof(float2) * slot_rows);
-    p->off_acc = take(sizeof(float) * slot_rows * c->head_dim);
+    p->off_acc = take(sizeof(float) * slot_rows * head_dim);
     p->total = off;
-    return PA_OK;
+}
+
+pa_status_t prefill_bind(const PrefillPlan &p, PrefillArgs *a, void *workspace) {
+    uint8_t *ws = (uint8_t *)workspace;
+    a->tq1 = p.tq1;
+    a->rows = p.rows;
+    a->nrt = p.nrt;
+    a->kt = p.kt;
+    a->extra = p.extra;
+    a->C = p.C;
+    a->max_tiles = p.max_tiles;
+    a->ctl = (int32_t *)(ws + p.off_ctl);
+    a->seq_tile0 = (int32_t *)(ws + p.off_tile0);
+    a->cu = (int32_t *)(ws + p.off_cu);
+    a->tiles = (PrefillTile *)(ws + p.off_tiles);
+    a->start_tile = (int32_t *)(ws + p.off_start);
+    a->ml = (float2 *)(ws + p.off_ml);
+    a->acc = (float *)(ws + p.off_acc);
+    a->err = device_error_word();
+    return a->err ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status_t prefill_launch_plan(PrefillArgs &a, cudaStream_t s) {
+    void *args[] = {&a};
+    return launch_pdl((const void *)prefill_plan_kernel, dim3(1), dim3(1024), args, 0, s) == cudaSuccess ? PA_OK
+                                                                                                       : PA_ERR_CUDA;
+}
+
+pa_status_t prefill_launch_merge(PrefillArgs &a, bool f32, int32_t head_dim, cudaStream_t s) {
+    if (a.C <= 1) return PA_OK;  // a single CTA cuts no tile
+    const void *fn = head_dim == 64    ? (f32 ? (const void *)prefill_merge_kernel<float, 64>
+                                              : (const void *)prefill_merge_kernel<__nv_bfloat16, 64>)
+                     : head_dim == 128 ? (f32 ? (const void *)prefill_merge_kernel<float, 128>
+                                              : (const void *)prefill_merge_kernel<__nv_bfloat16, 128>)
+                                       : (f32 ? (const void *)prefill_merge_kernel<float, 256>
+                                              : (const void *)prefill_merge_kernel<__nv_bfloat16, 256>);
+    void *args[] = {&a};
+    // 4 CTAs of 8 warps share the rows of a cut tile
+    return launch_pdl(fn, dim3(a.C - 1, 4), dim3(256), args, 0, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 pa_status_t prefill_launch(const PrefillPlan &p, const pa_cache_desc_t *c, PrefillArgs a, void *workspace,
                            cudaStream_t s) {
-    uint8_t *ws = (uint8_t *)workspace;
     a.Hk = c->num_kv_heads;
     a.G = a.H / a.Hk;
     a.NB = c->num_blocks;
     a.B = c->block_size;
-    a.tq1 = p.tq1;
-    a.rows = p.rows;
-    a.nrt = p.nrt;
-    a.kt = p.kt;
-    a.extra = p.extra;
-    a.C = p.C;
-    a.max_tiles = p.max_tiles;
-    a.ctl = (int32_t *)(ws + p.off_ctl);
-    a.seq_tile0 = (int32_t *)(ws + p.off_tile0);
-    a.cu = (int32_t *)(ws + p.off_cu);
-    a.tiles = (PrefillTile *)(ws + p.off_tiles);
-    a.start_tile = (int32_t *)(ws + p.off_start);
-    a.ml = (float2 *)(ws + p.off_ml);
-    a.acc = (float *)(ws + p.off_acc);
-    a.err = device_error_word();
-    if (!a.err) return PA_ERR_CUDA;
+    pa_status_t st = prefill_bind(p, &a, workspace);
+    if (st != PA_OK) return st;
     cudaGetLastError();  // clear a stale launch error so the checks below are ours
+    if ((st = prefill_launch_plan(a, s)) != PA_OK) return st;
     void *args[] = {&a};
-    if (launch_pdl((const void *)prefill_plan_kernel, dim3(1), dim3(1024), args, 0, s) != cudaSuccess) return PA_ERR_CUDA;
     size_t smem;
     const void *fn = p.tc ? prefill_tc_ptr(c->head_dim, &smem)
                           : prefill_simt_ptr(c->dtype, c->head_dim, c->layout, &smem);
@@ -126,18 +155,7 @@ pa_status_t prefill_launch(const PrefillPlan &p, const pa_cache_desc_t *c, Prefi
     } else if (launch_pdl(fn, dim3(p.C), dim3(p.threads), args, smem, s) != cudaSuccess) {
         return PA_ERR_CUDA;
     }
-    if (p.C > 1) {  // a single CTA cuts no tile
-        const bool f32 = c->dtype == PA_F32;
-        const void *mfn =
-            c->head_dim == 64    ? (f32 ? (const void *)prefill_merge_kernel<float, 64>
-                                        : (const void *)prefill_merge_kernel<__nv_bfloat16, 64>)
-            : c->head_dim == 128 ? (f32 ? (const void *)prefill_merge_kernel<float, 128>
-                                        : (const void *)prefill_merge_kernel<__nv_bfloat16, 128>)
-                                 : (f32 ? (const void *)prefill_merge_kernel<float, 256>
-                                        : (const void *)prefill_merge_kernel<__nv_bfloat16, 256>);
-        // 4 CTAs of 8 warps share the rows of a cut tile
-        if (launch_pdl(mfn, dim3(p.C - 1, 4), dim3(256), args, 0, s) != cudaSuccess) return PA_ERR_CUDA;
-    }
+    if ((st = prefill_launch_merge(a, c->dtype == PA_F32, c->head_dim, s)) != PA_OK) return st;
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

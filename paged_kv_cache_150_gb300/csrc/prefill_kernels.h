@@ -31,6 +31,16 @@ const void *prefill_tc_ptr(int D, size_t *smem);
 pa_status_t prefill_layout(bool tc, const pa_cache_desc_t *c, int32_t N, int32_t T, int32_t H, int32_t num_splits,
                            PrefillPlan *p);
 
+// The workspace behind p's shape (tiles, units, CTAs set) and head_dim.
+void prefill_workspace(PrefillPlan *p, int32_t N, int32_t head_dim);
+
+// Fills in the plan's part of a call's arguments; PA_ERR_CUDA without an error word.
+pa_status_t prefill_bind(const PrefillPlan &p, PrefillArgs *a, void *workspace);
+
+// Enqueue the work list, and the merge of the pieces (fp32 or bf16 output).
+pa_status_t prefill_launch_plan(PrefillArgs &a, cudaStream_t s);
+pa_status_t prefill_launch_merge(PrefillArgs &a, bool f32, int32_t head_dim, cudaStream_t s);
+
 // Enqueues the work list, the attention and the merge.  a holds the call's
 // arguments; the plan's fields and the workspace pointers are filled in here.
 pa_status_t prefill_launch(const PrefillPlan &p, const pa_cache_desc_t *c, PrefillArgs a, void *workspace,

@@ -36,7 +36,7 @@ struct PrefillArgs {
     const uint8_t *k_scale, *v_scale;  // 8-bit caches: biased scale exponents [NB, B, Hk]
     const int32_t *tables, *seq_lens;
     const int32_t *cu_q;  // nullptr: one new token per sequence
-    int32_t max_blocks, N, T, H, Hk, G, NB, B;
+    int32_t max_blocks, N, T, H, Hk, G, NB, B;  // (pa_decode_fp8's tensor-core kernel: Hk head groups of G query heads)
     int32_t tq1;          // tokens per row tile of the kernel (rows / G)
     int32_t rows;         // query rows of one row tile
     int32_t nrt;          // row tiles per tile (tq = tq1 * nrt)
