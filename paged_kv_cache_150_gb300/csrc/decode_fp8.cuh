@@ -9,7 +9,7 @@
 //     two so that its largest element lies in [2^14, 2^15): exact for every
 //     element within 2^28 of it;
 //   x = S 2^ek 2^eq scale log2(e);
-//   l += 2^(x - m),  O^T += v8^T P^T with P = 2^(x + ev - m') in fp16.
+//   p = 2^(x - m), l += p,  O^T += v8^T P^T with P = p 2^(ev + m - m') in fp16.
 // V's exponent goes into P, whose reference m' is the running maximum of
 // x + ev (m is that of x), so P stays within 2^8 whatever the rows' sizes; at
 // the end O is scaled by 2^(m' - m).  P's fp16 rounding (2^-11) is the only one
@@ -37,6 +37,7 @@ namespace pa {
 
 constexpr int kF8Warps = 8, kF8Threads = 32 * (kF8Warps + 1);
 constexpr int kF8SlotRows = 64;  // query rows of a piece: NH * G <= 64
+constexpr float kTopP = 256.f;   // 2^kLazyMaxSlack
 constexpr int kF8Extra = 2;      // weight of a sequence beside its units (prefill_plan.cuh)
 
 // The parts of a call beyond PrefillArgs (there G is NH * G and Hk the number
@@ -93,10 +94,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-// Two codes (a half word) to fp16 (exact).
-__device__ __forceinline__ uint32_t codes_f16x2(uint32_t w) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w, __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// The codes of a word's low and high half to fp16 (exact).
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 
 // Units of T tokens that the current segment takes: [j0, j1), none without keys.
@@ -168,6 +170,17 @@ __device__ __forceinline__ void f8_producer(const PrefillArgs &a, const F8Args &
         late = !mbar_wait_bounded(smem_u32(&full[k % f.stages]), (k / f.stages) & 1);
 }
 
+// Moves a warp's walk on: every lane works on its own copy and all store the
+// same one.
+__device__ __forceinline__ bool f8_next(PrefillCursor &cur, const PrefillArgs &a) {
+    PrefillCursor mine = cur;
+    __syncwarp();
+    const bool more = mine.next(a);
+    cur = mine;
+    __syncwarp();
+    return more;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kF8Threads, 2)
     decode_fp8_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -191,8 +204,15 @@ __global__ void __launch_bounds__(kF8Threads, 2)
     grid_dependency_wait();
     grid_launch_dependents();
     const int32_t c = blockIdx.x;
-    PrefillCursor cur;
-    if (!cur.init(a, c)) return;
+    // Each warp's walk, in shared memory: it is used between segments only.
+    __shared__ PrefillCursor curs[kF8Warps + 1];
+    PrefillCursor &cur = curs[warp];
+    {
+        PrefillCursor first;
+        if (!first.init(a, c)) return;
+        cur = first;  // the same in every lane
+    }
+    __syncwarp();
     if (warp == kF8Warps) {
         f8_producer<D>(a, f, smem, &tmk, &tmv, full, empty, cur, lane);
         return;
@@ -210,12 +230,18 @@ __global__ void __launch_bounds__(kF8Threads, 2)
     const uint32_t line = (uint32_t)(tk % f.gran);
     const uint32_t row_off = (uint32_t)(((tk / f.gran) * f.NH + h) * f.gran) * D + line * D;
     const uint32_t swz = (line >> SH) & SM;
-    auto chunk_addr = [&](uint32_t base, int j) { return base + row_off + ((((uint32_t)(j + (mi >> 1))) ^ swz) << 4); };
-    uint32_t n = 0;
+    // chunk j + (mi >> 1), j even: (j | mi >> 1) ^ swz = j ^ (mi >> 1 ^ swz), and
+    // tiles are aligned to 128 bytes
+    const uint32_t lane_off = row_off + ((((uint32_t)mi >> 1) ^ swz) << 4);
+    // scale bytes of token r of the slice
+    const uint32_t sc_head = (uint32_t)((sub * 16 + r) * f.Hk + h);
+    int st = 0;
+    uint32_t phase = 0;
     bool abort = false;
     do {
         const PrefillTile t = cur.t;
-        const int32_t keys = t.p0 + 1, je = f8_units_end(cur, f.T);
+        const int32_t keys = t.p0 + 1, j0 = cur.j0, je = f8_units_end(cur, f.T);
+        const uint32_t sc_off = sc_head + (uint32_t)(cur.kvh * f.NH);
         const int32_t head0 = (cur.kvh * f.NH + h) * f.G;  // first query head of this warp's KV head
         // Q: column n = query head r; per 16-element chunk this thread's elements 4 cq .. + 3
         uint32_t qf[NC][2];
@@ -252,49 +278,55 @@ __global__ void __launch_bounds__(kF8Threads, 2)
 #pragma unroll
         for (int j = 0; j < NC; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
         float m0 = -INFINITY, m1 = -INFINITY, v0 = -INFINITY, v1 = -INFINITY;  // m and m' of both columns
+        float c0 = 0.f, c1 = 0.f;                                              // 2^(m - m')
         float l0 = 0.f, l1 = 0.f;
-        for (int32_t j = cur.j0; j < je; ++j, ++n) {
-            const uint32_t st = n % f.stages;
-            if (!abort && !__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&full[st]), (n / f.stages) & 1))) {
+        for (int32_t j = j0; j < je; ++j) {
+            if (!abort && !__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&full[st]), phase))) {
                 // run on without waiting: every barrier still gets its
                 // arrivals; the error word marks the output as unreliable
                 if (lane == 0) atomicOr(a.err, kErrTimeout);
                 abort = true;
             }
-            const int32_t tok0 = j * f.T + sub * 16;
-            if (tok0 < keys) {
-                const uint32_t kb = tiles + st * 2 * L::kTile, vb = kb + L::kTile;
-                float s[2][4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[0][e] = s[1][e] = 0.f;
+            const int32_t rest = keys - (j * f.T + sub * 16);  // tokens of this slice and after it
+            if (rest > 0) {
+                const uint32_t kb = tiles + (uint32_t)st * 2 * L::kTile + lane_off, vb = kb + L::kTile;
+                // bytes of tokens r and r + 8; 255 (no write makes one) counts as 254
+                const uint8_t *ks = sc + (uint32_t)st * 2 * f.scale_bytes + sc_off, *vs = ks + f.scale_bytes;
+                const uint32_t ka = ks[0], kc = ks[8 * f.Hk], va = vs[0], vc = vs[8 * f.Hk];
+                float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j2 = 0; j2 < NC; j2 += 2) {
-                    uint32_t w0, w1, w2, w3;
-                    ldmatrix_x4(chunk_addr(kb, j2), w0, w1, w2, w3);
-                    mma_f16_16816(s[0], codes_f16x2(w0 & 0xffffu), codes_f16x2(w1 & 0xffffu), codes_f16x2(w0 >> 16),
-                                  codes_f16x2(w1 >> 16), qf[j2][0], qf[j2][1]);
-                    mma_f16_16816(s[1], codes_f16x2(w2 & 0xffffu), codes_f16x2(w3 & 0xffffu), codes_f16x2(w2 >> 16),
-                                  codes_f16x2(w3 >> 16), qf[j2 + 1][0], qf[j2 + 1][1]);
+                    uint32_t w[4], lo[4], hi[4];
+                    ldmatrix_x4(kb ^ (uint32_t)(j2 << 4), w[0], w[1], w[2], w[3]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) codes_f16(w[k], lo[k], hi[k]);
+                    mma_f16_16816(s, lo[0], lo[1], hi[0], hi[1], qf[j2][0], qf[j2][1]);
+                    mma_f16_16816(s, lo[2], lo[3], hi[2], hi[3], qf[j2 + 1][0], qf[j2 + 1][1]);
                 }
-                // tokens tok0 + r and tok0 + r + 8 of this thread
-                const uint8_t *ks = sc + (size_t)st * 2 * f.scale_bytes + (uint32_t)((sub * 16 + r) * f.Hk) +
-                                    (uint32_t)(cur.kvh * f.NH + h);
-                const uint8_t *vs = ks + f.scale_bytes;
-                // a byte of 255 (no write makes one) counts as 254
-                const float ka = __uint_as_float(min((uint32_t)ks[0], 254u) << 23);
-                const float kc = __uint_as_float(min((uint32_t)ks[8 * f.Hk], 254u) << 23);
-                const float va = (float)vs[0] - 127.f, vc = (float)vs[8 * f.Hk] - 127.f;
-                const bool in_a = tok0 + r < keys, in_c = tok0 + r + 8 < keys;
-                const float x0 = in_a ? (s[0][0] + s[1][0]) * ka * qs0 : -INFINITY;
-                const float x1 = in_a ? (s[0][1] + s[1][1]) * ka * qs1 : -INFINITY;
-                const float x2 = in_c ? (s[0][2] + s[1][2]) * kc * qs0 : -INFINITY;
-                const float x3 = in_c ? (s[0][3] + s[1][3]) * kc * qs1 : -INFINITY;
-                // Lazy running maxima (kLazyMaxSlack), columns over the 8
-                // lanes of a group.
-                float a0 = fmaxf(x0, x2), a1 = fmaxf(x1, x3);
-                float b0 = fmaxf(x0 + va, x2 + vc), b1 = fmaxf(x1 + va, x3 + vc);
-                if (__any_sync(0xffffffffu, a0 > m0 + kLazyMaxSlack || a1 > m1 + kLazyMaxSlack ||
-                                                b0 > v0 + kLazyMaxSlack || b1 > v1 + kLazyMaxSlack)) {
+                const float fa = __uint_as_float(min(ka, 254u) << 23), fc = __uint_as_float(min(kc, 254u) << 23);
+                float x0 = s[0] * (fa * qs0), x1 = s[1] * (fa * qs1);
+                float x2 = s[2] * (fc * qs0), x3 = s[3] * (fc * qs1);
+                if (rest < 16) {
+                    if (r >= rest) x0 = x1 = -INFINITY;
+                    if (r + 8 >= rest) x2 = x3 = -INFINITY;
+                }
+                const float ga = __uint_as_float(min(va, 254u) << 23), gc = __uint_as_float(min(vc, 254u) << 23);
+                float p0, p1, p2, p3, P0, P1, P2, P3;
+                auto weigh = [&]() {
+                    p0 = ex2_approx(x0 - m0), p1 = ex2_approx(x1 - m1);
+                    p2 = ex2_approx(x2 - m0), p3 = ex2_approx(x3 - m1);
+                    // the bound keeps a factor that overflows beside p = 0 finite
+                    P0 = p0 * fminf(ga * c0, 1e36f), P1 = p1 * fminf(ga * c1, 1e36f);
+                    P2 = p2 * fminf(gc * c0, 1e36f), P3 = p3 * fminf(gc * c1, 1e36f);
+                };
+                weigh();
+                // Lazy running maxima: moved only when some p or P passes
+                // 2^kLazyMaxSlack (always on a segment's first tokens).
+                const float top = fmaxf(fmaxf(fmaxf(p0, p1), fmaxf(p2, p3)), fmaxf(fmaxf(P0, P1), fmaxf(P2, P3)));
+                if (__any_sync(0xffffffffu, top > kTopP || m0 == -INFINITY || m1 == -INFINITY)) {
+                    const float ea = (float)min(va, 254u) - 127.f, ec = (float)min(vc, 254u) - 127.f;
+                    float a0 = fmaxf(x0, x2), a1 = fmaxf(x1, x3);
+                    float b0 = fmaxf(x0 + ea, x2 + ec), b1 = fmaxf(x1 + ea, x3 + ec);
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) {
                         a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, off));
@@ -302,48 +334,46 @@ __global__ void __launch_bounds__(kF8Threads, 2)
                         b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, off));
                         b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, off));
                     }
-                    a0 = fmaxf(a0, m0), a1 = fmaxf(a1, m1), b0 = fmaxf(b0, v0), b1 = fmaxf(b1, v1);
-                    // columns past G stay at 0 scores; a column of -inf scores keeps its references
+                    // a reference that stays (also at -inf) keeps its factor 1
                     if (a0 > m0) l0 *= ex2_approx(m0 - a0), m0 = a0;
                     if (a1 > m1) l1 *= ex2_approx(m1 - a1), m1 = a1;
                     const float f0 = b0 > v0 ? ex2_approx(v0 - b0) : 1.f, f1 = b1 > v1 ? ex2_approx(v1 - b1) : 1.f;
-                    v0 = b0, v1 = b1;
+                    v0 = fmaxf(v0, b0), v1 = fmaxf(v1, b1);
+                    c0 = ex2_approx(m0 - v0), c1 = ex2_approx(m1 - v1);
 #pragma unroll
                     for (int jj = 0; jj < NC; ++jj) o[jj][0] *= f0, o[jj][1] *= f1, o[jj][2] *= f0, o[jj][3] *= f1;
+                    weigh();
                 }
-                const float mr0 = m0 == -INFINITY ? 0.f : m0, mr1 = m1 == -INFINITY ? 0.f : m1;
-                const float vr0 = v0 == -INFINITY ? 0.f : v0, vr1 = v1 == -INFINITY ? 0.f : v1;
-                l0 += ex2_approx(x0 - mr0) + ex2_approx(x2 - mr0);
-                l1 += ex2_approx(x1 - mr1) + ex2_approx(x3 - mr1);
-                const uint32_t pb0 = movmatrix_trans(
-                    pack_f16x2(ex2_approx(x0 + (va - vr0)), ex2_approx(x1 + (va - vr1))));
-                const uint32_t pb1 = movmatrix_trans(
-                    pack_f16x2(ex2_approx(x2 + (vc - vr0)), ex2_approx(x3 + (vc - vr1))));
+                l0 += p0 + p2;
+                l1 += p1 + p3;
+                const uint32_t pb0 = movmatrix_trans(pack_f16x2(P0, P1));
+                const uint32_t pb1 = movmatrix_trans(pack_f16x2(P2, P3));
                 // Tokens past the sequence's end may hold NaN codes: zeros in
                 // their place (a word holds tokens 2 cq and 2 cq + 1).
-                uint32_t keep_a = 0xffffffffu, keep_c = 0xffffffffu;
-                if (tok0 + 16 > keys) {
-                    const int32_t rest = keys - tok0 - 2 * cq;
-                    keep_a = rest >= 2 ? 0xffffffffu : rest == 1 ? 0x0000ffffu : 0u;
-                    keep_c = rest >= 10 ? 0xffffffffu : rest == 9 ? 0x0000ffffu : 0u;
-                }
+                auto add_v = [&](uint32_t keep_a, uint32_t keep_c) {
 #pragma unroll
-                for (int j2 = 0; j2 < NC; j2 += 2) {
-                    uint32_t w0, w1, w2, w3;
-                    ldmatrix_x4_trans(chunk_addr(vb, j2), w0, w1, w2, w3);
-                    // codes (token, column): t0d0 t0d1 t1d0 t1d1 -> t0d0 t1d0, t0d1 t1d1
-                    w0 = __byte_perm(w0 & keep_a, 0u, 0x3120);
-                    w1 = __byte_perm(w1 & keep_c, 0u, 0x3120);
-                    w2 = __byte_perm(w2 & keep_a, 0u, 0x3120);
-                    w3 = __byte_perm(w3 & keep_c, 0u, 0x3120);
-                    mma_f16_16816(o[j2], codes_f16x2(w0 & 0xffffu), codes_f16x2(w0 >> 16), codes_f16x2(w1 & 0xffffu),
-                                  codes_f16x2(w1 >> 16), pb0, pb1);
-                    mma_f16_16816(o[j2 + 1], codes_f16x2(w2 & 0xffffu), codes_f16x2(w2 >> 16),
-                                  codes_f16x2(w3 & 0xffffu), codes_f16x2(w3 >> 16), pb0, pb1);
+                    for (int j2 = 0; j2 < NC; j2 += 2) {
+                        uint32_t w[4], lo[4], hi[4];
+                        ldmatrix_x4_trans(vb ^ (uint32_t)(j2 << 4), w[0], w[1], w[2], w[3]);
+                        // codes (token, column): t0d0 t0d1 t1d0 t1d1 -> t0d0 t1d0, t0d1 t1d1
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            codes_f16(__byte_perm(w[k] & (k & 1 ? keep_c : keep_a), 0u, 0x3120), lo[k], hi[k]);
+                        mma_f16_16816(o[j2], lo[0], hi[0], lo[1], hi[1], pb0, pb1);
+                        mma_f16_16816(o[j2 + 1], lo[2], hi[2], lo[3], hi[3], pb0, pb1);
+                    }
+                };
+                if (rest >= 16) {
+                    add_v(0xffffffffu, 0xffffffffu);
+                } else {
+                    const int32_t ra = rest - 2 * cq, rc = ra - 8;
+                    add_v(ra >= 2 ? 0xffffffffu : ra == 1 ? 0x0000ffffu : 0u,
+                          rc >= 2 ? 0xffffffffu : rc == 1 ? 0x0000ffffu : 0u);
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
+            if (++st == f.stages) st = 0, phase ^= 1u;
         }
         // l over the group's lanes; O in units of 2^m (in two steps: the
         // factor alone may leave fp32's range where the product does not)
@@ -457,7 +487,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
                 }
             }
         }
-    } while (cur.next(a));
+    } while (f8_next(cur, a));
 }
 
 }  // namespace pa
