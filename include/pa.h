@@ -352,8 +352,8 @@ int32_t pa_split_owner(int64_t total_blocks, int32_t num_splits, int64_t x);
  * heads of a KV head side by side), and the list of (KV head, tile, unit of
  * keys) is split evenly over persistent CTAs; a tile cut between CTAs is
  * merged by a second kernel.  The split depends only on the lengths and the
- * split count, so the same call gives the same bits every time.  Each call
- * launches 3 kernels on `stream` (work list, attention, merge).
+ * split count, so the same call gives the same bits every time.  A call
+ * launches up to 3 kernels on `stream` (work list, attention, merge).
  *
  * out, q        device [num_tokens, H, D], the cache's element type.
  * cu_q_lens     device int32 [num_seqs + 1], not decreasing, within

@@ -184,7 +184,7 @@ __device__ __forceinline__ bool f8_next(PrefillCursor &cur, const PrefillArgs &a
 template <int D>
 __global__ void __launch_bounds__(kF8Threads, 2)
     decode_fp8_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                      const PrefillArgs a, const F8Args f) {
+                      const __grid_constant__ PrefillArgs a, const F8Args f) {
     using L = F8Smem<D>;
     constexpr int NC = D / 16;      // 16-byte chunks of a code row
     constexpr int SH = D == 128 ? 0 : 1;  // TMA swizzle: chunk ^ (line & 7) of 128-byte lines, chunk ^ (line / 2 & 3) of 64-byte ones

@@ -117,7 +117,8 @@ pa_status_t prefill_launch_plan(PrefillArgs &a, cudaStream_t s) {
 }
 
 pa_status_t prefill_launch_merge(PrefillArgs &a, bool f32, int32_t head_dim, cudaStream_t s) {
-    if (a.C <= 1) return PA_OK;  // a single CTA cuts no tile
+    // a single CTA cuts no tile, nor is one of a single unit ever cut
+    if (a.C <= 1 || (int64_t)a.max_blocks * a.B <= a.kt) return PA_OK;
     const void *fn = head_dim == 64    ? (f32 ? (const void *)prefill_merge_kernel<float, 64>
                                               : (const void *)prefill_merge_kernel<__nv_bfloat16, 64>)
                      : head_dim == 128 ? (f32 ? (const void *)prefill_merge_kernel<float, 128>

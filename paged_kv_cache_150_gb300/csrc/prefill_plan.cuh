@@ -189,8 +189,10 @@ static __global__ void __launch_bounds__(1024) prefill_plan_kernel(const Prefill
 }
 
 // A CTA's walk over its range: segments of consecutive units of one tile.
-// The next tile is read a segment ahead, so that moving on waits for no load.
-struct PrefillCursor {
+// kAhead: the next tile is read a segment ahead, so that moving on waits for no
+// load (at the price of five registers).
+template <bool kAhead>
+struct PrefillWalk {
     int64_t x, hi;     // weight position of the current tile's start, end of the range
     int32_t kvh, k;    // KV head and tile of the current segment
     int32_t j0, j1;    // its units [j0, j1)
@@ -219,7 +221,7 @@ struct PrefillCursor {
         nu = a.cu[k + 1] - begin - a.extra;
         j0 = max(0, (int32_t)(lo - x) - a.extra);
         j1 = units_to_end(a);
-        read_next(a);
+        if constexpr (kAhead) read_next(a);
         return j1 > j0;
     }
     __device__ __forceinline__ int32_t units_to_end(const PrefillArgs &a) const {
@@ -238,18 +240,24 @@ struct PrefillCursor {
             k = 0;
             ++kvh;
         }
-        t = t_next;
-        nu = w_next - a.extra;
+        if constexpr (kAhead) {
+            t = t_next;
+            nu = w_next - a.extra;
+        } else {
+            t = a.tiles[k];
+            nu = a.cu[k + 1] - a.cu[k] - a.extra;
+        }
         j0 = 0;
         j1 = units_to_end(a);
         if (j1 == 0) return false;
-        read_next(a);
+        if constexpr (kAhead) read_next(a);
         return true;
     }
     __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == nu; }
     // Slot of this segment's piece: a range has at most two, its first segment's and its last one's.
     __device__ __forceinline__ int64_t slot(int32_t c) const { return 2 * (int64_t)c + (first ? 0 : 1); }
 };
+using PrefillCursor = PrefillWalk<true>;
 
 // Merge of the cut tiles: block (c - 1, y) folds the tile that the start of
 // CTA c's range cuts between units, if CTA c - 1 holds that tile's first unit

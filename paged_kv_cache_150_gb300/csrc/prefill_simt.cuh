@@ -103,7 +103,7 @@ __device__ __forceinline__ void add_pv(const float *Ps, const float *Vs, float (
 }
 
 template <typename T, typename CT, int D, int LAYOUT>
-__global__ void __launch_bounds__(kSimtThreads, D == 256 ? 1 : 2) prefill_simt_kernel(const PrefillArgs a) {
+__global__ void __launch_bounds__(kSimtThreads, D == 256 ? 1 : 2) prefill_simt_kernel(const __grid_constant__ PrefillArgs a) {
     using L = SimtSmem<D>;
     extern __shared__ __align__(16) float sm[];
     float *Qs = sm + L::kQ, *Ks = sm + L::kK, *Vs = sm + L::kV, *Ps = sm + L::kP;

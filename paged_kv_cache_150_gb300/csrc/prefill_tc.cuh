@@ -80,7 +80,8 @@ struct TcSegment {
     PrefillTile t;
     int32_t keys;   // keys the tile sees
     int32_t je[2], jend;
-    __device__ __forceinline__ TcSegment(const PrefillArgs &a, const PrefillCursor &cur) {
+    template <class Walk>
+    __device__ __forceinline__ TcSegment(const PrefillArgs &a, const Walk &cur) {
         t = cur.t;
         keys = t.p0 + t.ntok;
 #pragma unroll
@@ -103,7 +104,7 @@ struct TcSegment {
 template <int D, bool kIsV>
 __device__ __forceinline__ void tc_producer(const PrefillArgs &a, uint8_t *smem, const TcBars &bar,
                                             const CUtensorMap *tmq, const CUtensorMap *tm, int32_t gran,
-                                            PrefillCursor cur, int lane) {
+                                            int32_t c, int lane) {
     using L = TcPrefill<D>;
     if (lane == 0) {
         if (!kIsV) prefetch_tmap(tmq);
@@ -116,6 +117,8 @@ __device__ __forceinline__ void tc_producer(const PrefillArgs &a, uint8_t *smem,
     const uint32_t box_off = (uint32_t)panel * L::kPanel + (uint32_t)(bi * gran) * 128u;
     uint32_t n = kIsV ? 1 : 0, segs = 0;  // next ring entry, segments with units
     bool abort = false;
+    PrefillCursor cur;
+    if (!cur.init(a, c)) return;
     do {
         const TcSegment sg(a, cur);
         if (sg.jend <= cur.j0) continue;
@@ -209,13 +212,15 @@ __device__ __forceinline__ uint32_t odd_bits(uint32_t w) { return ((w & 0x7f807f
 
 template <int D>
 __device__ __forceinline__ void tc_guard(const PrefillArgs &a, uint8_t *smem, const TcBars &bar, const OddColumns &odd,
-                                         PrefillCursor cur, int lane) {
+                                         int32_t c, int lane) {
     using L = TcPrefill<D>;
     constexpr int kChunks = D / 8;
     const uint32_t ring = smem_u32(smem) + L::kRing;
     uint32_t n = 1, segs = 0, units = 0;  // ring entry of V, segments, guarded units
     uint32_t no[2] = {0, 0};              // earlier segments with units per row tile
     bool abort = false, dirty = false;
+    PrefillCursor cur;
+    if (!cur.init(a, c)) return;
     do {
         const TcSegment sg(a, cur);
         if (sg.jend <= cur.j0) continue;
@@ -294,7 +299,7 @@ __device__ __forceinline__ int32_t uniform(int32_t x) { return __shfl_sync(0xfff
 // earlier), and a row tile's S being complete says that its earlier O is too.
 template <int D>
 __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, const TcBars &bar, uint32_t tmem,
-                                          PrefillCursor cur, int lane) {
+                                          int32_t c, int lane) {
     using L = TcPrefill<D>;
     constexpr uint32_t IDESC_S = tc_idesc_bf16(128, kTcKeys, false, false);
     constexpr uint32_t IDESC_O = tc_idesc_bf16(128, D, false, true);
@@ -308,6 +313,8 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
     uint32_t np[2] = {0, 0};              // P tiles taken per row tile
     uint32_t no[2] = {0, 0};              // segments with units per row tile
     bool abort = false;
+    PrefillCursor cur;
+    if (!cur.init(a, c)) return;
     do {
         const TcSegment sg(a, cur);
         const int32_t j0 = uniform(cur.j0), jend = uniform(sg.jend), jg = uniform(guard_from(sg)),
@@ -393,7 +400,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
 // Four warps per row tile; a thread owns one query row (tensor-memory lane).
 template <int D>
 __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &bar, uint32_t tmem,
-                                           const OddColumns &odd, PrefillCursor cur, int32_t c,
+                                           const OddColumns &odd, int32_t c,
                                            int i, int warp, int lane) {
     using L = TcPrefill<D>;
     const int r = warp * 32 + lane;  // row of the row tile
@@ -404,6 +411,8 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
     const float sl = a.scale_log2;
     uint32_t ns = 0, no = 0, segs = 0;
     bool abort = false;
+    PrefillWalk<false> cur;
+    if (!cur.init(a, c)) return;
     do {
         const TcSegment sg(a, cur);
         const int32_t tok = i * a.tq1 + tok_r;
@@ -456,17 +465,17 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
                 const uint64_t sl2 = f32x2(sl, sl), mm2 = f32x2(-mref, -mref);
                 uint64_t sum[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t w[32];
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t w[16];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
+                    for (int k = 0; k < 16; ++k) {
                         float y0, y1;
-                        f32x2_get(fma_f32x2(f32x2(x[64 * h + 2 * k], x[64 * h + 2 * k + 1]), sl2, mm2), y0, y1);
+                        f32x2_get(fma_f32x2(f32x2(x[32 * h + 2 * k], x[32 * h + 2 * k + 1]), sl2, mm2), y0, y1);
                         const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
                         sum[k & 1] = add_f32x2(sum[k & 1], f32x2(p0, p1));
                         w[k] = pack_bf16x2(p0, p1);
                     }
-                    { uint32_t w0[16],w1[16]; for(int q=0;q<16;++q){w0[q]=w[q];w1[q]=w[16+q];} tmem_st16_async(tS+32*h,w0); tmem_st16_async(tS+32*h+16,w1);}
+                    tmem_st16_async(tS + 16 * h, w);
                 }
                 float s0, s1;
                 f32x2_get(add_f32x2(sum[0], sum[1]), s0, s1);
@@ -537,7 +546,8 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                      const __grid_constant__ CUtensorMap tmv, const PrefillArgs a, const int32_t gran) {
+                      const __grid_constant__ CUtensorMap tmv, const __grid_constant__ PrefillArgs a,
+                      const int32_t gran) {
     using L = TcPrefill<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -573,22 +583,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     grid_dependency_wait();
     grid_launch_dependents();
     const int32_t c = blockIdx.x;
-    PrefillCursor cur;
-    if (cur.init(a, c)) {
-        if (warp < 8) {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcSoftmaxRegs));
-            tc_softmax<D>(a, bar, tmem, odd, cur, c, warp >> 2, warp & 3, lane);
-        } else {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcOtherRegs));
-            if (warp == 8)
-                tc_issuer<D>(a, smem, bar, tmem, cur, lane);
-            else if (warp == 9)
-                tc_producer<D, false>(a, smem, bar, &tmq, &tmk, gran, cur, lane);
-            else if (warp == 10)
-                tc_producer<D, true>(a, smem, bar, &tmq, &tmv, gran, cur, lane);
-            else
-                tc_guard<D>(a, smem, bar, odd, cur, lane);
-        }
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcSoftmaxRegs));
+        tc_softmax<D>(a, bar, tmem, odd, c, warp >> 2, warp & 3, lane);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcOtherRegs));
+        if (warp == 8)
+            tc_issuer<D>(a, smem, bar, tmem, c, lane);
+        else if (warp == 9)
+            tc_producer<D, false>(a, smem, bar, &tmq, &tmk, gran, c, lane);
+        else if (warp == 10)
+            tc_producer<D, true>(a, smem, bar, &tmq, &tmv, gran, c, lane);
+        else
+            tc_guard<D>(a, smem, bar, odd, c, lane);
     }
     // The softmax warps have waited for the last o_full, which every MMA
     // precedes: nothing uses the tensor memory any more.
