@@ -7,9 +7,9 @@ namespace pa {
 template <typename T, typename CT, int LAYOUT>
 static const void *simt_for(int D, size_t *smem) {
     switch (D) {
-        case 64: *smem = SimtSmem<64>::kBytes; return (const void *)prefill_simt_kernel<T, CT, 64, LAYOUT>;
-        case 128: *smem = SimtSmem<128>::kBytes; return (const void *)prefill_simt_kernel<T, CT, 128, LAYOUT>;
-        case 256: *smem = SimtSmem<256>::kBytes; return (const void *)prefill_simt_kernel<T, CT, 256, LAYOUT>;
+        case 64: *smem = SimtSmem<64, simt_pipe<CT, 64, LAYOUT>()>::kBytes; return (const void *)prefill_simt_kernel<T, CT, 64, LAYOUT>;
+        case 128: *smem = SimtSmem<128, simt_pipe<CT, 128, LAYOUT>()>::kBytes; return (const void *)prefill_simt_kernel<T, CT, 128, LAYOUT>;
+        case 256: *smem = SimtSmem<256, simt_pipe<CT, 256, LAYOUT>()>::kBytes; return (const void *)prefill_simt_kernel<T, CT, 256, LAYOUT>;
     }
     return nullptr;
 }

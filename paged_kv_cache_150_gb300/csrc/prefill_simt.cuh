@@ -9,6 +9,9 @@
 // arithmetic is fp32 (8-bit codes are decoded, bf16 widened, as a tile is
 // staged).  Per four steps of the head dimension a thread makes 64 FMAs from
 // 8 16-byte shared loads (4 of them broadcasts), so the FMA pipes bound it.
+// fp32 rows of head_dim 64 and 128 are staged by cp.async a unit ahead, into
+// the second of two buffers, with the block-table entries read two units
+// ahead; the other kinds are staged in place.
 #pragma once
 
 #include <type_traits>
@@ -26,15 +29,28 @@ constexpr int kSimtRows = 64, kSimtKeys = 64, kSimtThreads = 256, kSimtExtra = 1
 // Shared memory: Q and K tiles with rows of D + 4 floats (rows of a 16-byte
 // column fall in distinct banks), V rows of D, P rows of 64 + 4, and the
 // element offset of each key's row.
-template <int D>
+template <int D, bool kPipe>
 struct SimtSmem {
+    static constexpr int kBufs = kPipe ? 2 : 1;
     static constexpr int kQ = 0;
     static constexpr int kK = kQ + kSimtRows * (D + 4);
-    static constexpr int kV = kK + kSimtKeys * (D + 4);
-    static constexpr int kP = kV + kSimtKeys * D;
+    static constexpr int kV = kK + kBufs * kSimtKeys * (D + 4);
+    static constexpr int kP = kV + kBufs * kSimtKeys * D;
     static constexpr int kSlots = kP + kSimtRows * (kSimtKeys + 4);
-    static constexpr size_t kBytes = (size_t)kSlots * 4 + kSimtKeys * 8;
+    static constexpr size_t kBytes = (size_t)kSlots * 4 + kBufs * kSimtKeys * 8;
 };
+// Whether a kind of cache is staged ahead.
+template <typename CT, int D, int LAYOUT>
+constexpr bool simt_pipe() {
+    return std::is_same<CT, float>::value && LAYOUT == PA_LAYOUT_ROW && D <= 128;
+}
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
@@ -103,10 +119,12 @@ __device__ __forceinline__ void add_pv(const float *Ps, const float *Vs, float (
 }
 
 template <typename T, typename CT, int D, int LAYOUT>
-__global__ void __launch_bounds__(kSimtThreads, D == 256 ? 1 : 2) prefill_simt_kernel(const __grid_constant__ PrefillArgs a) {
-    using L = SimtSmem<D>;
+__global__ void __launch_bounds__(kSimtThreads, D == 256 ? 1 : 2)
+    prefill_simt_kernel(const __grid_constant__ PrefillArgs a) {
+    constexpr bool kPipe = simt_pipe<CT, D, LAYOUT>();
+    using L = SimtSmem<D, kPipe>;
     extern __shared__ __align__(16) float sm[];
-    float *Qs = sm + L::kQ, *Ks = sm + L::kK, *Vs = sm + L::kV, *Ps = sm + L::kP;
+    float *Qs = sm + L::kQ, *Ps = sm + L::kP;
     int64_t *slots = reinterpret_cast<int64_t *>(sm + L::kSlots);
     constexpr int QS = D + 4, PS = kSimtKeys + 4, EV = D / 64;  // row strides, float4 columns per thread
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
@@ -118,7 +136,53 @@ __global__ void __launch_bounds__(kSimtThreads, D == 256 ? 1 : 2) prefill_simt_k
     do {
         const PrefillTile t = cur.t;
         const int32_t nrow = t.ntok * a.G;  // rows of this tile (<= 64)
-        __syncthreads();                    // the previous segment's reads of Qs
+        const int32_t keys = t.p0 + t.ntok, j0 = cur.j0, j1 = cur.j1;
+        const int32_t *row = a.tables + (int64_t)t.seq * a.max_blocks;
+        // Thread i < 64: the table entry of key i of unit j (0 without that
+        // key), and the slot it makes (-1: no key, or a bad entry: zeros).
+        auto entry = [&](int32_t j) -> int32_t {
+            const int64_t pos = (int64_t)j * kSimtKeys + tid;
+            return tid < kSimtKeys && j < j1 && pos < keys ? row[pos / a.B] : 0;
+        };
+        auto put_slot = [&](int32_t j, int32_t phys) {
+            if (tid >= kSimtKeys || j >= j1) return;
+            const int64_t pos = (int64_t)j * kSimtKeys + tid;
+            int64_t slot = -1;
+            if (pos < keys) {
+                if (phys < 0 || phys >= a.NB)
+                    atomicOr(a.err, kErrBounds);
+                else
+                    slot = (int64_t)phys * a.B + pos % a.B;
+            }
+            slots[(kPipe ? (j & 1) * kSimtKeys : 0) + tid] = slot;
+        };
+        auto k_buf = [&](int32_t j) { return sm + L::kK + (kPipe ? (j & 1) * kSimtKeys * QS : 0); };
+        auto v_buf = [&](int32_t j) { return sm + L::kV + (kPipe ? (j & 1) * kSimtKeys * D : 0); };
+        // K and V rows of unit j into its buffers (kPipe: asynchronously).
+        auto stage = [&](int32_t j) {
+            const int64_t *sl = slots + (kPipe ? (j & 1) * kSimtKeys : 0);
+            float *Ks = k_buf(j), *Vs = v_buf(j);
+            for (int e = tid; e < kSimtKeys * (D / 4); e += kSimtThreads) {
+                const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
+                const int64_t slot = sl[r];
+                if (kPipe && slot >= 0) {
+                    const int64_t at = (slot * a.Hk + cur.kvh) * D + d;
+                    cp_async16(Ks + r * QS + d, (const float *)a.k_cache + at);
+                    cp_async16(Vs + r * D + d, (const float *)a.v_cache + at);
+                } else {
+                    float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
+                    if (slot >= 0) {
+                        kx = cache4<CT, D, LAYOUT, false>(a, slot, cur.kvh, d);
+                        vx = cache4<CT, D, LAYOUT, true>(a, slot, cur.kvh, d);
+                    }
+                    *reinterpret_cast<float4 *>(Ks + r * QS + d) = kx;
+                    *reinterpret_cast<float4 *>(Vs + r * D + d) = vx;
+                }
+            }
+            if (kPipe) cp_async_commit();
+        };
+        int32_t phys = entry(j0), phys_next = kPipe ? entry(j0 + 1) : 0;
+        __syncthreads();  // the previous segment's reads of shared memory
         for (int e = tid; e < kSimtRows * (D / 4); e += kSimtThreads) {
             const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -127,6 +191,12 @@ __global__ void __launch_bounds__(kSimtThreads, D == 256 ? 1 : 2) prefill_simt_k
                 x = load4_any((const T *)a.q + ((int64_t)(t.row0 + tok) * a.H + (int64_t)cur.kvh * a.G + g) * D + d);
             }
             *reinterpret_cast<float4 *>(Qs + r * QS + d) = x;
+        }
+        if (kPipe) {
+            put_slot(j0, phys);
+            put_slot(j0 + 1, phys_next);
+            __syncthreads();
+            stage(j0);
         }
         float o[4][EV * 4], m[4], l[4];
         int32_t last[4];  // this thread's rows: last key position each sees
@@ -139,39 +209,36 @@ __global__ void __launch_bounds__(kSimtThreads, D == 256 ? 1 : 2) prefill_simt_k
 #pragma unroll
             for (int e = 0; e < EV * 4; ++e) o[i][e] = 0.f;
         }
-        const int32_t keys = t.p0 + t.ntok;
-        for (int32_t j = cur.j0; j < cur.j1; ++j) {
+        for (int32_t j = j0; j < j1; ++j) {
             const int32_t key0 = j * kSimtKeys;
-            const int32_t nk = max(0, min(kSimtKeys, keys - key0));
-            if (tid < kSimtKeys) {
-                int64_t slot = -1;
-                if (tid < nk) {
-                    const int32_t pos = key0 + tid, blk = pos / a.B;
-                    const int32_t phys = a.tables[(int64_t)t.seq * a.max_blocks + blk];
-                    if (phys < 0 || phys >= a.NB)
-                        atomicOr(a.err, kErrBounds);  // the block reads as zeros
-                    else
-                        slot = (int64_t)phys * a.B + (pos - blk * a.B);
-                }
-                slots[tid] = slot;
+            if (kPipe) {
+                if (j > j0) __syncthreads();  // the last unit's reads of the other buffers are done, slots of j + 1 written
+                if (j + 1 < j1) stage(j + 1);
+                phys = entry(j + 2);
+                if (j + 1 < j1)
+                    cp_async_wait<1>();
+                else
+                    cp_async_wait<0>();
+            } else {
+                if (j > j0) __syncthreads();
+                put_slot(j, phys);
+                if (j + 1 < j1) phys = entry(j + 1);
+                __syncthreads();
+                stage(j);
             }
-            __syncthreads();  // slots written; the previous unit's reads of K, V and P are done
-            bool odd = false;  // this thread staged a V element that is not finite
-            for (int e = tid; e < kSimtKeys * (D / 4); e += kSimtThreads) {
-                const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
-                const int64_t slot = slots[r];
-                float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
-                if (slot >= 0) {
-                    kx = cache4<CT, D, LAYOUT, false>(a, slot, cur.kvh, d);
-                    vx = cache4<CT, D, LAYOUT, true>(a, slot, cur.kvh, d);
+            const float *Ks = k_buf(j), *Vs = v_buf(j);
+            __syncthreads();  // unit j staged
+            // Keys that only some rows see: does V hold a value that is not finite?
+            bool bad = false;
+            if (key0 + kSimtKeys > t.p0 + 1) {
+                bool odd = false;
+                for (int e = tid; e < kSimtKeys * (D / 4); e += kSimtThreads) {
+                    const float4 vx = *reinterpret_cast<const float4 *>(Vs + e * 4);
+                    // a product with 0 is NaN exactly where an element is not finite
+                    odd = odd || vx.x * 0.f + vx.y * 0.f + (vx.z * 0.f + vx.w * 0.f) != 0.f;
                 }
-                *reinterpret_cast<float4 *>(Ks + r * QS + d) = kx;
-                *reinterpret_cast<float4 *>(Vs + r * D + d) = vx;
-                // the sum of the products is NaN exactly where an element is not finite
-                const float z = vx.x * 0.f + vx.y * 0.f + (vx.z * 0.f + vx.w * 0.f);
-                odd = odd || z != 0.f;
+                bad = __syncthreads_or(odd) != 0;
             }
-            const bool bad = __syncthreads_or(odd) != 0;
             // S: rows ty * 4 + i, keys tx + 16 * n
             float s[4][4];
 #pragma unroll
@@ -229,6 +296,7 @@ __global__ void __launch_bounds__(kSimtThreads, D == 256 ? 1 : 2) prefill_simt_k
                 add_pv<false, EV>(Ps, Vs, o, ty, tx, key0, last);
             else
                 add_pv<true, EV>(Ps, Vs, o, ty, tx, key0, last);
+            if (kPipe) put_slot(j + 2, phys);  // its buffer's slots were read when unit j was staged
         }
         const bool whole = cur.whole();
 #pragma unroll
@@ -244,13 +312,13 @@ __global__ void __launch_bounds__(kSimtThreads, D == 256 ? 1 : 2) prefill_simt_k
 #pragma unroll
                     for (int e = 0; e < 4; ++e) store_out(op + 64 * w + e, o[i][4 * w + e] * inv);
             } else {
-                const int64_t row = cur.slot(c) * kSimtRows + r;
-                float *ap = a.acc + row * D + tx * 4;
+                const int64_t row_p = cur.slot(c) * kSimtRows + r;
+                float *ap = a.acc + row_p * D + tx * 4;
 #pragma unroll
                 for (int w = 0; w < EV; ++w)
                     *reinterpret_cast<float4 *>(ap + 64 * w) =
                         make_float4(o[i][4 * w], o[i][4 * w + 1], o[i][4 * w + 2], o[i][4 * w + 3]);
-                if (tx == 0) a.ml[row] = make_float2(m[i], l[i]);
+                if (tx == 0) a.ml[row_p] = make_float2(m[i], l[i]);
             }
         }
     } while (cur.next(a));
