@@ -252,8 +252,39 @@ def pa_decode(q, k_cache, v_cache, block_tables, seq_lens, scale, out=None, work
     return out
 
 
+# The calls below are short on the device for small batches, so their host
+# side is kept short too: descriptors and default options are made once per
+# shape, and device pointers travel as plain integers.
+_desc_memo = {}
+_opts_memo = {}
+
+
 def _prefill_opts(num_splits, kernel):
-    return _lib.PrefillOpts(int(num_splits), _KERNELS[kernel])
+    o = _opts_memo.get((num_splits, kernel))
+    if o is None:
+        if len(_opts_memo) > 256:
+            _opts_memo.clear()
+        o = _opts_memo[(num_splits, kernel)] = _lib.PrefillOpts(int(num_splits), _KERNELS[kernel])
+    return o
+
+
+def _memo_desc(make, *tensors):
+    """Descriptor of caches (read-only once made), remembered by their shapes
+    and types."""
+    key = (make,) + tuple((t.shape, t.dtype) for t in tensors)
+    d = _desc_memo.get(key)
+    if d is None:
+        if len(_desc_memo) > 256:
+            _desc_memo.clear()
+        d = _desc_memo[key] = make(*tensors)
+    return d
+
+
+def _ptr(t, name, device, dtype=None):
+    """_dev's checks; the pointer as an integer."""
+    if t.get_device() != device or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+        return _dev(t, name, dtype, device).value or 0
+    return t.data_ptr()
 
 
 def pa_prefill_workspace_bytes(k_cache, num_tokens, num_seqs, num_heads, num_splits=0, kernel="auto"):
@@ -278,12 +309,12 @@ def pa_prefill(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, scale, ou
     belong to no sequence are left as they were (in a fresh ``out``:
     unspecified)."""
     torch = _torch()
-    desc = _cache_desc(k_cache, v_cache)
+    desc = _memo_desc(_cache_desc, k_cache, v_cache)
     T, H, D = q.shape
     N = seq_lens.shape[0]
     if D != desc.head_dim or q.dtype != k_cache.dtype:
         raise ValueError("q must be [num_tokens, num_heads, head_dim] in the cache's element type")
-    if block_tables.dim() != 2 or block_tables.shape[0] != N or seq_lens.shape != (N,):
+    if block_tables.dim() != 2 or block_tables.shape[0] != N or seq_lens.dim() != 1:
         raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
     if cu_q_lens.shape != (N + 1,):
         raise ValueError("cu_q_lens must be [num_seqs + 1]")
@@ -292,19 +323,19 @@ def pa_prefill(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, scale, ou
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must match q")
     d = _current_device()
-    o = _prefill_opts(num_splits, kernel)
+    o = ctypes.byref(_prefill_opts(num_splits, kernel))
+    dp = ctypes.byref(desc)
     lib = _lib.load()
     if workspace is None:
-        need = lib.pa_prefill_workspace_bytes(ctypes.byref(desc), N, T, H, ctypes.byref(o))
+        need = lib.pa_prefill_workspace_bytes(dp, N, T, H, o)
         if need == 0:
             raise PagedAttentionError("pa_prefill_workspace_bytes", _lib.PA_ERR_UNSUPPORTED)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    st = lib.pa_prefill(_dev(out, "out", device=d), _dev(q, "q", device=d), _dev(k_cache, "k_cache", device=d),
-                        _dev(v_cache, "v_cache", device=d), ctypes.byref(desc),
-                        _dev(block_tables, "block_tables", torch.int32, d), block_tables.shape[1],
-                        _dev(seq_lens, "seq_lens", torch.int32, d), _dev(cu_q_lens, "cu_q_lens", torch.int32, d), N, T,
-                        H, float(scale), _dev(workspace, "workspace", device=d),
-                        workspace.numel() * workspace.element_size(), ctypes.byref(o), _stream())
+    i32 = torch.int32
+    st = lib.pa_prefill(_ptr(out, "out", d), _ptr(q, "q", d), _ptr(k_cache, "k_cache", d), _ptr(v_cache, "v_cache", d),
+                        dp, _ptr(block_tables, "block_tables", d, i32), block_tables.shape[1],
+                        _ptr(seq_lens, "seq_lens", d, i32), _ptr(cu_q_lens, "cu_q_lens", d, i32), N, T, H, float(scale),
+                        _ptr(workspace, "workspace", d), workspace.nbytes, o, _stream())
     _lib.check("pa_prefill", st)
     return out
 
@@ -331,32 +362,31 @@ def _cache_desc_fp8(k_cache, v_cache=None, k_scale=None, v_scale=None):
     return _lib.CacheDesc(nb, bs, hk, d, _lib.PA_FP8_E4M3, _lib.PA_LAYOUT_ROW)
 
 
-def _check_rows(k, v, slot_mapping, desc):
+def _rows_call(name, k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale):
+    """pa_reshape_and_cache_fp8 or pa_gather_cache_fp8: the same arguments."""
+    desc = _memo_desc(_cache_desc_fp8, k_cache, v_cache, k_scale, v_scale)
+    if slot_mapping.dim() != 1:
+        raise ValueError("slot_mapping must be [num_tokens]")
     T = slot_mapping.shape[0]
-    for t in (k, v):
-        if tuple(t.shape) != (T, desc.num_kv_heads, desc.head_dim):
-            raise ValueError("k, v must be [num_tokens, num_kv_heads, head_dim] matching the cache and slot_mapping "
-                             "[num_tokens]")
+    want = (T, desc.num_kv_heads, desc.head_dim)
+    if k.shape != want or v.shape != want:
+        raise ValueError("k, v must be [num_tokens, num_kv_heads, head_dim] matching the cache and slot_mapping "
+                         "[num_tokens]")
     if k.dtype != v.dtype:
         raise TypeError("k and v element types differ")
-    return T, _dtype_code(k)
+    d = _current_device()
+    st = getattr(_lib.load(), name)(
+        _ptr(k, "k", d), _ptr(v, "v", d), _dtype_code(k), _ptr(slot_mapping, "slot_mapping", d, _torch().int32), T,
+        _ptr(k_cache, "k_cache", d), _ptr(v_cache, "v_cache", d), _ptr(k_scale, "k_scale", d),
+        _ptr(v_scale, "v_scale", d), ctypes.byref(desc), _stream())
+    _lib.check(name, st)
 
 
 def pa_reshape_and_cache_fp8(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale):
     """Quantise new tokens' K/V rows (fp32 or bf16) into the 8-bit caches at
     their slots: e4m3 codes and one power-of-two scale byte (2^(b - 127)) per
     token and KV head."""
-    torch = _torch()
-    desc = _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale)
-    if slot_mapping.dim() != 1:
-        raise ValueError("slot_mapping must be [num_tokens]")
-    T, dt = _check_rows(k, v, slot_mapping, desc)
-    d = _current_device()
-    st = _lib.load().pa_reshape_and_cache_fp8(
-        _dev(k, "k", device=d), _dev(v, "v", device=d), dt, _dev(slot_mapping, "slot_mapping", torch.int32, d), T,
-        _dev(k_cache, "k_cache", device=d), _dev(v_cache, "v_cache", device=d), _dev(k_scale, "k_scale", device=d),
-        _dev(v_scale, "v_scale", device=d), ctypes.byref(desc), _stream())
-    _lib.check("pa_reshape_and_cache_fp8", st)
+    _rows_call("pa_reshape_and_cache_fp8", k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale)
 
 
 def pa_gather_cache_fp8(k_cache, v_cache, k_scale, v_scale, slot_mapping, k=None, v=None, dtype=None):
@@ -364,38 +394,28 @@ def pa_gather_cache_fp8(k_cache, v_cache, k_scale, v_scale, slot_mapping, k=None
     values at the slots (zeros for negative slots), in ``k`` and ``v`` or in new
     tensors of ``dtype`` (default bfloat16)."""
     torch = _torch()
-    desc = _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale)
-    if slot_mapping.dim() != 1:
-        raise ValueError("slot_mapping must be [num_tokens]")
     if (k is None) != (v is None):
         raise ValueError("give both k and v or neither")
     if k is None:
-        shape = (slot_mapping.shape[0], desc.num_kv_heads, desc.head_dim)
-        k = torch.empty(shape, dtype=dtype or torch.bfloat16, device=k_cache.device)
+        k = torch.empty((slot_mapping.shape[0],) + tuple(k_cache.shape[2:]), dtype=dtype or torch.bfloat16,
+                        device=k_cache.device)
         v = torch.empty_like(k)
     elif dtype is not None and k.dtype != dtype:
         raise TypeError("k is %s, not %s" % (k.dtype, dtype))
-    T, dt = _check_rows(k, v, slot_mapping, desc)
-    d = _current_device()
-    st = _lib.load().pa_gather_cache_fp8(
-        _dev(k, "k", device=d), _dev(v, "v", device=d), dt, _dev(slot_mapping, "slot_mapping", torch.int32, d), T,
-        _dev(k_cache, "k_cache", device=d), _dev(v_cache, "v_cache", device=d), _dev(k_scale, "k_scale", device=d),
-        _dev(v_scale, "v_scale", device=d), ctypes.byref(desc), _stream())
-    _lib.check("pa_gather_cache_fp8", st)
+    _rows_call("pa_gather_cache_fp8", k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale)
     return k, v
 
 
 def pa_copy_blocks_fp8(k_cache, v_cache, k_scale, v_scale, src_dst_pairs):
     """pa_copy_blocks for an 8-bit cache: codes and scale bytes."""
-    torch = _torch()
-    desc = _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale)
+    desc = _memo_desc(_cache_desc_fp8, k_cache, v_cache, k_scale, v_scale)
     if src_dst_pairs.numel() == 0:
         return
     pairs = src_dst_pairs.reshape(-1, 2)
     d = _current_device()
     st = _lib.load().pa_copy_blocks_fp8(
-        _dev(k_cache, "k_cache", device=d), _dev(v_cache, "v_cache", device=d), _dev(k_scale, "k_scale", device=d),
-        _dev(v_scale, "v_scale", device=d), ctypes.byref(desc), _dev(pairs, "src_dst_pairs", torch.int32, d),
+        _ptr(k_cache, "k_cache", d), _ptr(v_cache, "v_cache", d), _ptr(k_scale, "k_scale", d),
+        _ptr(v_scale, "v_scale", d), ctypes.byref(desc), _ptr(pairs, "src_dst_pairs", d, _torch().int32),
         pairs.shape[0], _stream())
     _lib.check("pa_copy_blocks_fp8", st)
 
@@ -415,7 +435,7 @@ def pa_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
     """Decode attention over an 8-bit cache through block tables; q and the
     returned ``out`` are bfloat16 [N, H, D]."""
     torch = _torch()
-    desc = _cache_desc_fp8(k_cache, v_cache, k_scale, v_scale)
+    desc = _memo_desc(_cache_desc_fp8, k_cache, v_cache, k_scale, v_scale)
     N, H, D = q.shape
     if D != desc.head_dim:
         raise ValueError("q must be [num_seqs, num_heads, head_dim] matching the cache")
@@ -428,19 +448,20 @@ def pa_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must match q")
     d = _current_device()
-    o = _prefill_opts(num_splits, kernel)
+    o = ctypes.byref(_prefill_opts(num_splits, kernel))
+    dp = ctypes.byref(desc)
     lib = _lib.load()
     if workspace is None:
-        need = lib.pa_decode_fp8_workspace_bytes(ctypes.byref(desc), N, H, ctypes.byref(o))
+        need = lib.pa_decode_fp8_workspace_bytes(dp, N, H, o)
         if need == 0:
             raise PagedAttentionError("pa_decode_fp8_workspace_bytes", _lib.PA_ERR_UNSUPPORTED)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    i32 = torch.int32
     st = lib.pa_decode_fp8(
-        _dev(out, "out", device=d), _dev(q, "q", device=d), _dev(k_cache, "k_cache", device=d),
-        _dev(v_cache, "v_cache", device=d), _dev(k_scale, "k_scale", device=d), _dev(v_scale, "v_scale", device=d),
-        ctypes.byref(desc), _dev(block_tables, "block_tables", torch.int32, d), block_tables.shape[1],
-        _dev(seq_lens, "seq_lens", torch.int32, d), N, H, float(scale), _dev(workspace, "workspace", device=d),
-        workspace.numel() * workspace.element_size(), ctypes.byref(o), _stream())
+        _ptr(out, "out", d), _ptr(q, "q", d), _ptr(k_cache, "k_cache", d), _ptr(v_cache, "v_cache", d),
+        _ptr(k_scale, "k_scale", d), _ptr(v_scale, "v_scale", d), dp, _ptr(block_tables, "block_tables", d, i32),
+        block_tables.shape[1], _ptr(seq_lens, "seq_lens", d, i32), N, H, float(scale), _ptr(workspace, "workspace", d),
+        workspace.nbytes, o, _stream())
     _lib.check("pa_decode_fp8", st)
     return out
 
