@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
     {
         PrefillCursor first;
         if (!first.init(a, c)) return;
+        if (tid == 32 * kF8Warps) note_cut(a, c, first);
         cur = first;  // the same in every lane
     }
     __syncwarp();

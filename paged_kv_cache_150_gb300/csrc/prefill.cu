@@ -84,6 +84,7 @@ void prefill_workspace(PrefillPlan *p, int32_t N, int32_t head_dim) {
     p->off_cu = take(sizeof(int32_t) * (tiles + 1));
     p->off_tiles = take(sizeof(PrefillTile) * std::max<size_t>(tiles, 1));
     p->off_start = take(sizeof(int32_t) * (size_t)p->C);
+    p->off_merges = take(sizeof(MergeEntry) * (size_t)p->C);
     const size_t slot_rows = 2 * (size_t)p->C * p->nrt * p->rows;
     p->off_ml = take(sizeof(float2) * slot_rows);
     p->off_acc = take(sizeof(float) * slot_rows * head_dim);
@@ -104,6 +105,8 @@ pa_status_t prefill_bind(const PrefillPlan &p, PrefillArgs *a, void *workspace) 
     a->cu = (int32_t *)(ws + p.off_cu);
     a->tiles = (PrefillTile *)(ws + p.off_tiles);
     a->start_tile = (int32_t *)(ws + p.off_start);
+    a->merges = (MergeEntry *)(ws + p.off_merges);
+    a->few = (int64_t)p.max_tiles * a->Hk * 4 <= p.C ? 1 : 0;
     a->ml = (float2 *)(ws + p.off_ml);
     a->acc = (float *)(ws + p.off_acc);
     a->err = device_error_word();
@@ -126,6 +129,18 @@ pa_status_t prefill_launch_merge(PrefillArgs &a, bool f32, int32_t head_dim, cud
                                        : (f32 ? (const void *)prefill_merge_kernel<float, 256>
                                               : (const void *)prefill_merge_kernel<__nv_bfloat16, 256>);
     void *args[] = {&a};
+    if (a.few) {
+        const void *few = head_dim == 64    ? (f32 ? (const void *)prefill_merge_few_kernel<float, 64>
+                                                   : (const void *)prefill_merge_few_kernel<__nv_bfloat16, 64>)
+                          : head_dim == 128 ? (f32 ? (const void *)prefill_merge_few_kernel<float, 128>
+                                                   : (const void *)prefill_merge_few_kernel<__nv_bfloat16, 128>)
+                                            : (f32 ? (const void *)prefill_merge_few_kernel<float, 256>
+                                                   : (const void *)prefill_merge_few_kernel<__nv_bfloat16, 256>);
+        const int rows = a.tq1 * a.nrt * a.G;
+        const int64_t items = (int64_t)a.max_tiles * a.Hk * ((rows + kMergeWarps - 1) / kMergeWarps);
+        const int grid = (int)std::min<int64_t>(items, kMergeCtas * std::max(num_sms(), 1));
+        return launch_pdl(few, dim3(grid), dim3(32 * kMergeWarps), args, 0, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    }
     // 4 CTAs of 8 warps share the rows of a cut tile
     return launch_pdl(fn, dim3(a.C - 1, 4), dim3(256), args, 0, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

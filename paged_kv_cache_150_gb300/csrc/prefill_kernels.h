@@ -17,7 +17,7 @@ struct PrefillPlan {
     int32_t threads;   // of an attention CTA
     int32_t C, max_tiles;
     size_t smem;
-    size_t off_ctl, off_tile0, off_cu, off_tiles, off_start, off_ml, off_acc, total;
+    size_t off_ctl, off_tile0, off_cu, off_tiles, off_start, off_merges, off_ml, off_acc, total;
 };
 
 // Kernel and shared memory of prefill_simt_kernel for a cache element type

@@ -15,6 +15,8 @@
 // the same call gives the same bits every time.
 #pragma once
 
+#include <type_traits>
+
 #include "decode_merge.cuh"  // store_out
 #include "pa_internal.h"
 
@@ -26,6 +28,14 @@ struct PrefillTile {
     int32_t row0;  // row of q / out of its first token
     int32_t ntok;  // tokens in this tile
     int32_t p0;    // position of its first token (negative: before the sequence's first key)
+};
+
+// A tile cut between CTAs, for prefill_merge_few_kernel: pieces slot0 (of CTA
+// slot0 / 2, its first units), then the first slots of the CTAs up to c1.
+struct __align__(16) MergeEntry {
+    int32_t row0, rows;  // the tile's first row of q / out, its query rows
+    int32_t kvh, slot0, c1;
+    int32_t pad[3];
 };
 
 // The call, as its kernels see it (one struct, passed by value).
@@ -45,7 +55,9 @@ struct PrefillArgs {
     int32_t C;            // persistent CTAs
     int32_t max_tiles;    // capacity of tiles[] and cu[]
     float scale_log2;
-    int32_t *ctl;         // ctl[0]: tiles of the list
+    int32_t few;          // 1: the CTAs list the cut tiles (note_cut), prefill_merge_few_kernel merges them
+    int32_t *ctl;         // ctl[0]: tiles of the list, ctl[1]: cut tiles listed, ctl[2]: most query rows of one
+    MergeEntry *merges;   // [C] the cut tiles, in any order
     int32_t *seq_tile0;   // [N + 1] first tile of each sequence
     int32_t *cu;          // [max_tiles + 1] exclusive prefix sums of the tiles' weights
     PrefillTile *tiles;   // [max_tiles]
@@ -110,7 +122,7 @@ static __global__ void __launch_bounds__(1024) prefill_plan_kernel(const Prefill
     if (!ok) {
         if (tid == 0) {
             atomicOr(a.err, kErrBounds);
-            a.ctl[0] = 0;
+            a.ctl[0] = a.ctl[1] = a.ctl[2] = 0;
             a.cu[0] = 0;
         }
         return;
@@ -169,6 +181,7 @@ static __global__ void __launch_bounds__(1024) prefill_plan_kernel(const Prefill
     if (tid == 0) {
         a.cu[tiles] = units;
         a.ctl[0] = tiles;
+        a.ctl[1] = a.ctl[2] = 0;
     }
     __syncthreads();
     const int32_t *cu = in_smem ? cu_s : a.cu;
@@ -258,6 +271,114 @@ struct PrefillWalk {
     __device__ __forceinline__ int64_t slot(int32_t c) const { return 2 * (int64_t)c + (first ? 0 : 1); }
 };
 using PrefillCursor = PrefillWalk<true>;
+
+// With few tiles (a.few), CTA c, by one thread, lists the tile that its
+// range's start cuts between units, if CTA c - 1 holds that tile's first unit
+// (so each cut tile once).
+template <class Walk>
+__device__ __forceinline__ void note_cut(const PrefillArgs &a, int32_t c, const Walk &cur) {
+    if (!a.few || cur.j0 == 0) return;
+    const int64_t W = (int64_t)a.Hk * a.cu[cur.tiles];
+    const int32_t Ce = (int32_t)min(W, (int64_t)a.C);
+    const int32_t c0 = split_owner(cur.x + a.extra, W, Ce);
+    if (c0 != c - 1) return;
+    MergeEntry me{};
+    me.row0 = cur.t.row0;
+    me.rows = cur.t.ntok * a.G;
+    me.kvh = cur.kvh;
+    me.slot0 = 2 * c0 + (split_begin(c0, W, Ce) >= cur.x ? 0 : 1);
+    me.c1 = split_owner(cur.x + a.extra + cur.nu - 1, W, Ce);
+    a.merges[atomicAdd(a.ctl + 1, 1)] = me;
+    atomicMax(a.ctl + 2, me.rows);
+}
+
+// Merge of the listed tiles, few of them in many pieces each: a block takes 8
+// query rows of one, a warp per row, its lanes across the columns, kBatch
+// pieces in flight, folded in CTA order.  16 long contexts cut in 19 pieces
+// each: 8 us, where the kernel below, a block per CTA boundary and quarter of
+// the rows, most of them without work, took 16 to 20; with hundreds of tiles
+// cut in two or three pieces that one is the faster (its blocks find their
+// tile without a list).
+constexpr int kMergeWarps = 8, kMergeCtas = 4;  // per block, blocks per SM
+template <typename T, int D>
+static __global__ void __launch_bounds__(32 * kMergeWarps)
+    prefill_merge_few_kernel(const __grid_constant__ PrefillArgs a) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    constexpr int E = D / 32, NV = E == 8 ? 2 : 1, NE = E / NV;  // accumulator elements of a lane, vectors, elements of one
+    constexpr int kBatch = D == 256 ? 4 : 8;
+    using Vec = typename std::conditional<NE == 2, float2, float4>::type;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t slot_rows = (int64_t)a.nrt * a.rows;
+    const int32_t cuts = a.ctl[1], chunks = (a.ctl[2] + kMergeWarps - 1) / kMergeWarps;
+    for (int32_t item = blockIdx.x; item < cuts * chunks; item += gridDim.x) {
+        const MergeEntry me = a.merges[item % cuts];
+        const int32_t i = item / cuts * kMergeWarps + warp;  // query row of the tile
+        if (i >= me.rows) continue;
+        const int32_t tok = i / a.G, g = i - tok * a.G;
+        const int64_t row = (int64_t)(tok / a.tq1) * a.rows + (tok % a.tq1) * a.G + g;
+        const int32_t c0 = me.slot0 >> 1, np_all = me.c1 - c0 + 1;
+        auto piece = [&](int32_t p) {  // row of the p-th piece
+            return (p == 0 ? (int64_t)me.slot0 : 2 * (int64_t)(c0 + p)) * slot_rows + row;
+        };
+        float M = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = 0.f;
+        for (int32_t p0 = 0; p0 < np_all; p0 += 32) {
+            const int32_t np = min(32, np_all - p0);
+            // 32 pieces' statistics, one per lane, with the first accumulators in flight
+            float2 v = make_float2(-INFINITY, 0.f);
+            if (lane < np) v = __ldcg(&a.ml[piece(p0 + lane)]);
+            float wgt = 0.f;
+            for (int32_t b0 = 0; b0 < np; b0 += kBatch) {
+                Vec x[kBatch][NV];
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b)
+                    if (b0 + b < np) {
+                        const Vec *ap = reinterpret_cast<const Vec *>(a.acc + piece(p0 + b0 + b) * D + lane * E);
+#pragma unroll
+                        for (int e = 0; e < NV; ++e) x[b][e] = __ldcg(ap + e);
+                    }
+                if (b0 == 0) {
+                    float mb = v.x;
+#pragma unroll
+                    for (int s = 16; s > 0; s >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, s));
+                    const float Mn = fmaxf(M, mb), mref = Mn == -INFINITY ? 0.f : Mn;  // no key so far: zeros
+                    const float sc = ex2_approx(M - mref);
+                    wgt = ex2_approx(v.x - mref);
+                    float lw = wgt * v.y;
+#pragma unroll
+                    for (int s = 16; s > 0; s >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, s);
+                    l = l * sc + lw;
+                    M = Mn;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[e] *= sc;
+                }
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    const float w = __shfl_sync(0xffffffffu, wgt, (b0 + b) & 31);
+                    if (b0 + b < np) {
+#pragma unroll
+                        for (int e = 0; e < NV; ++e) {
+                            const float *xe = reinterpret_cast<const float *>(&x[b][e]);
+#pragma unroll
+                            for (int q = 0; q < NE; ++q) o[e * NE + q] = fmaf(w, xe[q], o[e * NE + q]);
+                        }
+                    }
+                }
+            }
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // a row without keys is zero
+        T *op = (T *)a.out + ((int64_t)(me.row0 + tok) * a.H + (int64_t)me.kvh * a.G + g) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {  // out is aligned to two elements
+            if constexpr (std::is_same<T, float>::value)
+                *reinterpret_cast<float2 *>(op + e) = make_float2(o[e] * inv, o[e + 1] * inv);
+            else
+                *reinterpret_cast<uint32_t *>(op + e) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+        }
+    }
+}
 
 // Merge of the cut tiles: block (c - 1, y) folds the tile that the start of
 // CTA c's range cuts between units, if CTA c - 1 holds that tile's first unit

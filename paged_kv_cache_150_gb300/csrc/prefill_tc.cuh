@@ -221,6 +221,7 @@ __device__ __forceinline__ void tc_guard(const PrefillArgs &a, uint8_t *smem, co
     bool abort = false, dirty = false;
     PrefillCursor cur;
     if (!cur.init(a, c)) return;
+    if (lane == 0) note_cut(a, c, cur);
     do {
         const TcSegment sg(a, cur);
         if (sg.jend <= cur.j0) continue;
