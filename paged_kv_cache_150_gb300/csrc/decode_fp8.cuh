@@ -122,12 +122,18 @@ __device__ __forceinline__ void f8_producer(const PrefillArgs &a, const F8Args &
     const uint32_t box_bytes = (uint32_t)(f.gran * f.NH * D), sc_bytes = (uint32_t)(f.gran * f.Hk);
     uint32_t n = 0;
     bool abort = false;
+    // table entry of this lane's box of unit j of a sequence (0 without that box)
+    auto entry_of = [&](const PrefillTile &t, int32_t j) {
+        return lane < nbox && (int64_t)j * f.T + lane * f.gran <= t.p0
+                   ? a.tables[(int64_t)t.seq * a.max_blocks + (j * f.T + lane * f.gran) / a.B]
+                   : 0;
+    };
+    int32_t phys = entry_of(cur.t, cur.j0), phys_next;
     do {
         const int32_t keys = cur.t.p0 + 1, je = f8_units_end(cur, f.T);
-        const int32_t *row = a.tables + (int64_t)cur.t.seq * a.max_blocks;
         auto has = [&](int32_t j) { return lane < nbox && (int64_t)j * f.T + lane * f.gran < keys; };
-        auto entry = [&](int32_t j) { return has(j) ? row[(j * f.T + lane * f.gran) / a.B] : 0; };
-        int32_t phys = je > cur.j0 ? entry(cur.j0) : 0;
+        auto entry = [&](int32_t j) { return entry_of(cur.t, j); };
+        phys_next = entry_of(cur.t_next, 0);  // the next segment starts with its sequence
         for (int32_t j = cur.j0; j < je; ++j, ++n) {
             const uint32_t st = n % f.stages;
             const bool box = has(j), good = phys >= 0 && phys < a.NB;
@@ -163,6 +169,7 @@ __device__ __forceinline__ void f8_producer(const PrefillArgs &a, const F8Args &
             }
         }
         if (__any_sync(0xffffffffu, abort)) break;
+        phys = phys_next;
     } while (cur.next(a));
     // copies in flight land before the CTA may exit
     bool late = false;
@@ -275,6 +282,11 @@ __global__ void __launch_bounds__(kF8Threads, 2)
             qs0 = __shfl_sync(0xffffffffu, back, (2 * cq) * 4);  // lane 4 n holds column n's
             qs1 = __shfl_sync(0xffffffffu, back, (2 * cq + 1) * 4);
         }
+        // The next sequence's queries of this head on their way to L2 (G * D * 2
+        // bytes, a line per lane).
+        if (lane * 64 < f.G * D)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"((const __nv_bfloat16 *)a.q +
+                                                          ((int64_t)cur.t_next.row0 * a.H + head0) * D + lane * 64));
         float o[NC][4];
 #pragma unroll
         for (int j = 0; j < NC; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
