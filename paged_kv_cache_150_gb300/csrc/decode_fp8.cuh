@@ -216,8 +216,9 @@ __global__ void __launch_bounds__(kF8Threads, 2)
     PrefillCursor &cur = curs[warp];
     {
         PrefillCursor first;
-        if (!first.init(a, c)) return;
-        if (tid == 32 * kF8Warps) note_cut(a, c, first);
+        const bool work = first.init(a, c);
+        if (tid == 32 * kF8Warps) note_cut(a, c, work, first);
+        if (!work) return;
         cur = first;  // the same in every lane
     }
     __syncwarp();

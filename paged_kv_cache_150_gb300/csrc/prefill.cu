@@ -141,8 +141,9 @@ pa_status_t prefill_launch_merge(PrefillArgs &a, bool f32, int32_t head_dim, cud
         const int grid = (int)std::min<int64_t>(items, kMergeCtas * std::max(num_sms(), 1));
         return launch_pdl(few, dim3(grid), dim3(32 * kMergeWarps), args, 0, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }
-    // 4 CTAs of 8 warps share the rows of a cut tile
-    return launch_pdl(fn, dim3(a.C - 1, 4), dim3(256), args, 0, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    // up to 8 blocks share the rows of a cut tile, 4 rows a warp
+    const int y = std::min((a.tq1 * a.nrt * a.G + 2 * kMergeWarps - 1) / (2 * kMergeWarps), 8);
+    return launch_pdl(fn, dim3(a.C - 1, y), dim3(32 * kMergeWarps), args, 0, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 pa_status_t prefill_launch(const PrefillPlan &p, const pa_cache_desc_t *c, PrefillArgs a, void *workspace,

@@ -30,7 +30,7 @@ struct PrefillTile {
     int32_t p0;    // position of its first token (negative: before the sequence's first key)
 };
 
-// A tile cut between CTAs, for prefill_merge_few_kernel: pieces slot0 (of CTA
+// A tile cut between CTAs, for the merge: pieces slot0 (of CTA
 // slot0 / 2, its first units), then the first slots of the CTAs up to c1.
 struct __align__(16) MergeEntry {
     int32_t row0, rows;  // the tile's first row of q / out, its query rows
@@ -55,9 +55,9 @@ struct PrefillArgs {
     int32_t C;            // persistent CTAs
     int32_t max_tiles;    // capacity of tiles[] and cu[]
     float scale_log2;
-    int32_t few;          // 1: the CTAs list the cut tiles (note_cut), prefill_merge_few_kernel merges them
+    int32_t few;          // 1: few tiles in many pieces, merged by prefill_merge_few_kernel
     int32_t *ctl;         // ctl[0]: tiles of the list, ctl[1]: cut tiles listed, ctl[2]: most query rows of one
-    MergeEntry *merges;   // [C] the cut tiles, in any order
+    MergeEntry *merges;   // [C] the cut tiles (note_cut)
     int32_t *seq_tile0;   // [N + 1] first tile of each sequence
     int32_t *cu;          // [max_tiles + 1] exclusive prefix sums of the tiles' weights
     PrefillTile *tiles;   // [max_tiles]
@@ -272,24 +272,31 @@ struct PrefillWalk {
 };
 using PrefillCursor = PrefillWalk<true>;
 
-// With few tiles (a.few), CTA c, by one thread, lists the tile that its
-// range's start cuts between units, if CTA c - 1 holds that tile's first unit
-// (so each cut tile once).
+// CTA c, by one thread: the tile that its range's start cuts between units,
+// for the merge, if CTA c - 1 holds that tile's first unit (so each cut tile
+// once).  With few tiles (a.few) the entries form a list; else entry c stands
+// at c, with no rows where there is nothing to merge.
 template <class Walk>
-__device__ __forceinline__ void note_cut(const PrefillArgs &a, int32_t c, const Walk &cur) {
-    if (!a.few || cur.j0 == 0) return;
-    const int64_t W = (int64_t)a.Hk * a.cu[cur.tiles];
-    const int32_t Ce = (int32_t)min(W, (int64_t)a.C);
-    const int32_t c0 = split_owner(cur.x + a.extra, W, Ce);
-    if (c0 != c - 1) return;
+__device__ __forceinline__ void note_cut(const PrefillArgs &a, int32_t c, bool work, const Walk &cur) {
     MergeEntry me{};
-    me.row0 = cur.t.row0;
-    me.rows = cur.t.ntok * a.G;
-    me.kvh = cur.kvh;
-    me.slot0 = 2 * c0 + (split_begin(c0, W, Ce) >= cur.x ? 0 : 1);
-    me.c1 = split_owner(cur.x + a.extra + cur.nu - 1, W, Ce);
-    a.merges[atomicAdd(a.ctl + 1, 1)] = me;
-    atomicMax(a.ctl + 2, me.rows);
+    if (work && cur.j0 > 0) {
+        const int64_t W = (int64_t)a.Hk * a.cu[cur.tiles];
+        const int32_t Ce = (int32_t)min(W, (int64_t)a.C);
+        const int32_t c0 = split_owner(cur.x + a.extra, W, Ce);
+        if (c0 == c - 1) {
+            me.row0 = cur.t.row0;
+            me.rows = cur.t.ntok * a.G;
+            me.kvh = cur.kvh;
+            me.slot0 = 2 * c0 + (split_begin(c0, W, Ce) >= cur.x ? 0 : 1);
+            me.c1 = split_owner(cur.x + a.extra + cur.nu - 1, W, Ce);
+        }
+    }
+    if (!a.few) {
+        a.merges[c] = me;
+    } else if (me.rows > 0) {
+        a.merges[atomicAdd(a.ctl + 1, 1)] = me;
+        atomicMax(a.ctl + 2, me.rows);
+    }
 }
 
 // Merge of the listed tiles, few of them in many pieces each: a block takes 8
@@ -380,84 +387,93 @@ static __global__ void __launch_bounds__(32 * kMergeWarps)
     }
 }
 
-// Merge of the cut tiles: block (c - 1, y) folds the tile that the start of
-// CTA c's range cuts between units, if CTA c - 1 holds that tile's first unit
-// (so each cut tile has one c).  One warp per query row; pieces in CTA order.
+// Merge of the cut tiles, many of them in a few pieces each: block (c - 1, y)
+// takes its share of the rows of entry c.  A warp folds two rows at once, its
+// lanes across the columns, up to four pieces of each in flight, in CTA order;
+// bound by the latency of two dependent reads through L2 (the entry, the
+// pieces).  150 tiles of 256 rows in two or three pieces (45 MB): 22 us with a
+// row at a time behind a search of the work list.
 template <typename T, int D>
-static __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs a) {
+static __global__ void __launch_bounds__(32 * kMergeWarps, D == 256 ? 2 : 4)
+    prefill_merge_kernel(const __grid_constant__ PrefillArgs a) {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int32_t c = blockIdx.x + 1;
-    const int32_t tiles = a.ctl[0], U = a.cu[tiles];
-    const int64_t W = (int64_t)a.Hk * U;
-    const int32_t Ce = (int32_t)min(W, (int64_t)a.C);
-    if (c >= Ce) return;
-    const int64_t x = split_begin(c, W, Ce);
-    const int32_t kvh = (int32_t)(x / U), k = a.start_tile[c];
-    const int64_t x0 = (int64_t)kvh * U + a.cu[k];
-    if (x - x0 <= a.extra) return;  // the range starts with its tile's first unit
-    const int32_t c0 = split_owner(x0 + a.extra, W, Ce);
-    if (c0 != c - 1) return;  // an earlier block's tile
-    const int32_t c1 = split_owner((int64_t)kvh * U + a.cu[k + 1] - 1, W, Ce);
-    const PrefillTile t = a.tiles[k];
-    const int lane = threadIdx.x & 31;
-    const int32_t wid = blockIdx.y * 8 + (threadIdx.x >> 5), nw = gridDim.y * 8;
+    constexpr int E = D / 32, NV = E == 8 ? 2 : 1, NE = E / NV;  // accumulator elements of a lane, vectors, elements of one
+    constexpr int kRows = 2, kBatch = 4;
+    using Vec = typename std::conditional<NE == 2, float2, float4>::type;
+    const MergeEntry me = a.merges[blockIdx.x + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t slot_rows = (int64_t)a.nrt * a.rows;
-    const int64_t first_slot = 2 * (int64_t)c0 + (split_begin(c0, W, Ce) >= x0 ? 0 : 1);
-    constexpr int E = D / 32;  // accumulator elements of a lane
-    for (int32_t i = wid; i < t.ntok * a.G; i += nw) {
-        const int32_t tok = i / a.G, g = i - tok * a.G;
-        const int64_t row = (int64_t)(tok / a.tq1) * a.rows + (tok % a.tq1) * a.G + g;
-        float M = -INFINITY, Ls = 0.f, o[E];
+    const int32_t c0 = me.slot0 >> 1, np = me.c1 - c0 + 1, stride = gridDim.y * kMergeWarps;
+    auto piece = [&](int32_t p) { return (p == 0 ? (int64_t)me.slot0 : 2 * (int64_t)(c0 + p)) * slot_rows; };
+    for (int32_t i0 = blockIdx.y * kMergeWarps + warp; i0 < me.rows; i0 += kRows * stride) {
+        int64_t row[kRows];
+        float M[kRows], l[kRows], o[kRows][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = 0.f;
-        for (int32_t p0 = c0; p0 <= c1; p0 += 32) {
-            // 32 pieces' statistics at a time, one per lane
-            const int32_t p = p0 + lane;
-            const int64_t idx = ((p == c0 ? first_slot : 2 * (int64_t)p) * slot_rows + row);
-            float2 v = make_float2(-INFINITY, 0.f);
-            if (p <= c1) v = __ldcg(&a.ml[idx]);
-            float mb = v.x;
+        for (int r = 0; r < kRows; ++r) {
+            const int32_t i = min(i0 + r * stride, me.rows - 1), tok = i / a.G;
+            row[r] = (int64_t)(tok / a.tq1) * a.rows + (tok % a.tq1) * a.G + (i - tok * a.G);
+            M[r] = -INFINITY;
+            l[r] = 0.f;
 #pragma unroll
-            for (int s = 16; s > 0; s >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, s));
-            const float Mn = fmaxf(M, mb);
-            if (Mn == -INFINITY && !__any_sync(0xffffffffu, v.y != 0.f)) continue;  // no key seen so far
-            const float mref = Mn == -INFINITY ? 0.f : Mn;
-            const float sc = ex2_approx(M - mref);
-            const float wgt = ex2_approx(v.x - mref);
-            float lw = wgt * v.y;
+            for (int e = 0; e < E; ++e) o[r][e] = 0.f;
+        }
+        for (int32_t p0 = 0; p0 < np; p0 += kBatch) {
+            Vec x[kRows][kBatch][NV];
+            float2 v[kRows][kBatch];
 #pragma unroll
-            for (int s = 16; s > 0; s >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, s);
-            Ls = Ls * sc + lw;
+            for (int r = 0; r < kRows; ++r)
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] *= sc;
-            const int32_t np = min(32, c1 - p0 + 1);
-#pragma unroll 4
-            for (int32_t j = 0; j < np; ++j) {
-                const float wj = __shfl_sync(0xffffffffu, wgt, j);
-                const int64_t ij = ((p0 + j == c0 ? first_slot : 2 * (int64_t)(p0 + j)) * slot_rows + row);
-                const float *ap = a.acc + ij * D + lane * E;
-                if constexpr (E % 4 == 0) {
+                for (int b = 0; b < kBatch; ++b) {
+                    v[r][b] = make_float2(-INFINITY, 0.f);
+                    if (p0 + b < np) {
+                        const int64_t at = piece(p0 + b) + row[r];
+                        v[r][b] = __ldcg(&a.ml[at]);
+                        const Vec *ap = reinterpret_cast<const Vec *>(a.acc + at * D + lane * E);
 #pragma unroll
-                    for (int e = 0; e < E; e += 4) {
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(ap + e));
-                        o[e] = fmaf(wj, y.x, o[e]);
-                        o[e + 1] = fmaf(wj, y.y, o[e + 1]);
-                        o[e + 2] = fmaf(wj, y.z, o[e + 2]);
-                        o[e + 3] = fmaf(wj, y.w, o[e + 3]);
+                        for (int e = 0; e < NV; ++e) x[r][b][e] = __ldcg(ap + e);
                     }
-                } else {
-                    const float2 y = __ldcg(reinterpret_cast<const float2 *>(ap));
-                    o[0] = fmaf(wj, y.x, o[0]);
-                    o[1] = fmaf(wj, y.y, o[1]);
+                }
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                float Mn = M[r];
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) Mn = fmaxf(Mn, v[r][b].x);
+                const float mref = Mn == -INFINITY ? 0.f : Mn;  // no key so far: zeros
+                const float sc = ex2_approx(M[r] - mref);
+                M[r] = Mn;
+                l[r] *= sc;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[r][e] *= sc;
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    if (p0 + b >= np) break;
+                    const float w = ex2_approx(v[r][b].x - mref);
+                    l[r] = fmaf(w, v[r][b].y, l[r]);
+#pragma unroll
+                    for (int e = 0; e < NV; ++e) {
+                        const float *xe = reinterpret_cast<const float *>(&x[r][b][e]);
+#pragma unroll
+                        for (int q = 0; q < NE; ++q) o[r][e * NE + q] = fmaf(w, xe[q], o[r][e * NE + q]);
+                    }
                 }
             }
-            M = Mn;
         }
-        const float inv = Ls == 0.f ? 0.f : 1.f / Ls;  // a row without keys is zero
-        T *op = (T *)a.out + ((int64_t)(t.row0 + tok) * a.H + (int64_t)kvh * a.G + g) * D + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) store_out(op + e, o[e] * inv);
+        for (int r = 0; r < kRows; ++r) {
+            const int32_t i = i0 + r * stride;
+            if (i >= me.rows) break;
+            const int32_t tok = i / a.G, g = i - tok * a.G;
+            const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];  // a row without keys is zero
+            T *op = (T *)a.out + ((int64_t)(me.row0 + tok) * a.H + (int64_t)me.kvh * a.G + g) * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {  // out is aligned to two elements
+                if constexpr (std::is_same<T, float>::value)
+                    *reinterpret_cast<float2 *>(op + e) = make_float2(o[r][e] * inv, o[r][e + 1] * inv);
+                else
+                    *reinterpret_cast<uint32_t *>(op + e) = pack_bf16x2(o[r][e] * inv, o[r][e + 1] * inv);
+            }
+        }
     }
 }
 

@@ -132,8 +132,9 @@ __global__ void __launch_bounds__(kSimtThreads, D == 256 ? 1 : 2)
     grid_launch_dependents();
     const int32_t c = blockIdx.x;
     PrefillCursor cur;
-    if (!cur.init(a, c)) return;
-    if (tid == 0) note_cut(a, c, cur);
+    const bool work = cur.init(a, c);
+    if (tid == 0) note_cut(a, c, work, cur);
+    if (!work) return;
     do {
         const PrefillTile t = cur.t;
         const int32_t nrow = t.ntok * a.G;  // rows of this tile (<= 64)

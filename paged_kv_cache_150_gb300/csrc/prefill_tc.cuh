@@ -220,8 +220,9 @@ __device__ __forceinline__ void tc_guard(const PrefillArgs &a, uint8_t *smem, co
     uint32_t no[2] = {0, 0};              // earlier segments with units per row tile
     bool abort = false, dirty = false;
     PrefillCursor cur;
-    if (!cur.init(a, c)) return;
-    if (lane == 0) note_cut(a, c, cur);
+    const bool work = cur.init(a, c);
+    if (lane == 0) note_cut(a, c, work, cur);
+    if (!work) return;
     do {
         const TcSegment sg(a, cur);
         if (sg.jend <= cur.j0) continue;
