@@ -494,7 +494,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
             ++no;
             tc_fence_after();
         }
-        const bool whole = cur.whole();
+        const bool whole = cur.whole(), out32 = ((uintptr_t)a.out & 31) == 0;
         const int64_t row = cur.slot(c) * (2 * kTcRows) + i * kTcRows + r;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const bool odd_tile = any && *odd.segment == (int32_t)segs;
@@ -519,19 +519,29 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
                     }
                 }
                 if (valid) {
+                    // A thread writes a row, so a store's lanes are rows
+                    // apart: whole sectors where out's alignment allows.
                     if (whole) {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 8)
-                            *reinterpret_cast<uint4 *>(op + d0 + k) =
-                                make_uint4(pack_bf16x2(o[k] * inv, o[k + 1] * inv),
-                                           pack_bf16x2(o[k + 2] * inv, o[k + 3] * inv),
-                                           pack_bf16x2(o[k + 4] * inv, o[k + 5] * inv),
-                                           pack_bf16x2(o[k + 6] * inv, o[k + 7] * inv));
-                    } else {
-                        float *ap = a.acc + row * D + d0;
+                        for (int k = 0; k < 32; k += 16) {
+                            uint32_t w[8];
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4)
-                            *reinterpret_cast<float4 *>(ap + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                            for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[k + 2 * e] * inv, o[k + 2 * e + 1] * inv);
+                            if (out32) {
+                                store32(op + d0 + k, w);
+                            } else {
+                                *reinterpret_cast<uint4 *>(op + d0 + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                                *reinterpret_cast<uint4 *>(op + d0 + k + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[k + e]);
+                            store32(a.acc + row * D + d0 + k, w);
+                        }
                     }
                 }
             }

@@ -205,6 +205,13 @@ __device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 32 bytes, 32-byte aligned, in one store (a whole sector of its line).
+__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
     uint64_t r;
