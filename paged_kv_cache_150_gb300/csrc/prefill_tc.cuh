@@ -28,7 +28,7 @@
 
 namespace pa {
 
-constexpr int kTcRows = 128, kTcKeys = 128, kTcThreads = 384, kTcExtra = 4;
+constexpr int kTcRows = 128, kTcKeys = 128, kTcThreads = 384, kTcExtra = 3;
 // Registers: 384 threads x 168 at launch; the two softmax warpgroups take 208
 // each (a row's 128 scores stay in registers), the third one keeps 88:
 // 256 x 208 + 128 x 88 = 384 x 168.

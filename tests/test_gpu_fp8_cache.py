@@ -236,6 +236,20 @@ def test_decode(H, Hk, D, block, kernel):
     assert torch.equal(out, pa.pa_decode_fp8(**b.dev, kernel=kernel))
 
 
+@pytest.mark.parametrize("H,Hk,D,block", [(32, 8, 128, 16), (64, 16, 64, 32), (6, 6, 128, 48), (8, 1, 128, 64)])
+def test_decode_tensor_core_kernel_by_name(H, Hk, D, block):
+    b = Batch([257, 40, 16, 3], H, Hk, D, block, seed=50)
+    b.check(pa.pa_decode_fp8(**b.dev, kernel="mma"))
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
+
+
+@pytest.mark.parametrize("H,Hk,D,block", [(8, 2, 256, 16), (8, 2, 128, 5), (7, 1, 64, 8)])
+def test_decode_tensor_core_kernel_refusals(H, Hk, D, block):
+    b = Batch([20], H, Hk, D, block, seed=51)
+    with pytest.raises(pa.PagedAttentionError):
+        pa.pa_decode_fp8(**b.dev, kernel="mma")
+
+
 @pytest.mark.parametrize("kernel", ["auto", "simt"])
 @pytest.mark.parametrize("splits", [1, 2, 5, 37, 900])
 def test_decode_any_split_count(kernel, splits):
