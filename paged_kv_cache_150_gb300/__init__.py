@@ -30,8 +30,14 @@ _KERNELS = {"auto": PA_KERNEL_AUTO, "simt": PA_KERNEL_SIMT, "mma": PA_KERNEL_MMA
 
 
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+_torch_module = None
 
 
 def _dtype_code(t):
@@ -259,6 +265,16 @@ _desc_memo = {}
 _opts_memo = {}
 
 
+def _here():
+    """(current device, its current stream as an integer)."""
+    c = _torch()._C
+    get_device, get_stream = getattr(c, "_cuda_getDevice", None), getattr(c, "_cuda_getCurrentRawStream", None)
+    if get_device is None or get_stream is None:
+        return _current_device(), _stream().value or 0
+    d = get_device()
+    return d, get_stream(d)
+
+
 def _prefill_opts(num_splits, kernel):
     o = _opts_memo.get((num_splits, kernel))
     if o is None:
@@ -268,16 +284,25 @@ def _prefill_opts(num_splits, kernel):
     return o
 
 
-def _memo_desc(make, *tensors):
-    """Descriptor of caches (read-only once made), remembered by their shapes
-    and types."""
-    key = (make,) + tuple((t.shape, t.dtype) for t in tensors)
+def _memo(make, key, *tensors):
+    """make(*tensors), a descriptor of caches that nobody writes to, remembered
+    by ``key``: their shapes and types."""
     d = _desc_memo.get(key)
     if d is None:
+        d = make(*tensors)
         if len(_desc_memo) > 256:
             _desc_memo.clear()
-        d = _desc_memo[key] = make(*tensors)
+        _desc_memo[key] = d
     return d
+
+
+def _memo_desc(k, v):
+    return _memo(_cache_desc, (k.shape, v.shape, k.dtype, v.dtype), k, v)
+
+
+def _memo_desc_fp8(k, v, ks, vs):
+    return _memo(_cache_desc_fp8, (k.shape, v.shape, ks.shape, vs.shape, k.dtype, v.dtype, ks.dtype, vs.dtype), k, v, ks,
+                 vs)
 
 
 def _ptr(t, name, device, dtype=None):
@@ -309,7 +334,7 @@ def pa_prefill(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, scale, ou
     belong to no sequence are left as they were (in a fresh ``out``:
     unspecified)."""
     torch = _torch()
-    desc = _memo_desc(_cache_desc, k_cache, v_cache)
+    desc = _memo_desc(k_cache, v_cache)
     T, H, D = q.shape
     N = seq_lens.shape[0]
     if D != desc.head_dim or q.dtype != k_cache.dtype:
@@ -322,7 +347,7 @@ def pa_prefill(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, scale, ou
         out = torch.empty_like(q)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must match q")
-    d = _current_device()
+    d, stream = _here()
     o = ctypes.byref(_prefill_opts(num_splits, kernel))
     dp = ctypes.byref(desc)
     lib = _lib.load()
@@ -335,7 +360,7 @@ def pa_prefill(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, scale, ou
     st = lib.pa_prefill(_ptr(out, "out", d), _ptr(q, "q", d), _ptr(k_cache, "k_cache", d), _ptr(v_cache, "v_cache", d),
                         dp, _ptr(block_tables, "block_tables", d, i32), block_tables.shape[1],
                         _ptr(seq_lens, "seq_lens", d, i32), _ptr(cu_q_lens, "cu_q_lens", d, i32), N, T, H, float(scale),
-                        _ptr(workspace, "workspace", d), workspace.nbytes, o, _stream())
+                        _ptr(workspace, "workspace", d), workspace.nbytes, o, stream)
     _lib.check("pa_prefill", st)
     return out
 
@@ -364,7 +389,7 @@ def _cache_desc_fp8(k_cache, v_cache=None, k_scale=None, v_scale=None):
 
 def _rows_call(name, k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale):
     """pa_reshape_and_cache_fp8 or pa_gather_cache_fp8: the same arguments."""
-    desc = _memo_desc(_cache_desc_fp8, k_cache, v_cache, k_scale, v_scale)
+    desc = _memo_desc_fp8(k_cache, v_cache, k_scale, v_scale)
     if slot_mapping.dim() != 1:
         raise ValueError("slot_mapping must be [num_tokens]")
     T = slot_mapping.shape[0]
@@ -374,11 +399,11 @@ def _rows_call(name, k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale):
                          "[num_tokens]")
     if k.dtype != v.dtype:
         raise TypeError("k and v element types differ")
-    d = _current_device()
+    d, stream = _here()
     st = getattr(_lib.load(), name)(
         _ptr(k, "k", d), _ptr(v, "v", d), _dtype_code(k), _ptr(slot_mapping, "slot_mapping", d, _torch().int32), T,
         _ptr(k_cache, "k_cache", d), _ptr(v_cache, "v_cache", d), _ptr(k_scale, "k_scale", d),
-        _ptr(v_scale, "v_scale", d), ctypes.byref(desc), _stream())
+        _ptr(v_scale, "v_scale", d), ctypes.byref(desc), stream)
     _lib.check(name, st)
 
 
@@ -408,15 +433,15 @@ def pa_gather_cache_fp8(k_cache, v_cache, k_scale, v_scale, slot_mapping, k=None
 
 def pa_copy_blocks_fp8(k_cache, v_cache, k_scale, v_scale, src_dst_pairs):
     """pa_copy_blocks for an 8-bit cache: codes and scale bytes."""
-    desc = _memo_desc(_cache_desc_fp8, k_cache, v_cache, k_scale, v_scale)
+    desc = _memo_desc_fp8(k_cache, v_cache, k_scale, v_scale)
     if src_dst_pairs.numel() == 0:
         return
     pairs = src_dst_pairs.reshape(-1, 2)
-    d = _current_device()
+    d, stream = _here()
     st = _lib.load().pa_copy_blocks_fp8(
         _ptr(k_cache, "k_cache", d), _ptr(v_cache, "v_cache", d), _ptr(k_scale, "k_scale", d),
         _ptr(v_scale, "v_scale", d), ctypes.byref(desc), _ptr(pairs, "src_dst_pairs", d, _torch().int32),
-        pairs.shape[0], _stream())
+        pairs.shape[0], stream)
     _lib.check("pa_copy_blocks_fp8", st)
 
 
@@ -435,7 +460,7 @@ def pa_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
     """Decode attention over an 8-bit cache through block tables; q and the
     returned ``out`` are bfloat16 [N, H, D]."""
     torch = _torch()
-    desc = _memo_desc(_cache_desc_fp8, k_cache, v_cache, k_scale, v_scale)
+    desc = _memo_desc_fp8(k_cache, v_cache, k_scale, v_scale)
     N, H, D = q.shape
     if D != desc.head_dim:
         raise ValueError("q must be [num_seqs, num_heads, head_dim] matching the cache")
@@ -447,7 +472,7 @@ def pa_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
         out = torch.empty_like(q)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must match q")
-    d = _current_device()
+    d, stream = _here()
     o = ctypes.byref(_prefill_opts(num_splits, kernel))
     dp = ctypes.byref(desc)
     lib = _lib.load()
@@ -461,7 +486,7 @@ def pa_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
         _ptr(out, "out", d), _ptr(q, "q", d), _ptr(k_cache, "k_cache", d), _ptr(v_cache, "v_cache", d),
         _ptr(k_scale, "k_scale", d), _ptr(v_scale, "v_scale", d), dp, _ptr(block_tables, "block_tables", d, i32),
         block_tables.shape[1], _ptr(seq_lens, "seq_lens", d, i32), N, H, float(scale), _ptr(workspace, "workspace", d),
-        workspace.nbytes, o, _stream())
+        workspace.nbytes, o, stream)
     _lib.check("pa_decode_fp8", st)
     return out
 

@@ -83,7 +83,7 @@ void prefill_workspace(PrefillPlan *p, int32_t N, int32_t head_dim) {
     p->off_tile0 = take(sizeof(int32_t) * ((size_t)N + 1));
     p->off_cu = take(sizeof(int32_t) * (tiles + 1));
     p->off_tiles = take(sizeof(PrefillTile) * std::max<size_t>(tiles, 1));
-    p->off_start = take(sizeof(int32_t) * (size_t)p->C);
+    p->off_start = take(sizeof(WalkStart) * (size_t)p->C);
     p->off_merges = take(sizeof(MergeEntry) * (size_t)p->C);
     const size_t slot_rows = 2 * (size_t)p->C * p->nrt * p->rows;
     p->off_ml = take(sizeof(float2) * slot_rows);
@@ -104,7 +104,7 @@ pa_status_t prefill_bind(const PrefillPlan &p, PrefillArgs *a, void *workspace) 
     a->seq_tile0 = (int32_t *)(ws + p.off_tile0);
     a->cu = (int32_t *)(ws + p.off_cu);
     a->tiles = (PrefillTile *)(ws + p.off_tiles);
-    a->start_tile = (int32_t *)(ws + p.off_start);
+    a->starts = (WalkStart *)(ws + p.off_start);
     a->merges = (MergeEntry *)(ws + p.off_merges);
     a->few = (int64_t)p.max_tiles * a->Hk * 4 <= p.C ? 1 : 0;
     a->ml = (float2 *)(ws + p.off_ml);

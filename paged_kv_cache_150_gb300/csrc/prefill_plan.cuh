@@ -30,6 +30,15 @@ struct PrefillTile {
     int32_t p0;    // position of its first token (negative: before the sequence's first key)
 };
 
+// Where a CTA's walk over its range starts (one read of 80 bytes instead of a
+// chain of dependent ones).
+struct __align__(16) WalkStart {
+    PrefillTile t, t_next;           // the first tile and the one after it
+    int64_t x, hi;                   // weight position of the tile's start, end of the range
+    int32_t kvh, k, j0, j1;
+    int32_t nu, tiles, w_next, work; // work: 0 for a CTA without units
+};
+
 // A tile cut between CTAs, for the merge: pieces slot0 (of CTA
 // slot0 / 2, its first units), then the first slots of the CTAs up to c1.
 struct __align__(16) MergeEntry {
@@ -56,12 +65,12 @@ struct PrefillArgs {
     int32_t max_tiles;    // capacity of tiles[] and cu[]
     float scale_log2;
     int32_t few;          // 1: few tiles in many pieces, merged by prefill_merge_few_kernel
-    int32_t *ctl;         // ctl[0]: tiles of the list, ctl[1]: cut tiles listed, ctl[2]: most query rows of one
+    int32_t *ctl;         // ctl[1]: cut tiles listed, ctl[2]: most query rows of one
     MergeEntry *merges;   // [C] the cut tiles (note_cut)
     int32_t *seq_tile0;   // [N + 1] first tile of each sequence
     int32_t *cu;          // [max_tiles + 1] exclusive prefix sums of the tiles' weights
     PrefillTile *tiles;   // [max_tiles]
-    int32_t *start_tile;  // [C] tile holding the first unit of each CTA's range
+    WalkStart *starts;    // [C]
     float2 *ml;           // [2 C][nrt * rows]
     float *acc;           // [2 C][nrt * rows][D]
     unsigned int *err;
@@ -98,6 +107,19 @@ __device__ __forceinline__ int32_t block_scan_1024(int32_t x, int32_t carry, int
     return carry + x + (w > 0 ? warp_incl[w - 1] : 0);
 }
 
+// Largest i in [0, n) with cu[i] <= x (cu not decreasing, cu[0] <= x).
+__device__ __forceinline__ int32_t last_at_most(const int32_t *cu, int32_t n, int32_t x) {
+    int32_t lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int32_t mid = (lo + hi + 1) >> 1;
+        if (cu[mid] <= x)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
 // One CTA: the tiles of every sequence, the prefix sums of their units, and
 // the tile in which each CTA's range starts.  Row offsets that are not
 // increasing within [0, T] void the whole call (no tile: out stays as it
@@ -105,9 +127,9 @@ __device__ __forceinline__ int32_t block_scan_1024(int32_t x, int32_t carry, int
 static __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillArgs a) {
     grid_dependency_wait();
     grid_launch_dependents();
-    constexpr int32_t kSmemCu = 8192;
+    constexpr int32_t kSmemCu = 8192, kSmemSeqs = 2048;
     __shared__ int32_t warp_incl[32];
-    __shared__ int32_t cu_s[kSmemCu];
+    __shared__ int32_t cu_s[kSmemCu], tile0_s[kSmemSeqs];
     const int tid = threadIdx.x;
     const int64_t max_len = (int64_t)a.max_blocks * a.B;
     const int32_t tq = a.tq1 * a.nrt;
@@ -122,11 +144,13 @@ static __global__ void __launch_bounds__(1024) prefill_plan_kernel(const Prefill
     if (!ok) {
         if (tid == 0) {
             atomicOr(a.err, kErrBounds);
-            a.ctl[0] = a.ctl[1] = a.ctl[2] = 0;
+            a.ctl[1] = a.ctl[2] = 0;
             a.cu[0] = 0;
         }
+        for (int32_t c = tid; c < a.C; c += 1024) a.starts[c] = WalkStart{};  // no work
         return;
     }
+    int32_t *tile0 = a.N <= kSmemSeqs ? tile0_s : a.seq_tile0;  // first tile of each sequence
     int32_t tiles = 0;
     for (int32_t base = 0; base < a.N; base += 1024) {
         const int32_t i = base + tid;
@@ -139,27 +163,21 @@ static __global__ void __launch_bounds__(1024) prefill_plan_kernel(const Prefill
         }
         int32_t total;
         const int32_t incl = block_scan_1024(nt, tiles, warp_incl, &total);
-        if (i < a.N) a.seq_tile0[i] = incl - nt;
+        if (i < a.N) tile0[i] = incl - nt;
         tiles = total;
     }
-    if (tid == 0) a.seq_tile0[a.N] = tiles;
-    __syncthreads();  // seq_tile0 (global memory) is read by this CTA's other threads
+    __syncthreads();  // tile0 is read by this CTA's other threads
     const bool in_smem = tiles + 1 <= kSmemCu;
     int32_t units = 0;
     for (int32_t base = 0; base < tiles; base += 1024) {
         const int32_t k = base + tid;
         int32_t u = 0;
         if (k < tiles) {
-            int32_t lo = 0, hi = a.N - 1;  // largest sequence with seq_tile0 <= k (it has tiles)
-            while (lo < hi) {
-                const int32_t mid = (lo + hi + 1) >> 1;
-                if (a.seq_tile0[mid] <= k)
-                    lo = mid;
-                else
-                    hi = mid - 1;
-            }
+            // the last sequence that starts at or before tile k (it has tiles);
+            // single queries: a tile each
+            const int32_t lo = a.cu_q ? last_at_most(tile0, a.N, k) : k;
             const int32_t r0 = a.cu_q ? a.cu_q[lo] : lo, n = a.cu_q ? a.cu_q[lo + 1] - r0 : 1;
-            const int32_t t0 = (k - a.seq_tile0[lo]) * tq;
+            const int32_t t0 = (k - tile0[lo]) * tq;
             int32_t L = a.seq_lens[lo];
             if (L < 0 || L > max_len) L = 0;
             PrefillTile t;
@@ -180,24 +198,33 @@ static __global__ void __launch_bounds__(1024) prefill_plan_kernel(const Prefill
     }
     if (tid == 0) {
         a.cu[tiles] = units;
-        a.ctl[0] = tiles;
         a.ctl[1] = a.ctl[2] = 0;
     }
     __syncthreads();
     const int32_t *cu = in_smem ? cu_s : a.cu;
     const int64_t W = (int64_t)a.Hk * units;
     const int32_t Ce = (int32_t)min(W, (int64_t)a.C);
-    for (int32_t c = tid; c < Ce; c += 1024) {
-        const int32_t r = (int32_t)(split_begin(c, W, Ce) % units);
-        int32_t lo = 0, hi = tiles - 1;
-        while (lo < hi) {
-            const int32_t mid = (lo + hi + 1) >> 1;
-            if (cu[mid] <= r)
-                lo = mid;
-            else
-                hi = mid - 1;
+    for (int32_t c = tid; c < a.C; c += 1024) {
+        WalkStart w{};
+        if (c < Ce) {
+            const int64_t lo = split_begin(c, W, Ce);
+            w.hi = split_begin((int64_t)c + 1, W, Ce);
+            w.kvh = (int32_t)(lo / units);
+            const int32_t r = (int32_t)(lo - (int64_t)w.kvh * units);
+            w.k = last_at_most(cu, tiles, r);
+            w.tiles = tiles;
+            const int32_t begin = cu[w.k], next = w.k + 1 == tiles ? 0 : w.k + 1;
+            auto end_of = [&](int32_t k) { return k + 1 == tiles ? units : cu[k + 1]; };
+            w.t = a.tiles[w.k];
+            w.t_next = a.tiles[next];
+            w.x = lo - (r - begin);
+            w.nu = end_of(w.k) - begin - a.extra;
+            w.w_next = end_of(next) - cu[next];
+            w.j0 = max(0, r - begin - a.extra);
+            w.j1 = (int32_t)max((int64_t)0, min((int64_t)w.nu, w.hi - w.x - a.extra));
+            w.work = w.j1 > w.j0 ? 1 : 0;
         }
-        a.start_tile[c] = lo;
+        a.starts[c] = w;
     }
 }
 
@@ -218,24 +245,11 @@ struct PrefillWalk {
 
     // False when the CTA has no work.
     __device__ __forceinline__ bool init(const PrefillArgs &a, int32_t c) {
-        tiles = a.ctl[0];
-        const int32_t U = a.cu[tiles];
-        const int64_t W = (int64_t)a.Hk * U;
-        const int32_t Ce = (int32_t)min(W, (int64_t)a.C);
-        if (c >= Ce) return false;
-        const int64_t lo = split_begin(c, W, Ce);
-        hi = split_begin((int64_t)c + 1, W, Ce);
-        kvh = (int32_t)(lo / U);
-        k = a.start_tile[c];
-        const int32_t begin = a.cu[k];
-        x = (int64_t)kvh * U + begin;
+        const WalkStart w = a.starts[c];
+        x = w.x, hi = w.hi, kvh = w.kvh, k = w.k, j0 = w.j0, j1 = w.j1, nu = w.nu, tiles = w.tiles;
         first = true;
-        t = a.tiles[k];
-        nu = a.cu[k + 1] - begin - a.extra;
-        j0 = max(0, (int32_t)(lo - x) - a.extra);
-        j1 = units_to_end(a);
-        if constexpr (kAhead) read_next(a);
-        return j1 > j0;
+        t = w.t, t_next = w.t_next, w_next = w.w_next;
+        return w.work != 0;
     }
     __device__ __forceinline__ int32_t units_to_end(const PrefillArgs &a) const {
         return (int32_t)max((int64_t)0, min((int64_t)nu, hi - x - a.extra));
