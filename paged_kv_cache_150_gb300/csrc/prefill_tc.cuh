@@ -502,17 +502,17 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
             (__nv_bfloat16 *)a.out + ((int64_t)(sg.t.row0 + tok) * a.H + (int64_t)cur.kvh * a.G + g) * D;
         if (warp_rows) {
 #pragma unroll 1
-            for (int d0 = 0; d0 < D; d0 += 32) {
-                float o[32];
+            for (int d0 = 0; d0 < D; d0 += 64) {
+                float o[64];
                 if (any) {
-                    tmem_ld32(tO + (uint32_t)d0, o);
+                    tmem_ld_cols(tO + (uint32_t)d0, o);
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = 0.f;
+                    for (int k = 0; k < 64; ++k) o[k] = 0.f;
                 }
                 if (odd_tile) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
+                    for (int k = 0; k < 64; ++k) {
                         if (last >= odd.first[d0 + k]) o[k] += INFINITY;
                         if (last >= odd.first[D + d0 + k]) o[k] -= INFINITY;
                         if (last >= odd.first[2 * D + d0 + k]) o[k] += __uint_as_float(0x7fffffffu);
@@ -523,7 +523,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
                     // apart: whole sectors where out's alignment allows.
                     if (whole) {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 16) {
+                        for (int k = 0; k < 64; k += 16) {
                             uint32_t w[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[k + 2 * e] * inv, o[k + 2 * e + 1] * inv);
@@ -536,7 +536,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
                         }
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 8) {
+                        for (int k = 0; k < 64; k += 8) {
                             uint32_t w[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[k + e]);
