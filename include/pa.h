@@ -413,8 +413,9 @@ pa_status_t pa_prefill(void *out, const void *q, const void *k_cache, const void
  *     of two per row and the probabilities to fp16, and sums in fp32).
  *     Requirements as pa_decode (H / Hk <= 8, D in {64, 128, 256}); q and out
  *     aligned to 4 bytes, the caches to 16.  The tensor-core kernel takes D 64
- *     or 128 and block sizes that are multiples of 8; CUDA cores take the
- *     rest.  opts: num_splits and kernel.
+ *     or 128, block sizes that are multiples of 8, and scale arrays aligned to
+ *     16 bytes with a multiple of 16 scale bytes in each piece of a block that
+ *     it copies; CUDA cores take the rest.  opts: num_splits and kernel.
  * Any D >= 1 and alignment can be written, read back and copied.
  * ---------------------------------------------------------------------- */
 pa_status_t pa_reshape_and_cache_fp8(const void *k, const void *v, int32_t dtype, const int32_t *slot_mapping,
