@@ -332,3 +332,67 @@ def test_python_refusals():
     with pytest.raises(ValueError):
         pa.pa_reshape_and_cache_fp8(k[:, :1].bfloat16(), k[:, :1].bfloat16(), slots, d["k_cache"], d["v_cache"],
                                     d["k_scale"], d["v_scale"])
+
+
+@pytest.mark.parametrize("n,H,Hk,D,block", [(2049, 8, 4, 64, 8), (8300, 4, 2, 128, 16), (2600, 4, 2, 64, 5)])
+def test_decode_more_sequences_than_shared_memory_lists(n, H, Hk, D, block):
+    b = Batch([i * 7 % 20 for i in range(n)], H, Hk, D, block, seed=n)
+    out = pa.pa_decode_fp8(**b.dev)
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
+    some = sorted({0, 1, 2047, 2048, n - 1} | set(range(0, n, 53)))
+    # the reference of a part of the batch: the same rows by another list
+    part = Batch.__new__(Batch)
+    part.__dict__.update(b.__dict__)
+    part.lens, part.tables, part.q = [b.lens[i] for i in some], b.tables[some], b.q[some]
+    part.check(out[some])
+
+
+@pytest.mark.parametrize("which", ["k_scale", "v_scale", "q", "out"])
+def test_decode_at_the_smallest_alignment(which):
+    b = Batch([700, 3, 129], 32, 8, 128, 16, seed=71)
+    kw = {}
+    if which.endswith("scale"):
+        x = b.dev[which]
+        y = torch.empty(x.numel() + 1, dtype=x.dtype, device="cuda")[1:].view(x.shape)
+        y.copy_(x)
+        b.dev[which] = y
+        with pytest.raises(pa.PagedAttentionError):
+            pa.pa_decode_fp8(**b.dev, kernel="mma")
+    else:
+        y = torch.empty(b.q.numel() + 2, dtype=BF, device="cuda")[2:].view(b.q.shape)
+        if which == "q":
+            y.copy_(b.q)
+            b.dev["q"] = y
+        else:
+            kw["out"] = y
+    b.check(pa.pa_decode_fp8(**b.dev, **kw))
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("kernel", ["mma", "simt"])
+def test_decode_a_query_row_that_is_not_finite_stays_alone(kernel, value):
+    b = Batch([700, 300], 32, 8, 128, 16, seed=72)
+    clean = pa.pa_decode_fp8(**b.dev, kernel=kernel)
+    b.check(clean)
+    b.dev["q"][0, 9, 3] = value
+    out = pa.pa_decode_fp8(**b.dev, kernel=kernel)
+    assert torch.isnan(out[0, 9]).all()
+    out[0, 9] = clean[0, 9]
+    b.check(out)
+
+
+def test_decode_two_calls_at_once():
+    bs = [Batch([3000, 900, 1], 32, 8, 128, 16, seed=s) for s in (73, 74)]
+    want = [pa.pa_decode_fp8(**b.dev) for b in bs]
+    streams = [torch.cuda.Stream() for _ in bs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(pa.pa_decode_fp8(**bs[i].dev))
+    torch.cuda.synchronize()
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
+    for w, outs in zip(want, got):
+        assert all(torch.equal(w, o) for o in outs)

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import paged_kv_cache_150_gb300 as pa
-from _chunks import Chunk
+from _chunks import Chunk, tolerance
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -264,3 +264,62 @@ def test_many_segments_per_cta_with_row_tiles_that_end_apart(splits):
     for _ in range(3):
         out = run(c, num_splits=splits)
     c.check(out, P_EPS[BF])
+
+
+def check_some(c, out, which):
+    """c.check for some of the sequences."""
+    for i in which:
+        if c.q_lens[i] == 0:
+            continue
+        ref, amount, dots, top = c.reference(i)
+        tol = tolerance(out.dtype, ref, amount, dots, top, c.seq_lens[i], ref.shape[-1], P_EPS[out.dtype])
+        err = (out[c.cu[i]:c.cu[i + 1]].double() - ref).abs()
+        assert float((err / tol).max()) <= 1.0, i
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,longest", [(2049, 40), (2600, 9), (8300, 3)])
+def test_more_sequences_and_tiles_than_shared_memory_lists(n, longest, dtype):
+    # the work list keeps 2048 sequences and 8191 tiles in shared memory, more in the workspace
+    lens = [1 + i * 7 % longest for i in range(n)]
+    c = Chunk([min(L, (i * 5) % 3 + (n > 8000)) for i, L in enumerate(lens)], lens, 4, 2, 64, 8, dtype, seed=n)
+    out = run(c)
+    check_some(c, out, sorted({0, 1, 1023, 1024, 2047, 2048, n - 2, n - 1} | set(range(0, n, 97))))
+
+
+@pytest.mark.parametrize("dtype,shift", [(BF, 2), (BF, 4), (F32, 2)])
+def test_q_and_out_at_the_smallest_alignment(dtype, shift):
+    c = Chunk([40, 1, 7], [300, 65, 7], 8, 2, 128, 16, dtype, seed=61)
+    q, out = (torch.empty(c.q.numel() + shift, dtype=dtype, device="cuda")[shift:].view(c.q.shape) for _ in range(2))
+    q.copy_(c.q)
+    c.dev["q"] = q
+    c.check(run(c, out=out), P_EPS[dtype])
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype,kernel", [(BF, "mma"), (BF, "simt"), (F32, "simt")])
+def test_a_query_row_that_is_not_finite_stays_alone(dtype, kernel, value):
+    c = Chunk([150, 3], [400, 90], 8, 2, 128, 16, dtype, seed=62)
+    clean = run(c, kernel=kernel)
+    c.check(clean, P_EPS[dtype])
+    c.dev["q"][17, 5, 3] = value
+    out = run(c, kernel=kernel)
+    assert torch.isnan(out[17, 5]).all()  # its scores hold NaN, or infinities of both signs
+    out[17, 5] = clean[17, 5]
+    c.check(out, P_EPS[dtype])
+
+
+def test_two_calls_at_once():
+    cs = [Chunk([700, 33], [2000, 5000], 32, 8, 128, 16, BF, seed=s) for s in (63, 64)]
+    want = [run(c) for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(pa.pa_prefill(**cs[i].dev))
+    torch.cuda.synchronize()
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
+    for w, outs in zip(want, got):
+        assert all(torch.equal(w, o) for o in outs)
