@@ -410,7 +410,9 @@ pa_status_t pa_prefill(void *out, const void *q, const void *k_cache, const void
  * pa_decode_fp8  pa_decode over the 8-bit cache: q and out are bf16, K_j and
  *     V_j the values, arithmetic in fp32 (the tensor-core kernel multiplies
  *     the codes as fp16, which holds them exactly, rounds q scaled by a power
- *     of two per row and the probabilities to fp16, and sums in fp32).
+ *     of two per row and the probabilities to fp16, and sums in fp32; a
+ *     probability is off by 2^-11 of itself or, if that is more, by 2^-32 of
+ *     the largest one, each times its V row's scale).
  *     Requirements as pa_decode (H / Hk <= 8, D in {64, 128, 256}); q and out
  *     aligned to 4 bytes, the caches to 16.  The tensor-core kernel takes D 64
  *     or 128, block sizes that are multiples of 8, and scale arrays aligned to

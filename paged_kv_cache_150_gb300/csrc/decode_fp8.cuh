@@ -10,10 +10,15 @@
 //     element within 2^28 of it;
 //   x = S 2^ek 2^eq scale log2(e);
 //   p = 2^(x - m), l += p,  O^T += v8^T P^T with P = p 2^(ev + m - m') in fp16.
-// V's exponent goes into P, whose reference m' is the running maximum of
-// x + ev (m is that of x), so P stays within 2^8 whatever the rows' sizes; at
-// the end O is scaled by 2^(m' - m).  P's fp16 rounding (2^-11) is the only one
-// beside fp32's and the output's.
+// V's exponent goes into P, whose reference m' lies kTopBits below the running
+// maximum of x + ev (m is that of x), so P's largest value stays within [2^7, 2^15]
+// whatever the rows' sizes, near the top of fp16's range; at the end O is scaled
+// by 2^(m' - m).  P is rounded to fp16 because the product takes it so: a relative
+// 2^-11, or, of a P below 2^-14 (2^-21 of the largest), an absolute 2^-25 (2^-32
+// of the largest; below that it counts as 0).  Over L keys the second kind adds
+// up to at most L 2^-32 of the largest p |v|; with the reference at the maximum
+// itself it was L 2^-25, more than the output's own rounding from 2^16 keys on.
+// It is the only rounding beside fp32's and the output's.
 //
 // Bound by the K and V bytes: 16 sequences of 32768 tokens (64 / 8 heads, head_dim
 // 128) take 168 us (6.4 TB/s) with the work list and the merge; head_dim 64
@@ -40,6 +45,9 @@ namespace pa {
 constexpr int kF8Warps = 8, kF8Threads = 32 * (kF8Warps + 1);
 constexpr int kF8SlotRows = 64;  // query rows of a piece: NH * G <= 64
 constexpr float kTopP = 256.f;   // 2^kLazyMaxSlack
+constexpr float kTopBits = 7.f;  // P's reference below the running maximum: P <= 2^(7 + kLazyMaxSlack) < 65504
+constexpr float kTopScale = 1.f / 128.f;  // 2^-kTopBits
+constexpr float kMaxFactor = 3.4e38f;  // of p: just under fp32's end
 constexpr int kF8Extra = 2;      // weight of a sequence beside its units (prefill_plan.cuh)
 
 // The parts of a call beyond PrefillArgs (there G is NH * G and Hk the number
@@ -332,13 +340,15 @@ __global__ void __launch_bounds__(kF8Threads, 2)
                     p0 = ex2_approx(x0 - m0), p1 = ex2_approx(x1 - m1);
                     p2 = ex2_approx(x2 - m0), p3 = ex2_approx(x3 - m1);
                     // the bound keeps a factor that overflows beside p = 0 finite
-                    P0 = p0 * fminf(ga * c0, 1e36f), P1 = p1 * fminf(ga * c1, 1e36f);
-                    P2 = p2 * fminf(gc * c0, 1e36f), P3 = p3 * fminf(gc * c1, 1e36f);
+                    P0 = p0 * fminf(ga * c0, kMaxFactor), P1 = p1 * fminf(ga * c1, kMaxFactor);
+                    P2 = p2 * fminf(gc * c0, kMaxFactor), P3 = p3 * fminf(gc * c1, kMaxFactor);
                 };
                 weigh();
                 // Lazy running maxima: moved only when some p or P passes
-                // 2^kLazyMaxSlack (always on a segment's first tokens).
-                const float top = fmaxf(fmaxf(fmaxf(p0, p1), fmaxf(p2, p3)), fmaxf(fmaxf(P0, P1), fmaxf(P2, P3)));
+                // 2^kLazyMaxSlack times its value at the maximum (always on a
+                // segment's first tokens).
+                const float top = fmaxf(fmaxf(fmaxf(p0, p1), fmaxf(p2, p3)),
+                                        kTopScale * fmaxf(fmaxf(P0, P1), fmaxf(P2, P3)));
                 if (__any_sync(0xffffffffu, top > kTopP || m0 == -INFINITY || m1 == -INFINITY)) {
                     const float ea = (float)min(va, 254u) - 127.f, ec = (float)min(vc, 254u) - 127.f;
                     float a0 = fmaxf(x0, x2), a1 = fmaxf(x1, x3);
@@ -353,6 +363,8 @@ __global__ void __launch_bounds__(kF8Threads, 2)
                     // a reference that stays (also at -inf) keeps its factor 1
                     if (a0 > m0) l0 *= ex2_approx(m0 - a0), m0 = a0;
                     if (a1 > m1) l1 *= ex2_approx(m1 - a1), m1 = a1;
+                    // 2^(m - m') stays finite: rows of zeros have the smallest exponent
+                    b0 = fmaxf(b0 - kTopBits, m0 - 126.f), b1 = fmaxf(b1 - kTopBits, m1 - 126.f);
                     const float f0 = b0 > v0 ? ex2_approx(v0 - b0) : 1.f, f1 = b1 > v1 ? ex2_approx(v1 - b1) : 1.f;
                     v0 = fmaxf(v0, b0), v1 = fmaxf(v1, b1);
                     c0 = ex2_approx(m0 - v0), c1 = ex2_approx(m1 - v1);

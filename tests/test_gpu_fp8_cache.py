@@ -396,3 +396,74 @@ def test_decode_two_calls_at_once():
     assert pa.pa_get_device_error(raise_on_error=False) == 0
     for w, outs in zip(want, got):
         assert all(torch.equal(w, o) for o in outs)
+
+
+class Given(Batch):
+    """One sequence with given rows k, v [L, Hk, D] (quantised by the library) and queries q [1, H, D]."""
+
+    def __init__(self, k, v, q, scale, block, seed):
+        g = torch.Generator().manual_seed(seed)
+        L, Hk, D = k.shape
+        self.lens, self.block, self.scale, self.q = [L], block, scale, q.to(BF)
+        self.tables, pool = make_tables(self.lens, block, g)
+        dev = pools(pool, block, Hk, D, fill=0x7f)
+        dev[2].fill_(255)
+        dev[3].fill_(255)
+        rows_of = slots_of(self.tables[0], L, block)
+        pa.pa_reshape_and_cache_fp8(k.to(BF).cuda(), v.to(BF).cuda(), rows_of.to(torch.int32).cuda(), *dev)
+        self.dev = dict(zip(("k_cache", "v_cache", "k_scale", "v_scale"), dev), q=self.q.cuda(), scale=scale,
+                        block_tables=self.tables.cuda(), seq_lens=torch.tensor(self.lens, dtype=torch.int32).cuda())
+        self.rows_of = rows_of
+        self.read()
+
+    def read(self):
+        """The values that the codes and scale bytes stand for."""
+        self.vals = []
+        for name in "kv":
+            codes = code_values()[self.dev[name + "_cache"].view(torch.uint8).cpu().flatten(0, 1).long()]
+            byte = self.dev[name + "_scale"].cpu().flatten(0, 1).double()
+            self.vals.append(codes * torch.where(byte == 255, math.nan, torch.exp2(byte - 127)).unsqueeze(-1))
+
+    def reference(self):
+        k, v = (x[self.rows_of].cuda() for x in self.vals)
+        return attention(self.q.cuda(), k, v, self.lens[0] - 1, self.scale) + (float(v.abs().max()),)
+
+
+@pytest.mark.parametrize("H,Hk,D", [(8, 8, 64), (16, 8, 128), (8, 1, 64), (8, 2, 128)])
+@pytest.mark.parametrize("below", [20.0, 22.5, 24.5, 25.25, 26.0])
+@pytest.mark.parametrize("splits", [1, 0])
+def test_decode_a_long_flat_tail_behind_one_large_weight(H, Hk, D, below, splits):
+    """A weight of 1 and 65535 of 2^-below, whose V rows are as large and lie in
+    other columns: the tail's sum must reach its columns as it reaches the
+    softmax's sum."""
+    L = 65536
+    k, v, q = torch.zeros(L, Hk, D), torch.zeros(L, Hk, D), torch.zeros(1, H, D)
+    whole = float(math.floor(below / 2) * 2)
+    q[..., :2] = 1.0
+    k[1:, :, 0], k[1:, :, 1] = -whole, whole - below  # e4m3 holds both beside each other
+    v[0, :, 0] = 1.0
+    v[1:, :, 1:] = 1.0
+    b = Given(k, v, q, math.log(2.0), 16, seed=80)
+    out = pa.pa_decode_fp8(**b.dev, kernel="mma", num_splits=splits).double()
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
+    ref, amount, dots, top, big = b.reference()
+    # P's reference is 2^7, an fp16 subnormal is off by 2^-25: 2^-32 of the largest weight for each key
+    tol = tolerance(BF, ref, amount, dots, top, L, D, 2.0 ** -11) + L * 2.0 ** -32 * big
+    assert float(((out - ref).abs() / tol).max()) <= 1.0
+
+
+def test_decode_values_of_every_size():
+    """V rows of zeros, of the smallest and of the largest scale byte that a write makes, alone and mixed."""
+    L, Hk, D = 200, 8, 64
+    g = torch.Generator().manual_seed(84)
+    sizes = [0.0, 2.0 ** -126, 2.0 ** -60, 1.0, 2.0 ** 60, 2.0 ** 112]
+    for pick in ([0], [1], [5], [0, 1], [0, 3], [1, 5], [2, 4], [0, 1, 2, 3, 4, 5]):
+        size = torch.tensor([sizes[i] for i in pick])[torch.randint(0, len(pick), (L, Hk, 1), generator=g)]
+        b = Given(torch.randn(L, Hk, D, generator=g), torch.randn(L, Hk, D, generator=g).clamp(-3, 3) * size,
+                  torch.randn(1, 16, D, generator=g), 0.125, 16, seed=85)
+        ref, amount, dots, top, big = b.reference()
+        tol = tolerance(BF, ref, amount, dots, top, L, D, 2.0 ** -11) + L * 2.0 ** -25 * big - 1e-30 + 2.0 ** -134
+        for kernel in ("mma", "simt"):
+            out = pa.pa_decode_fp8(**b.dev, kernel=kernel).double()
+            assert float(((out - ref).abs() / tol).max()) <= 1.0, (pick, kernel)
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
