@@ -388,8 +388,8 @@ pa_status_t pa_prefill(void *out, const void *q, const void *k_cache, const void
 /* ------------------------------------------------------------------------
  * 8-bit cache (PA_FP8_E4M3, PA_LAYOUT_ROW): e4m3 codes [NB, B, Hk, D] for K and
  * for V, and one scale byte per token and KV head in k_scale, v_scale
- * [NB, B, Hk].  Byte b stands for 2^(b - 127) (E8M0); an element's value is
- * code * 2^(b - 127).
+ * [NB, B, Hk].  Byte b stands for 2^(b - 127) (E8M0; 255, which no write
+ * makes, is NaN); an element's value is code * 2^(b - 127).
  *
  * Rule of the write: over the D values x of one token's one KV head, e is the
  * smallest integer in [-126, 120] with |x| <= 448 * 2^e for every finite x;

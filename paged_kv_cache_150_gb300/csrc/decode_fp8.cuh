@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
             const int32_t rest = keys - (j * f.T + sub * 16);  // tokens of this slice and after it
             if (rest > 0) {
                 const uint32_t kb = tiles + (uint32_t)st * 2 * L::kTile + lane_off, vb = kb + L::kTile;
-                // bytes of tokens r and r + 8; 255 (no write makes one) counts as 254
+                // scale bytes of tokens r and r + 8
                 const uint8_t *ks = sc + (uint32_t)st * 2 * f.scale_bytes + sc_off, *vs = ks + f.scale_bytes;
                 const uint32_t ka = ks[0], kc = ks[8 * f.Hk], va = vs[0], vc = vs[8 * f.Hk];
                 float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -327,14 +327,18 @@ __global__ void __launch_bounds__(kF8Threads, 2)
                     mma_f16_16816(s, lo[0], lo[1], hi[0], hi[1], qf[j2][0], qf[j2][1]);
                     mma_f16_16816(s, lo[2], lo[3], hi[2], hi[3], qf[j2 + 1][0], qf[j2 + 1][1]);
                 }
-                const float fa = __uint_as_float(min(ka, 254u) << 23), fc = __uint_as_float(min(kc, 254u) << 23);
+                // Byte 255 is NaN, K's or V's: the row's score takes it to l and to
+                // every column of O (V's own factor stays out of it, as it may
+                // belong to a masked token).
+                const float fa = max(ka, va) == 255u ? scale_of(255u) : scale_bits(ka);
+                const float fc = max(kc, vc) == 255u ? scale_of(255u) : scale_bits(kc);
                 float x0 = s[0] * (fa * qs0), x1 = s[1] * (fa * qs1);
                 float x2 = s[2] * (fc * qs0), x3 = s[3] * (fc * qs1);
                 if (rest < 16) {
                     if (r >= rest) x0 = x1 = -INFINITY;
                     if (r + 8 >= rest) x2 = x3 = -INFINITY;
                 }
-                const float ga = __uint_as_float(min(va, 254u) << 23), gc = __uint_as_float(min(vc, 254u) << 23);
+                const float ga = scale_bits(va), gc = scale_bits(vc);
                 float p0, p1, p2, p3, P0, P1, P2, P3;
                 auto weigh = [&]() {
                     p0 = ex2_approx(x0 - m0), p1 = ex2_approx(x1 - m1);
@@ -350,7 +354,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
                 const float top = fmaxf(fmaxf(fmaxf(p0, p1), fmaxf(p2, p3)),
                                         kTopScale * fmaxf(fmaxf(P0, P1), fmaxf(P2, P3)));
                 if (__any_sync(0xffffffffu, top > kTopP || m0 == -INFINITY || m1 == -INFINITY)) {
-                    const float ea = (float)min(va, 254u) - 127.f, ec = (float)min(vc, 254u) - 127.f;
+                    const float ea = (float)va - 127.f, ec = (float)vc - 127.f;
                     float a0 = fmaxf(x0, x2), a1 = fmaxf(x1, x3);
                     float b0 = fmaxf(x0 + ea, x2 + ec), b1 = fmaxf(x1 + ea, x3 + ec);
 #pragma unroll
@@ -446,11 +450,11 @@ __global__ void __launch_bounds__(kF8Threads, 2)
                     const int slot = (q - 1) * f.NH + h;
                     if (h0 < f.G) {
                         const float2 v = jm[slot * f.G + h0];
-                        l0 += M0 == -INFINITY ? 0.f : v.y * ex2_approx(v.x - M0);
+                        l0 += M0 == -INFINITY ? v.y : v.y * ex2_approx(v.x - M0);  // (0 or NaN without a maximum)
                     }
                     if (h1 < f.G) {
                         const float2 v = jm[slot * f.G + h1];
-                        l1 += M1 == -INFINITY ? 0.f : v.y * ex2_approx(v.x - M1);
+                        l1 += M1 == -INFINITY ? v.y : v.y * ex2_approx(v.x - M1);
                     }
                 }
             }

@@ -34,10 +34,10 @@ __device__ __forceinline__ uint32_t finite_bits(float x) {
 // 2^-e for e in [kScaleMin, kScaleMax] (a normal fp32 number).
 __device__ __forceinline__ float inv_scale(int32_t e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
 
+// 2^(b - 127) of a scale byte b < 255; infinity for 255.
+__device__ __forceinline__ float scale_bits(uint32_t b) { return __uint_as_float(max(b << 23, 0x00400000u)); }
 // 2^(b - 127) of a scale byte b (255, which no write produces, is NaN).
-__device__ __forceinline__ float scale_of(uint32_t b) {
-    return __uint_as_float(b == 0 ? 0x00400000u : (b == 255 ? 0x7fffffffu : b << 23));
-}
+__device__ __forceinline__ float scale_of(uint32_t b) { return b == 255 ? __uint_as_float(0x7fffffffu) : scale_bits(b); }
 
 // Four e4m3 codes of a word, byte 0 first.
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {

@@ -453,7 +453,7 @@ def test_decode_a_long_flat_tail_behind_one_large_weight(H, Hk, D, below, splits
 
 
 def test_decode_values_of_every_size():
-    """V rows of zeros, of the smallest and of the largest scale byte that a write makes, alone and mixed."""
+    """V rows of zeros, of the smallest scale byte that a write makes and of larger ones, alone and mixed."""
     L, Hk, D = 200, 8, 64
     g = torch.Generator().manual_seed(84)
     sizes = [0.0, 2.0 ** -126, 2.0 ** -60, 1.0, 2.0 ** 60, 2.0 ** 112]
@@ -467,3 +467,46 @@ def test_decode_values_of_every_size():
             out = pa.pa_decode_fp8(**b.dev, kernel=kernel).double()
             assert float(((out - ref).abs() / tol).max()) <= 1.0, (pick, kernel)
     assert pa.pa_get_device_error(raise_on_error=False) == 0
+
+
+@pytest.mark.parametrize("kernel", ["mma", "simt"])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_decode_a_seen_row_with_the_scale_byte_of_nan(kernel, which):
+    """Byte 255 is NaN in E8M0: the heads that read such a row get NaN, no other does."""
+    b = Batch([700, 300, 33, 1], 32, 8, 128, 16, seed=81)
+    clean = pa.pa_decode_fp8(**b.dev, kernel=kernel)
+    b.check(clean)
+    want = clean.clone()
+    for i, pos, h in ((0, 0, 1), (0, 699, 5), (1, 123, 0), (2, 32, 7), (3, 0, 2)):
+        at = int(slots_of(b.tables[i], b.lens[i], 16)[pos])
+        b.dev[which + "_scale"].view(-1, 8)[at, h] = 255
+        want[i, 4 * h:4 * h + 4] = math.nan
+    for splits in (0, 1, 7):
+        out = pa.pa_decode_fp8(**b.dev, kernel=kernel, num_splits=splits)
+        assert pa.pa_get_device_error(raise_on_error=False) == 0
+        assert torch.equal(torch.isnan(out), torch.isnan(want))
+        tight = torch.nan_to_num(out.double() - want.double()).abs().max()
+        assert float(tight) <= (0.0 if splits == 0 else 2.0 ** -7 * float(torch.nan_to_num(want).abs().max()))
+
+
+@pytest.mark.parametrize("kernel", ["mma", "simt"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_the_smallest_scale_byte(kernel, D):
+    """Byte 0 stands for 2^-127: K rows of it behind large queries, V rows of it alone, both at once."""
+    L, Hk, H = 300, 8, 16
+    g = torch.Generator().manual_seed(82)
+    q = torch.randn(1, H, D, generator=g) * 2.0 ** 118
+    for small_k, small_v in ((True, False), (False, True), (True, True)):
+        b = Given(torch.randn(L, Hk, D, generator=g), torch.randn(L, Hk, D, generator=g),
+                  q if small_k else q * 2.0 ** -118, 1.0 / math.sqrt(D), 16, seed=83)
+        for name, small in (("k", small_k), ("v", small_v)):
+            if small:
+                b.dev[name + "_scale"].view(-1, Hk)[b.rows_of.cuda()] = 0
+        b.read()
+        out = pa.pa_decode_fp8(**b.dev, kernel=kernel).double()
+        assert pa.pa_get_device_error(raise_on_error=False) == 0
+        ref, amount, dots, top, big = b.reference()
+        # bf16 is off by up to 2^-134 where it has no more bits left (below 2^-126)
+        tol = tolerance(BF, ref, amount, dots, top, L, D, 2.0 ** -11) + L * 2.0 ** -25 * big - 1e-30 + 2.0 ** -134
+        assert float(((out - ref).abs() / tol).max()) <= 1.0
+        assert float(ref.abs().max()) > 2.0 ** -126
