@@ -163,6 +163,7 @@ __device__ __forceinline__ void f8_producer(const PrefillArgs &a, const F8Args &
                 }
                 fence_proxy_async_smem();  // before a later copy to the same bytes
             }
+            __syncwarp();  // every lane's zeros are in place before lane 0 publishes the stage
             const uint32_t boxes = (uint32_t)__popc(__ballot_sync(0xffffffffu, box));
             const uint32_t goods = (uint32_t)__popc(__ballot_sync(0xffffffffu, box && good));
             const uint32_t fb = smem_u32(&full[st]);

@@ -510,3 +510,32 @@ def test_decode_the_smallest_scale_byte(kernel, D):
         tol = tolerance(BF, ref, amount, dots, top, L, D, 2.0 ** -11) + L * 2.0 ** -25 * big - 1e-30 + 2.0 ** -134
         assert float(((out - ref).abs() / tol).max()) <= 1.0
         assert float(ref.abs().max()) > 2.0 ** -126
+
+
+@pytest.mark.parametrize("H,Hk,D,block", [(8, 1, 128, 16), (4, 2, 64, 8), (8, 2, 128, 48), (32, 8, 128, 16)])
+@pytest.mark.parametrize("splits", [1, 3, 0])
+def test_decode_bad_pages_in_every_box_of_a_stage(H, Hk, D, block, splits):
+    """Bad entries at every place of a stage, one at a time, every other one and
+    all of them; the codes that they would have named hold NaN."""
+    lens = [block * n - 1 for n in range(1, 18)] + [block * 40] * 3
+    b = Batch(lens, H, Hk, D, block, seed=86)
+    tables, nb = b.tables.clone(), b.dev["k_cache"].shape[0]
+    bad = [(n, n) for n in range(17)] + [(17, n) for n in range(40)] + [(18, n) for n in range(0, 40, 2)]
+    bad += [(19, n) for n in range(1, 40, 3)]
+    for i, n in bad:
+        at = int(b.tables[i, n])
+        for name in "kv":
+            b.dev[name + "_cache"].view(torch.uint8)[at] = 0x7f
+            b.dev[name + "_scale"][at] = 255
+        rows_of = slots_of(b.tables[i], lens[i], block)[n * block:(n + 1) * block]
+        for x in b.vals:
+            x[rows_of] = 0
+        tables[i, n] = (-1, nb, -2 ** 31, 2 ** 31 - 1)[n % 4]
+    dev = dict(b.dev, block_tables=tables.cuda())
+    out = pa.pa_decode_fp8(**dev, kernel="mma", num_splits=splits)
+    assert pa.pa_get_device_error(raise_on_error=False) == pa._lib.PA_ERR_DEVICE_BOUNDS
+    b.check(out)
+    for _ in range(5):
+        assert torch.equal(out, pa.pa_decode_fp8(**dev, kernel="mma", num_splits=splits))
+    assert pa.pa_get_device_error(raise_on_error=False) == pa._lib.PA_ERR_DEVICE_BOUNDS
+    assert torch.count_nonzero(out[17]) == 0
