@@ -114,7 +114,7 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t &lo, uint32_t &hi
 // Units of T tokens that the current segment takes: [j0, j1), none without keys.
 __device__ __forceinline__ int32_t f8_units_end(const PrefillCursor &cur, int32_t T) {
     const int32_t keys = cur.t.p0 + 1;
-    return keys <= 0 ? cur.j0 : min(cur.j1, (keys + T - 1) / T);
+    return keys <= 0 ? cur.j0 : min(cur.j1, (keys - 1) / T + 1);  // keys + T may pass 2^31
 }
 
 template <int D>

@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kSimtThreads, D == 256 ? 1 : 2)
             __syncthreads();  // unit j staged
             // Keys that only some rows see: does V hold a value that is not finite?
             bool bad = false;
-            if (key0 + kSimtKeys > t.p0 + 1) {
+            if (t.p0 + 1 - key0 < kSimtKeys) {  // (key0 + kSimtKeys may pass 2^31)
                 bool odd = false;
                 for (int e = tid; e < kSimtKeys * (D / 4); e += kSimtThreads) {
                     const float4 vx = *reinterpret_cast<const float4 *>(Vs + e * 4);

@@ -539,3 +539,21 @@ def test_decode_bad_pages_in_every_box_of_a_stage(H, Hk, D, block, splits):
         assert torch.equal(out, pa.pa_decode_fp8(**dev, kernel="mma", num_splits=splits))
     assert pa.pa_get_device_error(raise_on_error=False) == pa._lib.PA_ERR_DEVICE_BOUNDS
     assert torch.count_nonzero(out[17]) == 0
+
+
+def test_decode_at_the_longest_reach():
+    """2^31 - 8 positions through a table that names one block over and over."""
+    block, n = 8 * 127 * 113, 3 * 5 * 29 * 43
+    L = block * n
+    assert L == 2 ** 31 - 8
+    kc, vc, ks, vs = pools(1, block, 2, 64)
+    ones = torch.ones(block, 2, 64, dtype=BF, device="cuda")
+    pa.pa_reshape_and_cache_fp8(torch.zeros_like(ones), ones, torch.arange(block, dtype=torch.int32, device="cuda"), kc, vc,
+                                ks, vs)
+    out = pa.pa_decode_fp8(torch.ones(1, 8, 64, dtype=BF, device="cuda"), kc, vc, ks, vs,
+                           torch.zeros(1, n, dtype=torch.int32, device="cuda"),
+                           torch.tensor([L], dtype=torch.int32, device="cuda"), 1.0, kernel="mma")
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
+    # every score is 0: the sums of a CTA are whole numbers below 2^24 times a
+    # power of two, the merge rounds once for each of at most 2^10 pieces
+    assert float((out.double() - 1).abs().max()) <= 2.0 ** -8 + 2.0 ** -13

@@ -323,3 +323,23 @@ def test_two_calls_at_once():
     assert pa.pa_get_device_error(raise_on_error=False) == 0
     for w, outs in zip(want, got):
         assert all(torch.equal(w, o) for o in outs)
+
+
+def test_chunk_at_the_longest_reach():
+    """The last two of 2^31 - 8 positions, through a table that names one block
+    over and over: the last position's V is not finite, and the row before does not see it."""
+    block, n = 8 * 127 * 113, 3 * 5 * 29 * 43
+    L = block * n
+    assert L == 2 ** 31 - 8
+    k, v = torch.zeros(2, block, 1, 64, device="cuda"), torch.ones(2, block, 1, 64, device="cuda")
+    v[1, -1] = math.nan
+    table = torch.zeros(1, n, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = pa.pa_prefill(torch.ones(2, 1, 64, device="cuda"), k, v, table, torch.tensor([L], **i32),
+                        torch.tensor([0, 2], **i32), 1.0)
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
+    # every score is 0: the sums of a CTA are whole numbers below 2^24, the merge
+    # rounds once for each of at most 2^10 pieces
+    assert float((out[0].double() - 1).abs().max()) <= 2.0 ** -13
+    assert torch.isnan(out[1]).all()
