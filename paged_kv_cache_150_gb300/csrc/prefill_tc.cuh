@@ -92,7 +92,7 @@ struct TcSegment {
         for (int i = 0; i < 2; ++i) {
             const int32_t n = min(t.ntok, (i + 1) * a.tq1);  // tokens up to this row tile's end
             const int32_t ki = t.ntok > i * a.tq1 ? max(t.p0 + n, 0) : 0;
-            je[i] = min(cur.j1, (ki + kTcKeys - 1) / kTcKeys);
+            je[i] = min(cur.j1, (int32_t)(((uint32_t)ki + kTcKeys - 1) / kTcKeys));  // the sum may pass 2^31
         }
         jend = max(je[0], je[1]);
     }

@@ -343,3 +343,18 @@ def test_chunk_at_the_longest_reach():
     # rounds once for each of at most 2^10 pieces
     assert float((out[0].double() - 1).abs().max()) <= 2.0 ** -13
     assert torch.isnan(out[1]).all()
+
+
+def test_tensor_core_chunk_at_the_longest_reach():
+    """As above on the tensor cores, with two heads per KV head."""
+    block, n = 8 * 127 * 113, 3 * 5 * 29 * 43
+    k, v = torch.zeros(2, block, 1, 64, dtype=BF, device="cuda"), torch.ones(2, block, 1, 64, dtype=BF, device="cuda")
+    v[1, -1] = math.nan
+    table = torch.zeros(1, n, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = pa.pa_prefill(torch.ones(2, 2, 64, dtype=BF, device="cuda"), k, v, table, torch.tensor([block * n], **i32),
+                        torch.tensor([0, 2], **i32), 1.0, kernel="mma")
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
+    assert float((out[0].double() - 1).abs().max()) <= 2.0 ** -8 + 2.0 ** -13
+    assert torch.isnan(out[1]).all()
