@@ -186,10 +186,14 @@ __device__ __forceinline__ void tc_producer(const PrefillArgs &a, uint8_t *smem,
 // of V before their products: rows past the tile's keys become zeros, and a
 // value that is not finite is replaced by 0 while its column keeps the first
 // position that holds +inf, -inf and NaN; the rows that see it add it at the
-// end.  odd.segment names the segment the columns belong to.
+// end.  odd.segment names, per row tile, the last segment with such a value in
+// the row tile's own units.  Its word is written before the product that ends
+// those units, so the row tile's wait for its O orders the two; units that only
+// the other row tile takes touch neither the word nor a position that its rows
+// see, whichever moment they read the columns at.
 struct OddColumns {
-    int32_t *first;    // [3][D]: +inf, -inf, NaN; kNone without one
-    int32_t *segment;  // 1-based count of segments with units; 0: none so far
+    int32_t *first;             // [3][D]: +inf, -inf, NaN; kNone without one
+    int32_t *segment;  // [2] 1-based count of segments with units; 0: none so far
     static constexpr int32_t kNone = 0x7fffffff;
 };
 
@@ -222,7 +226,8 @@ __device__ __forceinline__ void tc_guard(const PrefillArgs &a, uint8_t *smem, co
     const uint32_t ring = smem_u32(smem) + L::kRing;
     uint32_t n = 1, segs = 0, units = 0;  // ring entry of V, segments, guarded units
     uint32_t no[2] = {0, 0};              // earlier segments with units per row tile
-    bool abort = false, dirty = false;
+    uint32_t held = 0;                    // the segment that the columns belong to
+    bool abort = false;
     PrefillCursor cur;
     const bool work = cur.init(a, c);
     if (lane == 0) note_cut(a, c, work, cur);
@@ -261,7 +266,7 @@ __device__ __forceinline__ void tc_guard(const PrefillArgs &a, uint8_t *smem, co
                 for (int i = 0; i < 2; ++i)
                     if (no[i] > 0 && (j == cur.j0 || sg.je[i] <= cur.j0))
                         tc_wait(bar.o_free + 8 * i, (no[i] - 1) & 1, abort, a.err);
-                if (dirty && *odd.segment != (int32_t)segs)
+                if (held != 0 && held != segs)
                     for (int x = lane; x < 3 * D; x += 32) odd.first[x] = OddColumns::kNone;
                 __syncwarp();
                 for (e = r0 * kChunks + lane; e < nk * kChunks; e += 32) {
@@ -280,9 +285,10 @@ __device__ __forceinline__ void tc_guard(const PrefillArgs &a, uint8_t *smem, co
                     }
                     sts128(addr, make_uint4(w[0], w[1], w[2], w[3]));
                 }
-                dirty = true;
+                held = segs;
                 __syncwarp();
-                if (lane == 0) *odd.segment = (int32_t)segs;
+                if (lane == 0 && j < sg.je[0]) odd.segment[0] = (int32_t)segs;
+                if (lane == 1 && j < sg.je[1]) odd.segment[1] = (int32_t)segs;
             }
             fence_proxy_async_smem();  // the MMAs read these rows through the async proxy
             __syncwarp();
@@ -501,7 +507,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
         const bool whole = cur.whole(), out32 = ((uintptr_t)a.out & 31) == 0;
         const int64_t row = cur.slot(c) * (2 * kTcRows) + i * kTcRows + r;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const bool odd_tile = any && *odd.segment == (int32_t)segs;
+        const bool odd_tile = any && odd.segment[i] == (int32_t)segs;
         __nv_bfloat16 *op =
             (__nv_bfloat16 *)a.out + ((int64_t)(sg.t.row0 + tok) * a.H + (int64_t)cur.kvh * a.G + g) * D;
         if (warp_rows) {
@@ -517,9 +523,10 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
                 if (odd_tile) {
 #pragma unroll
                     for (int k = 0; k < 64; ++k) {
-                        if (last >= odd.first[d0 + k]) o[k] += INFINITY;
-                        if (last >= odd.first[D + d0 + k]) o[k] -= INFINITY;
-                        if (last >= odd.first[2 * D + d0 + k]) o[k] += __uint_as_float(0x7fffffffu);
+                        const int32_t *first = odd.first + d0 + k;
+                        if (last >= first[0]) o[k] += INFINITY;
+                        if (last >= first[D]) o[k] -= INFINITY;
+                        if (last >= first[2 * D]) o[k] += __uint_as_float(0x7fffffffu);
                     }
                 }
                 if (valid) {
@@ -569,8 +576,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const TcBars bar(smem_u32(smem + L::kBars), L::kStages);
     uint32_t *tmem_slot = (uint32_t *)(smem + L::kBars + 248);
-    const OddColumns odd{(int32_t *)(smem + L::kBars + 256), (int32_t *)(smem + L::kBars + 252)};
-    static_assert(96 + 16 * L::kStages <= 248, "the barriers fit");
+    const OddColumns odd{(int32_t *)(smem + L::kBars + 256), (int32_t *)(smem + L::kBars + 240)};
+    static_assert(96 + 16 * L::kStages <= 240, "the barriers fit");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         mbar_init(bar.q_full, 1);
@@ -587,7 +594,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(bar.kv_full + 8 * s, 1);
             mbar_init(bar.kv_free + 8 * s, 1);
         }
-        *odd.segment = 0;
+        odd.segment[0] = odd.segment[1] = 0;
         fence_mbarrier_init();
     }
     for (int e = tid; e < 3 * D; e += kTcThreads) odd.first[e] = OddColumns::kNone;

@@ -358,3 +358,54 @@ def test_tensor_core_chunk_at_the_longest_reach():
     assert pa.pa_get_device_error(raise_on_error=False) == 0
     assert float((out[0].double() - 1).abs().max()) <= 2.0 ** -8 + 2.0 ** -13
     assert torch.isnan(out[1]).all()
+
+
+def with_odd_values(c, seed, share=0.6):
+    """V values that are not finite at positions of the chunks' own tokens (and
+    some before them), of every kind, in most chunks; returns the number placed."""
+    from _chunks import slots_of
+    g = torch.Generator().manual_seed(seed)
+    Hk, D = c.v.shape[1:]
+    kinds = [math.inf, -math.inf, math.nan]
+    count = 0
+    for i, (n, L) in enumerate(zip(c.q_lens, c.seq_lens)):
+        if n == 0 or float(torch.rand(1, generator=g)) > share:
+            continue
+        rows = slots_of(c.tables[i], L, c.block)
+        for _ in range(int(torch.randint(1, 7, (1,), generator=g))):
+            pos = int(torch.randint(max(0, L - n - 2), L, (1,), generator=g))
+            h, d, kind = (int(torch.randint(0, m, (1,), generator=g)) for m in (Hk, D, 3))
+            c.v[rows[pos], h, d] = kinds[kind]
+            count += 1
+    c.dev["v_cache"] = c.v.view(c.dev["v_cache"].shape).cuda()
+    return count
+
+
+def check_odd(c, refs, out, p_eps):
+    """out against fp64 (refs, of c.reference) where the sums hold infinities and NaN."""
+    for i, (ref, amount, dots, top) in enumerate(refs):
+        got = out[c.cu[i]:c.cu[i + 1]].double()
+        fin = torch.isfinite(ref)
+        assert torch.equal(torch.isnan(got), torch.isnan(ref)), i
+        assert torch.equal(got[torch.isinf(ref)], ref[torch.isinf(ref)]), i
+        tol = tolerance(out.dtype, ref, amount, dots, top, c.seq_lens[i], ref.shape[-1], p_eps)
+        assert float(((got - ref).abs() / tol)[fin].max()) <= 1.0, i
+
+
+@pytest.mark.parametrize("H,Hk,D,block,dtype,kernel", [(8, 2, 128, 16, BF, "mma"), (4, 1, 64, 32, BF, "mma"),
+                                                       (16, 1, 128, 8, BF, "mma"), (8, 2, 128, 16, BF, "simt"),
+                                                       (4, 2, 64, 16, F32, "simt")])
+def test_odd_values_in_chunk_after_chunk(H, Hk, D, block, dtype, kernel):
+    """Many segments on a CTA, most of which hold values that are not finite, at
+    positions that only some of their rows see, one row tile, both or neither."""
+    q = [40, 200, 1, 64, 7, 300, 33, 129, 256, 2, 90, 65]
+    ctx = [60, 0, 127, 700, 128, 30, 0, 255, 5, 900, 129, 62]
+    for seed in (0, 1):
+        c = Chunk(q, [a + b for a, b in zip(q, ctx)], H, Hk, D, block, dtype, seed=90 + seed)
+        assert with_odd_values(c, seed) > 8
+        refs = [c.reference(i) for i in range(len(q))]
+        for splits in (1, 2, 3, 11, 0):
+            out = run(c, kernel=kernel, num_splits=splits)
+            check_odd(c, refs, out, P_EPS[BF] if kernel == "mma" else 0.0)
+            for _ in range(3):
+                assert torch.equal(run(c, kernel=kernel, num_splits=splits).view(torch.uint8), out.view(torch.uint8))
