@@ -164,6 +164,10 @@ pa_status_t prefill_launch(const PrefillPlan &p, const pa_cache_desc_t *c, Prefi
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return PA_ERR_CUDA;
     if (p.tc) {
+        // kTcUnitNs, some times what a unit takes, for each unit of a CTA's longest range
+        const int64_t tile_units = (int64_t)a.max_blocks * a.B / a.kt + 1 + a.extra;  // max_tiles times this is below 2^31
+        const int64_t range = (int64_t)a.Hk * (a.max_tiles * tile_units) / a.C + 1;
+        a.wait_ns = kWaitLimitNs + kTcUnitNs * (unsigned long long)std::min(range, (int64_t)1 << 40);
         CUtensorMap tmq, tmk, tmv;
         int32_t gran = gcd(c->block_size, kTcKeys);
         if (!encode_tc_maps(&tmq, &tmk, &tmv, a, c, gran)) return PA_ERR_CUDA;

@@ -74,6 +74,7 @@ struct PrefillArgs {
     float2 *ml;           // [2 C][nrt * rows]
     float *acc;           // [2 C][nrt * rows][D]
     unsigned int *err;
+    unsigned long long wait_ns;  // limit of the tcgen05 kernel's longest waits
 };
 
 __device__ __forceinline__ int32_t prefill_units(const PrefillTile &t, int32_t kt) {

@@ -33,6 +33,7 @@
 namespace pa {
 
 constexpr int kTcRows = 128, kTcKeys = 128, kTcThreads = 384, kTcExtra = 3;
+constexpr unsigned long long kTcUnitNs = 4096;
 // Registers: 384 threads x 168 at launch; the two softmax warpgroups take 208
 // each (a row's 128 scores stay in registers), the third one keeps 88:
 // 256 x 208 + 128 x 88 = 384 x 168.
@@ -71,9 +72,10 @@ struct TcBars {
 // A bounded wait that stays off once one ran out: the roles then run through
 // their loops without waiting, so that every barrier still gets its arrivals
 // and the CTA ends; the error word marks the call's output as unreliable.
-__device__ __forceinline__ void tc_wait(uint32_t bar, uint32_t parity, bool &abort, unsigned int *err) {
+__device__ __forceinline__ void tc_wait(uint32_t bar, uint32_t parity, bool &abort, unsigned int *err,
+                                        unsigned long long limit_ns = kWaitLimitNs) {
     if (abort) return;
-    if (!mbar_wait_bounded(bar, parity)) {
+    if (!mbar_wait_bounded(bar, parity, limit_ns)) {
         atomicOr(err, kErrTimeout);
         abort = true;
     }
@@ -192,7 +194,7 @@ __device__ __forceinline__ void tc_producer(const PrefillArgs &a, uint8_t *smem,
 // the other row tile takes touch neither the word nor a position that its rows
 // see, whichever moment they read the columns at.
 struct OddColumns {
-    int32_t *first;             // [3][D]: +inf, -inf, NaN; kNone without one
+    int32_t *first;    // [3][D]: +inf, -inf, NaN; kNone without one
     int32_t *segment;  // [2] 1-based count of segments with units; 0: none so far
     static constexpr int32_t kNone = 0x7fffffff;
 };
@@ -237,7 +239,10 @@ __device__ __forceinline__ void tc_guard(const PrefillArgs &a, uint8_t *smem, co
         if (sg.jend <= cur.j0) continue;
         ++segs;
         for (int32_t j = max(cur.j0, guard_from(sg)); j < sg.jend; ++j, ++units) {
-            tc_wait(bar.v_go, units & 1, abort, a.err);  // the issuer has seen V arrive
+            // The issuer has seen V arrive.  This wait and the softmax's for S
+            // may last while the other roles work through most of the CTA's
+            // range, so their limit grows with the range.
+            tc_wait(bar.v_go, units & 1, abort, a.err, a.wait_ns);
             const uint32_t vbase = ring + ((n + 2 * (uint32_t)(j - cur.j0)) % L::kStages) * L::kTile;
             const int32_t pos0 = j * kTcKeys;
             const int nk = min(kTcKeys, sg.keys - pos0), nk16 = (nk + 15) & ~15;
@@ -435,7 +440,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
         if (sg.jend > cur.j0) ++segs;
         float m = -INFINITY, l = 0.f;
         for (int32_t j = cur.j0; j < je; ++j) {
-            tc_wait(s_full, ns & 1, abort, a.err);
+            tc_wait(s_full, ns & 1, abort, a.err, a.wait_ns);
             ++ns;
             tc_fence_after();
             if (warp_rows) {

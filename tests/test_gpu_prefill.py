@@ -409,3 +409,16 @@ def test_odd_values_in_chunk_after_chunk(H, Hk, D, block, dtype, kernel):
             check_odd(c, refs, out, P_EPS[BF] if kernel == "mma" else 0.0)
             for _ in range(3):
                 assert torch.equal(run(c, kernel=kernel, num_splits=splits).view(torch.uint8), out.view(torch.uint8))
+
+
+def test_roles_that_idle_for_longer_than_a_wait_may_last():
+    """One CTA for 3 * 2^20 units (about 3 s) of sequences with a single new token, which the
+    second row tile sits out, then a chunk of 200 that it takes part in."""
+    block, n, seqs = 4096, 256, 384
+    k, v = torch.zeros(1, block, 1, 64, dtype=BF, device="cuda"), torch.ones(1, block, 1, 64, dtype=BF, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    lens, cu = [block * n] * seqs + [200], list(range(seqs + 1)) + [seqs + 200]
+    out = pa.pa_prefill(torch.ones(seqs + 200, 1, 64, dtype=BF, device="cuda"), k, v, torch.zeros(seqs + 1, n, **i32),
+                        torch.tensor(lens, **i32), torch.tensor(cu, **i32), 1.0, kernel="mma", num_splits=1)
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
+    assert bool((out == 1).all())  # every score is 0, every sum a whole number below 2^24
