@@ -557,3 +557,46 @@ def test_decode_at_the_longest_reach():
     # every score is 0: the sums of a CTA are whole numbers below 2^24 times a
     # power of two, the merge rounds once for each of at most 2^10 pieces
     assert float((out.double() - 1).abs().max()) <= 2.0 ** -8 + 2.0 ** -13
+
+
+@pytest.mark.parametrize("H,Hk,D,block", DECODE)
+def test_decode_on_the_cuda_cores(H, Hk, D, block):
+    """fp32 probabilities: no allowance for their rounding."""
+    b = Batch([1, 0, 15, 16, 17, 31, 33, 64, 65, 700, 129], H, Hk, D, block, seed=H + D + block)
+    out = pa.pa_decode_fp8(**b.dev, kernel="simt")
+    for i, L in enumerate(b.lens):
+        at = slots_of(b.tables[i], L, block)
+        ref, amount, dots, top = attention(b.q[i:i + 1].cuda(), b.vals[0][at].cuda(), b.vals[1][at].cuda(), L - 1, b.scale)
+        tol = tolerance(BF, ref, amount, dots, top, L, D, 0.0)
+        assert float(((out[i:i + 1].double() - ref).abs() / tol).max()) <= 1.0, (i, L)
+
+
+@pytest.mark.parametrize("H,Hk,D,block", DECODE)
+def test_which_kernel_a_decode_takes(H, Hk, D, block):
+    b = Batch([300, 17, 1], H, Hk, D, block, seed=102)
+    out = pa.pa_decode_fp8(**b.dev)
+    step = math.gcd(block, 128 // max(n for n in (1, 2, 4, 8) if Hk % n == 0))
+    if D <= 128 and block % 8 == 0 and step * Hk % 16 == 0:
+        assert torch.equal(out, pa.pa_decode_fp8(**b.dev, kernel="mma"))
+    else:
+        assert torch.equal(out, pa.pa_decode_fp8(**b.dev, kernel="simt"))
+        with pytest.raises(pa.PagedAttentionError):
+            pa.pa_decode_fp8(**b.dev, kernel="mma")
+
+
+@pytest.mark.parametrize("D,block", [(64, 16), (128, 16), (256, 4)])
+def test_fp32_chunk_attention_over_rows_read_back(D, block):
+    """A chunk over a pool of rows read back in fp32: nothing is rounded to fewer bits on the way."""
+    b = Batch([303], 8, 2, D, block, seed=103)
+    rows_of = slots_of(b.tables[0], 303, block)
+    n = -(-303 // block)
+    slots = torch.cat([rows_of, torch.full((n * block - 303,), -1)]).to(torch.int32).cuda()
+    k8, v8 = pa.pa_gather_cache_fp8(b.dev["k_cache"], b.dev["v_cache"], b.dev["k_scale"], b.dev["v_scale"], slots, dtype=F32)
+    q = torch.randn(64, 8, D, generator=torch.Generator().manual_seed(104)).cuda()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = pa.pa_prefill(q, k8.view(n, block, 2, D), v8.view(n, block, 2, D), torch.arange(n, **i32)[None].contiguous(),
+                        torch.tensor([303], **i32), torch.tensor([0, 64], **i32), b.scale)
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
+    ref, amount, dots, top = attention(q, b.vals[0][rows_of].cuda(), b.vals[1][rows_of].cuda(), 303 - 64, b.scale)
+    tol = tolerance(F32, ref, amount, dots, top, 303, D, 0.0)
+    assert float(((out.double() - ref).abs() / tol).max()) <= 1.0

@@ -422,3 +422,47 @@ def test_roles_that_idle_for_longer_than_a_wait_may_last():
                         torch.tensor(lens, **i32), torch.tensor(cu, **i32), 1.0, kernel="mma", num_splits=1)
     assert pa.pa_get_device_error(raise_on_error=False) == 0
     assert bool((out == 1).all())  # every score is 0, every sum a whole number below 2^24
+
+
+@pytest.mark.parametrize("H,Hk,D,block,dtype", SHAPES)
+def test_ragged_chunks_on_the_cuda_cores(H, Hk, D, block, dtype):
+    """fp32 probabilities: no allowance for their rounding."""
+    c = Chunk(*RAGGED, H, Hk, D, block, dtype, seed=H * 1000 + D + block)
+    c.check(run(c, kernel="simt"), 0.0)
+
+
+@pytest.mark.parametrize("dtype,D,block", [(F32, 64, 4), (F32, 128, 16), (BF, 128, 16), (BF, 64, 32)])
+def test_split_layout_on_the_cuda_cores(dtype, D, block):
+    c = Chunk(*RAGGED, 8, 2, D, block, dtype, seed=11, layout="split")
+    c.check(run(c), 0.0)
+
+
+def on_tensor_cores(D, block, dtype):
+    return dtype == BF and D in (64, 128) and block % 8 == 0
+
+
+@pytest.mark.parametrize("H,Hk,D,block,dtype", SHAPES)
+def test_which_kernel_a_call_takes(H, Hk, D, block, dtype):
+    """auto is the tensor-core kernel, bit for bit, where that takes the call, and the CUDA cores' where not."""
+    c = Chunk(*RAGGED, H, Hk, D, block, dtype, seed=101)
+    out = run(c)
+    if on_tensor_cores(D, block, dtype):
+        assert torch.equal(out, run(c, kernel="mma")) and not torch.equal(out, run(c, kernel="simt"))
+    else:
+        assert torch.equal(out, run(c, kernel="simt"))
+        with pytest.raises(pa.PagedAttentionError):
+            run(c, kernel="mma")
+
+
+@pytest.mark.parametrize("splits", [1, 2, 3, 7, 40, 1000])
+def test_any_split_count_by_kernel(splits):
+    c = Chunk([3, 200, 1, 70], [3000, 200, 700, 1025], 8, 2, 128, 16, BF, seed=5)
+    c.check(run(c, kernel="mma", num_splits=splits), P_EPS[BF])
+    c.check(run(c, kernel="simt", num_splits=splits), 0.0)
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257])
+def test_lengths_around_tile_edges_by_kernel(n):
+    c = Chunk([n, 1, n, min(n, 3)], [n, n, n + 128, n + 1], 8, 2, 128, 16, BF, seed=n)
+    c.check(run(c, kernel="mma"), P_EPS[BF])
+    c.check(run(c, kernel="simt"), 0.0)
