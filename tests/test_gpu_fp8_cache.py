@@ -600,3 +600,12 @@ def test_fp32_chunk_attention_over_rows_read_back(D, block):
     ref, amount, dots, top = attention(q, b.vals[0][rows_of].cuda(), b.vals[1][rows_of].cuda(), 303 - 64, b.scale)
     tol = tolerance(F32, ref, amount, dots, top, 303, D, 0.0)
     assert float(((out.double() - ref).abs() / tol).max()) <= 1.0
+
+
+@pytest.mark.parametrize("kernel", ["mma", "simt"])
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 2.0 ** -40, 8.0])
+def test_decode_scales_of_every_sign_and_size(kernel, scale):
+    b = Batch([700, 1, 40], 32, 8, 128, 16, seed=105)
+    b.scale = b.dev["scale"] = scale
+    b.check(pa.pa_decode_fp8(**b.dev, kernel=kernel))
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
