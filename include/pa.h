@@ -14,7 +14,10 @@
  *   side", comment on k_cache).  Token slot s of the pool is block s / B,
  *   offset s % B.  PA_LAYOUT_SPLIT is the vLLM layout (see pa_layout_t).
  * - Element types: PA_F32 (IEEE fp32) or PA_BF16 (bfloat16).  q, k, v, out
- *   and both caches share the cache's element type.  Arithmetic is fp32.
+ *   and both caches share the cache's element type.  Scores, softmax
+ *   statistics and sums are fp32.  The tensor-core kernels round the
+ *   probabilities to the type that they multiply (bf16; fp16 over the 8-bit
+ *   cache); the CUDA-core ones (PA_KERNEL_SIMT) keep them in fp32.
  *   PA_FP8_E4M3 is the element type of an 8-bit cache (the calls named _fp8
  *   only; see "8-bit cache").
  * - Pointers named "device" must be CUDA device memory (or managed memory)
@@ -365,6 +368,9 @@ int32_t pa_split_owner(int64_t total_blocks, int32_t num_splits, int64_t x);
  * K and V at positions past L_i are never used, whatever they hold; a K or V
  * that is not finite at a position that a row does not see does not reach
  * that row.
+ * Rounding: the tensor-core kernel multiplies V by probabilities rounded to
+ * bf16 (2^-8 of each one's share of the output at most); PA_KERNEL_SIMT keeps
+ * them in fp32, so that only the output is rounded.
  * Requirements: H % Hk == 0, H / Hk <= 64, D in {64, 128, 256}, fp32 or bf16,
  *               either layout; q and out aligned to 2 elements, the caches to
  *               16 bytes.  The tensor-core kernel (tcgen05) takes bf16, D 64 or

@@ -346,9 +346,15 @@ cudaError_t launch_read(T *k, T *v, const int32_t *slots, int32_t T_, const uint
     }
     uint32_t total = (uint32_t)((int64_t)T_ * Hk * vecs);
     void *args[] = {&k, &v, &slots, &total, &Hk, &vecs, &kc, &vc, &ks, &vs, &ns, &err};
-    // fp32 rows, four bytes out for one in, ran faster one pass per thread (159
-    // against 173 us for 100003 x 8 x 128), bf16 rows on one wave (98 against
-    // 104 us)
+    // fp32 rows, four bytes out for one in, run faster one pass per thread, bf16
+    // rows on one wave, at every size measured (us; one pass, one wave):
+    //   tokens x heads x D    fp32           bf16
+    //     5000 x 8 x 128       10.9   11.8     8.6    8.8
+    //    20000 x 8 x 128       33.7   36.6    22.5   21.7
+    //   131072 x 8 x 128      213.1  221.4   135.7  125.0
+    //   131072 x 8 x 64       106.1  111.0    69.7   63.3
+    //   131072 x 1 x 128       29.3   31.2    20.8   18.7
+    //    60000 x 8 x 256      191.7  205.1   122.4  118.5
     const int64_t ctas = ((int64_t)total + 256 * kReadRows - 1) / (256 * kReadRows);
     const int grid = sizeof(T) == 4 ? (int)ctas : grid_for(ctas, kReadCtas);
     return launch_pdl((const void *)read_fp8_kernel<T>, dim3(grid), dim3(256), args, 0, s);

@@ -21,8 +21,9 @@
 // It is the only rounding beside fp32's and the output's.
 //
 // Bound by the K and V bytes: 16 sequences of 32768 tokens (64 / 8 heads, head_dim
-// 128) take 168 us (6.4 TB/s) with the work list and the merge; head_dim 64
-// reaches 4.2 TB/s.  A CTA is 8 consumer warps and a TMA producer,
+// 128) take 169 to 174 us (6.2 to 6.4 TB/s) with the work list and the merge. The
+// same bytes with 4 / 2 / 1 KV heads 174 / 181 / 221 us; head_dim 64 reaches 4.2 to
+// 4.7 TB/s with 8 KV heads and 2.7 with one.  A CTA is 8 consumer warps and a TMA producer,
 // two CTAs per SM; a stage is 8 slices of 16 tokens of one KV head (K and V,
 // 32 KiB at head_dim 128): NH heads (the largest of 8, 4, 2, 1 that divides Hk)
 // x 128 / NH tokens, so that a stage is one contiguous piece of every block it

@@ -14,14 +14,23 @@
 // into P, the other's O += P V and next S run.  Tensor memory holds S (128
 // columns) and O (D columns) of both, 512 columns at head_dim 128.
 //
+// P is bf16 because kind::f16 takes both operands of one type and V is bf16: an
+// error of at most 2^-8 of each key's share (measured over whole outputs
+// 0.0020 to 0.0024 against 64 bits, 0.0015 to 0.0017 of it the output's own rounding).
+// fp16 would round finer but needs V converted, and its range; fp32 P is the
+// CUDA-core kernel's.  The maximum, the sum and O are fp32, and the sum is of the
+// probabilities before they are rounded.
+//
 // The MMAs take 4 * 128 * 128 * D FLOPs of tensor time per unit and row tile,
 // the softmax 128 exponentials per row; both pipes are close to busy at
 // head_dim 128, so long prompts are bound by them, and chunks of few rows over
-// long contexts by the K and V bytes.  Measured (32 / 8 heads, head_dim 128, the
-// whole call): a prompt of 8192 tokens 358 to 361 us (1520 to 1536 TFLOP/s), 2048
-// tokens behind 30720 642 to 681 us (1564 to 1640), 5 tokens of 64 sequences over
-// 4096 178 us (6.0 TB/s).  The extra weight of a tile, 1 / 2 / 3 / 4 units:
-// 412 / 380 / 361 / 365 us on that prompt, no difference on long contexts.
+// long contexts by the K and V bytes.  Measured, whole calls repeated on one set
+// of inputs (32 / 8 heads, head_dim 128; boxes and clocks differ): a prompt of 8192
+// tokens 356 to 363 us (1515 to 1546 TFLOP/s), 2048 tokens behind 30720 624 to 678
+// us (1571 to 1706), 5 tokens of 64 sequences over 4096 176 to 181 us (5.9 to 6.1
+// TB/s).  With three sets of inputs in turn that prompt takes 387 to 389 us (1413
+// to 1419).  The extra weight of a tile, 1 / 2 / 3 / 4 units: 412 / 380 / 361 /
+// 365 us on that prompt, no difference on long contexts.
 #pragma once
 
 #include <cuda.h>  // CUtensorMap

@@ -117,10 +117,9 @@ __host__ __device__ constexpr uint32_t tc_idesc_bf16(int M, int N, bool a_mn_maj
 
 // The same with A and B from shared memory (ss) or A from tensor memory (ts:
 // lane = row, two bf16 of consecutive k per column), issued under a predicate
-// rather than a branch: the warp stays converged, so descriptors and
-// addresses can live in uniform registers.  Behind a branch on the lane each
-// MMA cost its own moves into uniform registers (78 to 115 cycles per issue
-// against the 64 that a 128 x 128 x 16 product takes).
+// rather than a branch, so that the warp stays converged.  Measured in the
+// attention loop: 78 to 115 cycles per issue behind a branch on the lane,
+// against the 64 that a 128 x 128 x 16 product takes.
 __device__ __forceinline__ void tc_mma_bf16_ss_if(uint32_t issue, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                                   uint32_t idesc, uint32_t accumulate) {
     asm volatile(
