@@ -113,3 +113,58 @@ def test_prompt_in_chunks_then_samples():
                         i32([L]), i32([0, 64]), SCALE)
     check(out, q[:64], k8[:L], v8[:L], L - 64, 2.0 ** -8)
     assert pa.pa_get_device_error(raise_on_error=False) == 0
+
+
+FIRST_CALLS = """
+import sys
+import torch
+import paged_kv_cache_150_gb300 as pa
+
+g = torch.Generator(device="cuda").manual_seed(9)
+bf = torch.bfloat16
+i32 = dict(dtype=torch.int32, device="cuda")
+nb, b, hk, d, h = 12, 16, 8, 128, 32
+kc, vc = (torch.randn(nb, b, hk, d, generator=g, device="cuda").to(bf) for _ in range(2))
+q, one = torch.randn(40, h, d, generator=g, device="cuda").to(bf), torch.randn(2, h, d, generator=g, device="cuda").to(bf)
+codes = [torch.zeros(nb, b, hk, d, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2)]
+scales = [torch.full((nb, b, hk), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
+back = [torch.empty(nb * b, hk, d, dtype=bf, device="cuda") for _ in range(2)]
+slots, pairs = torch.arange(nb * b, **i32), torch.tensor([[2, 10], [3, 11]], **i32)
+tables = torch.tensor([[4, 1, 0, 5], [11, 10, 9, 2]], **i32)
+lens, cu = torch.tensor([60, 33], **i32), torch.tensor([0, 30, 40], **i32)
+out, out32, out8 = torch.empty_like(q), torch.empty_like(q), torch.empty_like(one)
+
+
+def step():
+    pa.pa_reshape_and_cache_fp8(kc.view(-1, hk, d), vc.view(-1, hk, d), slots, *codes, *scales)
+    pa.pa_copy_blocks_fp8(*codes, *scales, pairs)
+    pa.pa_decode_fp8(one, *codes, *scales, tables, lens, 0.1, out=out8)
+    pa.pa_gather_cache_fp8(*codes, *scales, slots, k=back[0], v=back[1])
+    pa.pa_prefill(q, kc, vc, tables, lens, cu, 0.1, out=out)
+    pa.pa_prefill(q, kc, vc, tables, lens, cu, 0.1, out=out32, kernel="simt")
+
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+graph.replay()
+torch.cuda.synchronize()
+got = [x.clone() for x in (out, out32, out8, *back, *scales)]
+for x in (out, out32, out8, *back):
+    x.zero_()
+step()
+assert pa.pa_get_device_error(raise_on_error=False) == 0
+for x, y in zip(got, (out, out32, out8, *back, *scales)):
+    assert torch.equal(x, y) and torch.count_nonzero(x)
+print("captured first")
+"""
+
+
+def test_the_first_calls_of_a_process_can_be_captured():
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "captured first" in done.stdout, done.stderr[-2000:]
