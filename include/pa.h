@@ -18,8 +18,8 @@
  *   statistics and sums are fp32.  The tensor-core kernels round the
  *   probabilities to the type that they multiply (bf16; fp16 over the 8-bit
  *   cache); the CUDA-core ones (PA_KERNEL_SIMT) keep them in fp32.
- *   PA_FP8_E4M3 is the element type of an 8-bit cache (the calls named _fp8
- *   only; see "8-bit cache").
+ *   PA_FP8_E4M3 and PA_FP8_E4M3_BLOCK are the element types of an 8-bit cache
+ *   (the calls named _fp8 only; see "8-bit cache").
  * - Pointers named "device" must be CUDA device memory (or managed memory)
  *   of the current device; "host" pointers are ordinary host memory.  The
  *   caller owns every buffer.  The library never allocates device memory and
@@ -53,7 +53,7 @@ typedef enum pa_status {
     PA_ERR_INVALID_ARG = -1,    /* null pointer, bad shape or size */
     PA_ERR_UNSUPPORTED = -2,    /* valid request with no compiled kernel variant */
     PA_ERR_CUDA = -3,           /* a CUDA runtime/driver call failed */
-    PA_ERR_NO_BLOCKS = -4,      /* block manager: the free list cannot satisfy the request */
+    PA_ERR_NO_BLOCKS = -4,      /* block manager, pa_extend_tables: the free list cannot satisfy the request */
     PA_ERR_DEVICE_BOUNDS = -5,  /* a kernel met an index outside the pool or the table */
     PA_ERR_DEVICE_TIMEOUT = -6, /* a kernel's bounded wait on an mbarrier ran out */
     PA_ERR_WORKSPACE = -7,      /* the decode workspace is smaller than required */
@@ -61,7 +61,7 @@ typedef enum pa_status {
     PA_ERR_HOST_MEMORY = -9     /* a host allocation failed (no C++ exception ever leaves a call) */
 } pa_status_t;
 
-typedef enum pa_dtype { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2 } pa_dtype_t;
+typedef enum pa_dtype { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2, PA_FP8_E4M3_BLOCK = 3 } pa_dtype_t;
 
 /* Cache layouts.  Both keep each physical block contiguous (B * Hk * D
  * elements per tensor), so block copies and the block-table walk are the same.
@@ -392,6 +392,26 @@ pa_status_t pa_prefill(void *out, const void *q, const void *k_cache, const void
                        const pa_prefill_opts_t *opts, pa_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * pa_cross - attention to an encoder's states in the paged cache.
+ *
+ * Sequence i has n_i = cu_q_lens[i + 1] - cu_q_lens[i] decoder tokens, the rows
+ * cu_q_lens[i] .. of q and out, and kv_lens[i] encoder positions, a length of
+ * its own, whose K and V are in the cache.  Every token sees all of them:
+ *     out[cu_q_lens[i] + r, h, :] = sum_j softmax_j(scale * q . K_j) V_j, j < kv_lens[i],
+ * with K_j, V_j as in pa_decode.  kv_lens[i] = 0 gives zeros, n_i = 0 nothing.
+ * One token per sequence is pa_decode over kv_lens, which is faster there.
+ *
+ * Arguments, work split, rounding, kernels and requirements are those of
+ * pa_prefill, kv_lens in place of seq_lens; a K or V that is not finite at a
+ * position past kv_lens[i] does not reach the output, one before it does.
+ * pa_prefill_workspace_bytes gives the workspace.
+ * ---------------------------------------------------------------------- */
+pa_status_t pa_cross(void *out, const void *q, const void *k_cache, const void *v_cache, const pa_cache_desc_t *cache,
+                     const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *kv_lens,
+                     const int32_t *cu_q_lens, int32_t num_seqs, int32_t num_tokens, int32_t num_heads, float scale,
+                     void *workspace, size_t workspace_bytes, const pa_prefill_opts_t *opts, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * 8-bit cache (PA_FP8_E4M3, PA_LAYOUT_ROW): e4m3 codes [NB, B, Hk, D] for K and
  * for V, and one scale byte per token and KV head in k_scale, v_scale
  * [NB, B, Hk].  Byte b stands for 2^(b - 127) (E8M0; 255, which no write
@@ -448,9 +468,125 @@ pa_status_t pa_decode_fp8(void *out, const void *q, const void *k_cache, const v
                           pa_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * 8-bit cache with block scales (PA_FP8_E4M3_BLOCK, PA_LAYOUT_ROW): e4m3 codes
+ * [NB, B, Hk, D] as above, and one scale byte per block and KV head in k_scale,
+ * v_scale [NB, Hk]; an element's value is code * 2^(b - 127) with the byte b of
+ * its block and head.
+ *
+ * pa_write_blocks_fp8  writes the new tokens of a batch.  Sequence i has n_i =
+ *     cu_q_lens[i + 1] - cu_q_lens[i] of them, the rows cu_q_lens[i] .. of k and
+ *     v [num_tokens, Hk, D] (type dtype, PA_F32 or PA_BF16), at its positions
+ *     seq_lens[i] - n_i .. seq_lens[i] - 1, as in pa_prefill.  For every block
+ *     that receives a token, and every KV head, e is the smallest integer in
+ *     [-126, 120] with |x| <= 448 * 2^e for every finite x of the call's rows in
+ *     that block; where the block holds earlier positions of the sequence, e
+ *     is at least the e of its byte.  The byte becomes e + 127, a code is x *
+ *     2^-e rounded to the nearest e4m3 (ties to even, infinities to +-448, NaN
+ *     stays NaN).  If e grows, the codes of the block's earlier positions are
+ *     rounded anew (code * 2^(old e - e), nearest e4m3): exact unless they fall
+ *     under the smallest normal e4m3.  Bytes above 247, which no write makes,
+ *     count as 247 here and are left as they are.
+ *     A block that a call writes belongs to one sequence of the call (copy shared
+ *     ones first).  Positions behind the last new one are left as they were.
+ *     Recorded as PA_ERR_DEVICE_BOUNDS: row offsets that pa_prefill would
+ *     refuse (nothing is written), a length outside [n_i, the table's reach]
+ *     (the sequence is skipped), an entry outside the pool (the block is
+ *     skipped).  k and v need their element's alignment only, and D is any
+ *     number >= 1.
+ * pa_prefill_fp8  pa_prefill over this cache: q and out are bf16 [num_tokens, H,
+ *     D], K_j and V_j the values.  The tensor-core kernel (tcgen05; D 64 or 128,
+ *     block sizes that are multiples of 8, scale > 0 and finite, 16-byte aligned
+ *     q and out) turns codes into bf16, which holds every value with a byte in
+ *     [14, 240] exactly (smaller and larger ones round, underflow or overflow as
+ *     bf16 does), and works as pa_prefill's; CUDA cores take the rest in fp32.
+ *     Requirements as pa_prefill, and the caches aligned to 16 bytes.
+ * pa_decode_fp8, pa_gather_cache_fp8 and pa_copy_blocks_fp8 take this cache as
+ *     they take the other 8-bit one; pa_decode_fp8's tensor-core kernel needs no
+ *     alignment of the scale bytes here.  pa_reshape_and_cache_fp8 does not
+ *     (PA_ERR_UNSUPPORTED): single slots do not say what else a block holds.
+ * ---------------------------------------------------------------------- */
+pa_status_t pa_write_blocks_fp8(const void *k, const void *v, int32_t dtype, const int32_t *block_tables,
+                                int32_t max_blocks_per_seq, const int32_t *seq_lens, const int32_t *cu_q_lens,
+                                int32_t num_seqs, int32_t num_tokens, void *k_cache, void *v_cache, uint8_t *k_scale,
+                                uint8_t *v_scale, const pa_cache_desc_t *cache, pa_stream_t stream);
+
+size_t pa_prefill_fp8_workspace_bytes(const pa_cache_desc_t *cache, int32_t num_seqs, int32_t num_tokens,
+                                      int32_t num_heads, const pa_prefill_opts_t *opts);
+
+pa_status_t pa_prefill_fp8(void *out, const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+                           const uint8_t *v_scale, const pa_cache_desc_t *cache, const int32_t *block_tables,
+                           int32_t max_blocks_per_seq, const int32_t *seq_lens, const int32_t *cu_q_lens,
+                           int32_t num_seqs, int32_t num_tokens, int32_t num_heads, float scale, void *workspace,
+                           size_t workspace_bytes, const pa_prefill_opts_t *opts, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Tables on the GPU: the bookkeeping of a step (blocks, block tables, lengths,
+ * row offsets, slots) from the requests' lengths, without the host, so that a
+ * step can be captured into a graph.  For sequences that share no blocks: forks,
+ * copy-on-write and prefix caching are the host block manager's.  The same calls
+ * in the same order give the tables and slots that the host block manager gives
+ * for the same free stack.
+ *
+ * pa_tables_t names the state, all of it device memory of the caller:
+ *   tables [num_rows, max_blocks_per_row]  block table of each row (a request
+ *          lives in a row); entries past a row's blocks are never read.
+ *   lens [num_rows]  tokens held by each row; a row holds ceil(lens / B) blocks.
+ *   free_list [num_blocks], free_count [1]  the stack of free blocks, bottom
+ *          first: entries [0, free_count), the last is taken first.
+ * lens_out and free_count_out receive the lengths of all rows and the count
+ * after the call; NULL: in place.  With buffers of their own the state before
+ * the call stays (extend leaves the stack's entries and the tables' used ones
+ * as they are), so that a step can be made again, or given up.
+ * rows [num_reqs]: the row of each request, all distinct; NULL: request i is
+ * row i.  num_reqs <= num_rows.
+ *
+ * pa_extend_tables  request i gets new_lens[i] >= 0 more tokens, and the blocks
+ *     that they need off the stack, request by request.  Receives for the batch:
+ *       batch_tables [num_reqs, batch_width]  (optional) the requests' tables,
+ *              -1 behind a request's blocks: pa_decode's block_tables;
+ *       seq_lens [num_reqs]  lengths, the new tokens included;
+ *       cu_q_lens [num_reqs + 1]  row offsets of the new tokens;
+ *       slot_mapping [max_tokens]  slot of every new token, -1 in the rows behind
+ *              the last one.
+ *     All or nothing: a call that asks for more blocks than are free records
+ *     PA_ERR_NO_BLOCKS; one with a row outside the tables or named twice, a
+ *     length below 0 or past its row, more than max_tokens tokens, more blocks
+ *     than batch_width or a count outside [0, num_blocks] records
+ *     PA_ERR_DEVICE_BOUNDS.  Such a call changes no state and receives no new
+ *     token: lengths as before (0 where there is none), cu_q_lens all 0, slots
+ *     all -1.  A block id outside the pool gives slots of -1 and is recorded.
+ * pa_release_tables  the requests' blocks go onto the stack, request by request,
+ *     each from its first block to its last, and their lengths become 0.  The
+ *     same refusals (also more blocks than the pool has); ids are not checked
+ *     before they are pushed, one outside the pool is recorded.
+ * workspace  device scratch of pa_tables_workspace_bytes(num_reqs, num_rows)
+ *     bytes, 256-byte aligned; calls that share it must be ordered on one stream.
+ * Two kernels per call (release without a request: one).
+ * ---------------------------------------------------------------------- */
+typedef struct pa_tables {
+    int32_t *tables;
+    int32_t *lens, *lens_out;
+    int32_t *free_list;
+    int32_t *free_count, *free_count_out;
+    int32_t num_rows, max_blocks_per_row;
+    int32_t num_blocks, block_size;
+} pa_tables_t;
+
+size_t pa_tables_workspace_bytes(int32_t num_reqs, int32_t num_rows);
+
+pa_status_t pa_extend_tables(const pa_tables_t *state, const int32_t *rows, const int32_t *new_lens, int32_t num_reqs,
+                             int32_t *batch_tables, int32_t batch_width, int32_t *seq_lens, int32_t *cu_q_lens,
+                             int32_t *slot_mapping, int32_t max_tokens, void *workspace, size_t workspace_bytes,
+                             pa_stream_t stream);
+
+pa_status_t pa_release_tables(const pa_tables_t *state, const int32_t *rows, int32_t num_reqs, void *workspace,
+                              size_t workspace_bytes, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * pa_get_device_error - synchronise `stream`, then read and clear the error
  * word of the current device.  Returns PA_OK, PA_ERR_DEVICE_BOUNDS,
- * PA_ERR_DEVICE_TIMEOUT or PA_ERR_CUDA.
+ * PA_ERR_DEVICE_TIMEOUT, PA_ERR_DEVICE_PLAN, PA_ERR_NO_BLOCKS
+ * (pa_extend_tables) or PA_ERR_CUDA.
  * ---------------------------------------------------------------------- */
 pa_status_t pa_get_device_error(pa_stream_t stream);
 

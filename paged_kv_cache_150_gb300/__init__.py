@@ -13,7 +13,13 @@ Calls (same names as the C ABI):
   pa_prefill(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, scale, ...)
   pa_reshape_and_cache_fp8, pa_gather_cache_fp8, pa_copy_blocks_fp8,
   pa_decode_fp8: the same over an 8-bit cache (float8_e4m3fn codes and one
-  power-of-two scale byte per token and KV head)
+  power-of-two scale byte per token and KV head, or per block and KV head:
+  scale arrays [num_blocks, block_size, Hk] or [num_blocks, Hk])
+  pa_write_blocks_fp8, pa_prefill_fp8: write and chunk attention of the cache
+  with block scales
+  pa_cross(q, k_cache, v_cache, block_tables, kv_lens, cu_q_lens, scale, ...)
+  pa_extend_tables, pa_release_tables: block tables, lengths and slots of a step
+  built on the GPU
   pa_get_device_error()
   BlockManager: the host block manager (free list, refcounts, fork,
   copy-on-write, slot mapping).
@@ -323,24 +329,18 @@ def pa_prefill_workspace_bytes(k_cache, num_tokens, num_seqs, num_heads, num_spl
     return int(n)
 
 
-def pa_prefill(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, scale, out=None, workspace=None,
-               num_splits=0, kernel="auto"):
-    """Attention of a chunk of new tokens over the paged cache; returns ``out``
-    [T, H, D].
-
-    Rows cu_q_lens[i] .. cu_q_lens[i + 1] - 1 of ``q`` are the new tokens of
-    sequence i, the last ones of its seq_lens[i] positions; their K and V are
-    in the cache already.  Each sees the positions up to its own.  Rows that
-    belong to no sequence are left as they were (in a fresh ``out``:
-    unspecified)."""
+def _chunk_call(name, sizes, desc, q, k_cache, v_cache, scales, block_tables, lens, lens_name, cu_q_lens, scale, out,
+                workspace, num_splits, kernel):
+    """A chunk-attention call of the library (the same arguments for all of them,
+    but for an 8-bit cache's scales); ``sizes``: its workspace query."""
     torch = _torch()
-    desc = _memo_desc(k_cache, v_cache)
     T, H, D = q.shape
-    N = seq_lens.shape[0]
-    if D != desc.head_dim or q.dtype != k_cache.dtype:
-        raise ValueError("q must be [num_tokens, num_heads, head_dim] in the cache's element type")
-    if block_tables.dim() != 2 or block_tables.shape[0] != N or seq_lens.dim() != 1:
-        raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
+    N = lens.shape[0]
+    if D != desc.head_dim or q.dtype != (torch.bfloat16 if scales else k_cache.dtype):
+        raise ValueError("q must be [num_tokens, num_heads, head_dim] in %s"
+                         % ("bfloat16" if scales else "the cache's element type"))
+    if block_tables.dim() != 2 or block_tables.shape[0] != N or lens.dim() != 1:
+        raise ValueError("block_tables must be [num_seqs, max_blocks] and %s [num_seqs]" % lens_name)
     if cu_q_lens.shape != (N + 1,):
         raise ValueError("cu_q_lens must be [num_seqs + 1]")
     if out is None:
@@ -352,22 +352,56 @@ def pa_prefill(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, scale, ou
     dp = ctypes.byref(desc)
     lib = _lib.load()
     if workspace is None:
-        need = lib.pa_prefill_workspace_bytes(dp, N, T, H, o)
+        need = getattr(lib, sizes)(dp, N, T, H, o)
         if need == 0:
-            raise PagedAttentionError("pa_prefill_workspace_bytes", _lib.PA_ERR_UNSUPPORTED)
+            raise PagedAttentionError(sizes, _lib.PA_ERR_UNSUPPORTED)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     i32 = torch.int32
-    st = lib.pa_prefill(_ptr(out, "out", d), _ptr(q, "q", d), _ptr(k_cache, "k_cache", d), _ptr(v_cache, "v_cache", d),
-                        dp, _ptr(block_tables, "block_tables", d, i32), block_tables.shape[1],
-                        _ptr(seq_lens, "seq_lens", d, i32), _ptr(cu_q_lens, "cu_q_lens", d, i32), N, T, H, float(scale),
-                        _ptr(workspace, "workspace", d), workspace.nbytes, o, stream)
-    _lib.check("pa_prefill", st)
+    st = getattr(lib, name)(_ptr(out, "out", d), _ptr(q, "q", d), _ptr(k_cache, "k_cache", d), _ptr(v_cache, "v_cache", d),
+                            *[_ptr(t, n, d) for n, t in zip(("k_scale", "v_scale"), scales)],
+                            dp, _ptr(block_tables, "block_tables", d, i32), block_tables.shape[1],
+                            _ptr(lens, lens_name, d, i32), _ptr(cu_q_lens, "cu_q_lens", d, i32), N, T, H, float(scale),
+                            _ptr(workspace, "workspace", d), workspace.nbytes, o, stream)
+    _lib.check(name, st)
     return out
+
+
+def pa_prefill(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, scale, out=None, workspace=None,
+               num_splits=0, kernel="auto"):
+    """Attention of a chunk of new tokens over the paged cache; returns ``out``
+    [T, H, D].
+
+    Rows cu_q_lens[i] .. cu_q_lens[i + 1] - 1 of ``q`` are the new tokens of
+    sequence i, the last ones of its seq_lens[i] positions; their K and V are
+    in the cache already.  Each sees the positions up to its own.  Rows that
+    belong to no sequence are left as they were (in a fresh ``out``:
+    unspecified)."""
+    return _chunk_call("pa_prefill", "pa_prefill_workspace_bytes", _memo_desc(k_cache, v_cache), q, k_cache, v_cache, (),
+                       block_tables, seq_lens, "seq_lens", cu_q_lens, scale, out, workspace, num_splits, kernel)
+
+
+def pa_cross_workspace_bytes(k_cache, num_tokens, num_seqs, num_heads, num_splits=0, kernel="auto"):
+    """Workspace bytes of pa_cross for a batch of num_tokens decoder tokens."""
+    return pa_prefill_workspace_bytes(k_cache, num_tokens, num_seqs, num_heads, num_splits, kernel)
+
+
+def pa_cross(q, k_cache, v_cache, block_tables, kv_lens, cu_q_lens, scale, out=None, workspace=None, num_splits=0,
+             kernel="auto"):
+    """Attention of decoder tokens to an encoder's states in the paged cache;
+    returns ``out`` [T, H, D].
+
+    Rows cu_q_lens[i] .. cu_q_lens[i + 1] - 1 of ``q`` are sequence i's tokens;
+    each sees all kv_lens[i] positions of its block table (zeros where there are
+    none).  Rows that belong to no sequence are left as they were.  One token
+    per sequence is pa_decode over kv_lens."""
+    return _chunk_call("pa_cross", "pa_prefill_workspace_bytes", _memo_desc(k_cache, v_cache), q, k_cache, v_cache, (),
+                       block_tables, kv_lens, "kv_lens", cu_q_lens, scale, out, workspace, num_splits, kernel)
 
 
 def _cache_desc_fp8(k_cache, v_cache=None, k_scale=None, v_scale=None):
     """Descriptor of an 8-bit cache: codes float8_e4m3fn [NB, B, Hk, D], scale
-    bytes uint8 [NB, B, Hk]."""
+    bytes uint8 [NB, B, Hk] (one per token and KV head) or [NB, Hk] (one per
+    block and KV head)."""
     torch = _torch()
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         if t is None:
@@ -376,15 +410,16 @@ def _cache_desc_fp8(k_cache, v_cache=None, k_scale=None, v_scale=None):
             raise TypeError("%s must be float8_e4m3fn, got %s" % (name, t.dtype))
         if t.dim() != 4 or t.shape != k_cache.shape:
             raise ValueError("caches must be K, V [num_blocks, block_size, num_kv_heads, head_dim]")
+    nb, bs, hk, d = k_cache.shape
+    block = k_scale is not None and k_scale.dim() == 2
     for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
         if t is None:
             continue
         if t.dtype != torch.uint8:
             raise TypeError("%s must be uint8, got %s" % (name, t.dtype))
-        if t.shape != k_cache.shape[:3]:
-            raise ValueError("%s must be [num_blocks, block_size, num_kv_heads]" % name)
-    nb, bs, hk, d = k_cache.shape
-    return _lib.CacheDesc(nb, bs, hk, d, _lib.PA_FP8_E4M3, _lib.PA_LAYOUT_ROW)
+        if t.shape != ((nb, hk) if block else (nb, bs, hk)):
+            raise ValueError("%s must be [num_blocks, block_size, num_kv_heads], or both [num_blocks, num_kv_heads]" % name)
+    return _lib.CacheDesc(nb, bs, hk, d, _lib.PA_FP8_E4M3_BLOCK if block else _lib.PA_FP8_E4M3, _lib.PA_LAYOUT_ROW)
 
 
 def _rows_call(name, k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale):
@@ -410,8 +445,40 @@ def _rows_call(name, k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale):
 def pa_reshape_and_cache_fp8(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale):
     """Quantise new tokens' K/V rows (fp32 or bf16) into the 8-bit caches at
     their slots: e4m3 codes and one power-of-two scale byte (2^(b - 127)) per
-    token and KV head."""
+    token and KV head.  With block scales: pa_write_blocks_fp8."""
     _rows_call("pa_reshape_and_cache_fp8", k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale)
+
+
+def pa_write_blocks_fp8(k, v, block_tables, seq_lens, cu_q_lens, k_cache, v_cache, k_scale, v_scale):
+    """Quantise new tokens' K/V rows (fp32 or bf16) into 8-bit caches with block
+    scales (uint8 [num_blocks, num_kv_heads], 2^(b - 127)).
+
+    Rows cu_q_lens[i] .. cu_q_lens[i + 1] - 1 of ``k`` and ``v`` [num_tokens, Hk,
+    D] are the last of sequence i's seq_lens[i] positions, as in pa_prefill.  A
+    block takes the scale of its largest row; one that holds earlier positions
+    keeps its own unless the new rows need a larger one, and its codes are then
+    rounded anew.  A block that is written must belong to one sequence."""
+    torch = _torch()
+    desc = _memo_desc_fp8(k_cache, v_cache, k_scale, v_scale)
+    if desc.dtype != _lib.PA_FP8_E4M3_BLOCK:
+        raise ValueError("k_scale and v_scale must be [num_blocks, num_kv_heads]")
+    N = seq_lens.shape[0]
+    if k.shape != v.shape or k.shape[1:] != (desc.num_kv_heads, desc.head_dim):
+        raise ValueError("k, v must be [num_tokens, num_kv_heads, head_dim] matching the cache")
+    if k.dtype != v.dtype:
+        raise TypeError("k and v element types differ")
+    if block_tables.dim() != 2 or block_tables.shape[0] != N or seq_lens.dim() != 1:
+        raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
+    if cu_q_lens.shape != (N + 1,):
+        raise ValueError("cu_q_lens must be [num_seqs + 1]")
+    d, stream = _here()
+    i32 = torch.int32
+    st = _lib.load().pa_write_blocks_fp8(
+        _ptr(k, "k", d), _ptr(v, "v", d), _dtype_code(k), _ptr(block_tables, "block_tables", d, i32),
+        block_tables.shape[1], _ptr(seq_lens, "seq_lens", d, i32), _ptr(cu_q_lens, "cu_q_lens", d, i32), N, k.shape[0],
+        _ptr(k_cache, "k_cache", d), _ptr(v_cache, "v_cache", d), _ptr(k_scale, "k_scale", d),
+        _ptr(v_scale, "v_scale", d), ctypes.byref(desc), stream)
+    _lib.check("pa_write_blocks_fp8", st)
 
 
 def pa_gather_cache_fp8(k_cache, v_cache, k_scale, v_scale, slot_mapping, k=None, v=None, dtype=None):
@@ -445,9 +512,10 @@ def pa_copy_blocks_fp8(k_cache, v_cache, k_scale, v_scale, src_dst_pairs):
     _lib.check("pa_copy_blocks_fp8", st)
 
 
-def pa_decode_fp8_workspace_bytes(k_cache, num_seqs, num_heads, num_splits=0, kernel="auto"):
-    """Workspace bytes of pa_decode_fp8."""
-    desc = _cache_desc_fp8(k_cache)
+def pa_decode_fp8_workspace_bytes(k_cache, num_seqs, num_heads, num_splits=0, kernel="auto", k_scale=None):
+    """Workspace bytes of pa_decode_fp8; ``k_scale``: the scales of a cache with
+    block scales (may be left out for one with a scale per token)."""
+    desc = _cache_desc_fp8(k_cache, k_scale=k_scale)
     o = _prefill_opts(num_splits, kernel)
     n = _lib.load().pa_decode_fp8_workspace_bytes(ctypes.byref(desc), int(num_seqs), int(num_heads), ctypes.byref(o))
     if n == 0:
@@ -489,6 +557,122 @@ def pa_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
         workspace.nbytes, o, stream)
     _lib.check("pa_decode_fp8", st)
     return out
+
+
+def _desc_block(k_cache):
+    """Descriptor of an 8-bit cache with block scales, from its codes alone."""
+    desc = _cache_desc_fp8(k_cache)
+    desc.dtype = _lib.PA_FP8_E4M3_BLOCK
+    return desc
+
+
+def pa_prefill_fp8_workspace_bytes(k_cache, num_tokens, num_seqs, num_heads, num_splits=0, kernel="auto"):
+    """Workspace bytes of pa_prefill_fp8 for a batch of num_tokens new tokens."""
+    o = _prefill_opts(num_splits, kernel)
+    n = _lib.load().pa_prefill_fp8_workspace_bytes(ctypes.byref(_desc_block(k_cache)), int(num_seqs), int(num_tokens),
+                                                   int(num_heads), ctypes.byref(o))
+    if n == 0:
+        raise PagedAttentionError("pa_prefill_fp8_workspace_bytes", _lib.PA_ERR_UNSUPPORTED)
+    return int(n)
+
+
+def pa_prefill_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, cu_q_lens, scale, out=None,
+                   workspace=None, num_splits=0, kernel="auto"):
+    """pa_prefill over an 8-bit cache with block scales (uint8 [num_blocks, Hk]);
+    q and the returned ``out`` are bfloat16 [T, H, D]."""
+    return _chunk_call("pa_prefill_fp8", "pa_prefill_fp8_workspace_bytes", _memo_desc_fp8(k_cache, v_cache, k_scale, v_scale),
+                       q, k_cache, v_cache, (k_scale, v_scale), block_tables, seq_lens, "seq_lens", cu_q_lens, scale, out,
+                       workspace, num_splits, kernel)
+
+
+def pa_tables_workspace_bytes(num_reqs, num_rows):
+    """Workspace bytes of pa_extend_tables and pa_release_tables."""
+    n = _lib.load().pa_tables_workspace_bytes(int(num_reqs), int(num_rows))
+    if n == 0:
+        raise PagedAttentionError("pa_tables_workspace_bytes", _lib.PA_ERR_INVALID_ARG)
+    return int(n)
+
+
+def _tables_state(d, tables, lens, free_list, free_count, block_size, lens_out, free_count_out):
+    i32 = _torch().int32
+    if tables.dim() != 2:
+        raise ValueError("tables must be [num_rows, max_blocks_per_row]")
+    R, W = tables.shape
+    for name, t in (("lens", lens), ("lens_out", lens_out)):
+        if t is not None and t.shape != (R,):
+            raise ValueError("%s must be [num_rows]" % name)
+    if free_list.dim() != 1:
+        raise ValueError("free_list must be [num_blocks]")
+    for name, t in (("free_count", free_count), ("free_count_out", free_count_out)):
+        if t is not None and t.numel() != 1:
+            raise ValueError("%s must hold one number" % name)
+    return _lib.Tables(_ptr(tables, "tables", d, i32), _ptr(lens, "lens", d, i32),
+                       None if lens_out is None else _ptr(lens_out, "lens_out", d, i32),
+                       _ptr(free_list, "free_list", d, i32), _ptr(free_count, "free_count", d, i32),
+                       None if free_count_out is None else _ptr(free_count_out, "free_count_out", d, i32),
+                       R, W, free_list.shape[0], int(block_size))
+
+
+def _tables_rows(d, rows, n):
+    if rows is None:
+        return None
+    if rows.shape != (n,):
+        raise ValueError("rows must be [num_reqs]")
+    return _ptr(rows, "rows", d, _torch().int32)
+
+
+def pa_extend_tables(tables, lens, free_list, free_count, new_lens, block_size, max_tokens, rows=None, lens_out=None,
+                     free_count_out=None, batch_width=None, out=None, workspace=None):
+    """Blocks, block tables, lengths and slots for new_lens[i] more tokens of each
+    request, built on the GPU (all tensors int32 on it); returns (block_tables
+    [N, batch_width], seq_lens [N], cu_q_lens [N + 1], slot_mapping [max_tokens]).
+
+    The state is ``tables`` [R, max_blocks] and ``lens`` [R] (a row per request),
+    and the stack of free blocks ``free_list`` [num_blocks] with ``free_count``
+    [1].  ``rows`` [N]: each request's row, all distinct (default: request i is
+    row i).  ``lens`` and ``free_count`` are brought up to date in place, or in
+    ``lens_out`` and ``free_count_out``.  A call that cannot be met (too few free
+    blocks, a bad row or length, more than max_tokens tokens) changes nothing
+    and gives lengths as before, offsets 0 and slots -1; pa_get_device_error
+    tells.  ``batch_width`` defaults to max_blocks."""
+    torch = _torch()
+    i32 = torch.int32
+    d, stream = _here()
+    state = _tables_state(d, tables, lens, free_list, free_count, block_size, lens_out, free_count_out)
+    N = new_lens.shape[0]
+    if new_lens.dim() != 1 or N > state.num_rows:
+        raise ValueError("new_lens must be [num_reqs], at most one request for each row")
+    width = state.max_blocks_per_row if batch_width is None else int(batch_width)
+    max_tokens = int(max_tokens)
+    shapes = ((N, width), (N,), (N + 1,), (max_tokens,))
+    if out is None:
+        out = tuple(torch.empty(s, dtype=i32, device=tables.device) for s in shapes)
+    elif tuple(tuple(t.shape) for t in out) != shapes:
+        raise ValueError("out must be block_tables [N, batch_width], seq_lens [N], cu_q_lens [N + 1], slot_mapping [max_tokens]")
+    if workspace is None:
+        workspace = torch.empty(pa_tables_workspace_bytes(N, state.num_rows), dtype=torch.uint8, device=tables.device)
+    bt, sl, cu, slots = (_ptr(t, n, d, i32) for n, t in zip(("block_tables", "seq_lens", "cu_q_lens", "slot_mapping"), out))
+    st = _lib.load().pa_extend_tables(ctypes.byref(state), _tables_rows(d, rows, N), _ptr(new_lens, "new_lens", d, i32), N,
+                                      bt, width, sl, cu, slots, max_tokens, _ptr(workspace, "workspace", d),
+                                      workspace.nbytes, stream)
+    _lib.check("pa_extend_tables", st)
+    return out
+
+
+def pa_release_tables(tables, lens, free_list, free_count, rows, block_size, lens_out=None, free_count_out=None,
+                      workspace=None):
+    """Give the blocks of the requests in ``rows`` (int32, distinct) back to the
+    stack and set their lengths to 0; the state as in pa_extend_tables."""
+    d, stream = _here()
+    state = _tables_state(d, tables, lens, free_list, free_count, block_size, lens_out, free_count_out)
+    if rows.dim() != 1 or rows.shape[0] > state.num_rows:
+        raise ValueError("rows must be [num_reqs], at most one request for each row")
+    N = rows.shape[0]
+    if workspace is None:
+        workspace = _torch().empty(pa_tables_workspace_bytes(N, state.num_rows), dtype=_torch().uint8, device=tables.device)
+    st = _lib.load().pa_release_tables(ctypes.byref(state), _tables_rows(d, rows, N), N, _ptr(workspace, "workspace", d),
+                                       workspace.nbytes, stream)
+    _lib.check("pa_release_tables", st)
 
 
 def shared_prefix_plan(block_tables, seq_lens, block_size, num_heads, num_kv_heads, min_shared_blocks=1):
@@ -786,7 +970,8 @@ __all__ = [
     "pa_decode_default_splits", "pa_decode_shared_tc", "pa_decode_launch_count", "pa_get_device_error", "pa_selftest_wait_timeout",
     "pa_prefill", "pa_prefill_workspace_bytes",
     "pa_reshape_and_cache_fp8", "pa_gather_cache_fp8", "pa_copy_blocks_fp8", "pa_decode_fp8",
-    "pa_decode_fp8_workspace_bytes",
+    "pa_decode_fp8_workspace_bytes", "pa_write_blocks_fp8", "pa_prefill_fp8", "pa_prefill_fp8_workspace_bytes",
+    "pa_cross", "pa_cross_workspace_bytes", "pa_extend_tables", "pa_release_tables", "pa_tables_workspace_bytes",
     "pa_split_range", "pa_split_owner",
     "BlockManager", "PagedAttentionError", "sampling_memory", "simulate", "version",
 ]

@@ -22,6 +22,7 @@ PA_ERR_HOST_MEMORY = -9
 PA_F32 = 0
 PA_BF16 = 1
 PA_FP8_E4M3 = 2
+PA_FP8_E4M3_BLOCK = 3
 
 PA_NO_ALLOC_SCRATCH_BYTES = 16 << 20  # include/pa.h
 
@@ -67,6 +68,12 @@ class SharedPlanInfo(ctypes.Structure):
                 ("shared_blocks", ctypes.c_int64), ("saved_blocks", ctypes.c_int64)]
 
 
+class Tables(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("tables", "lens", "lens_out", "free_list", "free_count",
+                                               "free_count_out")] + \
+               [(n, ctypes.c_int32) for n in ("num_rows", "max_blocks_per_row", "num_blocks", "block_size")]
+
+
 # symbol -> (restype, argtypes)
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -76,6 +83,7 @@ _PI64 = ctypes.POINTER(ctypes.c_int64)
 _DESC = ctypes.POINTER(CacheDesc)
 _OPTS = ctypes.POINTER(DecodeOpts)
 _POPTS = ctypes.POINTER(PrefillOpts)
+_TABLES = ctypes.POINTER(Tables)
 
 SIGNATURES = {
     "pa_status_string": (ctypes.c_char_p, [_I32]),
@@ -95,6 +103,15 @@ SIGNATURES = {
     "pa_prefill_workspace_bytes": (ctypes.c_size_t, [_DESC, _I32, _I32, _I32, _POPTS]),
     "pa_prefill": (_I32, [_P, _P, _P, _P, _DESC, _P, _I32, _P, _P, _I32, _I32, _I32, ctypes.c_float, _P,
                           ctypes.c_size_t, _POPTS, _P]),
+    "pa_cross": (_I32, [_P, _P, _P, _P, _DESC, _P, _I32, _P, _P, _I32, _I32, _I32, ctypes.c_float, _P,
+                        ctypes.c_size_t, _POPTS, _P]),
+    "pa_write_blocks_fp8": (_I32, [_P, _P, _I32, _P, _I32, _P, _P, _I32, _I32, _P, _P, _P, _P, _DESC, _P]),
+    "pa_prefill_fp8_workspace_bytes": (ctypes.c_size_t, [_DESC, _I32, _I32, _I32, _POPTS]),
+    "pa_prefill_fp8": (_I32, [_P, _P, _P, _P, _P, _P, _DESC, _P, _I32, _P, _P, _I32, _I32, _I32, ctypes.c_float, _P,
+                              ctypes.c_size_t, _POPTS, _P]),
+    "pa_tables_workspace_bytes": (ctypes.c_size_t, [_I32, _I32]),
+    "pa_extend_tables": (_I32, [_TABLES, _P, _P, _I32, _P, _I32, _P, _P, _P, _I32, _P, ctypes.c_size_t, _P]),
+    "pa_release_tables": (_I32, [_TABLES, _P, _I32, _P, ctypes.c_size_t, _P]),
     "pa_reshape_and_cache_fp8": (_I32, [_P, _P, _I32, _P, _I32, _P, _P, _P, _P, _DESC, _P]),
     "pa_gather_cache_fp8": (_I32, [_P, _P, _I32, _P, _I32, _P, _P, _P, _P, _DESC, _P]),
     "pa_copy_blocks_fp8": (_I32, [_P, _P, _P, _P, _DESC, _P, _I32, _P]),

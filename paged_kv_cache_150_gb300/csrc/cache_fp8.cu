@@ -5,93 +5,9 @@
 // its largest |x| is a shuffle reduction within the group, then every lane
 // encodes the values it still holds.  Read-back: one pass the other way.  Both
 // are bound by HBM traffic (x once, codes and one scale byte once).
-#include "fp8_codec.cuh"
+#include "fp8_rows.cuh"
 
 namespace pa {
-
-// A group's 16 bytes of a row in fp32.
-template <typename T>
-struct Vec16;
-template <>
-struct Vec16<float> {
-    static constexpr int N = 4;
-    static __device__ __forceinline__ void load(const uint4 &u, float (&x)[4]) {
-        x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z),
-        x[3] = __uint_as_float(u.w);
-    }
-    // Largest finite |x| over the rows that L lanes hold of K and of V, as fp32 bits.
-    template <int L>
-    static __device__ __forceinline__ void row_max(const uint4 &k, const uint4 &v, uint32_t &ka, uint32_t &va) {
-        auto lane_max = [](const uint4 &u) {
-            return max(max(finite_bits(__uint_as_float(u.x)), finite_bits(__uint_as_float(u.y))),
-                       max(finite_bits(__uint_as_float(u.z)), finite_bits(__uint_as_float(u.w))));
-        };
-        ka = lane_max(k), va = lane_max(v);
-        if constexpr (L == 32) {
-            ka = __reduce_max_sync(0xffffffffu, ka);
-            va = __reduce_max_sync(0xffffffffu, va);
-        } else {
-#pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1) {
-                ka = max(ka, __shfl_xor_sync(0xffffffffu, ka, o));
-                va = max(va, __shfl_xor_sync(0xffffffffu, va, o));
-            }
-        }
-    }
-    static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
-        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-    }
-};
-template <>
-struct Vec16<__nv_bfloat16> {
-    static constexpr int N = 8;
-    static __device__ __forceinline__ void load(const uint4 &u, float (&x)[8]) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    }
-    // The same in 16-bit pairs: K's and V's maxima travel in one word.
-    template <int L>
-    static __device__ __forceinline__ void row_max(const uint4 &k, const uint4 &v, uint32_t &ka, uint32_t &va) {
-        auto lane_max = [](const uint4 &u) {
-            const uint32_t w[4] = {u.x & 0x7fff7fffu, u.y & 0x7fff7fffu, u.z & 0x7fff7fffu, u.w & 0x7fff7fffu};
-            uint32_t m = 0, odd = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                m = __vmaxu2(m, w[i]);
-                odd |= (w[i] + 0x00800080u) & 0x80008000u;  // an exponent of all ones
-            }
-            if (odd) {
-                m = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & ~__vcmpgeu2(w[i], 0x7f807f80u));
-            }
-            return max(m >> 16, m & 0xffffu);
-        };
-        uint32_t m = lane_max(k) << 16 | lane_max(v);
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-        ka = m & 0xffff0000u, va = m << 16;
-    }
-    static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
-        return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                          pack_bf16x2(x[6], x[7]));
-    }
-};
-
-// N codes (one vector's) to and from memory.
-template <int N>
-__device__ __forceinline__ void store_codes(uint8_t *p, const float (&x)[N], float inv) {
-    if constexpr (N == 8) {
-        *reinterpret_cast<uint2 *>(p) = make_uint2(encode4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
-                                                   encode4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
-    } else {
-        *reinterpret_cast<uint32_t *>(p) = encode4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-    }
-}
 
 // Rows (write) and vectors (read) that a lane has in flight, of K and of V,
 // and the CTAs of 256 threads resident per SM that its registers are held to.
@@ -159,11 +75,6 @@ __global__ void __launch_bounds__(256, kWriteCtas) write_fp8_kernel(const T *__r
     }
 }
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void from_f32(float *p, float x) { *p = x; }
-__device__ __forceinline__ void from_f32(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
-
 // Write, any row length and alignment: one warp per row, two passes over it
 // (the second finds it in L1 or L2), one element per lane at a time.
 template <typename T>
@@ -206,15 +117,22 @@ __global__ void __launch_bounds__(256) write_fp8_any_kernel(const T *__restrict_
     }
 }
 
+// Row of the scale bytes of slot s, head h: one per slot (kBlock false) or one
+// per block of B slots.
+template <bool kBlock>
+__device__ __forceinline__ int64_t scale_row(int32_t s, uint32_t h, uint32_t Hk, uint32_t B) {
+    return (int64_t)(kBlock ? (uint32_t)s / B : (uint32_t)s) * Hk + h;
+}
+
 // Read-back, D a multiple of the 16-byte output vector's elements and fewer
 // than 2^31 vectors: one output vector per thread and pass, kReadRows passes of
 // K and V in flight.
-template <typename T>
+template <typename T, bool kBlock>
 __global__ void __launch_bounds__(256, kReadCtas) read_fp8_kernel(T *__restrict__ k, T *__restrict__ v,
                                                        const int32_t *__restrict__ slots, uint32_t total, uint32_t Hk,
                                                        uint32_t vecs, const uint8_t *__restrict__ kc,
                                                        const uint8_t *__restrict__ vc, const uint8_t *__restrict__ ks,
-                                                       const uint8_t *__restrict__ vs, int64_t num_slots,
+                                                       const uint8_t *__restrict__ vs, uint32_t B, int64_t num_slots,
                                                        unsigned int *__restrict__ err) {
     grid_dependency_wait();
     grid_launch_dependents();
@@ -238,8 +156,9 @@ __global__ void __launch_bounds__(256, kReadCtas) read_fp8_kernel(T *__restrict_
                     const int64_t src = (int64_t)s * Hk + (r - t * Hk);
                     kq[u] = __ldcs(reinterpret_cast<const Code *>(kc) + src * vecs + c);
                     vq[u] = __ldcs(reinterpret_cast<const Code *>(vc) + src * vecs + c);
-                    kb[u] = __ldg(ks + src);
-                    vb[u] = __ldg(vs + src);
+                    const int64_t sr = scale_row<kBlock>(s, r - t * Hk, Hk, B);
+                    kb[u] = __ldg(ks + sr);
+                    vb[u] = __ldg(vs + sr);
                 }
             }
         }
@@ -267,14 +186,14 @@ __global__ void __launch_bounds__(256, kReadCtas) read_fp8_kernel(T *__restrict_
 }
 
 // Read-back, any row length and alignment: one element per thread.
-template <typename T>
+template <typename T, bool kBlock>
 __global__ void __launch_bounds__(256) read_fp8_any_kernel(T *__restrict__ k, T *__restrict__ v,
                                                            const int32_t *__restrict__ slots, int64_t total,
                                                            int32_t Hk, int32_t D, const uint8_t *__restrict__ kc,
                                                            const uint8_t *__restrict__ vc,
                                                            const uint8_t *__restrict__ ks,
-                                                           const uint8_t *__restrict__ vs, int64_t num_slots,
-                                                           unsigned int *__restrict__ err) {
+                                                           const uint8_t *__restrict__ vs, uint32_t B,
+                                                           int64_t num_slots, unsigned int *__restrict__ err) {
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t stride = (int64_t)gridDim.x * blockDim.x;
@@ -287,8 +206,9 @@ __global__ void __launch_bounds__(256) read_fp8_any_kernel(T *__restrict__ k, T 
             if (d == 0) atomicOr(err, kErrBounds);
         } else if (s >= 0) {
             const int64_t src = (int64_t)s * Hk + (r - t * Hk);
-            kx = decode4(kc[src * D + d]).x * scale_of(ks[src]);
-            vx = decode4(vc[src * D + d]).x * scale_of(vs[src]);
+            const int64_t sr = scale_row<kBlock>(s, (uint32_t)(r - t * Hk), (uint32_t)Hk, B);
+            kx = decode4(kc[src * D + d]).x * scale_of(ks[sr]);
+            vx = decode4(vc[src * D + d]).x * scale_of(vs[sr]);
         }
         from_f32(k + i, kx);
         from_f32(v + i, vx);
@@ -297,18 +217,8 @@ __global__ void __launch_bounds__(256) read_fp8_any_kernel(T *__restrict__ k, T 
 
 namespace {
 
-// Work's CTAs, at most per_sm per SM (one wave).
-int grid_for(int64_t ctas, int per_sm) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>(ctas, (int64_t)std::max(num_sms(), 1) * per_sm));
-}
 // The vector kernels count in 32 bits, with room for one grid stride past the end.
 constexpr int64_t kIndexMax = (int64_t)1 << 31;
-
-template <typename T>
-bool aligned_rows(int32_t D, const void *x, const void *y, const void *a, const void *b) {
-    constexpr int N = Vec16<T>::N;
-    return D % N == 0 && (((uintptr_t)x | (uintptr_t)y) & 15) == 0 && (((uintptr_t)a | (uintptr_t)b) & (N - 1)) == 0;
-}
 
 template <typename T>
 cudaError_t launch_write(const T *k, const T *v, const int32_t *slots, int32_t T_, uint8_t *kc, uint8_t *vc, uint8_t *ks,
@@ -333,19 +243,20 @@ cudaError_t launch_write(const T *k, const T *v, const int32_t *slots, int32_t T
     return launch_pdl(fn, dim3(grid_for((rows + per_cta - 1) / per_cta, kWriteCtas)), dim3(256), args, 0, s);
 }
 
-template <typename T>
+template <typename T, bool kBlock>
 cudaError_t launch_read(T *k, T *v, const int32_t *slots, int32_t T_, const uint8_t *kc, const uint8_t *vc,
                         const uint8_t *ks, const uint8_t *vs, const pa_cache_desc_t *c, unsigned int *err,
                         cudaStream_t s) {
     int64_t ns = (int64_t)c->num_blocks * c->block_size;
     int32_t Hk = c->num_kv_heads, D = c->head_dim, vecs = D / Vec16<T>::N;
+    uint32_t B = (uint32_t)c->block_size;
     if (!aligned_rows<T>(D, k, v, kc, vc) || (int64_t)T_ * Hk * vecs >= kIndexMax) {
         int64_t total = (int64_t)T_ * Hk * D;
-        void *args[] = {&k, &v, &slots, &total, &Hk, &D, &kc, &vc, &ks, &vs, &ns, &err};
-        return launch_pdl((const void *)read_fp8_any_kernel<T>, dim3(grid_for((total + 255) / 256, 8)), dim3(256), args, 0, s);
+        void *args[] = {&k, &v, &slots, &total, &Hk, &D, &kc, &vc, &ks, &vs, &B, &ns, &err};
+        return launch_pdl((const void *)read_fp8_any_kernel<T, kBlock>, dim3(grid_for((total + 255) / 256, 8)), dim3(256), args, 0, s);
     }
     uint32_t total = (uint32_t)((int64_t)T_ * Hk * vecs);
-    void *args[] = {&k, &v, &slots, &total, &Hk, &vecs, &kc, &vc, &ks, &vs, &ns, &err};
+    void *args[] = {&k, &v, &slots, &total, &Hk, &vecs, &kc, &vc, &ks, &vs, &B, &ns, &err};
     // fp32 rows, four bytes out for one in, run faster one pass per thread, bf16
     // rows on one wave, at every size measured (us; one pass, one wave):
     //   tokens x heads x D    fp32           bf16
@@ -357,7 +268,7 @@ cudaError_t launch_read(T *k, T *v, const int32_t *slots, int32_t T_, const uint
     //    60000 x 8 x 256      191.7  205.1   122.4  118.5
     const int64_t ctas = ((int64_t)total + 256 * kReadRows - 1) / (256 * kReadRows);
     const int grid = sizeof(T) == 4 ? (int)ctas : grid_for(ctas, kReadCtas);
-    return launch_pdl((const void *)read_fp8_kernel<T>, dim3(grid), dim3(256), args, 0, s);
+    return launch_pdl((const void *)read_fp8_kernel<T, kBlock>, dim3(grid), dim3(256), args, 0, s);
 }
 
 pa_status_t check_rows_call(const pa_cache_desc_t *cache, int32_t num_tokens, int32_t dtype) {
@@ -377,6 +288,7 @@ extern "C" pa_status_t pa_reshape_and_cache_fp8(const void *k, const void *v, in
                                                 uint8_t *v_scale, const pa_cache_desc_t *cache, pa_stream_t stream) try {
     const pa_status_t st = check_rows_call(cache, num_tokens, dtype);
     if (st != PA_OK) return st;
+    if (cache->dtype == PA_FP8_E4M3_BLOCK) return PA_ERR_UNSUPPORTED;  // pa_write_blocks_fp8
     if (num_tokens == 0) return PA_OK;
     if (!k || !v || !slot_mapping || !k_cache || !v_cache || !k_scale || !v_scale) return PA_ERR_INVALID_ARG;
     if (((uintptr_t)k | (uintptr_t)v) % (size_t)dtype_bytes(dtype) != 0) return PA_ERR_INVALID_ARG;
@@ -408,11 +320,14 @@ extern "C" pa_status_t pa_gather_cache_fp8(void *k, void *v, int32_t dtype, cons
     if (!err) return PA_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
     cudaGetLastError();
-    const cudaError_t e =
-        dtype == PA_BF16 ? launch_read((__nv_bfloat16 *)k, (__nv_bfloat16 *)v, slot_mapping, num_tokens,
-                                       (const uint8_t *)k_cache, (const uint8_t *)v_cache, k_scale, v_scale, cache, err, s)
-                         : launch_read((float *)k, (float *)v, slot_mapping, num_tokens, (const uint8_t *)k_cache,
-                                       (const uint8_t *)v_cache, k_scale, v_scale, cache, err, s);
+    const uint8_t *kc = (const uint8_t *)k_cache, *vc = (const uint8_t *)v_cache;
+    auto read = [&](auto *ko, auto *vo) {
+        using T = std::remove_pointer_t<decltype(ko)>;
+        return cache->dtype == PA_FP8_E4M3_BLOCK
+                   ? launch_read<T, true>(ko, vo, slot_mapping, num_tokens, kc, vc, k_scale, v_scale, cache, err, s)
+                   : launch_read<T, false>(ko, vo, slot_mapping, num_tokens, kc, vc, k_scale, v_scale, cache, err, s);
+    };
+    const cudaError_t e = dtype == PA_BF16 ? read((__nv_bfloat16 *)k, (__nv_bfloat16 *)v) : read((float *)k, (float *)v);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 } catch (...) {
     return host_failure();
@@ -432,7 +347,9 @@ extern "C" pa_status_t pa_copy_blocks_fp8(void *k_cache, void *v_cache, uint8_t 
     cudaGetLastError();
     const int64_t rows = (int64_t)cache->block_size * cache->num_kv_heads;
     launch_copy_blocks(k_cache, v_cache, rows * cache->head_dim, cache->num_blocks, src_dst_pairs, num_pairs, err, s);
-    launch_copy_blocks(k_scale, v_scale, rows, cache->num_blocks, src_dst_pairs, num_pairs, err, s);
+    // a block's scale bytes: one per row, or one per head
+    const int64_t scales = cache->dtype == PA_FP8_E4M3_BLOCK ? cache->num_kv_heads : rows;
+    launch_copy_blocks(k_scale, v_scale, scales, cache->num_blocks, src_dst_pairs, num_pairs, err, s);
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 } catch (...) {
     return host_failure();

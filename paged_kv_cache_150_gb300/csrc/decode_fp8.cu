@@ -14,14 +14,15 @@ int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 // The tensor-core kernel's shape for this cache; false if it does not take it.
 bool f8_shape(const pa_cache_desc_t *c, int G, F8Args *f, size_t *smem) {
     const int D = c->head_dim, Hk = c->num_kv_heads;
-    if ((D != 64 && D != 128) || c->block_size % 8 != 0 || Hk > 256) return false;
+    const bool block = c->dtype == PA_FP8_E4M3_BLOCK;
+    if ((D != 64 && D != 128) || c->block_size % 8 != 0 || (!block && Hk > 256)) return false;
     f->Hk = Hk;
     f->G = G;
     f->NH = Hk % 8 == 0 ? 8 : Hk % 4 == 0 ? 4 : Hk % 2 == 0 ? 2 : 1;
     f->T = kF8Warps * 16 / f->NH;
     f->gran = gcd(c->block_size, f->T);
-    if (f->gran * Hk % 16 != 0) return false;  // a box's scale bytes are copied in 16-byte pieces
-    f->scale_bytes = (uint32_t)(f->T * Hk);
+    if (!block && f->gran * Hk % 16 != 0) return false;  // a box's scale bytes are copied in 16-byte pieces
+    f->scale_bytes = block ? kF8BlockBytes : (uint32_t)(f->T * Hk);
     auto bytes = [&](int stages) {
         return D == 128 ? F8Smem<128>::bytes(stages, f->scale_bytes, f->NH, G)
                         : F8Smem<64>::bytes(stages, f->scale_bytes, f->NH, G);
@@ -32,8 +33,10 @@ bool f8_shape(const pa_cache_desc_t *c, int G, F8Args *f, size_t *smem) {
     return *smem <= 112 * 1024;
 }
 
-const void *f8_kernel(int D) {
-    return D == 128 ? (const void *)decode_fp8_kernel<128> : (const void *)decode_fp8_kernel<64>;
+const void *f8_kernel(const pa_cache_desc_t *c) {
+    if (c->dtype == PA_FP8_E4M3_BLOCK)
+        return c->head_dim == 128 ? (const void *)decode_fp8_kernel<128, true> : (const void *)decode_fp8_kernel<64, true>;
+    return c->head_dim == 128 ? (const void *)decode_fp8_kernel<128, false> : (const void *)decode_fp8_kernel<64, false>;
 }
 
 struct F8Plan {
@@ -66,7 +69,7 @@ pa_status_t decode_fp8_plan(const pa_cache_desc_t *c, int32_t N, int32_t H, cons
     p.threads = kF8Threads;
     p.max_tiles = N;
     p.smem = smem;
-    p.C = splits > 0 ? splits : default_ctas(f8_kernel(c->head_dim), kF8Threads, smem);
+    p.C = splits > 0 ? splits : default_ctas(f8_kernel(c), kF8Threads, smem);
     if (p.C <= 0) return PA_ERR_CUDA;
     prefill_workspace(&p, N, c->head_dim);
     return PA_OK;
@@ -95,7 +98,7 @@ extern "C" size_t pa_decode_fp8_workspace_bytes(const pa_cache_desc_t *cache, in
     F8Plan pl;
     if (decode_fp8_plan(cache, num_seqs, num_heads, opts, true, &pl) != PA_OK) return 0;
     const size_t need = pl.p.total;
-    if (!pl.mma || (opts && opts->kernel == PA_KERNEL_MMA)) return need;
+    if (!pl.mma || cache->dtype == PA_FP8_E4M3_BLOCK || (opts && opts->kernel == PA_KERNEL_MMA)) return need;
     // a call whose scale bytes are not aligned needs the CUDA-core layout
     if (decode_fp8_plan(cache, num_seqs, num_heads, opts, false, &pl) != PA_OK) return 0;
     return std::max(need, pl.p.total);
@@ -109,7 +112,8 @@ extern "C" pa_status_t pa_decode_fp8(void *out, const void *q, const void *k_cac
                                      int32_t num_seqs, int32_t num_heads, float scale, void *workspace,
                                      size_t workspace_bytes, const pa_prefill_opts_t *opts, pa_stream_t stream) try {
     F8Plan pl;
-    const bool aligned = ((uintptr_t)k_scale | (uintptr_t)v_scale) % 16 == 0;
+    // block scales are read byte by byte where they are not aligned
+    const bool aligned = (cache && cache->dtype == PA_FP8_E4M3_BLOCK) || ((uintptr_t)k_scale | (uintptr_t)v_scale) % 16 == 0;
     pa_status_t st = decode_fp8_plan(cache, num_seqs, num_heads, opts, aligned, &pl);
     if (st != PA_OK) return st;
     const PrefillPlan &p = pl.p;
@@ -138,6 +142,7 @@ extern "C" pa_status_t pa_decode_fp8(void *out, const void *q, const void *k_cac
     a.max_blocks = max_blocks_per_seq;
     a.N = num_seqs;
     a.T = num_seqs;
+    a.step = 1;
     a.H = num_heads;
     a.scale_log2 = scale * 1.4426950408889634f;
     cudaStream_t s = (cudaStream_t)stream;
@@ -150,7 +155,7 @@ extern "C" pa_status_t pa_decode_fp8(void *out, const void *q, const void *k_cac
     if ((st = prefill_bind(p, &a, workspace)) != PA_OK) return st;
     CUtensorMap tmk, tmv;
     if (!encode_codes_map(&tmk, k_cache, cache, f) || !encode_codes_map(&tmv, v_cache, cache, f)) return PA_ERR_CUDA;
-    const void *fn = f8_kernel(cache->head_dim);
+    const void *fn = f8_kernel(cache);
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem) != cudaSuccess)
         return PA_ERR_CUDA;
     cudaGetLastError();

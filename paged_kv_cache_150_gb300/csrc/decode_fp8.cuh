@@ -57,8 +57,11 @@ struct F8Args {
     int32_t Hk, G, NH, T;   // KV heads, query heads per KV head, KV heads and tokens of a stage
     int32_t gran;           // tokens of a box: gcd(block size, T)
     int32_t stages;
-    uint32_t scale_bytes;   // of K (or V) per stage: T * Hk
+    uint32_t scale_bytes;   // of K (or V) per stage: T * Hk; kF8BlockBytes with block scales
 };
+// Block scales of a stage: NH bytes for each of its T / gran boxes, a box lying in
+// one block; T NH = 128 and gran >= 8, so 16 at most.
+constexpr uint32_t kF8BlockBytes = 16;
 
 template <int D>
 struct F8Smem {
@@ -118,7 +121,29 @@ __device__ __forceinline__ int32_t f8_units_end(const PrefillCursor &cur, int32_
     return keys <= 0 ? cur.j0 : min(cur.j1, (keys - 1) / T + 1);  // keys + T may pass 2^31
 }
 
-template <int D>
+// The block scales of NH heads, and their way to a stage.  p need not be aligned.
+__device__ __forceinline__ uint64_t load_scales(const uint8_t *p, int32_t NH) {
+    if (((uintptr_t)p & (uintptr_t)(NH - 1)) == 0) {
+        if (NH == 8) return __ldg(reinterpret_cast<const unsigned long long *>(p));
+        if (NH == 4) return __ldg(reinterpret_cast<const uint32_t *>(p));
+        if (NH == 2) return __ldg(reinterpret_cast<const uint16_t *>(p));
+    }
+    uint64_t v = 0;
+    for (int32_t i = 0; i < NH; ++i) v |= (uint64_t)__ldg(p + i) << (8 * i);
+    return v;
+}
+__device__ __forceinline__ void store_scales(uint32_t dst, uint64_t v, int32_t NH) {
+    if (NH == 8)
+        asm volatile("st.shared.u64 [%0], %1;" ::"r"(dst), "l"(v) : "memory");
+    else if (NH == 4)
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"((uint32_t)v) : "memory");
+    else if (NH == 2)
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst), "h"((uint16_t)v) : "memory");
+    else
+        asm volatile("st.shared.u8 [%0], %1;" ::"r"(dst), "r"((uint32_t)v) : "memory");
+}
+
+template <int D, bool kBlock>
 __device__ __forceinline__ void f8_producer(const PrefillArgs &a, const F8Args &f, uint8_t *smem, const CUtensorMap *tmk,
                                             const CUtensorMap *tmv, uint64_t *full, uint64_t *empty, PrefillCursor cur,
                                             int lane) {
@@ -130,7 +155,8 @@ __device__ __forceinline__ void f8_producer(const PrefillArgs &a, const F8Args &
     const uint64_t policy = l2_policy_evict_first();  // the codes are read once
     const uint32_t tiles = smem_u32(smem), scales = tiles + L::scales(f.stages);
     const int32_t nbox = f.T / f.gran;  // at most 16, one per lane
-    const uint32_t box_bytes = (uint32_t)(f.gran * f.NH * D), sc_bytes = (uint32_t)(f.gran * f.Hk);
+    const uint32_t box_bytes = (uint32_t)(f.gran * f.NH * D);
+    const uint32_t sc_bytes = (uint32_t)(kBlock ? f.NH : f.gran * f.Hk);  // scale bytes of a box
     uint32_t n = 0;
     bool abort = false;
     // table entry of this lane's box of unit j of a sequence (0 without that box)
@@ -139,9 +165,25 @@ __device__ __forceinline__ void f8_producer(const PrefillArgs &a, const F8Args &
                    ? a.tables[(int64_t)t.seq * a.max_blocks + (j * f.T + lane * f.gran) / a.B]
                    : 0;
     };
+    // With block scales a lane brings its box's bytes itself: asked for a unit
+    // ahead, and so the table entry two units ahead.
+    auto scales_of = [&](int32_t p, uint64_t &k, uint64_t &v) {
+        k = v = 0;  // a bad entry: zeros, the smallest scale
+        if (lane < nbox && p >= 0 && p < a.NB) {
+            const int64_t at = (int64_t)p * f.Hk + cur.kvh * f.NH;
+            k = load_scales(a.k_scale + at, f.NH);
+            v = load_scales(a.v_scale + at, f.NH);
+        }
+    };
     int32_t phys = entry_of(cur.t, cur.j0), phys_next;
     do {
         const int32_t keys = cur.t.p0 + 1, je = f8_units_end(cur, f.T);
+        uint64_t ksc = 0, vsc = 0;
+        int32_t phys_1 = 0;
+        if constexpr (kBlock) {
+            if (cur.j0 < je) scales_of(phys, ksc, vsc);
+            if (cur.j0 + 1 < je) phys_1 = entry_of(cur.t, cur.j0 + 1);
+        }
         auto has = [&](int32_t j) { return lane < nbox && (int64_t)j * f.T + lane * f.gran < keys; };
         auto entry = [&](int32_t j) { return entry_of(cur.t, j); };
         phys_next = entry_of(cur.t_next, 0);  // the next segment starts with its sequence
@@ -149,14 +191,29 @@ __device__ __forceinline__ void f8_producer(const PrefillArgs &a, const F8Args &
             const uint32_t st = n % f.stages;
             const bool box = has(j), good = phys >= 0 && phys < a.NB;
             const int32_t at = good ? phys * a.B + (j * f.T + lane * f.gran) % a.B : a.NB * a.B;
-            if (j + 1 < je) phys = entry(j + 1);
+            const uint64_t ks_now = ksc, vs_now = vsc;
+            if (j + 1 < je) {
+                if constexpr (kBlock) {
+                    phys = phys_1;
+                    scales_of(phys, ksc, vsc);
+                    if (j + 2 < je) phys_1 = entry(j + 2);
+                } else {
+                    phys = entry(j + 1);
+                }
+            }
             if (n >= (uint32_t)f.stages && !abort && !mbar_wait_bounded(smem_u32(&empty[st]), (n / f.stages + 1) & 1)) {
                 atomicOr(a.err, kErrTimeout);
                 abort = true;
             }
             if (__any_sync(0xffffffffu, abort)) break;
             const uint32_t ks = scales + st * 2 * f.scale_bytes + (uint32_t)lane * sc_bytes, vs = ks + f.scale_bytes;
-            if (box && !good) {  // a bad entry reads zeros: codes past the pool, the smallest scale
+            if constexpr (kBlock) {
+                if (box) {
+                    if (!good) atomicOr(a.err, kErrBounds);
+                    store_scales(ks, ks_now, f.NH);
+                    store_scales(vs, vs_now, f.NH);
+                }
+            } else if (box && !good) {  // a bad entry reads zeros: codes past the pool, the smallest scale
                 atomicOr(a.err, kErrBounds);
                 for (uint32_t i = 0; i < sc_bytes; i += 4) {
                     asm volatile("st.shared.u32 [%0], %1;" ::"r"(ks + i), "r"(0u) : "memory");
@@ -164,17 +221,17 @@ __device__ __forceinline__ void f8_producer(const PrefillArgs &a, const F8Args &
                 }
                 fence_proxy_async_smem();  // before a later copy to the same bytes
             }
-            __syncwarp();  // every lane's zeros are in place before lane 0 publishes the stage
+            __syncwarp();  // every lane's bytes are in place before lane 0 publishes the stage
             const uint32_t boxes = (uint32_t)__popc(__ballot_sync(0xffffffffu, box));
             const uint32_t goods = (uint32_t)__popc(__ballot_sync(0xffffffffu, box && good));
             const uint32_t fb = smem_u32(&full[st]);
-            if (lane == 0) mbar_arrive_expect_tx(fb, 2 * (boxes * box_bytes + goods * sc_bytes));
+            if (lane == 0) mbar_arrive_expect_tx(fb, 2 * (boxes * box_bytes + (kBlock ? 0 : goods * sc_bytes)));
             __syncwarp();
             if (box) {
                 const uint32_t dst = tiles + st * 2 * L::kTile + (uint32_t)lane * box_bytes;
                 tma_load_3d_hint(dst, tmk, fb, 0, at, cur.kvh * f.NH, policy);
                 tma_load_3d_hint(dst + L::kTile, tmv, fb, 0, at, cur.kvh * f.NH, policy);
-                if (good) {
+                if (!kBlock && good) {
                     bulk_load(ks, a.k_scale + (int64_t)at * f.Hk, sc_bytes, fb);
                     bulk_load(vs, a.v_scale + (int64_t)at * f.Hk, sc_bytes, fb);
                 }
@@ -200,7 +257,8 @@ __device__ __forceinline__ bool f8_next(PrefillCursor &cur, const PrefillArgs &a
     return more;
 }
 
-template <int D>
+// kBlock: one scale per block and KV head; else one per token and KV head.
+template <int D, bool kBlock>
 __global__ void __launch_bounds__(kF8Threads, 2)
     decode_fp8_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                       const __grid_constant__ PrefillArgs a, const F8Args f) {
@@ -235,7 +293,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
     }
     __syncwarp();
     if (warp == kF8Warps) {
-        f8_producer<D>(a, f, smem, &tmk, &tmv, full, empty, cur, lane);
+        f8_producer<D, kBlock>(a, f, smem, &tmk, &tmv, full, empty, cur, lane);
         return;
     }
 
@@ -254,15 +312,16 @@ __global__ void __launch_bounds__(kF8Threads, 2)
     // chunk j + (mi >> 1), j even: (j | mi >> 1) ^ swz = j ^ (mi >> 1 ^ swz), and
     // tiles are aligned to 128 bytes
     const uint32_t lane_off = row_off + ((((uint32_t)mi >> 1) ^ swz) << 4);
-    // scale bytes of token r of the slice
-    const uint32_t sc_head = (uint32_t)((sub * 16 + r) * f.Hk + h);
+    // scale bytes of tokens r and r + 8 of the slice
+    const uint32_t sc_head = (uint32_t)(kBlock ? (sub * 16 + r) / f.gran * f.NH + h : (sub * 16 + r) * f.Hk + h);
+    const uint32_t sc_8 = (uint32_t)(kBlock ? (sub * 16 + r + 8) / f.gran * f.NH + h : 8 * f.Hk + sc_head) - sc_head;
     int st = 0;
     uint32_t phase = 0;
     bool abort = false;
     do {
         const PrefillTile t = cur.t;
         const int32_t keys = t.p0 + 1, j0 = cur.j0, je = f8_units_end(cur, f.T);
-        const uint32_t sc_off = sc_head + (uint32_t)(cur.kvh * f.NH);
+        const uint32_t sc_off = sc_head + (uint32_t)(kBlock ? 0 : cur.kvh * f.NH);
         const int32_t head0 = (cur.kvh * f.NH + h) * f.G;  // first query head of this warp's KV head
         // Q: column n = query head r; per 16-element chunk this thread's elements 4 cq .. + 3
         uint32_t qf[NC][2];
@@ -318,7 +377,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
                 const uint32_t kb = tiles + (uint32_t)st * 2 * L::kTile + lane_off, vb = kb + L::kTile;
                 // scale bytes of tokens r and r + 8
                 const uint8_t *ks = sc + (uint32_t)st * 2 * f.scale_bytes + sc_off, *vs = ks + f.scale_bytes;
-                const uint32_t ka = ks[0], kc = ks[8 * f.Hk], va = vs[0], vc = vs[8 * f.Hk];
+                const uint32_t ka = ks[0], kc = ks[sc_8], va = vs[0], vc = vs[sc_8];
                 float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j2 = 0; j2 < NC; j2 += 2) {

@@ -52,11 +52,11 @@ __device__ __forceinline__ float4 decode4(uint32_t w) {
     return make_float4(a.x, a.y, b.x, b.y);
 }
 
-// An 8-bit pool's descriptor: row layout, PA_FP8_E4M3.
+// An 8-bit pool's descriptor: row layout, a scale per token or per block.
 inline pa_status_t validate_fp8_desc(const pa_cache_desc_t *c) {
     if (!c) return PA_ERR_INVALID_ARG;
     if (c->num_blocks <= 0 || c->block_size <= 0 || c->num_kv_heads <= 0 || c->head_dim <= 0) return PA_ERR_INVALID_ARG;
-    if (c->dtype != PA_FP8_E4M3) return PA_ERR_INVALID_ARG;
+    if (c->dtype != PA_FP8_E4M3 && c->dtype != PA_FP8_E4M3_BLOCK) return PA_ERR_INVALID_ARG;
     if (c->layout != PA_LAYOUT_ROW) return c->layout == PA_LAYOUT_SPLIT ? PA_ERR_UNSUPPORTED : PA_ERR_INVALID_ARG;
     if ((int64_t)c->num_blocks * c->block_size >= ((int64_t)1 << 31)) return PA_ERR_INVALID_ARG;
     if ((int64_t)c->num_kv_heads * c->head_dim >= ((int64_t)1 << 31)) return PA_ERR_INVALID_ARG;

@@ -194,6 +194,7 @@ extern "C" pa_status_t pa_get_device_error(pa_stream_t stream) {
     if (word & kErrTimeout) return PA_ERR_DEVICE_TIMEOUT;
     if (word & (kErrBounds | kErrLength)) return PA_ERR_DEVICE_BOUNDS;
     if (word & kErrPlan) return PA_ERR_DEVICE_PLAN;
+    if (word & kErrNoBlocks) return PA_ERR_NO_BLOCKS;
     return PA_OK;
 }
 

@@ -19,6 +19,7 @@ enum : unsigned int {
     kErrLength = 2u,   // sequence length outside [0, max_blocks * B]
     kErrTimeout = 4u,  // a bounded mbarrier wait ran out
     kErrPlan = 8u,     // a shared-prefix plan that does not match its decode call
+    kErrNoBlocks = 16u,  // the free stack does not hold what a step's tables need
 };
 
 // Bound on any single mbarrier wait (nanoseconds of %globaltimer).

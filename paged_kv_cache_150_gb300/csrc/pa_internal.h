@@ -14,7 +14,7 @@
 
 namespace pa {
 
-inline int dtype_bytes(int32_t dtype) { return dtype == PA_F32 ? 4 : dtype == PA_FP8_E4M3 ? 1 : 2; }
+inline int dtype_bytes(int32_t dtype) { return dtype == PA_F32 ? 4 : dtype == PA_FP8_E4M3 || dtype == PA_FP8_E4M3_BLOCK ? 1 : 2; }
 
 inline pa_status_t validate_cache_desc(const pa_cache_desc_t *c) {
     if (!c) return PA_ERR_INVALID_ARG;

@@ -180,11 +180,20 @@ pa_status_t prefill_launch(const PrefillPlan &p, const pa_cache_desc_t *c, Prefi
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+namespace {
+
+// Which call: its caches' kind and what a token sees.
+struct ChunkKind {
+    bool fp8;      // pa_prefill_fp8: an 8-bit cache with block scales, q and out bf16
+    int32_t step;  // PrefillArgs
+};
+
 // The call's plan; fits: its scale and alignment suit the tcgen05 kernel.
-static pa_status_t prefill_plan_of(const pa_cache_desc_t *c, int32_t N, int32_t T, int32_t H,
-                                   const pa_prefill_opts_t *opts, bool fits, PrefillPlan *p) {
-    const pa_status_t st = validate_cache_desc(c);
+pa_status_t prefill_plan_of(const ChunkKind &kind, const pa_cache_desc_t *c, int32_t N, int32_t T, int32_t H,
+                            const pa_prefill_opts_t *opts, bool fits, PrefillPlan *p) {
+    const pa_status_t st = kind.fp8 ? validate_fp8_desc(c) : validate_cache_desc(c);
     if (st != PA_OK) return st;
+    if (c->dtype == PA_FP8_E4M3) return PA_ERR_UNSUPPORTED;  // a scale per token: read back first
     if (N < 0 || T < 0 || H <= 0 || H % c->num_kv_heads != 0) return PA_ERR_INVALID_ARG;
     const int want = opts ? opts->kernel : PA_KERNEL_AUTO;
     if (want != PA_KERNEL_AUTO && want != PA_KERNEL_SIMT && want != PA_KERNEL_MMA) return PA_ERR_INVALID_ARG;
@@ -196,19 +205,78 @@ static pa_status_t prefill_plan_of(const pa_cache_desc_t *c, int32_t N, int32_t 
     return prefill_layout(tc, c, N, T, H, opts ? opts->num_splits : 0, p);
 }
 
+size_t chunk_workspace_bytes(const ChunkKind &kind, const pa_cache_desc_t *cache, int32_t num_seqs, int32_t num_tokens,
+                             int32_t num_heads, const pa_prefill_opts_t *opts) {
+    PrefillPlan p;
+    if (prefill_plan_of(kind, cache, num_seqs, num_tokens, num_heads, opts, true, &p) != PA_OK) return 0;
+    const size_t need = p.total;
+    if (!p.tc || (opts && opts->kernel == PA_KERNEL_MMA)) return need;
+    // a call whose scale or alignment keeps it from the tcgen05 kernel needs the other layout
+    if (prefill_plan_of(kind, cache, num_seqs, num_tokens, num_heads, opts, false, &p) != PA_OK) return 0;
+    return std::max(need, p.total);
+}
+
+pa_status_t chunk_call(const ChunkKind &kind, void *out, const void *q, const void *k_cache, const void *v_cache,
+                       const uint8_t *k_scale, const uint8_t *v_scale, const pa_cache_desc_t *cache,
+                       const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                       const int32_t *cu_q_lens, int32_t num_seqs, int32_t num_tokens, int32_t num_heads, float scale,
+                       void *workspace, size_t workspace_bytes, const pa_prefill_opts_t *opts, pa_stream_t stream) {
+    PrefillPlan p;
+    const bool fits = scale > 0.f && scale < INFINITY && ((uintptr_t)q | (uintptr_t)out) % 16 == 0;
+    const pa_status_t st = prefill_plan_of(kind, cache, num_seqs, num_tokens, num_heads, opts, fits, &p);
+    if (st != PA_OK) return st;
+    if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens || !cu_q_lens || !workspace)
+        return PA_ERR_INVALID_ARG;
+    if (kind.fp8 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+    if (max_blocks_per_seq <= 0 || (int64_t)num_seqs * max_blocks_per_seq >= ((int64_t)1 << 31) ||
+        (int64_t)max_blocks_per_seq * cache->block_size >= ((int64_t)1 << 31))
+        return PA_ERR_INVALID_ARG;
+    // the units of a KV head are counted in 32 bits
+    if ((int64_t)p.max_tiles * ((int64_t)max_blocks_per_seq * cache->block_size / p.kt + 1 + p.extra) >= ((int64_t)1 << 31))
+        return PA_ERR_UNSUPPORTED;
+    if (!(scale == scale)) return PA_ERR_INVALID_ARG;
+    if (((uintptr_t)workspace & 255) != 0) return PA_ERR_INVALID_ARG;
+    if (workspace_bytes < p.total) return PA_ERR_WORKSPACE;
+    const int eb = cache->dtype == PA_F32 ? 4 : 2;  // of q and out
+    if (((uintptr_t)q | (uintptr_t)out) % (size_t)(eb * 2) != 0) return PA_ERR_INVALID_ARG;
+    if (((uintptr_t)k_cache | (uintptr_t)v_cache) % 16 != 0) return PA_ERR_INVALID_ARG;
+    PrefillArgs a{};
+    a.q = q;
+    a.out = out;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.tables = block_tables;
+    a.seq_lens = seq_lens;
+    a.cu_q = cu_q_lens;
+    a.max_blocks = max_blocks_per_seq;
+    a.N = num_seqs;
+    a.T = num_tokens;
+    a.H = num_heads;
+    a.step = kind.step;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    return prefill_launch(p, cache, a, workspace, (cudaStream_t)stream);
+}
+
+constexpr ChunkKind kPrefill{false, 1}, kCross{false, 0}, kPrefillFp8{true, 1};
+
+}  // namespace
 }  // namespace pa
 
 using namespace pa;
 
 extern "C" size_t pa_prefill_workspace_bytes(const pa_cache_desc_t *cache, int32_t num_seqs, int32_t num_tokens,
                                              int32_t num_heads, const pa_prefill_opts_t *opts) try {
-    PrefillPlan p;
-    if (prefill_plan_of(cache, num_seqs, num_tokens, num_heads, opts, true, &p) != PA_OK) return 0;
-    const size_t need = p.total;
-    if (!p.tc || (opts && opts->kernel == PA_KERNEL_MMA)) return need;
-    // a call whose scale or alignment keeps it from the tcgen05 kernel needs the other layout
-    if (prefill_plan_of(cache, num_seqs, num_tokens, num_heads, opts, false, &p) != PA_OK) return 0;
-    return std::max(need, p.total);
+    return chunk_workspace_bytes(kPrefill, cache, num_seqs, num_tokens, num_heads, opts);
+} catch (...) {
+    return 0;
+}
+
+extern "C" size_t pa_prefill_fp8_workspace_bytes(const pa_cache_desc_t *cache, int32_t num_seqs, int32_t num_tokens,
+                                                 int32_t num_heads, const pa_prefill_opts_t *opts) try {
+    return chunk_workspace_bytes(kPrefillFp8, cache, num_seqs, num_tokens, num_heads, opts);
 } catch (...) {
     return 0;
 }
@@ -219,39 +287,31 @@ extern "C" pa_status_t pa_prefill(void *out, const void *q, const void *k_cache,
                                   int32_t num_seqs, int32_t num_tokens, int32_t num_heads, float scale,
                                   void *workspace, size_t workspace_bytes, const pa_prefill_opts_t *opts,
                                   pa_stream_t stream) try {
-    PrefillPlan p;
-    const bool fits = scale > 0.f && scale < INFINITY && ((uintptr_t)q | (uintptr_t)out) % 16 == 0;
-    const pa_status_t st = prefill_plan_of(cache, num_seqs, num_tokens, num_heads, opts, fits, &p);
-    if (st != PA_OK) return st;
-    if (num_seqs == 0 || num_tokens == 0) return PA_OK;
-    if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens || !cu_q_lens || !workspace)
-        return PA_ERR_INVALID_ARG;
-    if (max_blocks_per_seq <= 0 || (int64_t)num_seqs * max_blocks_per_seq >= ((int64_t)1 << 31) ||
-        (int64_t)max_blocks_per_seq * cache->block_size >= ((int64_t)1 << 31))
-        return PA_ERR_INVALID_ARG;
-    // the units of a KV head are counted in 32 bits
-    if ((int64_t)p.max_tiles * ((int64_t)max_blocks_per_seq * cache->block_size / p.kt + 1 + p.extra) >= ((int64_t)1 << 31))
-        return PA_ERR_UNSUPPORTED;
-    if (!(scale == scale)) return PA_ERR_INVALID_ARG;
-    if (((uintptr_t)workspace & 255) != 0) return PA_ERR_INVALID_ARG;
-    if (workspace_bytes < p.total) return PA_ERR_WORKSPACE;
-    const int eb = dtype_bytes(cache->dtype);
-    if (((uintptr_t)q | (uintptr_t)out) % (size_t)(eb * 2) != 0) return PA_ERR_INVALID_ARG;
-    if (((uintptr_t)k_cache | (uintptr_t)v_cache) % 16 != 0) return PA_ERR_INVALID_ARG;
-    PrefillArgs a{};
-    a.q = q;
-    a.out = out;
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
-    a.tables = block_tables;
-    a.seq_lens = seq_lens;
-    a.cu_q = cu_q_lens;
-    a.max_blocks = max_blocks_per_seq;
-    a.N = num_seqs;
-    a.T = num_tokens;
-    a.H = num_heads;
-    a.scale_log2 = scale * 1.4426950408889634f;
-    return prefill_launch(p, cache, a, workspace, (cudaStream_t)stream);
+    return chunk_call(kPrefill, out, q, k_cache, v_cache, nullptr, nullptr, cache, block_tables, max_blocks_per_seq,
+                      seq_lens, cu_q_lens, num_seqs, num_tokens, num_heads, scale, workspace, workspace_bytes, opts, stream);
+} catch (...) {
+    return host_failure();
+}
+
+extern "C" pa_status_t pa_cross(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                const pa_cache_desc_t *cache, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                const int32_t *kv_lens, const int32_t *cu_q_lens, int32_t num_seqs, int32_t num_tokens,
+                                int32_t num_heads, float scale, void *workspace, size_t workspace_bytes,
+                                const pa_prefill_opts_t *opts, pa_stream_t stream) try {
+    return chunk_call(kCross, out, q, k_cache, v_cache, nullptr, nullptr, cache, block_tables, max_blocks_per_seq, kv_lens,
+                      cu_q_lens, num_seqs, num_tokens, num_heads, scale, workspace, workspace_bytes, opts, stream);
+} catch (...) {
+    return host_failure();
+}
+
+extern "C" pa_status_t pa_prefill_fp8(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                      const uint8_t *k_scale, const uint8_t *v_scale, const pa_cache_desc_t *cache,
+                                      const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                      const int32_t *cu_q_lens, int32_t num_seqs, int32_t num_tokens, int32_t num_heads,
+                                      float scale, void *workspace, size_t workspace_bytes,
+                                      const pa_prefill_opts_t *opts, pa_stream_t stream) try {
+    return chunk_call(kPrefillFp8, out, q, k_cache, v_cache, k_scale, v_scale, cache, block_tables, max_blocks_per_seq,
+                      seq_lens, cu_q_lens, num_seqs, num_tokens, num_heads, scale, workspace, workspace_bytes, opts, stream);
 } catch (...) {
     return host_failure();
 }

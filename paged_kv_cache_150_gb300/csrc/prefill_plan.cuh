@@ -27,7 +27,7 @@ struct PrefillTile {
     int32_t seq;   // sequence (block-table row)
     int32_t row0;  // row of q / out of its first token
     int32_t ntok;  // tokens in this tile
-    int32_t p0;    // position of its first token (negative: before the sequence's first key)
+    int32_t p0;    // last position that its first token sees: its own (negative: before the sequence's first key)
 };
 
 // Where a CTA's walk over its range starts (one read of 80 bytes instead of a
@@ -64,6 +64,7 @@ struct PrefillArgs {
     int32_t C;            // persistent CTAs
     int32_t max_tiles;    // capacity of tiles[] and cu[]
     float scale_log2;
+    int32_t step;         // positions that each token sees more than the one before it: 1, or 0 where all see all (pa_cross)
     int32_t few;          // 1: few tiles in many pieces, merged by prefill_merge_few_kernel
     int32_t *ctl;         // ctl[1]: cut tiles listed, ctl[2]: most query rows of one
     MergeEntry *merges;   // [C] the cut tiles (note_cut)
@@ -77,8 +78,13 @@ struct PrefillArgs {
     unsigned long long wait_ns;  // limit of the tcgen05 kernel's longest waits
 };
 
-__device__ __forceinline__ int32_t prefill_units(const PrefillTile &t, int32_t kt) {
-    const int32_t keys = t.p0 + t.ntok;
+// Keys that the first n tokens of a tile see (n >= 1); none where negative.
+__device__ __forceinline__ int32_t prefill_keys(const PrefillTile &t, int32_t n, int32_t step) {
+    return t.p0 + 1 + step * (n - 1);
+}
+
+__device__ __forceinline__ int32_t prefill_units(const PrefillTile &t, int32_t kt, int32_t step) {
+    const int32_t keys = prefill_keys(t, t.ntok, step);
     return keys <= kt ? 1 : (int32_t)(((int64_t)keys + kt - 1) / kt);  // no key: one unit that writes zeros
 }
 
@@ -185,9 +191,9 @@ static __global__ void __launch_bounds__(1024) prefill_plan_kernel(const Prefill
             t.seq = lo;
             t.row0 = r0 + t0;
             t.ntok = min(tq, n - t0);
-            t.p0 = L - n + t0;
+            t.p0 = a.step ? L - n + t0 : L - 1;
             a.tiles[k] = t;
-            u = prefill_units(t, a.kt) + a.extra;
+            u = prefill_units(t, a.kt, a.step) + a.extra;
         }
         int32_t total;
         const int32_t incl = block_scan_1024(u, units, warp_incl, &total);

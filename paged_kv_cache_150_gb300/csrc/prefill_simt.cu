@@ -16,6 +16,7 @@ static const void *simt_for(int D, size_t *smem) {
 
 const void *prefill_simt_ptr(int cache_dtype, int D, int layout, size_t *smem) {
     if (cache_dtype == PA_FP8_E4M3) return simt_for<__nv_bfloat16, CacheE4m3, PA_LAYOUT_ROW>(D, smem);
+    if (cache_dtype == PA_FP8_E4M3_BLOCK) return simt_for<__nv_bfloat16, CacheE4m3Block, PA_LAYOUT_ROW>(D, smem);
     if (cache_dtype == PA_F32)
         return layout == PA_LAYOUT_ROW ? simt_for<float, float, PA_LAYOUT_ROW>(D, smem)
                                        : simt_for<float, float, PA_LAYOUT_SPLIT>(D, smem);

@@ -23,8 +23,10 @@
 
 namespace pa {
 
-// Element kinds of a cache, as the kernels read them.
+// Element kinds of a cache, as the kernels read them: e4m3 with a scale per
+// token, or per block, and KV head.
 struct CacheE4m3 {};
+struct CacheE4m3Block {};
 
 constexpr int kSimtRows = 64, kSimtKeys = 64, kSimtThreads = 256, kSimtExtra = 1;
 
@@ -62,13 +64,15 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
 }
 
 // Four elements at d (a multiple of 4) of the K or V row of slot `slot`, KV
-// head kvh.  CT: float, __nv_bfloat16 or CacheE4m3 (row layout only).
+// head kvh.  CT: float, __nv_bfloat16, CacheE4m3 or CacheE4m3Block (these in the
+// row layout only).
 template <typename CT, int D, int LAYOUT, bool IS_V>
 __device__ __forceinline__ float4 cache4(const PrefillArgs &a, int64_t slot, int32_t kvh, int d) {
     const void *base = IS_V ? a.v_cache : a.k_cache;
-    if constexpr (std::is_same<CT, CacheE4m3>::value) {
+    if constexpr (std::is_same<CT, CacheE4m3>::value || std::is_same<CT, CacheE4m3Block>::value) {
         const int64_t row = slot * a.Hk + kvh;
-        const float s = scale_of(__ldg((IS_V ? a.v_scale : a.k_scale) + row));
+        const int64_t at = std::is_same<CT, CacheE4m3>::value ? row : slot / a.B * a.Hk + kvh;
+        const float s = scale_of(__ldg((IS_V ? a.v_scale : a.k_scale) + at));
         const float4 x = decode4(__ldg(reinterpret_cast<const uint32_t *>((const uint8_t *)base + row * D + d)));
         return make_float4(x.x * s, x.y * s, x.z * s, x.w * s);
     } else if constexpr (LAYOUT == PA_LAYOUT_ROW) {
@@ -140,7 +144,7 @@ __global__ void __launch_bounds__(kSimtThreads, D == 256 ? 1 : 2)
     do {
         const PrefillTile t = cur.t;
         const int32_t nrow = t.ntok * a.G;  // rows of this tile (<= 64)
-        const int32_t keys = t.p0 + t.ntok, j0 = cur.j0, j1 = cur.j1;
+        const int32_t keys = prefill_keys(t, t.ntok, a.step), j0 = cur.j0, j1 = cur.j1;
         const int32_t *row = a.tables + (int64_t)t.seq * a.max_blocks;
         // Thread i < 64: the table entry of key i of unit j (0 without that
         // key), and the slot it makes (-1: no key, or a bad entry: zeros).
@@ -207,7 +211,7 @@ __global__ void __launch_bounds__(kSimtThreads, D == 256 ? 1 : 2)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = ty * 4 + i;
-            last[i] = r < nrow ? t.p0 + r / a.G : -1;
+            last[i] = r < nrow ? t.p0 + a.step * (r / a.G) : -1;
             m[i] = -INFINITY;
             l[i] = 0.f;
 #pragma unroll

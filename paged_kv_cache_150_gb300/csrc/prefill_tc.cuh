@@ -98,11 +98,11 @@ struct TcSegment {
     template <class Walk>
     __device__ __forceinline__ TcSegment(const PrefillArgs &a, const Walk &cur) {
         t = cur.t;
-        keys = t.p0 + t.ntok;
+        keys = prefill_keys(t, t.ntok, a.step);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int32_t n = min(t.ntok, (i + 1) * a.tq1);  // tokens up to this row tile's end
-            const int32_t ki = t.ntok > i * a.tq1 ? max(t.p0 + n, 0) : 0;
+            const int32_t ki = t.ntok > i * a.tq1 ? max(prefill_keys(t, n, a.step), 0) : 0;
             je[i] = min(cur.j1, (int32_t)(((uint32_t)ki + kTcKeys - 1) / kTcKeys));  // the sum may pass 2^31
         }
         jend = max(je[0], je[1]);
@@ -444,7 +444,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
         const int32_t tok = i * a.tq1 + tok_r;
         const bool valid = tok_r < a.tq1 && tok < sg.t.ntok;
         const bool warp_rows = __any_sync(0xffffffffu, valid);
-        const int32_t last = sg.t.p0 + tok;
+        const int32_t last = sg.t.p0 + a.step * tok;  // last key that this row sees
         const int32_t je = sg.je[i];
         if (sg.jend > cur.j0) ++segs;
         float m = -INFINITY, l = 0.f;
