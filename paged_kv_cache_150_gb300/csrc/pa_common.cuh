@@ -257,6 +257,15 @@ __device__ __forceinline__ void tma_load_4d_hint(uint32_t dst, const void *tmap,
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const void *tmap, uint32_t bar, int32_t c0, int32_t c1,
+                                                 int32_t c2, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+        "l"(tmap), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+        : "memory");
+}
+
 // L2 policy that evicts these lines first: KV tiles are read once per step.
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
     uint64_t p;

@@ -14,7 +14,7 @@ namespace {
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 bool tc_supported(const pa_cache_desc_t *c, int G) {
-    return c->dtype == PA_BF16 && c->layout == PA_LAYOUT_ROW && (c->head_dim == 64 || c->head_dim == 128) &&
+    return (c->dtype == PA_BF16 || c->dtype == PA_FP8_E4M3_BLOCK) && c->layout == PA_LAYOUT_ROW && (c->head_dim == 64 || c->head_dim == 128) &&
            c->block_size % 8 == 0 && G <= 64;
 }
 
@@ -23,7 +23,8 @@ int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 // Maps of the tcgen05 kernel: K and V as {64 elements, NB * B rows, D / 64
 // panels, Hk heads} in boxes of gran rows of one panel and head; q as {64, D / 64
 // panels, H, T} in boxes of tq1 tokens x G heads of one panel.  All boxes land
-// as 128-byte lines with the 128-byte swizzle.
+// as 128-byte lines with the 128-byte swizzle.  An 8-bit cache: K and V as {D
+// codes, NB * B rows, Hk heads} in boxes of gran rows of one head, not swizzled.
 bool encode_tc_maps(CUtensorMap *q, CUtensorMap *k, CUtensorMap *v, const PrefillArgs &a, const pa_cache_desc_t *c,
                     int gran) {
     auto fn = encode_fn();
@@ -36,13 +37,23 @@ bool encode_tc_maps(CUtensorMap *q, CUtensorMap *k, CUtensorMap *v, const Prefil
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
+    const bool fp8 = c->dtype == PA_FP8_E4M3_BLOCK;
+    auto codes = [&](CUtensorMap *m, const void *base) {
+        const cuuint64_t dims[3] = {D, (cuuint64_t)c->num_blocks * c->block_size, Hk}, strides[2] = {Hk * D, D};
+        const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)gran, 1};
+        return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
     const cuuint64_t kd[4] = {64, (cuuint64_t)c->num_blocks * c->block_size, D / 64, Hk};
     const cuuint64_t ks[3] = {Hk * D * 2, 128, D * 2};
     const cuuint32_t kb[4] = {64, (cuuint32_t)gran, 1, 1};
     const cuuint64_t qd[4] = {64, D / 64, (cuuint64_t)a.H, (cuuint64_t)a.T};
     const cuuint64_t qs[3] = {128, D * 2, (cuuint64_t)a.H * D * 2};
     const cuuint32_t qb[4] = {64, 1, (cuuint32_t)a.G, (cuuint32_t)a.tq1};
-    return enc(k, a.k_cache, kd, ks, kb) && enc(v, a.v_cache, kd, ks, kb) && enc(q, a.q, qd, qs, qb);
+    if (!(fp8 ? codes(k, a.k_cache) && codes(v, a.v_cache) : enc(k, a.k_cache, kd, ks, kb) && enc(v, a.v_cache, kd, ks, kb)))
+        return false;
+    return enc(q, a.q, qd, qs, qb);
 }
 
 }  // namespace
@@ -50,7 +61,8 @@ bool encode_tc_maps(CUtensorMap *q, CUtensorMap *k, CUtensorMap *v, const Prefil
 pa_status_t prefill_layout(bool tc, const pa_cache_desc_t *c, int32_t N, int32_t T, int32_t H, int32_t num_splits,
                            PrefillPlan *p) {
     const int32_t G = H / c->num_kv_heads;
-    const void *fn = tc ? prefill_tc_ptr(c->head_dim, &p->smem)
+    int threads = kSimtThreads;
+    const void *fn = tc ? prefill_tc_ptr(c->head_dim, c->dtype == PA_FP8_E4M3_BLOCK, &p->smem, &threads)
                         : prefill_simt_ptr(c->dtype, c->head_dim, c->layout, &p->smem);
     if (!fn) return PA_ERR_UNSUPPORTED;
     p->tc = tc;
@@ -58,7 +70,7 @@ pa_status_t prefill_layout(bool tc, const pa_cache_desc_t *c, int32_t N, int32_t
     p->nrt = tc ? 2 : 1;
     p->kt = tc ? kTcKeys : kSimtKeys;
     p->extra = tc ? kTcExtra : kSimtExtra;
-    p->threads = tc ? kTcThreads : kSimtThreads;
+    p->threads = threads;
     p->tq1 = p->rows / G;
     const int64_t tq = (int64_t)p->tq1 * p->nrt;
     const int64_t tiles = (int64_t)N + T / tq;  // sum of ceil(n_i / tq)
@@ -158,7 +170,8 @@ pa_status_t prefill_launch(const PrefillPlan &p, const pa_cache_desc_t *c, Prefi
     if ((st = prefill_launch_plan(a, s)) != PA_OK) return st;
     void *args[] = {&a};
     size_t smem;
-    const void *fn = p.tc ? prefill_tc_ptr(c->head_dim, &smem)
+    int threads;
+    const void *fn = p.tc ? prefill_tc_ptr(c->head_dim, c->dtype == PA_FP8_E4M3_BLOCK, &smem, &threads)
                           : prefill_simt_ptr(c->dtype, c->head_dim, c->layout, &smem);
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)

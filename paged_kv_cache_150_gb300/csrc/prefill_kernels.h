@@ -24,8 +24,8 @@ struct PrefillPlan {
 // (q and out: fp32 for PA_F32, else bf16), head_dim and layout; nullptr if none.
 const void *prefill_simt_ptr(int cache_dtype, int D, int layout, size_t *smem);
 
-// prefill_tc_kernel for head_dim 64 or 128.
-const void *prefill_tc_ptr(int D, size_t *smem);
+// prefill_tc_kernel for head_dim 64 or 128, over a bf16 cache or an 8-bit one with block scales.
+const void *prefill_tc_ptr(int D, bool fp8, size_t *smem, int *threads);
 
 // Lays out a call of the CUDA-core kernel (tc false) or the tcgen05 one.
 pa_status_t prefill_layout(bool tc, const pa_cache_desc_t *c, int32_t N, int32_t T, int32_t H, int32_t num_splits,

@@ -36,6 +36,7 @@
 #include <cuda.h>  // CUtensorMap
 
 #include "decode_merge.cuh"
+#include "fp8_codec.cuh"
 #include "prefill_plan.cuh"
 #include "tc_ptx.cuh"
 
@@ -47,16 +48,27 @@ constexpr unsigned long long kTcUnitNs = 4096;
 // each (a row's 128 scores stay in registers), the third one keeps 88:
 // 256 x 208 + 128 x 88 = 384 x 168.
 constexpr int kTcSoftmaxRegs = 208, kTcOtherRegs = 88;
+// The 8-bit form has a fourth warpgroup, the converters: 512 threads x 128 at
+// launch, 256 x kTcSoftmaxRegs8 + 128 x (kTcOtherRegs8 + kTcConvertRegs) = 512 x 128.
+constexpr int kTcThreads8 = 512, kTcSoftmaxRegs8 = 200, kTcOtherRegs8 = 64, kTcConvertRegs = 48;
 
-template <int D>
+// kFp8: codes arrive in a ring of their own (raw) and are turned into the bf16
+// units of the ring that the MMAs read.
+template <int D, bool kFp8>
 struct TcPrefill {
     static constexpr int kPanels = D / 64;
     static constexpr uint32_t kPanel = 128 * 128;            // 128 rows of 64 bf16
     static constexpr uint32_t kTile = kPanels * kPanel;      // Q row tile, K or V unit
-    static constexpr int kStages = D == 128 ? 5 : 8;         // ring of K and V units
+    static constexpr int kStages = kFp8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);  // ring of K and V units
+    static constexpr int kRaw = kFp8 ? (D == 128 ? 4 : 8) : 0;  // units of codes on their way (64 KiB)
+    static constexpr uint32_t kRawTile = 128 * D;
+    static constexpr int kThreads = kFp8 ? kTcThreads8 : kTcThreads;
     static constexpr uint32_t kRing = 2 * kTile;             // after the two Q row tiles
-    static constexpr uint32_t kBars = kRing + kStages * kTile;
-    static constexpr uint32_t kBytes = kBars + 256 + 3 * D * 4;  // barriers; columns with odd values
+    static constexpr uint32_t kRawRing = kRing + kStages * kTile;
+    static constexpr uint32_t kBars = kRawRing + kRaw * kRawTile;
+    static constexpr uint32_t kRawBars = kBars + 256 + 3 * D * 4;  // barriers; columns with odd values
+    static constexpr uint32_t kMeta = kRawBars + 16 * kRaw;  // per raw unit: scale bytes of its boxes, their number
+    static constexpr uint32_t kBytes = kMeta + 32 * kRaw;
     static constexpr size_t kSmem = kBytes + 1024;           // the base is aligned to 1024
     static constexpr uint32_t kS = 0, kO = 256;              // tensor-memory columns: S0, S1, O0, O1
 };
@@ -64,7 +76,8 @@ struct TcPrefill {
 // Barriers of a CTA, in shared memory.
 struct TcBars {
     uint32_t q_full, q_free, v_go, v_ok, kv_full, kv_free, s_full, p_full, o_full, o_free;  // addresses; arrays 8 bytes apart
-    __device__ __forceinline__ TcBars(uint32_t base, int stages) {
+    uint32_t raw_full, raw_free;
+    __device__ __forceinline__ TcBars(uint32_t base, int stages, uint32_t raw, int raw_stages) {
         q_full = base;
         q_free = base + 8;
         s_full = base + 16;
@@ -75,6 +88,8 @@ struct TcBars {
         v_ok = base + 88;
         kv_full = base + 96;
         kv_free = kv_full + 8 * (uint32_t)stages;
+        raw_full = raw;
+        raw_free = raw + 8 * (uint32_t)raw_stages;
     }
 };
 
@@ -109,6 +124,15 @@ struct TcSegment {
     }
 };
 
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, const uint4 &v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // ----------------------------------------------------------- TMA producers
 // One warp for K (and the Q rows), one for V.  Entry n of the ring is K of a
 // unit for even n, V for odd n.  A unit is 128 / gran boxes per panel, gran =
@@ -120,7 +144,7 @@ template <int D, bool kIsV>
 __device__ __forceinline__ void tc_producer(const PrefillArgs &a, uint8_t *smem, const TcBars &bar,
                                             const CUtensorMap *tmq, const CUtensorMap *tm, int32_t gran,
                                             int32_t c, int lane) {
-    using L = TcPrefill<D>;
+    using L = TcPrefill<D, false>;
     if (lane == 0) {
         if (!kIsV) prefetch_tmap(tmq);
         prefetch_tmap(tm);
@@ -190,6 +214,174 @@ __device__ __forceinline__ void tc_producer(const PrefillArgs &a, uint8_t *smem,
     }
 }
 
+// ------------------------------------------------- 8-bit cache: producers
+// As above, but an entry n is 128 rows of D codes in the raw ring, a box one
+// block's rows (gran of them), with the box's scale byte brought by its lane: the
+// byte is asked for a unit ahead, the table entry two.  The K warp ends the
+// ring with an entry of kRawEnd boxes, at which the converters stop.
+constexpr int32_t kRawEnd = -1;
+
+template <int D, bool kIsV>
+__device__ __forceinline__ void tc_producer8(const PrefillArgs &a, uint8_t *smem, const TcBars &bar,
+                                             const CUtensorMap *tmq, const CUtensorMap *tm, int32_t gran,
+                                             int32_t c, int lane) {
+    using L = TcPrefill<D, true>;
+    if (lane == 0) {
+        if (!kIsV) prefetch_tmap(tmq);
+        prefetch_tmap(tm);
+    }
+    const uint32_t q_dst = smem_u32(smem), raw = q_dst + L::kRawRing, meta = q_dst + L::kMeta;
+    const int32_t nbm = kTcKeys / gran;  // boxes of a unit (at most 16), one per lane
+    const uint8_t *scales = kIsV ? a.v_scale : a.k_scale;
+    const uint64_t policy = l2_policy_evict_first();
+    uint32_t n = kIsV ? 1 : 0, segs = 0;  // next entry, segments with units
+    bool abort = false;
+    PrefillWalk<false> cur;
+    if (cur.init(a, c)) {
+        do {
+            const TcSegment sg(a, cur);
+            if (sg.jend <= cur.j0) continue;
+            const int32_t *row = a.tables + (int64_t)sg.t.seq * a.max_blocks;
+            auto has_key = [&](int32_t j) { return lane < nbm && (int64_t)j * kTcKeys + lane * gran < sg.keys; };
+            auto entry = [&](int32_t j) { return j < sg.jend && has_key(j) ? row[(j * kTcKeys + lane * gran) / a.B] : 0; };
+            auto scale_at = [&](int32_t p) -> uint32_t {  // a bad entry: the smallest scale, of codes that are zeros
+                return lane < nbm && p >= 0 && p < a.NB ? scales[(int64_t)p * a.Hk + cur.kvh] : 0u;
+            };
+            int32_t phys = entry(cur.j0), phys_1 = entry(cur.j0 + 1);
+            if (!kIsV) {
+                if (segs > 0) tc_wait(bar.q_free, (segs - 1) & 1, abort, a.err);
+                if (__any_sync(0xffffffffu, abort)) break;
+                if (lane == 0) {
+                    const int32_t nrt = sg.t.ntok > a.tq1 ? 2 : 1;
+                    mbar_arrive_expect_tx(bar.q_full, (uint32_t)(nrt * L::kPanels * a.tq1 * a.G) * 128u);
+                    for (int32_t i = 0; i < nrt; ++i)
+                        for (int32_t p = 0; p < L::kPanels; ++p)
+                            tma_load_4d(q_dst + i * L::kTile + p * L::kPanel, tmq, bar.q_full, 0, p, cur.kvh * a.G,
+                                        sg.t.row0 + i * a.tq1);
+                }
+            }
+            uint32_t sc = scale_at(phys);
+            ++segs;
+            for (int32_t j = cur.j0; j < sg.jend; ++j, n += 2) {
+                const bool box = has_key(j);
+                int32_t at = a.NB * a.B;  // a bad entry reads zeros: the box lies past the pool
+                if (phys >= 0 && phys < a.NB)
+                    at = phys * a.B + (j * kTcKeys + lane * gran) % a.B;
+                else if (box)
+                    atomicOr(a.err, kErrBounds);
+                const uint32_t sc_now = sc;
+                phys = phys_1;
+                sc = scale_at(phys);
+                phys_1 = entry(j + 2);
+                const uint32_t boxes = (uint32_t)__popc(__ballot_sync(0xffffffffu, box));
+                const uint32_t st = n % L::kRaw;
+                if (n >= L::kRaw) tc_wait(bar.raw_free + 8 * st, (n / L::kRaw + 1) & 1, abort, a.err);
+                if (__any_sync(0xffffffffu, abort)) break;
+                if (box) asm volatile("st.shared.u8 [%0], %1;" ::"r"(meta + st * 32 + (uint32_t)lane), "r"(sc_now) : "memory");
+                if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(meta + st * 32 + 16), "r"(boxes) : "memory");
+                __syncwarp();  // in place before lane 0 publishes the entry
+                if (lane == 0) mbar_arrive_expect_tx(bar.raw_full + 8 * st, boxes * (uint32_t)gran * D);
+                __syncwarp();
+                if (box)
+                    tma_load_3d_hint(raw + st * L::kRawTile + (uint32_t)(lane * gran) * D, tm, bar.raw_full + 8 * st, 0, at,
+                                     cur.kvh, policy);
+            }
+            if (__any_sync(0xffffffffu, abort)) break;
+        } while (cur.next(a));
+    }
+    // This warp's copies in flight, and the issuer's last arrivals on the free
+    // barriers, land before the CTA may exit (the copies before the end entry
+    // takes its barrier a phase on).
+    bool late = false;
+    const uint32_t total = n - (kIsV ? 1u : 0u), mine = kIsV ? 1u : 0u;
+    for (uint32_t k = (total > (uint32_t)L::kRaw ? total - L::kRaw : 0) + mine; k < total; k += 2)
+        tc_wait(bar.raw_full + 8 * (k % L::kRaw), (k / L::kRaw) & 1, late, a.err);
+    if (!kIsV) {
+        static_assert(L::kRaw % 2 == 0, "K's entries and V's have slots of their own");
+        const uint32_t st = n % L::kRaw;
+        if (n >= L::kRaw) tc_wait(bar.raw_free + 8 * st, (n / L::kRaw + 1) & 1, abort, a.err);
+        if (lane == 0 && !abort) {
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(meta + st * 32 + 16), "r"(kRawEnd) : "memory");
+            mbar_arrive(bar.raw_full + 8 * st);
+        }
+    }
+    for (uint32_t k = total > (uint32_t)L::kStages ? total - L::kStages : 0; k < total; ++k)
+        if ((k & 1u) == mine) tc_wait(bar.kv_free + 8 * (k % L::kStages), (k / L::kStages) & 1, late, a.err);
+    if (!kIsV && segs > 0) {
+        tc_wait(bar.q_full, (segs - 1) & 1, late, a.err);
+        tc_wait(bar.q_free, (segs - 1) & 1, late, a.err);
+    }
+}
+
+// ------------------------------------------------------- 8-bit: converters
+// Four warps turn entry n of the raw ring into entry n of the bf16 ring: code *
+// 2^(byte - 127), in fp32 and then bf16 (one rounding, of values that bf16 holds
+// exactly unless they leave its range).  A thread takes 16 codes at a time (a
+// 16-byte load), eight consecutive lanes a 128-byte piece, and stores them as
+// two 16-byte chunks of a swizzled 128-byte line; in the second panel the odd
+// chunk goes first, so that eight lanes' stores fall into distinct banks (in one
+// panel, head_dim 64, rows alternate by themselves).  Per two codes: a
+// conversion to fp16, two to fp32, a packed product, a packed conversion.
+__device__ __forceinline__ void codes_bf16(uint32_t w, uint64_t s2, uint32_t &lo, uint32_t &hi) {
+    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+    const float2 x = __half22float2(__half2(a)), y = __half22float2(__half2(b));
+    float u, v;
+    f32x2_get(mul_f32x2(f32x2(x.x, x.y), s2), u, v);
+    lo = pack_bf16x2(u, v);
+    f32x2_get(mul_f32x2(f32x2(y.x, y.y), s2), u, v);
+    hi = pack_bf16x2(u, v);
+}
+
+template <int D>
+__device__ __forceinline__ void tc_converter(const PrefillArgs &a, uint8_t *smem, const TcBars &bar, int32_t gran, int tid) {
+    using L = TcPrefill<D, true>;
+    constexpr int kChunks = D / 16, kRowsPass = 128 / kChunks;  // 16-code pieces of a row, rows of the four warps at once
+    const uint32_t raw = smem_u32(smem) + L::kRawRing, ring = smem_u32(smem) + L::kRing;
+    const uint8_t *meta = smem + L::kMeta;
+    const int lane = tid & 31, r0 = tid / kChunks, ch = tid % kChunks;
+    const int shift = __ffs(gran) - 1;  // gran = gcd(block size, 128)
+    const uint32_t src = (uint32_t)tid * 16u;
+    const uint32_t line = (uint32_t)(ch >> 2) * L::kPanel + (uint32_t)r0 * 128u;
+    // rows of a thread are a multiple of 8 apart: their swizzle is the same
+    const uint32_t odd = D == 128 ? (uint32_t)(ch >> 2) : 0u;  // the chunk stored first
+    const uint32_t c0 = ((uint32_t)(ch & 3) * 2u + odd) ^ (uint32_t)(r0 & 7), c1 = c0 ^ 1u;
+    bool abort = false;
+    for (uint32_t n = 0;; ++n) {
+        const uint32_t rs = n % L::kRaw, st = n % L::kStages;
+        tc_wait(bar.raw_full + 8 * rs, (n / L::kRaw) & 1, abort, a.err, a.wait_ns);
+        const int32_t boxes = *reinterpret_cast<const volatile int32_t *>(meta + rs * 32 + 16);
+        if (__any_sync(0xffffffffu, abort || boxes == kRawEnd)) break;
+        if (n >= L::kStages) tc_wait(bar.kv_free + 8 * st, (n / L::kStages + 1) & 1, abort, a.err, a.wait_ns);
+        if (__any_sync(0xffffffffu, abort)) break;
+        const int32_t rows = boxes * gran;
+        const uint32_t from = raw + rs * L::kRawTile + src, to = ring + st * L::kTile + line;
+#pragma unroll 2
+        for (int p = 0; p < 128 / kRowsPass; ++p) {
+            const int row = p * kRowsPass + r0;
+            if (row < rows) {
+                const uint4 w = lds128(from + (uint32_t)p * (kRowsPass * D));
+                const float s = scale_of(*reinterpret_cast<const volatile uint8_t *>(meta + rs * 32 + (row >> shift)));
+                const uint64_t s2 = f32x2(s, s);
+                uint4 x, y;
+                codes_bf16(w.x, s2, x.x, x.y);
+                codes_bf16(w.y, s2, x.z, x.w);
+                codes_bf16(w.z, s2, y.x, y.y);
+                codes_bf16(w.w, s2, y.z, y.w);
+                const uint32_t at = to + (uint32_t)p * (kRowsPass * 128);
+                sts128(at + (c0 << 4), odd ? y : x);
+                sts128(at + (c1 << 4), odd ? x : y);
+            }
+        }
+        fence_proxy_async_smem();  // the MMAs read the unit through the async proxy
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(bar.kv_full + 8 * st);
+            mbar_arrive(bar.raw_free + 8 * rs);
+        }
+    }
+}
+
 // --------------------------------------------------------------- V's guard
 // 0 x V is not 0 where V is not finite, and the products run over whole units:
 // keys that only some rows of a tile see (its own tokens, from position
@@ -215,24 +407,16 @@ template <int D>
 __device__ __forceinline__ uint32_t v_chunk(uint32_t vbase, int e) {  // address of 16-byte chunk e % (D / 8) of row e / (D / 8)
     constexpr int kChunks = D / 8;
     const int r = e / kChunks, ch = e % kChunks;
-    return vbase + (uint32_t)(ch >> 3) * TcPrefill<D>::kPanel + (uint32_t)r * 128u +
+    return vbase + (uint32_t)(ch >> 3) * TcPrefill<D, false>::kPanel + (uint32_t)r * 128u +
            (uint32_t)(((ch & 7) ^ (r & 7)) << 4);
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ void sts128(uint32_t addr, const uint4 &v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 // Sign bits of the halves whose exponent is all ones (bf16 infinities and NaN).
 __device__ __forceinline__ uint32_t odd_bits(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
-template <int D>
+template <int D, bool kFp8>
 __device__ __forceinline__ void tc_guard(const PrefillArgs &a, uint8_t *smem, const TcBars &bar, const OddColumns &odd,
                                          int32_t c, int lane) {
-    using L = TcPrefill<D>;
+    using L = TcPrefill<D, kFp8>;
     constexpr int kChunks = D / 8;
     const uint32_t ring = smem_u32(smem) + L::kRing;
     uint32_t n = 1, segs = 0, units = 0;  // ring entry of V, segments, guarded units
@@ -323,10 +507,10 @@ __device__ __forceinline__ int32_t uniform(int32_t x) { return __shfl_sync(0xfff
 // One warp; one elected lane issues.  MMAs of one thread complete in order, so S of a
 // unit may be computed over the P of the one before (its O += P V was issued
 // earlier), and a row tile's S being complete says that its earlier O is too.
-template <int D>
+template <int D, bool kFp8>
 __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, const TcBars &bar, uint32_t tmem,
                                           int32_t c, int lane) {
-    using L = TcPrefill<D>;
+    using L = TcPrefill<D, kFp8>;
     constexpr uint32_t IDESC_S = tc_idesc_bf16(128, kTcKeys, false, false);
     constexpr uint32_t IDESC_O = tc_idesc_bf16(128, D, false, true);
     const uint32_t ring = smem_u32(smem) + L::kRing;
@@ -424,11 +608,11 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
 
 // ----------------------------------------------------------------- softmax
 // Four warps per row tile; a thread owns one query row (tensor-memory lane).
-template <int D>
+template <int D, bool kFp8>
 __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &bar, uint32_t tmem,
                                            const OddColumns &odd, int32_t c,
                                            int i, int warp, int lane) {
-    using L = TcPrefill<D>;
+    using L = TcPrefill<D, kFp8>;
     const int r = warp * 32 + lane;  // row of the row tile
     const uint32_t t_lane = (uint32_t)(warp * 32) << 16;
     const uint32_t tS = tmem + L::kS + i * 128 + t_lane, tO = tmem + L::kO + i * D + t_lane;
@@ -580,15 +764,15 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
     } while (cur.next(a));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kTcThreads, 1)
+template <int D, bool kFp8>
+__global__ void __launch_bounds__(TcPrefill<D, kFp8>::kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const __grid_constant__ PrefillArgs a,
                       const int32_t gran) {
-    using L = TcPrefill<D>;
+    using L = TcPrefill<D, kFp8>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    const TcBars bar(smem_u32(smem + L::kBars), L::kStages);
+    const TcBars bar(smem_u32(smem + L::kBars), L::kStages, smem_u32(smem + L::kRawBars), L::kRaw);
     uint32_t *tmem_slot = (uint32_t *)(smem + L::kBars + 248);
     const OddColumns odd{(int32_t *)(smem + L::kBars + 256), (int32_t *)(smem + L::kBars + 240)};
     static_assert(96 + 16 * L::kStages <= 240, "the barriers fit");
@@ -605,13 +789,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(bar.o_free + 8 * i, 4);
         }
         for (int s = 0; s < L::kStages; ++s) {
-            mbar_init(bar.kv_full + 8 * s, 1);
+            mbar_init(bar.kv_full + 8 * s, kFp8 ? 4 : 1);
             mbar_init(bar.kv_free + 8 * s, 1);
+        }
+        for (int s = 0; s < L::kRaw; ++s) {
+            mbar_init(bar.raw_full + 8 * s, 1);
+            mbar_init(bar.raw_free + 8 * s, 4);
         }
         odd.segment[0] = odd.segment[1] = 0;
         fence_mbarrier_init();
     }
-    for (int e = tid; e < 3 * D; e += kTcThreads) odd.first[e] = OddColumns::kNone;
+    for (int e = tid; e < 3 * D; e += L::kThreads) odd.first[e] = OddColumns::kNone;
     if (warp == 8) tmem_alloc(smem_u32(tmem_slot), 512);
     tc_fence_before();
     __syncthreads();
@@ -621,18 +809,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     grid_launch_dependents();
     const int32_t c = blockIdx.x;
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcSoftmaxRegs));
-        tc_softmax<D>(a, bar, tmem, odd, c, warp >> 2, warp & 3, lane);
-    } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcOtherRegs));
-        if (warp == 8)
-            tc_issuer<D>(a, smem, bar, tmem, c, lane);
-        else if (warp == 9)
-            tc_producer<D, false>(a, smem, bar, &tmq, &tmk, gran, c, lane);
-        else if (warp == 10)
-            tc_producer<D, true>(a, smem, bar, &tmq, &tmv, gran, c, lane);
-        else
-            tc_guard<D>(a, smem, bar, odd, c, lane);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFp8 ? kTcSoftmaxRegs8 : kTcSoftmaxRegs));
+        tc_softmax<D, kFp8>(a, bar, tmem, odd, c, warp >> 2, warp & 3, lane);
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFp8 ? kTcOtherRegs8 : kTcOtherRegs));
+        if (warp == 8) {
+            tc_issuer<D, kFp8>(a, smem, bar, tmem, c, lane);
+        } else if (warp == 9) {
+            if constexpr (kFp8)
+                tc_producer8<D, false>(a, smem, bar, &tmq, &tmk, gran, c, lane);
+            else
+                tc_producer<D, false>(a, smem, bar, &tmq, &tmk, gran, c, lane);
+        } else if (warp == 10) {
+            if constexpr (kFp8)
+                tc_producer8<D, true>(a, smem, bar, &tmq, &tmv, gran, c, lane);
+            else
+                tc_producer<D, true>(a, smem, bar, &tmq, &tmv, gran, c, lane);
+        } else {
+            tc_guard<D, kFp8>(a, smem, bar, odd, c, lane);
+        }
+    } else if constexpr (kFp8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcConvertRegs));
+        tc_converter<D>(a, smem, bar, gran, tid - 384);
     }
     // The softmax warps have waited for the last o_full, which every MMA
     // precedes: nothing uses the tensor memory any more.
