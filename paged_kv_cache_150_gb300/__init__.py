@@ -644,6 +644,8 @@ def pa_extend_tables(tables, lens, free_list, free_count, new_lens, block_size, 
         raise ValueError("new_lens must be [num_reqs], at most one request for each row")
     width = state.max_blocks_per_row if batch_width is None else int(batch_width)
     max_tokens = int(max_tokens)
+    if width <= 0 or max_tokens < 0:
+        raise ValueError("batch_width must be positive and max_tokens not negative")
     shapes = ((N, width), (N,), (N + 1,), (max_tokens,))
     if out is None:
         out = tuple(torch.empty(s, dtype=i32, device=tables.device) for s in shapes)
