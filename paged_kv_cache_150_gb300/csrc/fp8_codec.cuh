@@ -52,6 +52,13 @@ __device__ __forceinline__ float4 decode4(uint32_t w) {
     return make_float4(a.x, a.y, b.x, b.y);
 }
 
+// The codes of a word's low and high half to fp16 (exact).
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
 // An 8-bit pool's descriptor: row layout, a scale per token or per block.
 inline pa_status_t validate_fp8_desc(const pa_cache_desc_t *c) {
     if (!c) return PA_ERR_INVALID_ARG;

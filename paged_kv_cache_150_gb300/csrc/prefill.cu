@@ -24,7 +24,8 @@ int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 // panels, Hk heads} in boxes of gran rows of one panel and head; q as {64, D / 64
 // panels, H, T} in boxes of tq1 tokens x G heads of one panel.  All boxes land
 // as 128-byte lines with the 128-byte swizzle.  An 8-bit cache: K and V as {D
-// codes, NB * B rows, Hk heads} in boxes of gran rows of one head, not swizzled.
+// codes, NB * B rows, Hk heads} in boxes of gran rows of one head, their 128-byte
+// lines swizzled at head_dim 128.
 bool encode_tc_maps(CUtensorMap *q, CUtensorMap *k, CUtensorMap *v, const PrefillArgs &a, const pa_cache_desc_t *c,
                     int gran) {
     auto fn = encode_fn();
@@ -42,7 +43,8 @@ bool encode_tc_maps(CUtensorMap *q, CUtensorMap *k, CUtensorMap *v, const Prefil
         const cuuint64_t dims[3] = {D, (cuuint64_t)c->num_blocks * c->block_size, Hk}, strides[2] = {Hk * D, D};
         const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)gran, 1};
         return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, one,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
     const cuuint64_t kd[4] = {64, (cuuint64_t)c->num_blocks * c->block_size, D / 64, Hk};

@@ -50,7 +50,7 @@ constexpr unsigned long long kTcUnitNs = 4096;
 constexpr int kTcSoftmaxRegs = 208, kTcOtherRegs = 88;
 // The 8-bit form has a fourth warpgroup, the converters: 512 threads x 128 at
 // launch, 256 x kTcSoftmaxRegs8 + 128 x (kTcOtherRegs8 + kTcConvertRegs) = 512 x 128.
-constexpr int kTcThreads8 = 512, kTcSoftmaxRegs8 = 200, kTcOtherRegs8 = 64, kTcConvertRegs = 48;
+constexpr int kTcThreads8 = 512, kTcSoftmaxRegs8 = 192, kTcOtherRegs8 = 64, kTcConvertRegs = 64;
 
 // kFp8: codes arrive in a ring of their own (raw) and are turned into the bf16
 // units of the ring that the MMAs read.
@@ -67,9 +67,9 @@ struct TcPrefill {
     static constexpr uint32_t kRawRing = kRing + kStages * kTile;
     static constexpr uint32_t kBars = kRawRing + kRaw * kRawTile;
     static constexpr uint32_t kRawBars = kBars + 256 + 3 * D * 4;  // barriers; columns with odd values
-    static constexpr uint32_t kMeta = kRawBars + 16 * kRaw;  // per raw unit: scale bytes of its boxes, their number
-    static constexpr uint32_t kBytes = kMeta + 32 * kRaw;
-    static constexpr size_t kSmem = kBytes + 1024;           // the base is aligned to 1024
+    static constexpr uint32_t kMeta = kRawBars + 16 * kRaw, kMetaBytes = 80;  // per raw unit: scales of its (up to 16) boxes, their number
+    static constexpr uint32_t kBytes = kMeta + kMetaBytes * kRaw;
+    static constexpr size_t kSmem = kBytes;
     static constexpr uint32_t kS = 0, kO = 256;              // tensor-memory columns: S0, S1, O0, O1
 };
 
@@ -128,6 +128,14 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
+}
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void sts_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t addr, const uint4 &v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -277,8 +285,8 @@ __device__ __forceinline__ void tc_producer8(const PrefillArgs &a, uint8_t *smem
                 const uint32_t st = n % L::kRaw;
                 if (n >= L::kRaw) tc_wait(bar.raw_free + 8 * st, (n / L::kRaw + 1) & 1, abort, a.err);
                 if (__any_sync(0xffffffffu, abort)) break;
-                if (box) asm volatile("st.shared.u8 [%0], %1;" ::"r"(meta + st * 32 + (uint32_t)lane), "r"(sc_now) : "memory");
-                if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(meta + st * 32 + 16), "r"(boxes) : "memory");
+                if (box) sts_u32(meta + st * L::kMetaBytes + (uint32_t)lane * 4, __float_as_uint(scale_of(sc_now)));
+                if (lane == 0) sts_u32(meta + st * L::kMetaBytes + 64, boxes);
                 __syncwarp();  // in place before lane 0 publishes the entry
                 if (lane == 0) mbar_arrive_expect_tx(bar.raw_full + 8 * st, boxes * (uint32_t)gran * D);
                 __syncwarp();
@@ -292,16 +300,16 @@ __device__ __forceinline__ void tc_producer8(const PrefillArgs &a, uint8_t *smem
     // This warp's copies in flight, and the issuer's last arrivals on the free
     // barriers, land before the CTA may exit (the copies before the end entry
     // takes its barrier a phase on).
+    static_assert(L::kRaw % 2 == 0, "K's entries and V's have slots of their own");
     bool late = false;
-    const uint32_t total = n - (kIsV ? 1u : 0u), mine = kIsV ? 1u : 0u;
+    const uint32_t mine = kIsV ? 1u : 0u, total = n - mine;
     for (uint32_t k = (total > (uint32_t)L::kRaw ? total - L::kRaw : 0) + mine; k < total; k += 2)
         tc_wait(bar.raw_full + 8 * (k % L::kRaw), (k / L::kRaw) & 1, late, a.err);
     if (!kIsV) {
-        static_assert(L::kRaw % 2 == 0, "K's entries and V's have slots of their own");
         const uint32_t st = n % L::kRaw;
         if (n >= L::kRaw) tc_wait(bar.raw_free + 8 * st, (n / L::kRaw + 1) & 1, abort, a.err);
         if (lane == 0 && !abort) {
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(meta + st * 32 + 16), "r"(kRawEnd) : "memory");
+            sts_u32(meta + st * L::kMetaBytes + 64, (uint32_t)kRawEnd);
             mbar_arrive(bar.raw_full + 8 * st);
         }
     }
@@ -314,18 +322,20 @@ __device__ __forceinline__ void tc_producer8(const PrefillArgs &a, uint8_t *smem
 }
 
 // ------------------------------------------------------- 8-bit: converters
-// Four warps turn entry n of the raw ring into entry n of the bf16 ring: code *
-// 2^(byte - 127), in fp32 and then bf16 (one rounding, of values that bf16 holds
-// exactly unless they leave its range).  A thread takes 16 codes at a time (a
-// 16-byte load), eight consecutive lanes a 128-byte piece, and stores them as
-// two 16-byte chunks of a swizzled 128-byte line; in the second panel the odd
-// chunk goes first, so that eight lanes' stores fall into distinct banks (in one
-// panel, head_dim 64, rows alternate by themselves).  Per two codes: a
-// conversion to fp16, two to fp32, a packed product, a packed conversion.
+// Four warps turn entry n of the raw ring into entry n of the bf16 ring: code * 2^(byte - 127), in fp32 and then bf16 (one
+// rounding, of values that bf16 holds exactly unless they leave its range).  Per
+// two codes: a conversion to fp16, two to fp32, a packed product, a packed
+// conversion.  (Shifting codes into place as bf16 and one packed bf16 product
+// took as many instructions with the look for NaN codes, and longer.)
+// A thread takes 16 codes at a time (a 16-byte load) and stores them as two
+// 16-byte chunks of a swizzled 128-byte line.  Eight lanes' loads and stores fall
+// into distinct banks: at head_dim 128 they hold four pieces each of rows r and r ^ 5,
+// whose swizzles differ in both the bit that parts the halves of a line of codes
+// and the one that parts even from odd chunks; at head_dim 64 of rows r and r + 1.
 __device__ __forceinline__ void codes_bf16(uint32_t w, uint64_t s2, uint32_t &lo, uint32_t &hi) {
-    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-    const float2 x = __half22float2(__half2(a)), y = __half22float2(__half2(b));
+    uint32_t a, b;
+    codes_f16(w, a, b);
+    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&a)), y = __half22float2(*reinterpret_cast<const __half2 *>(&b));
     float u, v;
     f32x2_get(mul_f32x2(f32x2(x.x, x.y), s2), u, v);
     lo = pack_bf16x2(u, v);
@@ -336,42 +346,50 @@ __device__ __forceinline__ void codes_bf16(uint32_t w, uint64_t s2, uint32_t &lo
 template <int D>
 __device__ __forceinline__ void tc_converter(const PrefillArgs &a, uint8_t *smem, const TcBars &bar, int32_t gran, int tid) {
     using L = TcPrefill<D, true>;
-    constexpr int kChunks = D / 16, kRowsPass = 128 / kChunks;  // 16-code pieces of a row, rows of the four warps at once
+    constexpr int kRowsPass = D == 128 ? 16 : 32;  // rows of the four warps at once
+    constexpr int kPasses = 128 / kRowsPass, kBatch = 2;  // loads of a thread in flight
     const uint32_t raw = smem_u32(smem) + L::kRawRing, ring = smem_u32(smem) + L::kRing;
-    const uint8_t *meta = smem + L::kMeta;
-    const int lane = tid & 31, r0 = tid / kChunks, ch = tid % kChunks;
+    const uint32_t meta = smem_u32(smem) + L::kMeta;
+    const int lane = tid & 31;
     const int shift = __ffs(gran) - 1;  // gran = gcd(block size, 128)
-    const uint32_t src = (uint32_t)tid * 16u;
-    const uint32_t line = (uint32_t)(ch >> 2) * L::kPanel + (uint32_t)r0 * 128u;
+    // D 128: the first two warps take the first panel, the others the second
+    const int r0 = D == 128 ? ((tid >> 2) & 8) | (((tid >> 3) & 3) ^ (tid & 4 ? 5 : 0)) : tid >> 2;
+    const uint32_t panel = D == 128 ? (uint32_t)tid >> 6 : 0u, ch = (uint32_t)tid & 3u;
+    const uint32_t src = D == 128 ? (uint32_t)r0 * 128u + (((panel * 4u + ch) ^ (uint32_t)(r0 & 7)) << 4) : (uint32_t)tid * 16u;
     // rows of a thread are a multiple of 8 apart: their swizzle is the same
-    const uint32_t odd = D == 128 ? (uint32_t)(ch >> 2) : 0u;  // the chunk stored first
-    const uint32_t c0 = ((uint32_t)(ch & 3) * 2u + odd) ^ (uint32_t)(r0 & 7), c1 = c0 ^ 1u;
+    const uint32_t dst = panel * L::kPanel + (uint32_t)r0 * 128u + (((ch * 2u) ^ (uint32_t)(r0 & 7)) << 4);
     bool abort = false;
     for (uint32_t n = 0;; ++n) {
         const uint32_t rs = n % L::kRaw, st = n % L::kStages;
         tc_wait(bar.raw_full + 8 * rs, (n / L::kRaw) & 1, abort, a.err, a.wait_ns);
-        const int32_t boxes = *reinterpret_cast<const volatile int32_t *>(meta + rs * 32 + 16);
+        const int32_t boxes = __float_as_int(lds_f32(meta + rs * L::kMetaBytes + 64));
         if (__any_sync(0xffffffffu, abort || boxes == kRawEnd)) break;
         if (n >= L::kStages) tc_wait(bar.kv_free + 8 * st, (n / L::kStages + 1) & 1, abort, a.err, a.wait_ns);
         if (__any_sync(0xffffffffu, abort)) break;
         const int32_t rows = boxes * gran;
-        const uint32_t from = raw + rs * L::kRawTile + src, to = ring + st * L::kTile + line;
-#pragma unroll 2
-        for (int p = 0; p < 128 / kRowsPass; ++p) {
-            const int row = p * kRowsPass + r0;
-            if (row < rows) {
-                const uint4 w = lds128(from + (uint32_t)p * (kRowsPass * D));
-                const float s = scale_of(*reinterpret_cast<const volatile uint8_t *>(meta + rs * 32 + (row >> shift)));
-                const uint64_t s2 = f32x2(s, s);
-                uint4 x, y;
-                codes_bf16(w.x, s2, x.x, x.y);
-                codes_bf16(w.y, s2, x.z, x.w);
-                codes_bf16(w.z, s2, y.x, y.y);
-                codes_bf16(w.w, s2, y.z, y.w);
-                const uint32_t at = to + (uint32_t)p * (kRowsPass * 128);
-                sts128(at + (c0 << 4), odd ? y : x);
-                sts128(at + (c1 << 4), odd ? x : y);
+        const uint32_t from = raw + rs * L::kRawTile + src, to = ring + st * L::kTile + dst, scales = meta + rs * L::kMetaBytes;
+        auto scale = [&](int p) { return lds_f32(scales + (uint32_t)(((p * kRowsPass + r0) >> shift) * 4)); };
+        uint4 w[kBatch];
+        float s[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) w[b] = lds128(from + (uint32_t)b * (kRowsPass * D)), s[b] = scale(b);
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {  // rows past the boxes: whatever the ring holds
+            if (p % kBatch == 0 && p * kRowsPass >= rows) break;
+            const uint4 v = w[p % kBatch];
+            const uint64_t s2 = f32x2(s[p % kBatch], s[p % kBatch]);
+            if (p + kBatch < kPasses) {
+                w[p % kBatch] = lds128(from + (uint32_t)(p + kBatch) * (kRowsPass * D));
+                s[p % kBatch] = scale(p + kBatch);
             }
+            uint4 x, y;
+            codes_bf16(v.x, s2, x.x, x.y);
+            codes_bf16(v.y, s2, x.z, x.w);
+            codes_bf16(v.z, s2, y.x, y.y);
+            codes_bf16(v.w, s2, y.z, y.w);
+            const uint32_t at = to + (uint32_t)p * (kRowsPass * 128);
+            sts128(at, x);
+            sts128(at ^ 16u, y);
         }
         fence_proxy_async_smem();  // the MMAs read the unit through the async proxy
         __syncwarp();
@@ -770,8 +788,12 @@ __global__ void __launch_bounds__(TcPrefill<D, kFp8>::kThreads, 1)
                       const __grid_constant__ CUtensorMap tmv, const __grid_constant__ PrefillArgs a,
                       const int32_t gran) {
     using L = TcPrefill<D, kFp8>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t smem_tc[];
+    uint8_t *smem = smem_tc;
+    if ((smem_u32(smem) & 1023) != 0) {  // no room to align it here (the layout fills the CTA's limit)
+        if (threadIdx.x == 0) atomicOr(a.err, kErrTimeout);
+        return;
+    }
     const TcBars bar(smem_u32(smem + L::kBars), L::kStages, smem_u32(smem + L::kRawBars), L::kRaw);
     uint32_t *tmem_slot = (uint32_t *)(smem + L::kBars + 248);
     const OddColumns odd{(int32_t *)(smem + L::kBars + 256), (int32_t *)(smem + L::kBars + 240)};
