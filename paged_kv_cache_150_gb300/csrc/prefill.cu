@@ -200,7 +200,7 @@ namespace {
 // Which call: its caches' kind and what a token sees.
 struct ChunkKind {
     bool fp8;      // pa_prefill_fp8: an 8-bit cache with block scales, q and out bf16
-    int32_t step;  // PrefillArgs
+    int32_t step, pair;  // PrefillArgs
 };
 
 // The call's plan; fits: its scale and alignment suit the tcgen05 kernel.
@@ -271,11 +271,13 @@ pa_status_t chunk_call(const ChunkKind &kind, void *out, const void *q, const vo
     a.T = num_tokens;
     a.H = num_heads;
     a.step = kind.step;
+    a.pair = kind.pair;
     a.scale_log2 = scale * 1.4426950408889634f;
     return prefill_launch(p, cache, a, workspace, (cudaStream_t)stream);
 }
 
-constexpr ChunkKind kPrefill{false, 1}, kCross{false, 0}, kPrefillFp8{true, 1};
+// pa_prefill keeps its order of summation: no shared tiles.
+constexpr ChunkKind kPrefill{false, 1, 0}, kCross{false, 0, 1}, kPrefillFp8{true, 1, 1};
 
 }  // namespace
 }  // namespace pa

@@ -65,6 +65,7 @@ struct PrefillArgs {
     int32_t max_tiles;    // capacity of tiles[] and cu[]
     float scale_log2;
     int32_t step;         // positions that each token sees more than the one before it: 1, or 0 where all see all (pa_cross)
+    int32_t pair;         // 1: both softmax warpgroups of the tcgen05 kernel share a tile of one row tile (TcSegment)
     int32_t few;          // 1: few tiles in many pieces, merged by prefill_merge_few_kernel
     int32_t *ctl;         // ctl[1]: cut tiles listed, ctl[2]: most query rows of one
     MergeEntry *merges;   // [C] the cut tiles (note_cut)

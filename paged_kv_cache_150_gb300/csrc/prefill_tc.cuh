@@ -50,7 +50,7 @@ constexpr unsigned long long kTcUnitNs = 4096;
 constexpr int kTcSoftmaxRegs = 208, kTcOtherRegs = 88;
 // The 8-bit form has a fourth warpgroup, the converters: 512 threads x 128 at
 // launch, 256 x kTcSoftmaxRegs8 + 128 x (kTcOtherRegs8 + kTcConvertRegs) = 512 x 128.
-constexpr int kTcThreads8 = 512, kTcSoftmaxRegs8 = 192, kTcOtherRegs8 = 64, kTcConvertRegs = 64;
+constexpr int kTcThreads8 = 512, kTcSoftmaxRegs8 = 200, kTcOtherRegs8 = 56, kTcConvertRegs = 56;
 
 // kFp8: codes arrive in a ring of their own (raw) and are turned into the bf16
 // units of the ring that the MMAs read.
@@ -67,8 +67,10 @@ struct TcPrefill {
     static constexpr uint32_t kRawRing = kRing + kStages * kTile;
     static constexpr uint32_t kBars = kRawRing + kRaw * kRawTile;
     static constexpr uint32_t kRawBars = kBars + 256 + 3 * D * 4;  // barriers; columns with odd values
-    static constexpr uint32_t kMeta = kRawBars + 16 * kRaw, kMetaBytes = 80;  // per raw unit: scales of its (up to 16) boxes, their number
+    static constexpr uint32_t kMl = kRawBars + 16 * kRaw;  // (m, l) of the second warpgroup's rows
+    static constexpr uint32_t kMeta = kMl + 1024, kMetaBytes = 48;  // per raw unit: scales of its (up to 16) boxes as bf16, their number
     static constexpr uint32_t kBytes = kMeta + kMetaBytes * kRaw;
+    static_assert(kBytes <= 227 * 1024, "a CTA's shared memory");
     static constexpr size_t kSmem = kBytes;
     static constexpr uint32_t kS = 0, kO = 256;              // tensor-memory columns: S0, S1, O0, O1
 };
@@ -76,7 +78,7 @@ struct TcPrefill {
 // Barriers of a CTA, in shared memory.
 struct TcBars {
     uint32_t q_full, q_free, v_go, v_ok, kv_full, kv_free, s_full, p_full, o_full, o_free;  // addresses; arrays 8 bytes apart
-    uint32_t raw_full, raw_free;
+    uint32_t x_full, raw_full, raw_free;
     __device__ __forceinline__ TcBars(uint32_t base, int stages, uint32_t raw, int raw_stages) {
         q_full = base;
         q_free = base + 8;
@@ -88,6 +90,7 @@ struct TcBars {
         v_ok = base + 88;
         kv_full = base + 96;
         kv_free = kv_full + 8 * (uint32_t)stages;
+        x_full = base + 232;
         raw_full = raw;
         raw_free = raw + 8 * (uint32_t)raw_stages;
     }
@@ -105,11 +108,18 @@ __device__ __forceinline__ void tc_wait(uint32_t bar, uint32_t parity, bool &abo
     }
 }
 
-// Units of a segment that each row tile takes: [j0, je[i]).
+// Units of a segment that each row tile takes: [j0, je[i]).  A tile of one row
+// tile would leave the second softmax warpgroup idle and wait, unit after unit,
+// for its own softmax between two products: with a.pair the two warpgroups hold
+// the same rows and take the units in turn, the first one j0, j0 + 2, .., and the
+// first one joins the two results at the segment's end.
 struct TcSegment {
     PrefillTile t;
     int32_t keys;   // keys the tile sees
     int32_t je[2], jend;
+    bool pair;
+    // Whether warpgroup i has units of the segment.
+    __device__ __forceinline__ bool has(int i, int32_t j0) const { return pair ? j0 + i < jend : j0 < je[i]; }
     template <class Walk>
     __device__ __forceinline__ TcSegment(const PrefillArgs &a, const Walk &cur) {
         t = cur.t;
@@ -121,6 +131,7 @@ struct TcSegment {
             je[i] = min(cur.j1, (int32_t)(((uint32_t)ki + kTcKeys - 1) / kTcKeys));  // the sum may pass 2^31
         }
         jend = max(je[0], je[1]);
+        pair = a.pair && t.ntok <= a.tq1;
     }
 };
 
@@ -129,10 +140,18 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
-__device__ __forceinline__ float lds_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+__device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
+}
+__device__ __forceinline__ float lds_bf16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+    return __uint_as_float((uint32_t)v << 16);
+}
+__device__ __forceinline__ void sts_u16(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
 }
 __device__ __forceinline__ void sts_u32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
@@ -285,8 +304,8 @@ __device__ __forceinline__ void tc_producer8(const PrefillArgs &a, uint8_t *smem
                 const uint32_t st = n % L::kRaw;
                 if (n >= L::kRaw) tc_wait(bar.raw_free + 8 * st, (n / L::kRaw + 1) & 1, abort, a.err);
                 if (__any_sync(0xffffffffu, abort)) break;
-                if (box) sts_u32(meta + st * L::kMetaBytes + (uint32_t)lane * 4, __float_as_uint(scale_of(sc_now)));
-                if (lane == 0) sts_u32(meta + st * L::kMetaBytes + 64, boxes);
+                if (box) sts_u16(meta + st * L::kMetaBytes + (uint32_t)lane * 2, __float_as_uint(scale_of(sc_now)) >> 16);
+                if (lane == 0) sts_u32(meta + st * L::kMetaBytes + 32, boxes);
                 __syncwarp();  // in place before lane 0 publishes the entry
                 if (lane == 0) mbar_arrive_expect_tx(bar.raw_full + 8 * st, boxes * (uint32_t)gran * D);
                 __syncwarp();
@@ -309,7 +328,7 @@ __device__ __forceinline__ void tc_producer8(const PrefillArgs &a, uint8_t *smem
         const uint32_t st = n % L::kRaw;
         if (n >= L::kRaw) tc_wait(bar.raw_free + 8 * st, (n / L::kRaw + 1) & 1, abort, a.err);
         if (lane == 0 && !abort) {
-            sts_u32(meta + st * L::kMetaBytes + 64, (uint32_t)kRawEnd);
+            sts_u32(meta + st * L::kMetaBytes + 32, (uint32_t)kRawEnd);
             mbar_arrive(bar.raw_full + 8 * st);
         }
     }
@@ -362,13 +381,13 @@ __device__ __forceinline__ void tc_converter(const PrefillArgs &a, uint8_t *smem
     for (uint32_t n = 0;; ++n) {
         const uint32_t rs = n % L::kRaw, st = n % L::kStages;
         tc_wait(bar.raw_full + 8 * rs, (n / L::kRaw) & 1, abort, a.err, a.wait_ns);
-        const int32_t boxes = __float_as_int(lds_f32(meta + rs * L::kMetaBytes + 64));
+        const int32_t boxes = (int32_t)lds_u32(meta + rs * L::kMetaBytes + 32);
         if (__any_sync(0xffffffffu, abort || boxes == kRawEnd)) break;
         if (n >= L::kStages) tc_wait(bar.kv_free + 8 * st, (n / L::kStages + 1) & 1, abort, a.err, a.wait_ns);
         if (__any_sync(0xffffffffu, abort)) break;
         const int32_t rows = boxes * gran;
         const uint32_t from = raw + rs * L::kRawTile + src, to = ring + st * L::kTile + dst, scales = meta + rs * L::kMetaBytes;
-        auto scale = [&](int p) { return lds_f32(scales + (uint32_t)(((p * kRowsPass + r0) >> shift) * 4)); };
+        auto scale = [&](int p) { return lds_bf16(scales + (uint32_t)(((p * kRowsPass + r0) >> shift) * 2)); };
         uint4 w[kBatch];
         float s[kBatch];
 #pragma unroll
@@ -512,7 +531,7 @@ __device__ __forceinline__ void tc_guard(const PrefillArgs &a, uint8_t *smem, co
         }
         n += 2 * (uint32_t)(sg.jend - cur.j0);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) no[i] += cur.j0 < sg.je[i] ? 1 : 0;
+        for (int i = 0; i < 2; ++i) no[i] += sg.has(i, cur.j0) ? 1 : 0;
     } while (cur.next(a));
 }
 
@@ -548,25 +567,76 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
         const int32_t j0 = uniform(cur.j0), jend = uniform(sg.jend), jg = uniform(guard_from(sg)),
                       keys = uniform(sg.keys);
         const int32_t je[2] = {uniform(sg.je[0]), uniform(sg.je[1])};
+        const bool pair = uniform(sg.pair) != 0;
         if (jend <= j0) continue;
         tc_wait(bar.q_full, segs & 1, abort, a.err);
         ++segs;
-        auto issue_s = [&](int i, uint32_t slot) {
+        auto issue_s = [&](int i, uint32_t slot, int q) {  // row tile q of Q
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 const uint32_t off = ((uint32_t)(k >> 2) * L::kPanel + (uint32_t)(k & 3) * 32) >> 4;
-                tc_mma_bf16_ss_if(one, tmem + L::kS + i * 128, q_desc + (uint32_t)(i * (L::kTile >> 4) + off),
+                tc_mma_bf16_ss_if(one, tmem + L::kS + i * 128, q_desc + (uint32_t)(q * (L::kTile >> 4) + off),
                                   k_desc + (slot * (L::kTile >> 4) + off), IDESC_S, k > 0 ? 1u : 0u);
             }
             tc_commit_if(one, bar.s_full + 8 * i);
         };
+        if (pair) {  // the warpgroups take the units in turn, both with Q's first row tile
+            const uint32_t base = n;
+            n += 2 * (uint32_t)(jend - j0);
+            auto s_of = [&](int i, int32_t j) {
+                const uint32_t ek = base + 2 * (uint32_t)(j - j0), sk = ek % L::kStages;
+                tc_wait(bar.kv_full + 8 * sk, (ek / L::kStages) & 1, abort, a.err);
+                tc_fence_after();
+                issue_s(i, sk, 0);
+                tc_commit_if(one, bar.kv_free + 8 * sk);
+                if (j + 1 == jend) tc_commit_if(one, bar.q_free);
+            };
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (j0 + i < jend) s_of(i, j0 + i);
+            for (int32_t jb = j0; jb < jend; jb += 2) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int32_t j = jb + i;
+                    if (j >= jend) break;
+                    const uint32_t ev = base + 2 * (uint32_t)(j - j0) + 1, sv = ev % L::kStages;
+                    tc_wait(bar.kv_full + 8 * sv, (ev / L::kStages) & 1, abort, a.err);
+                    const bool guarded = j >= jg;
+                    int ksteps = kTcKeys / 16;
+                    if (guarded) {
+                        ksteps = min(ksteps, (keys - j * kTcKeys + 15) / 16);
+                        if (one) mbar_arrive(bar.v_go);
+                    }
+                    if (jb == j0) {  // O is about to be overwritten: its earlier rows have been read
+                        if (no[i] > 0) tc_wait(bar.o_free + 8 * i, (no[i] - 1) & 1, abort, a.err);
+                        ++no[i];
+                    }
+                    tc_wait(bar.p_full + 8 * i, np[i] & 1, abort, a.err);
+                    ++np[i];
+                    if (guarded) {
+                        tc_wait(bar.v_ok, units & 1, abort, a.err);
+                        ++units;
+                    }
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < ksteps; ++k)
+                        tc_mma_bf16_ts_if(one, tmem + L::kO + i * D, tmem + L::kS + i * 128 + k * 8,
+                                          v_desc + (sv * (L::kTile >> 4) + (uint32_t)k * 128u), IDESC_O,
+                                          jb > j0 || k > 0 ? 1u : 0u);
+                    if (j + 2 >= jend) tc_commit_if(one, bar.o_full + 8 * i);
+                    tc_commit_if(one, bar.kv_free + 8 * sv);
+                    if (j + 2 < jend) s_of(i, j + 2);
+                }
+            }
+            continue;
+        }
         const uint32_t st = n % L::kStages;
         tc_wait(bar.kv_full + 8 * st, (n / L::kStages) & 1, abort, a.err);
         ++n;
         tc_fence_after();
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            if (j0 < je[i]) issue_s(i, st);
+            if (j0 < je[i]) issue_s(i, st, i);
         tc_commit_if(one, bar.kv_free + 8 * st);
         if (j0 + 1 == jend) tc_commit_if(one, bar.q_free);
         for (int32_t j = j0; j < jend; ++j) {
@@ -611,7 +681,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
                 if (more && i == 0) tc_wait(bar.kv_full + 8 * sk, (nk / L::kStages) & 1, abort, a.err);
                 if (j + 1 < je[i]) {
                     tc_fence_after();
-                    issue_s(i, sk);
+                    issue_s(i, sk, i);
                 }
             }
             if (guarded) ++units;
@@ -628,7 +698,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
 // Four warps per row tile; a thread owns one query row (tensor-memory lane).
 template <int D, bool kFp8>
 __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &bar, uint32_t tmem,
-                                           const OddColumns &odd, int32_t c,
+                                           const OddColumns &odd, float2 *ml, int32_t c,
                                            int i, int warp, int lane) {
     using L = TcPrefill<D, kFp8>;
     const int r = warp * 32 + lane;  // row of the row tile
@@ -637,20 +707,21 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
     const uint32_t s_full = bar.s_full + 8 * i, p_full = bar.p_full + 8 * i;
     const int tok_r = r / a.G, g = r - tok_r * a.G;
     const float sl = a.scale_log2;
-    uint32_t ns = 0, no = 0, segs = 0;
+    uint32_t ns = 0, no = 0, segs = 0, nx = 0;
     bool abort = false;
     PrefillWalk<false> cur;
     if (!cur.init(a, c)) return;
     do {
         const TcSegment sg(a, cur);
-        const int32_t tok = i * a.tq1 + tok_r;
+        const int32_t tok = (sg.pair ? 0 : i * a.tq1) + tok_r;
         const bool valid = tok_r < a.tq1 && tok < sg.t.ntok;
         const bool warp_rows = __any_sync(0xffffffffu, valid);
         const int32_t last = sg.t.p0 + a.step * tok;  // last key that this row sees
-        const int32_t je = sg.je[i];
+        // This warpgroup's units: every one of its row tile's, or every other one.
+        const int32_t je = sg.pair ? sg.jend : sg.je[i], jf = cur.j0 + (sg.pair ? i : 0), dj = sg.pair ? 2 : 1;
         if (sg.jend > cur.j0) ++segs;
         float m = -INFINITY, l = 0.f;
-        for (int32_t j = cur.j0; j < je; ++j) {
+        for (int32_t j = jf; j < je; j += dj) {
             tc_wait(s_full, ns & 1, abort, a.err, a.wait_ns);
             ++ns;
             tc_fence_after();
@@ -678,7 +749,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
                     const float al = grow ? ex2_approx(m - mn) : 1.f;
                     m = mn;
                     l *= al;
-                    if (j > cur.j0) {
+                    if (j > jf) {
 #pragma unroll 1
                         for (int d0 = 0; d0 < D; d0 += 32) {
                             float o[32];
@@ -714,11 +785,32 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
             __syncwarp();
             if (lane == 0) mbar_arrive(p_full);
         }
-        const bool any = je > cur.j0;
+        const bool any = je > jf;
         if (any) {
             tc_wait(bar.o_full + 8 * i, no & 1, abort, a.err);
             ++no;
             tc_fence_after();
+        }
+        if (sg.pair && i == 1) {  // the first warpgroup takes over: it reads both O, and frees them
+            if (any) {
+                ml[r] = make_float2(m, l);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar.x_full);
+            }
+            continue;
+        }
+        const bool join = sg.pair && cur.j0 + 1 < sg.jend;
+        float w0 = 1.f, w1 = 0.f;
+        if (join) {
+            tc_wait(bar.x_full, nx & 1, abort, a.err);
+            ++nx;
+            tc_fence_after();
+            const float2 y = ml[r];
+            const float mn = fmaxf(m, y.x), mref = mn == -INFINITY ? 0.f : mn;  // a row without keys: zeros
+            w0 = ex2_approx(m - mref), w1 = ex2_approx(y.x - mref);
+            l = w0 * l + w1 * y.y;
+            m = mn;
         }
         const bool whole = cur.whole(), out32 = ((uintptr_t)a.out & 31) == 0;
         const int64_t row = cur.slot(c) * (2 * kTcRows) + i * kTcRows + r;
@@ -735,6 +827,15 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
                 } else {
 #pragma unroll
                     for (int k = 0; k < 64; ++k) o[k] = 0.f;
+                }
+                if (join) {
+#pragma unroll
+                    for (int h = 0; h < 64; h += 32) {
+                        float y[32];
+                        tmem_ld32(tO + (uint32_t)(D + d0 + h), y);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[h + k] = fmaf(w1, y[k], w0 * o[h + k]);
+                    }
                 }
                 if (odd_tile) {
 #pragma unroll
@@ -778,6 +879,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar.o_free + 8 * i);
+            if (lane == 0 && join) mbar_arrive(bar.o_free + 8);
         }
     } while (cur.next(a));
 }
@@ -797,13 +899,14 @@ __global__ void __launch_bounds__(TcPrefill<D, kFp8>::kThreads, 1)
     const TcBars bar(smem_u32(smem + L::kBars), L::kStages, smem_u32(smem + L::kRawBars), L::kRaw);
     uint32_t *tmem_slot = (uint32_t *)(smem + L::kBars + 248);
     const OddColumns odd{(int32_t *)(smem + L::kBars + 256), (int32_t *)(smem + L::kBars + 240)};
-    static_assert(96 + 16 * L::kStages <= 240, "the barriers fit");
+    static_assert(96 + 16 * L::kStages <= 232, "the barriers fit");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         mbar_init(bar.q_full, 1);
         mbar_init(bar.q_free, 1);
         mbar_init(bar.v_go, 1);
         mbar_init(bar.v_ok, 1);
+        mbar_init(bar.x_full, 4);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar.s_full + 8 * i, 1);
             mbar_init(bar.p_full + 8 * i, 4);
@@ -832,7 +935,7 @@ __global__ void __launch_bounds__(TcPrefill<D, kFp8>::kThreads, 1)
     const int32_t c = blockIdx.x;
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFp8 ? kTcSoftmaxRegs8 : kTcSoftmaxRegs));
-        tc_softmax<D, kFp8>(a, bar, tmem, odd, c, warp >> 2, warp & 3, lane);
+        tc_softmax<D, kFp8>(a, bar, tmem, odd, (float2 *)(smem + L::kMl), c, warp >> 2, warp & 3, lane);
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFp8 ? kTcOtherRegs8 : kTcOtherRegs));
         if (warp == 8) {
