@@ -50,7 +50,7 @@ constexpr unsigned long long kTcUnitNs = 4096;
 constexpr int kTcSoftmaxRegs = 208, kTcOtherRegs = 88;
 // The 8-bit form has a fourth warpgroup, the converters: 512 threads x 128 at
 // launch, 256 x kTcSoftmaxRegs8 + 128 x (kTcOtherRegs8 + kTcConvertRegs) = 512 x 128.
-constexpr int kTcThreads8 = 512, kTcSoftmaxRegs8 = 200, kTcOtherRegs8 = 56, kTcConvertRegs = 56;
+constexpr int kTcThreads8 = 512, kTcSoftmaxRegs8 = 192, kTcOtherRegs8 = 64, kTcConvertRegs = 64;
 
 // kFp8: codes arrive in a ring of their own (raw) and are turned into the bf16
 // units of the ring that the MMAs read.
@@ -66,9 +66,9 @@ struct TcPrefill {
     static constexpr uint32_t kRing = 2 * kTile;             // after the two Q row tiles
     static constexpr uint32_t kRawRing = kRing + kStages * kTile;
     static constexpr uint32_t kBars = kRawRing + kRaw * kRawTile;
-    static constexpr uint32_t kRawBars = kBars + 256 + 3 * D * 4;  // barriers; columns with odd values
+    static constexpr uint32_t kRawBars = kBars + 288 + 3 * D * 4;  // barriers; columns with odd values
     static constexpr uint32_t kMl = kRawBars + 16 * kRaw;  // (m, l) of the second warpgroup's rows
-    static constexpr uint32_t kMeta = kMl + 1024, kMetaBytes = 48;  // per raw unit: scales of its (up to 16) boxes as bf16, their number
+    static constexpr uint32_t kMeta = kMl + (kFp8 ? 0 : 1024), kMetaBytes = 80;  // per raw unit: scales of its (up to 16) boxes, their number
     static constexpr uint32_t kBytes = kMeta + kMetaBytes * kRaw;
     static_assert(kBytes <= 227 * 1024, "a CTA's shared memory");
     static constexpr size_t kSmem = kBytes;
@@ -81,16 +81,16 @@ struct TcBars {
     uint32_t x_full, raw_full, raw_free;
     __device__ __forceinline__ TcBars(uint32_t base, int stages, uint32_t raw, int raw_stages) {
         q_full = base;
-        q_free = base + 8;
-        s_full = base + 16;
-        p_full = base + 32;
-        o_full = base + 48;
-        o_free = base + 64;
-        v_go = base + 80;
-        v_ok = base + 88;
-        kv_full = base + 96;
+        q_free = base + 16;
+        s_full = base + 32;
+        p_full = base + 48;
+        o_full = base + 64;
+        o_free = base + 80;
+        v_go = base + 96;
+        v_ok = base + 104;
+        x_full = base + 112;
+        kv_full = base + 120;
         kv_free = kv_full + 8 * (uint32_t)stages;
-        x_full = base + 232;
         raw_full = raw;
         raw_free = raw + 8 * (uint32_t)raw_stages;
     }
@@ -111,15 +111,20 @@ __device__ __forceinline__ void tc_wait(uint32_t bar, uint32_t parity, bool &abo
 // Units of a segment that each row tile takes: [j0, je[i]).  A tile of one row
 // tile would leave the second softmax warpgroup idle and wait, unit after unit,
 // for its own softmax between two products: with a.pair the two warpgroups hold
-// the same rows and take the units in turn, the first one j0, j0 + 2, .., and the
-// first one joins the two results at the segment's end.
+// the same rows and take the units in turn, and the one that had the first unit
+// joins the two results at the segment's end.  That one changes from such a
+// segment to the next (`first`, counted alike by every role).  (Not over the 8-bit
+// cache, where the converters are what bounds a unit.)
+template <bool kFp8>
 struct TcSegment {
     PrefillTile t;
     int32_t keys;   // keys the tile sees
     int32_t je[2], jend;
     bool pair;
     // Whether warpgroup i has units of the segment.
-    __device__ __forceinline__ bool has(int i, int32_t j0) const { return pair ? j0 + i < jend : j0 < je[i]; }
+    __device__ __forceinline__ bool has(int i, int32_t j0, int first) const {
+        return pair ? j0 + (i ^ first) < jend : j0 < je[i];
+    }
     template <class Walk>
     __device__ __forceinline__ TcSegment(const PrefillArgs &a, const Walk &cur) {
         t = cur.t;
@@ -131,7 +136,7 @@ struct TcSegment {
             je[i] = min(cur.j1, (int32_t)(((uint32_t)ki + kTcKeys - 1) / kTcKeys));  // the sum may pass 2^31
         }
         jend = max(je[0], je[1]);
-        pair = a.pair && t.ntok <= a.tq1;
+        pair = !kFp8 && a.pair && t.ntok <= a.tq1;
     }
 };
 
@@ -140,24 +145,56 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
-__device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
     return v;
-}
-__device__ __forceinline__ float lds_bf16(uint32_t addr) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-    return __uint_as_float((uint32_t)v << 16);
-}
-__device__ __forceinline__ void sts_u16(uint32_t addr, uint32_t v) {
-    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
 }
 __device__ __forceinline__ void sts_u32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t addr, const uint4 &v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// ------------------------------------------------------------------ Q slots
+// Q's two row tiles in shared memory, each with barriers of its own.  A tile of
+// two row tiles takes both; one of a single row tile takes them in turn, so that
+// its rows, and the K behind them, are fetched while the tile before is at work.
+// The K producer and the issuer count alike.
+struct QSlots {
+    uint32_t n0 = 0, n1 = 0;  // tiles that each slot has held
+    int next = 0;             // the slot of the next tile of a single row tile
+    __device__ __forceinline__ uint32_t &n(int s) { return s ? n1 : n0; }
+};
+// K producer: waits for the slots of a tile's rows and fetches them.
+template <class L>
+__device__ __forceinline__ void load_q(const PrefillArgs &a, const PrefillTile &t, int32_t kvh, uint32_t q_dst,
+                                       const TcBars &bar, const CUtensorMap *tmq, QSlots &q, bool &abort, int lane) {
+    const bool two = t.ntok > a.tq1;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        if (!two && s != q.next) continue;
+        if (q.n(s) > 0) tc_wait(bar.q_free + 8 * s, (q.n(s) - 1) & 1, abort, a.err);
+        ++q.n(s);
+        if (__any_sync(0xffffffffu, abort)) return;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar.q_full + 8 * s, (uint32_t)(L::kPanels * a.tq1 * a.G) * 128u);
+            for (int32_t p = 0; p < L::kPanels; ++p)
+                tma_load_4d(q_dst + s * L::kTile + p * L::kPanel, tmq, bar.q_full + 8 * s, 0, p, kvh * a.G,
+                            t.row0 + (two ? s * a.tq1 : 0));
+        }
+    }
+    if (!two) q.next ^= 1;
+}
+// The last fetches and the issuer's last arrivals on the free barriers.
+__device__ __forceinline__ void drain_q(const TcBars &bar, QSlots &q, bool &late, unsigned int *err) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        if (q.n(s) == 0) continue;
+        tc_wait(bar.q_full + 8 * s, (q.n(s) - 1) & 1, late, err);
+        tc_wait(bar.q_free + 8 * s, (q.n(s) - 1) & 1, late, err);
+    }
 }
 
 // ----------------------------------------------------------- TMA producers
@@ -181,30 +218,22 @@ __device__ __forceinline__ void tc_producer(const PrefillArgs &a, uint8_t *smem,
     const int32_t bi = lane % nbm, panel = lane / nbm;
     const bool has_box = panel < L::kPanels;
     const uint32_t box_off = (uint32_t)panel * L::kPanel + (uint32_t)(bi * gran) * 128u;
-    uint32_t n = kIsV ? 1 : 0, segs = 0;  // next ring entry, segments with units
+    uint32_t n = kIsV ? 1 : 0;  // next ring entry
+    QSlots q;
     bool abort = false;
     PrefillCursor cur;
     if (!cur.init(a, c)) return;
     do {
-        const TcSegment sg(a, cur);
+        const TcSegment<false> sg(a, cur);
         if (sg.jend <= cur.j0) continue;
         const int32_t *row = a.tables + (int64_t)sg.t.seq * a.max_blocks;
         auto has_key = [&](int32_t j) { return has_box && (int64_t)j * kTcKeys + bi * gran < sg.keys; };
         auto entry = [&](int32_t j) { return has_key(j) ? row[(j * kTcKeys + bi * gran) / a.B] : 0; };
         int32_t phys = entry(cur.j0);
         if (!kIsV) {
-            if (segs > 0) tc_wait(bar.q_free, (segs - 1) & 1, abort, a.err);
+            load_q<L>(a, sg.t, cur.kvh, q_dst, bar, tmq, q, abort, lane);
             if (__any_sync(0xffffffffu, abort)) break;
-            if (lane == 0) {
-                const int32_t nrt = sg.t.ntok > a.tq1 ? 2 : 1;
-                mbar_arrive_expect_tx(bar.q_full, (uint32_t)(nrt * L::kPanels * a.tq1 * a.G) * 128u);
-                for (int32_t i = 0; i < nrt; ++i)
-                    for (int32_t p = 0; p < L::kPanels; ++p)
-                        tma_load_4d(q_dst + i * L::kTile + p * L::kPanel, tmq, bar.q_full, 0, p, cur.kvh * a.G,
-                                    sg.t.row0 + i * a.tq1);
-            }
         }
-        ++segs;
         for (int32_t j = cur.j0; j < sg.jend; ++j, n += 2) {
             const int32_t p = j * kTcKeys + bi * gran;
             const bool box = has_key(j);
@@ -235,10 +264,7 @@ __device__ __forceinline__ void tc_producer(const PrefillArgs &a, uint8_t *smem,
         tc_wait(bar.kv_full + 8 * (k % L::kStages), (k / L::kStages) & 1, late, a.err);
         tc_wait(bar.kv_free + 8 * (k % L::kStages), (k / L::kStages) & 1, late, a.err);
     }
-    if (!kIsV && segs > 0) {
-        tc_wait(bar.q_full, (segs - 1) & 1, late, a.err);
-        tc_wait(bar.q_free, (segs - 1) & 1, late, a.err);
-    }
+    if (!kIsV) drain_q(bar, q, late, a.err);
 }
 
 // ------------------------------------------------- 8-bit cache: producers
@@ -261,12 +287,13 @@ __device__ __forceinline__ void tc_producer8(const PrefillArgs &a, uint8_t *smem
     const int32_t nbm = kTcKeys / gran;  // boxes of a unit (at most 16), one per lane
     const uint8_t *scales = kIsV ? a.v_scale : a.k_scale;
     const uint64_t policy = l2_policy_evict_first();
-    uint32_t n = kIsV ? 1 : 0, segs = 0;  // next entry, segments with units
+    uint32_t n = kIsV ? 1 : 0;  // next entry
+    QSlots q;
     bool abort = false;
     PrefillWalk<false> cur;
     if (cur.init(a, c)) {
         do {
-            const TcSegment sg(a, cur);
+            const TcSegment<true> sg(a, cur);
             if (sg.jend <= cur.j0) continue;
             const int32_t *row = a.tables + (int64_t)sg.t.seq * a.max_blocks;
             auto has_key = [&](int32_t j) { return lane < nbm && (int64_t)j * kTcKeys + lane * gran < sg.keys; };
@@ -276,19 +303,10 @@ __device__ __forceinline__ void tc_producer8(const PrefillArgs &a, uint8_t *smem
             };
             int32_t phys = entry(cur.j0), phys_1 = entry(cur.j0 + 1);
             if (!kIsV) {
-                if (segs > 0) tc_wait(bar.q_free, (segs - 1) & 1, abort, a.err);
+                load_q<L>(a, sg.t, cur.kvh, q_dst, bar, tmq, q, abort, lane);
                 if (__any_sync(0xffffffffu, abort)) break;
-                if (lane == 0) {
-                    const int32_t nrt = sg.t.ntok > a.tq1 ? 2 : 1;
-                    mbar_arrive_expect_tx(bar.q_full, (uint32_t)(nrt * L::kPanels * a.tq1 * a.G) * 128u);
-                    for (int32_t i = 0; i < nrt; ++i)
-                        for (int32_t p = 0; p < L::kPanels; ++p)
-                            tma_load_4d(q_dst + i * L::kTile + p * L::kPanel, tmq, bar.q_full, 0, p, cur.kvh * a.G,
-                                        sg.t.row0 + i * a.tq1);
-                }
             }
             uint32_t sc = scale_at(phys);
-            ++segs;
             for (int32_t j = cur.j0; j < sg.jend; ++j, n += 2) {
                 const bool box = has_key(j);
                 int32_t at = a.NB * a.B;  // a bad entry reads zeros: the box lies past the pool
@@ -304,8 +322,8 @@ __device__ __forceinline__ void tc_producer8(const PrefillArgs &a, uint8_t *smem
                 const uint32_t st = n % L::kRaw;
                 if (n >= L::kRaw) tc_wait(bar.raw_free + 8 * st, (n / L::kRaw + 1) & 1, abort, a.err);
                 if (__any_sync(0xffffffffu, abort)) break;
-                if (box) sts_u16(meta + st * L::kMetaBytes + (uint32_t)lane * 2, __float_as_uint(scale_of(sc_now)) >> 16);
-                if (lane == 0) sts_u32(meta + st * L::kMetaBytes + 32, boxes);
+                if (box) sts_u32(meta + st * L::kMetaBytes + (uint32_t)lane * 4, __float_as_uint(scale_of(sc_now)));
+                if (lane == 0) sts_u32(meta + st * L::kMetaBytes + 64, boxes);
                 __syncwarp();  // in place before lane 0 publishes the entry
                 if (lane == 0) mbar_arrive_expect_tx(bar.raw_full + 8 * st, boxes * (uint32_t)gran * D);
                 __syncwarp();
@@ -328,16 +346,13 @@ __device__ __forceinline__ void tc_producer8(const PrefillArgs &a, uint8_t *smem
         const uint32_t st = n % L::kRaw;
         if (n >= L::kRaw) tc_wait(bar.raw_free + 8 * st, (n / L::kRaw + 1) & 1, abort, a.err);
         if (lane == 0 && !abort) {
-            sts_u32(meta + st * L::kMetaBytes + 32, (uint32_t)kRawEnd);
+            sts_u32(meta + st * L::kMetaBytes + 64, (uint32_t)kRawEnd);
             mbar_arrive(bar.raw_full + 8 * st);
         }
     }
     for (uint32_t k = total > (uint32_t)L::kStages ? total - L::kStages : 0; k < total; ++k)
         if ((k & 1u) == mine) tc_wait(bar.kv_free + 8 * (k % L::kStages), (k / L::kStages) & 1, late, a.err);
-    if (!kIsV && segs > 0) {
-        tc_wait(bar.q_full, (segs - 1) & 1, late, a.err);
-        tc_wait(bar.q_free, (segs - 1) & 1, late, a.err);
-    }
+    if (!kIsV) drain_q(bar, q, late, a.err);
 }
 
 // ------------------------------------------------------- 8-bit: converters
@@ -381,13 +396,13 @@ __device__ __forceinline__ void tc_converter(const PrefillArgs &a, uint8_t *smem
     for (uint32_t n = 0;; ++n) {
         const uint32_t rs = n % L::kRaw, st = n % L::kStages;
         tc_wait(bar.raw_full + 8 * rs, (n / L::kRaw) & 1, abort, a.err, a.wait_ns);
-        const int32_t boxes = (int32_t)lds_u32(meta + rs * L::kMetaBytes + 32);
+        const int32_t boxes = __float_as_int(lds_f32(meta + rs * L::kMetaBytes + 64));
         if (__any_sync(0xffffffffu, abort || boxes == kRawEnd)) break;
         if (n >= L::kStages) tc_wait(bar.kv_free + 8 * st, (n / L::kStages + 1) & 1, abort, a.err, a.wait_ns);
         if (__any_sync(0xffffffffu, abort)) break;
         const int32_t rows = boxes * gran;
         const uint32_t from = raw + rs * L::kRawTile + src, to = ring + st * L::kTile + dst, scales = meta + rs * L::kMetaBytes;
-        auto scale = [&](int p) { return lds_bf16(scales + (uint32_t)(((p * kRowsPass + r0) >> shift) * 2)); };
+        auto scale = [&](int p) { return lds_f32(scales + (uint32_t)(((p * kRowsPass + r0) >> shift) * 4)); };
         uint4 w[kBatch];
         float s[kBatch];
 #pragma unroll
@@ -438,7 +453,8 @@ struct OddColumns {
 };
 
 // First unit of a segment that holds keys for the guard.
-__device__ __forceinline__ int32_t guard_from(const TcSegment &sg) { return max(sg.t.p0 + 1, 0) / kTcKeys; }
+template <class Segment>
+__device__ __forceinline__ int32_t guard_from(const Segment &sg) { return max(sg.t.p0 + 1, 0) / kTcKeys; }
 
 template <int D>
 __device__ __forceinline__ uint32_t v_chunk(uint32_t vbase, int e) {  // address of 16-byte chunk e % (D / 8) of row e / (D / 8)
@@ -459,13 +475,14 @@ __device__ __forceinline__ void tc_guard(const PrefillArgs &a, uint8_t *smem, co
     uint32_t n = 1, segs = 0, units = 0;  // ring entry of V, segments, guarded units
     uint32_t no[2] = {0, 0};              // earlier segments with units per row tile
     uint32_t held = 0;                    // the segment that the columns belong to
+    int first = 0;                        // (TcSegment)
     bool abort = false;
     PrefillCursor cur;
     const bool work = cur.init(a, c);
     if (lane == 0) note_cut(a, c, work, cur);
     if (!work) return;
     do {
-        const TcSegment sg(a, cur);
+        const TcSegment<kFp8> sg(a, cur);
         if (sg.jend <= cur.j0) continue;
         ++segs;
         for (int32_t j = max(cur.j0, guard_from(sg)); j < sg.jend; ++j, ++units) {
@@ -499,7 +516,7 @@ __device__ __forceinline__ void tc_guard(const PrefillArgs &a, uint8_t *smem, co
                 // j0 has been waited for there (its barrier may be a phase on).
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    if (no[i] > 0 && (j == cur.j0 || sg.je[i] <= cur.j0))
+                    if (no[i] > 0 && (sg.pair || j == cur.j0 || sg.je[i] <= cur.j0))
                         tc_wait(bar.o_free + 8 * i, (no[i] - 1) & 1, abort, a.err);
                 if (held != 0 && held != segs)
                     for (int x = lane; x < 3 * D; x += 32) odd.first[x] = OddColumns::kNone;
@@ -531,7 +548,8 @@ __device__ __forceinline__ void tc_guard(const PrefillArgs &a, uint8_t *smem, co
         }
         n += 2 * (uint32_t)(sg.jend - cur.j0);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) no[i] += sg.has(i, cur.j0) ? 1 : 0;
+        for (int i = 0; i < 2; ++i) no[i] += sg.has(i, cur.j0, first) ? 1 : 0;
+        if (sg.pair) first ^= 1;
     } while (cur.next(a));
 }
 
@@ -556,22 +574,36 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
     const uint64_t q_desc = smem_desc_sw128(smem_u32(smem), 16, 1024), k_desc = smem_desc_sw128(ring, 16, 1024),
                    v_desc = smem_desc_sw128(ring, L::kPanel, 1024);
     const uint32_t one = elect_one();
-    uint32_t n = 0, segs = 0, units = 0;  // ring entries consumed, segments, guarded units
+    uint32_t n = 0, units = 0;  // ring entries consumed, guarded units
+    QSlots qs;
     uint32_t np[2] = {0, 0};              // P tiles taken per row tile
     uint32_t no[2] = {0, 0};              // segments with units per row tile
+    int first = 0;                        // (TcSegment)
     bool abort = false;
     PrefillCursor cur;
     if (!cur.init(a, c)) return;
     do {
-        const TcSegment sg(a, cur);
+        const TcSegment<kFp8> sg(a, cur);
         const int32_t j0 = uniform(cur.j0), jend = uniform(sg.jend), jg = uniform(guard_from(sg)),
                       keys = uniform(sg.keys);
         const int32_t je[2] = {uniform(sg.je[0]), uniform(sg.je[1])};
         const bool pair = uniform(sg.pair) != 0;
         if (jend <= j0) continue;
-        tc_wait(bar.q_full, segs & 1, abort, a.err);
-        ++segs;
-        auto issue_s = [&](int i, uint32_t slot, int q) {  // row tile q of Q
+        const bool two = uniform(sg.t.ntok > a.tq1) != 0;
+        const int q0 = uniform(two ? 0 : qs.next);  // Q's slot of the first row tile
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            if (two || s == q0) {
+                tc_wait(bar.q_full + 8 * s, qs.n(s) & 1, abort, a.err);
+                ++qs.n(s);
+            }
+        if (!two) qs.next ^= 1;
+        auto free_q = [&]() {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (two || s == q0) tc_commit_if(one, bar.q_free + 8 * s);
+        };
+        auto issue_s = [&](int i, uint32_t slot, int q) {  // slot q of Q
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 const uint32_t off = ((uint32_t)(k >> 2) * L::kPanel + (uint32_t)(k & 3) * 32) >> 4;
@@ -587,46 +619,43 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
                 const uint32_t ek = base + 2 * (uint32_t)(j - j0), sk = ek % L::kStages;
                 tc_wait(bar.kv_full + 8 * sk, (ek / L::kStages) & 1, abort, a.err);
                 tc_fence_after();
-                issue_s(i, sk, 0);
+                issue_s(i, sk, q0);
                 tc_commit_if(one, bar.kv_free + 8 * sk);
-                if (j + 1 == jend) tc_commit_if(one, bar.q_free);
+                if (j + 1 == jend) free_q();
             };
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (j0 + i < jend) s_of(i, j0 + i);
-            for (int32_t jb = j0; jb < jend; jb += 2) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int32_t j = jb + i;
-                    if (j >= jend) break;
-                    const uint32_t ev = base + 2 * (uint32_t)(j - j0) + 1, sv = ev % L::kStages;
-                    tc_wait(bar.kv_full + 8 * sv, (ev / L::kStages) & 1, abort, a.err);
-                    const bool guarded = j >= jg;
-                    int ksteps = kTcKeys / 16;
-                    if (guarded) {
-                        ksteps = min(ksteps, (keys - j * kTcKeys + 15) / 16);
-                        if (one) mbar_arrive(bar.v_go);
-                    }
-                    if (jb == j0) {  // O is about to be overwritten: its earlier rows have been read
-                        if (no[i] > 0) tc_wait(bar.o_free + 8 * i, (no[i] - 1) & 1, abort, a.err);
-                        ++no[i];
-                    }
-                    tc_wait(bar.p_full + 8 * i, np[i] & 1, abort, a.err);
-                    ++np[i];
-                    if (guarded) {
-                        tc_wait(bar.v_ok, units & 1, abort, a.err);
-                        ++units;
-                    }
-                    tc_fence_after();
+            int i = first;  // warpgroup of unit j
+            s_of(i, j0);
+            if (j0 + 1 < jend) s_of(i ^ 1, j0 + 1);
+            first ^= 1;
 #pragma unroll 1
-                    for (int k = 0; k < ksteps; ++k)
-                        tc_mma_bf16_ts_if(one, tmem + L::kO + i * D, tmem + L::kS + i * 128 + k * 8,
-                                          v_desc + (sv * (L::kTile >> 4) + (uint32_t)k * 128u), IDESC_O,
-                                          jb > j0 || k > 0 ? 1u : 0u);
-                    if (j + 2 >= jend) tc_commit_if(one, bar.o_full + 8 * i);
-                    tc_commit_if(one, bar.kv_free + 8 * sv);
-                    if (j + 2 < jend) s_of(i, j + 2);
+            for (int32_t j = j0; j < jend; ++j, i ^= 1) {
+                const uint32_t ev = base + 2 * (uint32_t)(j - j0) + 1, sv = ev % L::kStages;
+                tc_wait(bar.kv_full + 8 * sv, (ev / L::kStages) & 1, abort, a.err);
+                const bool guarded = j >= jg;
+                int ksteps = kTcKeys / 16;
+                if (guarded) {
+                    ksteps = min(ksteps, (keys - j * kTcKeys + 15) / 16);
+                    if (one) mbar_arrive(bar.v_go);
                 }
+                const bool begins = j < j0 + 2;
+                if (begins) {  // O is about to be overwritten: its earlier rows have been read
+                    const uint32_t k = i ? no[1]++ : no[0]++;
+                    if (k > 0) tc_wait(bar.o_free + 8 * i, (k - 1) & 1, abort, a.err);
+                }
+                tc_wait(bar.p_full + 8 * i, (i ? np[1]++ : np[0]++) & 1, abort, a.err);
+                if (guarded) {
+                    tc_wait(bar.v_ok, units & 1, abort, a.err);
+                    ++units;
+                }
+                tc_fence_after();
+#pragma unroll 1
+                for (int k = 0; k < ksteps; ++k)
+                    tc_mma_bf16_ts_if(one, tmem + L::kO + i * D, tmem + L::kS + i * 128 + k * 8,
+                                      v_desc + (sv * (L::kTile >> 4) + (uint32_t)k * 128u), IDESC_O,
+                                      !begins || k > 0 ? 1u : 0u);
+                if (j + 2 >= jend) tc_commit_if(one, bar.o_full + 8 * i);
+                tc_commit_if(one, bar.kv_free + 8 * sv);
+                if (j + 2 < jend) s_of(i, j + 2);
             }
             continue;
         }
@@ -636,9 +665,9 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
         tc_fence_after();
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            if (j0 < je[i]) issue_s(i, st, i);
+            if (j0 < je[i]) issue_s(i, st, two ? i : q0);
         tc_commit_if(one, bar.kv_free + 8 * st);
-        if (j0 + 1 == jend) tc_commit_if(one, bar.q_free);
+        if (j0 + 1 == jend) free_q();
         for (int32_t j = j0; j < jend; ++j) {
             const bool more = j + 1 < jend;
             const uint32_t nv = n, nk = n + 1;  // ring entries of this unit's V and the next one's K
@@ -681,13 +710,13 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
                 if (more && i == 0) tc_wait(bar.kv_full + 8 * sk, (nk / L::kStages) & 1, abort, a.err);
                 if (j + 1 < je[i]) {
                     tc_fence_after();
-                    issue_s(i, sk, i);
+                    issue_s(i, sk, two ? i : q0);
                 }
             }
             if (guarded) ++units;
             tc_commit_if(one, bar.kv_free + 8 * sv);
             if (more) tc_commit_if(one, bar.kv_free + 8 * sk);
-            if (j + 2 == jend) tc_commit_if(one, bar.q_free);
+            if (j + 2 == jend) free_q();
         }
     } while (uniform(cur.next(a)));
     // Every MMA ends in an o_full that the softmax warps wait for; nothing of
@@ -703,22 +732,25 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
     using L = TcPrefill<D, kFp8>;
     const int r = warp * 32 + lane;  // row of the row tile
     const uint32_t t_lane = (uint32_t)(warp * 32) << 16;
-    const uint32_t tS = tmem + L::kS + i * 128 + t_lane, tO = tmem + L::kO + i * D + t_lane;
+    const uint32_t tS = tmem + L::kS + i * 128 + t_lane, tO = tmem + L::kO + i * D + t_lane, tO_other = tmem + L::kO + (1 - i) * D + t_lane;
     const uint32_t s_full = bar.s_full + 8 * i, p_full = bar.p_full + 8 * i;
     const int tok_r = r / a.G, g = r - tok_r * a.G;
     const float sl = a.scale_log2;
     uint32_t ns = 0, no = 0, segs = 0, nx = 0;
+    int first = 0;
     bool abort = false;
     PrefillWalk<false> cur;
     if (!cur.init(a, c)) return;
     do {
-        const TcSegment sg(a, cur);
+        const TcSegment<kFp8> sg(a, cur);
         const int32_t tok = (sg.pair ? 0 : i * a.tq1) + tok_r;
         const bool valid = tok_r < a.tq1 && tok < sg.t.ntok;
         const bool warp_rows = __any_sync(0xffffffffu, valid);
         const int32_t last = sg.t.p0 + a.step * tok;  // last key that this row sees
         // This warpgroup's units: every one of its row tile's, or every other one.
-        const int32_t je = sg.pair ? sg.jend : sg.je[i], jf = cur.j0 + (sg.pair ? i : 0), dj = sg.pair ? 2 : 1;
+        const int32_t je = sg.pair ? sg.jend : sg.je[i], jf = cur.j0 + (sg.pair ? i ^ first : 0), dj = sg.pair ? 2 : 1;
+        const bool second = sg.pair && i != first;
+        if (sg.pair && sg.jend > cur.j0) first ^= 1;
         if (sg.jend > cur.j0) ++segs;
         float m = -INFINITY, l = 0.f;
         for (int32_t j = jf; j < je; j += dj) {
@@ -791,12 +823,13 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
             ++no;
             tc_fence_after();
         }
-        if (sg.pair && i == 1) {  // the first warpgroup takes over: it reads both O, and frees them
+        if (second) {  // the other warpgroup takes over: it reads both O, and frees them
             if (any) {
                 ml[r] = make_float2(m, l);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar.x_full);
+                ++nx;
             }
             continue;
         }
@@ -815,7 +848,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
         const bool whole = cur.whole(), out32 = ((uintptr_t)a.out & 31) == 0;
         const int64_t row = cur.slot(c) * (2 * kTcRows) + i * kTcRows + r;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const bool odd_tile = any && odd.segment[i] == (int32_t)segs;
+        const bool odd_tile = any && odd.segment[sg.pair ? 0 : i] == (int32_t)segs;
         __nv_bfloat16 *op =
             (__nv_bfloat16 *)a.out + ((int64_t)(sg.t.row0 + tok) * a.H + (int64_t)cur.kvh * a.G + g) * D;
         if (warp_rows) {
@@ -832,7 +865,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
 #pragma unroll
                     for (int h = 0; h < 64; h += 32) {
                         float y[32];
-                        tmem_ld32(tO + (uint32_t)(D + d0 + h), y);
+                        tmem_ld32(tO_other + (uint32_t)(d0 + h), y);
 #pragma unroll
                         for (int k = 0; k < 32; ++k) o[h + k] = fmaf(w1, y[k], w0 * o[h + k]);
                     }
@@ -879,7 +912,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar.o_free + 8 * i);
-            if (lane == 0 && join) mbar_arrive(bar.o_free + 8);
+            if (lane == 0 && join) mbar_arrive(bar.o_free + 8 * (1 - i));
         }
     } while (cur.next(a));
 }
@@ -897,17 +930,17 @@ __global__ void __launch_bounds__(TcPrefill<D, kFp8>::kThreads, 1)
         return;
     }
     const TcBars bar(smem_u32(smem + L::kBars), L::kStages, smem_u32(smem + L::kRawBars), L::kRaw);
-    uint32_t *tmem_slot = (uint32_t *)(smem + L::kBars + 248);
-    const OddColumns odd{(int32_t *)(smem + L::kBars + 256), (int32_t *)(smem + L::kBars + 240)};
-    static_assert(96 + 16 * L::kStages <= 232, "the barriers fit");
+    uint32_t *tmem_slot = (uint32_t *)(smem + L::kBars + 264);
+    const OddColumns odd{(int32_t *)(smem + L::kBars + 288), (int32_t *)(smem + L::kBars + 256)};
+    static_assert(120 + 16 * L::kStages <= 256, "the barriers fit");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        mbar_init(bar.q_full, 1);
-        mbar_init(bar.q_free, 1);
         mbar_init(bar.v_go, 1);
         mbar_init(bar.v_ok, 1);
         mbar_init(bar.x_full, 4);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(bar.q_full + 8 * i, 1);
+            mbar_init(bar.q_free + 8 * i, 1);
             mbar_init(bar.s_full + 8 * i, 1);
             mbar_init(bar.p_full + 8 * i, 4);
             mbar_init(bar.o_full + 8 * i, 1);
