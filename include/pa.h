@@ -561,7 +561,7 @@ pa_status_t pa_prefill_fp8(void *out, const void *q, const void *k_cache, const 
  *     before they are pushed, one outside the pool is recorded.
  * workspace  device scratch of pa_tables_workspace_bytes(num_reqs, num_rows)
  *     bytes, 256-byte aligned; calls that share it must be ordered on one stream.
- * Two kernels per call (release without a request: one).
+ * One kernel per call, or two for larger batches.
  * ---------------------------------------------------------------------- */
 typedef struct pa_tables {
     int32_t *tables;

@@ -594,31 +594,24 @@ def pa_tables_workspace_bytes(num_reqs, num_rows):
 
 
 def _tables_state(d, tables, lens, free_list, free_count, block_size, lens_out, free_count_out):
-    i32 = _torch().int32
+    """The state's arguments; its tensors' shapes are checked here."""
     if tables.dim() != 2:
         raise ValueError("tables must be [num_rows, max_blocks_per_row]")
     R, W = tables.shape
-    for name, t in (("lens", lens), ("lens_out", lens_out)):
-        if t is not None and t.shape != (R,):
-            raise ValueError("%s must be [num_rows]" % name)
-    if free_list.dim() != 1:
-        raise ValueError("free_list must be [num_blocks]")
-    for name, t in (("free_count", free_count), ("free_count_out", free_count_out)):
-        if t is not None and t.numel() != 1:
-            raise ValueError("%s must hold one number" % name)
-    return _lib.Tables(_ptr(tables, "tables", d, i32), _ptr(lens, "lens", d, i32),
-                       None if lens_out is None else _ptr(lens_out, "lens_out", d, i32),
-                       _ptr(free_list, "free_list", d, i32), _ptr(free_count, "free_count", d, i32),
-                       None if free_count_out is None else _ptr(free_count_out, "free_count_out", d, i32),
-                       R, W, free_list.shape[0], int(block_size))
-
-
-def _tables_rows(d, rows, n):
-    if rows is None:
-        return None
-    if rows.shape != (n,):
-        raise ValueError("rows must be [num_reqs]")
-    return _ptr(rows, "rows", d, _torch().int32)
+    if lens.shape != (R,) or free_list.dim() != 1 or free_count.numel() != 1:
+        raise ValueError("lens must be [num_rows], free_list [num_blocks] and free_count one number")
+    lo = co = None
+    i32 = _torch().int32
+    if lens_out is not None:
+        if lens_out.shape != (R,):
+            raise ValueError("lens_out must be [num_rows]")
+        lo = _ptr(lens_out, "lens_out", d, i32)
+    if free_count_out is not None:
+        if free_count_out.numel() != 1:
+            raise ValueError("free_count_out must hold one number")
+        co = _ptr(free_count_out, "free_count_out", d, i32)
+    return _lib.Tables(_ptr(tables, "tables", d, i32), _ptr(lens, "lens", d, i32), lo, _ptr(free_list, "free_list", d, i32),
+                       _ptr(free_count, "free_count", d, i32), co, R, W, free_list.shape[0], block_size)
 
 
 def pa_extend_tables(tables, lens, free_list, free_count, new_lens, block_size, max_tokens, rows=None, lens_out=None,
@@ -639,24 +632,28 @@ def pa_extend_tables(tables, lens, free_list, free_count, new_lens, block_size, 
     i32 = torch.int32
     d, stream = _here()
     state = _tables_state(d, tables, lens, free_list, free_count, block_size, lens_out, free_count_out)
-    N = new_lens.shape[0]
-    if new_lens.dim() != 1 or N > state.num_rows:
+    N, R = new_lens.shape[0], state.num_rows
+    if new_lens.dim() != 1 or N > R:
         raise ValueError("new_lens must be [num_reqs], at most one request for each row")
     width = state.max_blocks_per_row if batch_width is None else int(batch_width)
-    max_tokens = int(max_tokens)
     if width <= 0 or max_tokens < 0:
         raise ValueError("batch_width must be positive and max_tokens not negative")
-    shapes = ((N, width), (N,), (N + 1,), (max_tokens,))
     if out is None:
-        out = tuple(torch.empty(s, dtype=i32, device=tables.device) for s in shapes)
-    elif tuple(tuple(t.shape) for t in out) != shapes:
+        out = tuple(torch.empty(s, dtype=i32, device=tables.device) for s in ((N, width), (N,), (N + 1,), (max_tokens,)))
+    bt, sl, cu, slots = out
+    if bt.shape != (N, width) or sl.shape != (N,) or cu.shape != (N + 1,) or slots.shape != (max_tokens,):
         raise ValueError("out must be block_tables [N, batch_width], seq_lens [N], cu_q_lens [N + 1], slot_mapping [max_tokens]")
+    r = None
+    if rows is not None:
+        if rows.shape != (N,):
+            raise ValueError("rows must be [num_reqs]")
+        r = _ptr(rows, "rows", d, i32)
     if workspace is None:
-        workspace = torch.empty(pa_tables_workspace_bytes(N, state.num_rows), dtype=torch.uint8, device=tables.device)
-    bt, sl, cu, slots = (_ptr(t, n, d, i32) for n, t in zip(("block_tables", "seq_lens", "cu_q_lens", "slot_mapping"), out))
-    st = _lib.load().pa_extend_tables(ctypes.byref(state), _tables_rows(d, rows, N), _ptr(new_lens, "new_lens", d, i32), N,
-                                      bt, width, sl, cu, slots, max_tokens, _ptr(workspace, "workspace", d),
-                                      workspace.nbytes, stream)
+        workspace = torch.empty(pa_tables_workspace_bytes(N, R), dtype=torch.uint8, device=tables.device)
+    st = _lib.load().pa_extend_tables(
+        state, r, _ptr(new_lens, "new_lens", d, i32), N, _ptr(bt, "block_tables", d, i32), width,
+        _ptr(sl, "seq_lens", d, i32), _ptr(cu, "cu_q_lens", d, i32), _ptr(slots, "slot_mapping", d, i32), max_tokens,
+        _ptr(workspace, "workspace", d), workspace.nbytes, stream)
     _lib.check("pa_extend_tables", st)
     return out
 
@@ -667,12 +664,12 @@ def pa_release_tables(tables, lens, free_list, free_count, rows, block_size, len
     stack and set their lengths to 0; the state as in pa_extend_tables."""
     d, stream = _here()
     state = _tables_state(d, tables, lens, free_list, free_count, block_size, lens_out, free_count_out)
-    if rows.dim() != 1 or rows.shape[0] > state.num_rows:
+    N, R = rows.shape[0], state.num_rows
+    if rows.dim() != 1 or N > R:
         raise ValueError("rows must be [num_reqs], at most one request for each row")
-    N = rows.shape[0]
     if workspace is None:
-        workspace = _torch().empty(pa_tables_workspace_bytes(N, state.num_rows), dtype=_torch().uint8, device=tables.device)
-    st = _lib.load().pa_release_tables(ctypes.byref(state), _tables_rows(d, rows, N), N, _ptr(workspace, "workspace", d),
+        workspace = _torch().empty(pa_tables_workspace_bytes(N, R), dtype=_torch().uint8, device=tables.device)
+    st = _lib.load().pa_release_tables(state, _ptr(rows, "rows", d, _torch().int32), N, _ptr(workspace, "workspace", d),
                                        workspace.nbytes, stream)
     _lib.check("pa_release_tables", st)
 
