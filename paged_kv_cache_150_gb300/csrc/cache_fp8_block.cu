@@ -3,10 +3,10 @@
 // A block and KV head share one exponent: e = max over the call's rows in that
 // block of the row exponent (fp8_codec.cuh), and at least the e that the block
 // has where it holds earlier positions; codes are e4m3(x 2^-e).  So the unit of
-// work is (sequence, block it touches, KV head, K or V): a team of W warps loads
-// the unit's rows once (16-byte vectors, up to kVecs a thread, all in flight
-// together), reduces the largest |x|, and encodes what it still holds in
-// registers.  No unit shares a block with another, so there are no atomics and
+// work is (sequence, block it touches, KV head): a team of W warps loads the
+// unit's rows of K and V once (16-byte vectors, up to kVecs of each a thread, all
+// in flight together), reduces the largest |x|, and encodes what it still holds
+// in registers.  No unit shares a block with another, so there are no atomics and
 // the result does not depend on any order.  A unit's rows are Hk * D elements
 // apart, D contiguous ones each.
 //
@@ -22,7 +22,8 @@
 
 namespace pa {
 
-constexpr int kVecs = 8;          // vectors of a thread in registers
+constexpr int kVecs = 8;             // vectors of K, and of V, that a thread holds
+constexpr int kWriteBlocksCtas = 2;  // resident CTAs per SM that its registers are held to
 constexpr int kCuSmem = 2048;     // offsets kept in shared memory
 constexpr int kByteMax = kScaleMax + kScaleBias;  // largest byte that a write makes
 
@@ -32,7 +33,7 @@ struct WriteBlocksArgs {
     int32_t max_blocks, N, T;
     uint8_t *kc, *vc, *ks, *vs;
     int32_t NB, B, Hk, D;
-    uint32_t units;  // numbers of units, of which each has 2 * Hk items
+    uint32_t units;  // numbers of units, of which each has Hk items
     unsigned int *err;
 };
 
@@ -122,85 +123,101 @@ __device__ __forceinline__ void team_sync(int team) {
         asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(32 * W) : "memory");
 }
 
-// Rows of whole 16-byte vectors (vecs of them), a team of W of the CTA's 8 warps
-// per item.
+// Codes that a block holds from before (rows [0, held) of one head), recoded by f;
+// members of a team of n threads.
+__device__ __forceinline__ void recode_rows(uint8_t *codes, int32_t held, int32_t D, int64_t stride, float f, uint32_t ti,
+                                            uint32_t n) {
+    const uint32_t wr = (uint32_t)D / 4;
+    for (uint32_t i = ti; i < (uint32_t)held * wr; i += n) {
+        const uint32_t row = i / wr;
+        uint32_t *p = reinterpret_cast<uint32_t *>(codes + (int64_t)row * stride) + (i - row * wr);
+        const float4 y = decode4(*p);
+        *p = encode4(y.x * f, y.y * f, y.z * f, y.w * f);
+    }
+}
+
+// Rows of whole 16-byte vectors, as many per row (vecs) as divide the team and as
+// many per block as its registers hold: a team of W of the CTA's 8 warps takes a
+// unit and `heads` of its KV heads, one after the other, K and V together.  A
+// thread's vectors are the same column of rows a step apart.
+// 48 prompts of 700 to 4500 tokens (8 heads, head_dim 128, bf16; 591 MB): 107 us,
+// 5.5 TB/s, 0.82 of the copy bandwidth.  With a search per head and a division per
+// vector it took 152 instructions per vector of 8 values and 161 us; with half the
+// vectors per thread and 3 or 4 CTAs 109 and 113 us.  One token of 64 sequences:
+// 4.5 us.
 template <typename T, int W>
-__global__ void __launch_bounds__(256) write_blocks_kernel(const __grid_constant__ WriteBlocksArgs a) {
+__global__ void __launch_bounds__(256, kWriteBlocksCtas) write_blocks_kernel(const __grid_constant__ WriteBlocksArgs a, const int32_t heads) {
     grid_dependency_wait();
     grid_launch_dependents();
     constexpr int N = Vec16<T>::N, kTeam = 32 * W, kTeams = 8 / W;
     __shared__ int32_t cu_s[kCuSmem];
-    __shared__ uint32_t tops[8];
+    __shared__ uint32_t tops[2][8];
     if (!load_offsets(a, cu_s)) return;
     const int32_t *cu = a.N < kCuSmem ? cu_s : a.cu;
     const int team = threadIdx.x / kTeam, ti = threadIdx.x % kTeam, warp = threadIdx.x >> 5;
-    const uint32_t vecs = (uint32_t)a.D / N, stride = (uint32_t)a.Hk * vecs;  // of a row, and from row to row
-    const uint64_t items = (uint64_t)a.units * 2 * a.Hk;
+    const uint32_t Hk = (uint32_t)a.Hk, vecs = (uint32_t)a.D / N, stride = Hk * vecs;  // of a row, and from row to row
+    const int32_t my_row = ti / (int32_t)vecs, rows_step = kTeam / (int32_t)vecs;
+    const uint32_t my_at = (uint32_t)my_row * stride + ((uint32_t)ti - (uint32_t)my_row * vecs), step = (uint32_t)rows_step * stride;
+    const uint32_t groups = (Hk + (uint32_t)heads - 1) / (uint32_t)heads;
+    const uint64_t items = (uint64_t)a.units * groups;
     for (uint64_t item = (uint64_t)blockIdx.x * kTeams + team; item < items; item += (uint64_t)gridDim.x * kTeams) {
-        const uint32_t u = (uint32_t)(item / (2 * a.Hk)), hs = (uint32_t)(item - (uint64_t)u * 2 * a.Hk);
-        const bool is_v = hs >= (uint32_t)a.Hk;
-        const uint32_t h = is_v ? hs - a.Hk : hs;
+        const uint32_t u = (uint32_t)(item / groups), h0 = (uint32_t)(item - (uint64_t)u * groups) * (uint32_t)heads;
         const WriteUnit w = find_unit(a, cu, u);
         if (w.phys < 0) continue;  // the same for the whole team
-        const uint4 *x = reinterpret_cast<const uint4 *>(is_v ? a.v : a.k) + ((int64_t)w.row0 * a.Hk + h) * vecs;
-        uint8_t *codes = (is_v ? a.vc : a.kc) + (((int64_t)w.phys * a.B + w.off) * a.Hk + h) * a.D;
-        uint8_t *scale = (is_v ? a.vs : a.ks) + (int64_t)w.phys * a.Hk + h;
-        const uint32_t old = w.held > 0 ? *scale : 0u;
-        const uint32_t total = (uint32_t)w.ntok * vecs;
-        uint4 r[kVecs];
-        uint32_t top = 0;
-        auto load = [&](uint32_t e0) {
+        const int64_t from = (int64_t)w.row0 * stride + h0 * vecs + my_at;
+        const uint4 *src[2] = {reinterpret_cast<const uint4 *>(a.k) + from, reinterpret_cast<const uint4 *>(a.v) + from};
+        const int64_t to = (((int64_t)w.phys * a.B + w.off) * stride + h0 * vecs + my_at) * N;
+        uint8_t *dst[2] = {a.kc + to, a.vc + to};
+        const int64_t sc = (int64_t)w.phys * Hk + h0;
+        const int32_t left = w.ntok - my_row;  // this thread's rows: j * rows_step < left
+        const uint32_t h1 = min(h0 + (uint32_t)heads, Hk);
+        for (uint32_t h = h0; h < h1; ++h) {
+            uint8_t *scale[2] = {a.ks + sc + (h - h0), a.vs + sc + (h - h0)};
+            uint32_t old[2] = {0u, 0u};
+            if (w.held > 0) old[0] = *scale[0], old[1] = *scale[1];
+            uint4 r[2][kVecs];
 #pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                const uint32_t e = e0 + j * kTeam + ti, row = e / vecs;
-                r[j] = e < total ? __ldcs(x + (int64_t)row * stride + (e - row * vecs)) : make_uint4(0u, 0u, 0u, 0u);
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j)
+                    r[s][j] = j * rows_step < left ? __ldcs(src[s] + j * step) : make_uint4(0u, 0u, 0u, 0u);
+            uint32_t top[2] = {0u, 0u};
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j) top[s] = max(top[s], Vec16<T>::largest(r[s][j]));
+                top[s] = __reduce_max_sync(0xffffffffu, top[s]);
             }
-        };
-        for (uint32_t e0 = 0; e0 < total; e0 += kVecs * kTeam) {
-            load(e0);
+            if constexpr (W > 1) {
+                if ((threadIdx.x & 31) == 0) tops[0][warp] = top[0], tops[1][warp] = top[1];
+                team_sync<W>(team);
 #pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                float f[N];
-                Vec16<T>::load(r[j], f);
-#pragma unroll
-                for (int k = 0; k < N; ++k) top = max(top, finite_bits(f[k]));
+                for (int k = 0; k < W; ++k) top[0] = max(top[0], tops[0][team * W + k]), top[1] = max(top[1], tops[1][team * W + k]);
             }
-        }
-        top = __reduce_max_sync(0xffffffffu, top);
-        if constexpr (W > 1) {
-            if ((threadIdx.x & 31) == 0) tops[warp] = top;
-            team_sync<W>(team);
 #pragma unroll
-            for (int k = 0; k < W; ++k) top = max(top, tops[team * W + k]);
-        }
-        uint32_t byte;
-        const int32_t e = block_exponent(top, w.held, old, &byte);
-        const float inv = inv_scale(e);
-        for (uint32_t e0 = 0; e0 < total; e0 += kVecs * kTeam) {
-            if (total > kVecs * kTeam) load(e0);  // more than the registers hold: read again
+            for (int s = 0; s < 2; ++s) {
+                uint32_t byte;
+                const int32_t e = block_exponent(Vec16<T>::bits(top[s]), w.held, old[s], &byte);
+                const float inv = inv_scale(e);
 #pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                const uint32_t v = e0 + j * kTeam + ti, row = v / vecs;
-                if (v < total) {
-                    float f[N];
-                    Vec16<T>::load(r[j], f);
-                    store_codes<N>(codes + ((int64_t)row * stride + (v - row * vecs)) * N, f, inv);
+                for (int j = 0; j < kVecs; ++j)
+                    if (j * rows_step < left) {
+                        float f[N];
+                        Vec16<T>::load(r[s][j], f);
+                        store_codes<N>(dst[s] + (uint64_t)j * step * N, f, inv);
+                    }
+                if (w.held > 0) {
+                    const float f = recode_factor(e, old[s]);
+                    if (f != 1.f)
+                        recode_rows((s ? a.vc : a.kc) + ((int64_t)w.phys * a.B * Hk + h) * a.D, w.held, a.D, (int64_t)Hk * a.D, f, ti, kTeam);
                 }
+                old[s] = byte;
             }
+            team_sync<W>(team);  // the old bytes and tops have been read
+            if (ti < 2) *scale[ti] = (uint8_t)old[ti];
+            src[0] += vecs, src[1] += vecs;
+            dst[0] += a.D, dst[1] += a.D;
         }
-        const float f = recode_factor(e, old);
-        if (w.held > 0 && f != 1.f) {
-            uint32_t *words = reinterpret_cast<uint32_t *>(codes - (int64_t)w.off * a.Hk * a.D);
-            const uint32_t wr = (uint32_t)a.D / 4;
-            for (uint32_t i = ti; i < (uint32_t)w.held * wr; i += kTeam) {
-                const uint32_t row = i / wr;
-                uint32_t *p = words + (int64_t)row * a.Hk * wr + (i - row * wr);
-                const float4 y = decode4(*p);
-                *p = encode4(y.x * f, y.y * f, y.z * f, y.w * f);
-            }
-        }
-        team_sync<W>(team);  // old and tops have been read
-        if (ti == 0) *scale = (uint8_t)byte;
     }
 }
 
@@ -253,19 +270,25 @@ namespace {
 template <typename T>
 cudaError_t launch_write_blocks(const WriteBlocksArgs &a, cudaStream_t s) {
     WriteBlocksArgs arg = a;
-    void *args[] = {&arg};
-    const int64_t items = (int64_t)a.units * 2 * a.Hk;
-    const int64_t vecs = (int64_t)a.D / Vec16<T>::N * a.B;  // of a whole block and head
-    if (!aligned_rows<T>(a.D, a.k, a.v, a.kc, a.vc) || vecs >= ((int64_t)1 << 30) ||
-        (int64_t)a.Hk * a.D >= ((int64_t)1 << 30))
+    const int64_t vecs = a.D / Vec16<T>::N, block_vecs = vecs * a.B;  // of a row, of a block and head
+    int W = 1;  // as few warps as hold a block and head
+    while (W < 8 && block_vecs > 32 * kVecs * W) W *= 2;
+    if (!aligned_rows<T>(a.D, a.k, a.v, a.kc, a.vc) || block_vecs > 32 * kVecs * W || 32 * W % vecs != 0 ||
+        block_vecs * a.Hk >= ((int64_t)1 << 28)) {
+        void *args[] = {&arg};
+        const int64_t items = (int64_t)a.units * 2 * a.Hk;
         return launch_pdl((const void *)write_blocks_any_kernel<T>, dim3(grid_for((items + 7) / 8, 8)), dim3(256), args, 0, s);
-    // a whole block in the registers of as few warps as hold it
-    const int W = vecs <= 32 * kVecs ? 1 : vecs <= 64 * kVecs ? 2 : vecs <= 128 * kVecs ? 4 : 8;
+    }
     const void *fn = W == 1   ? (const void *)write_blocks_kernel<T, 1>
                      : W == 2 ? (const void *)write_blocks_kernel<T, 2>
                      : W == 4 ? (const void *)write_blocks_kernel<T, 4>
                               : (const void *)write_blocks_kernel<T, 8>;
-    return launch_pdl(fn, dim3(grid_for((items * W + 7) / 8, 4)), dim3(256), args, 0, s);
+    // All heads of a unit by one team where that still fills the GPU, else one.
+    const int64_t teams = (int64_t)std::max(num_sms(), 1) * kWriteBlocksCtas * (8 / W);
+    int32_t heads = (int64_t)a.units >= 2 * teams ? a.Hk : 1;
+    const int64_t items = (int64_t)a.units * ((a.Hk + heads - 1) / heads);
+    void *args[] = {&arg, &heads};
+    return launch_pdl(fn, dim3(grid_for((items * W + 7) / 8, kWriteBlocksCtas)), dim3(256), args, 0, s);
 }
 
 }  // namespace

@@ -16,14 +16,16 @@ struct Vec16<float> {
         x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z),
         x[3] = __uint_as_float(u.w);
     }
+    // Largest finite |x| of a vector, in a form that compares by size; its fp32 bits.
+    static __device__ __forceinline__ uint32_t largest(const uint4 &u) {
+        return max(max(finite_bits(__uint_as_float(u.x)), finite_bits(__uint_as_float(u.y))),
+                   max(finite_bits(__uint_as_float(u.z)), finite_bits(__uint_as_float(u.w))));
+    }
+    static __device__ __forceinline__ uint32_t bits(uint32_t m) { return m; }
     // Largest finite |x| over the rows that L lanes hold of K and of V, as fp32 bits.
     template <int L>
     static __device__ __forceinline__ void row_max(const uint4 &k, const uint4 &v, uint32_t &ka, uint32_t &va) {
-        auto lane_max = [](const uint4 &u) {
-            return max(max(finite_bits(__uint_as_float(u.x)), finite_bits(__uint_as_float(u.y))),
-                       max(finite_bits(__uint_as_float(u.z)), finite_bits(__uint_as_float(u.w))));
-        };
-        ka = lane_max(k), va = lane_max(v);
+        ka = largest(k), va = largest(v);
         if constexpr (L == 32) {
             ka = __reduce_max_sync(0xffffffffu, ka);
             va = __reduce_max_sync(0xffffffffu, va);
@@ -50,25 +52,27 @@ struct Vec16<__nv_bfloat16> {
             x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
+    // Largest finite |x| of a vector as bf16 bits; its fp32 bits.
+    static __device__ __forceinline__ uint32_t largest(const uint4 &u) {
+        const uint32_t w[4] = {u.x & 0x7fff7fffu, u.y & 0x7fff7fffu, u.z & 0x7fff7fffu, u.w & 0x7fff7fffu};
+        uint32_t m = 0, odd = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m = __vmaxu2(m, w[i]);
+            odd |= (w[i] + 0x00800080u) & 0x80008000u;  // an exponent of all ones
+        }
+        if (odd) {
+            m = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & ~__vcmpgeu2(w[i], 0x7f807f80u));
+        }
+        return max(m >> 16, m & 0xffffu);
+    }
+    static __device__ __forceinline__ uint32_t bits(uint32_t m) { return m << 16; }
     // The same in 16-bit pairs: K's and V's maxima travel in one word.
     template <int L>
     static __device__ __forceinline__ void row_max(const uint4 &k, const uint4 &v, uint32_t &ka, uint32_t &va) {
-        auto lane_max = [](const uint4 &u) {
-            const uint32_t w[4] = {u.x & 0x7fff7fffu, u.y & 0x7fff7fffu, u.z & 0x7fff7fffu, u.w & 0x7fff7fffu};
-            uint32_t m = 0, odd = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                m = __vmaxu2(m, w[i]);
-                odd |= (w[i] + 0x00800080u) & 0x80008000u;  // an exponent of all ones
-            }
-            if (odd) {
-                m = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & ~__vcmpgeu2(w[i], 0x7f807f80u));
-            }
-            return max(m >> 16, m & 0xffffu);
-        };
-        uint32_t m = lane_max(k) << 16 | lane_max(v);
+        uint32_t m = largest(k) << 16 | largest(v);
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
         ka = m & 0xffff0000u, va = m << 16;
