@@ -129,8 +129,9 @@ pa_status_t prefill_bind(const PrefillPlan &p, PrefillArgs *a, void *workspace) 
 
 pa_status_t prefill_launch_plan(PrefillArgs &a, cudaStream_t s) {
     void *args[] = {&a};
-    return launch_pdl((const void *)prefill_plan_kernel, dim3(1), dim3(1024), args, 0, s) == cudaSuccess ? PA_OK
-                                                                                                       : PA_ERR_CUDA;
+    const bool small = a.N <= 256 && a.max_tiles <= 256;
+    const void *fn = small ? (const void *)prefill_plan_kernel<512> : (const void *)prefill_plan_kernel<1024>;
+    return launch_pdl(fn, dim3(1), dim3(small ? 512 : 1024), args, 0, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 pa_status_t prefill_launch_merge(PrefillArgs &a, bool f32, int32_t head_dim, cudaStream_t s) {
@@ -272,6 +273,7 @@ pa_status_t chunk_call(const ChunkKind &kind, void *out, const void *q, const vo
     a.H = num_heads;
     a.step = kind.step;
     a.pair = kind.pair;
+    a.min_w = 1;
     a.scale_log2 = scale * 1.4426950408889634f;
     return prefill_launch(p, cache, a, workspace, (cudaStream_t)stream);
 }

@@ -7,6 +7,8 @@
 
 namespace pa {
 
+constexpr int32_t kMinWeight = 4;  // weight that a CTA's range of decode units should have (active_ctas)
+
 // Shape of one call: which kernel, its tiles, and the workspace behind it.
 struct PrefillPlan {
     bool tc;           // tcgen05 kernel

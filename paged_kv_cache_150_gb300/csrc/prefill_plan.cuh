@@ -62,6 +62,7 @@ struct PrefillArgs {
     int32_t kt;           // keys per unit
     int32_t extra;        // weight of a tile beside its units
     int32_t C;            // persistent CTAs
+    int32_t min_w;        // weight that a CTA's range should have (active_ctas); 1: any
     int32_t max_tiles;    // capacity of tiles[] and cu[]
     float scale_log2;
     int32_t step;         // positions that each token sees more than the one before it: 1, or 0 where all see all (pa_cross)
@@ -89,9 +90,23 @@ __device__ __forceinline__ int32_t prefill_units(const PrefillTile &t, int32_t k
     return keys <= kt ? 1 : (int32_t)(((int64_t)keys + kt - 1) / kt);  // no key: one unit that writes zeros
 }
 
-// Inclusive block-wide scan of x over 1024 threads plus carry; returns this
+// CTAs that share a list of weight W: all of them, one for each weight at most;
+// with min_w, no more than give ranges of that weight, or kFewCtas.  Decode's units
+// are short, and a list of some hundreds cut into as many pieces as there are
+// CTAs is slow to merge: one sequence of 4000 tokens over the 8-bit cache (252
+// units) on 304 CTAs 37.7 us, on 63 18.2; four short ones (20 units) on 20 CTAs
+// 10.7 us, on 5 11.5.
+constexpr int64_t kFewCtas = 48;
+__device__ __forceinline__ int32_t active_ctas(const PrefillArgs &a, int64_t W) {
+    const int64_t most = a.min_w > 1 ? max(W / a.min_w, min(W, kFewCtas)) : W;
+    return (int32_t)min(most, (int64_t)a.C);
+}
+
+// Inclusive scan of x over a block of kThreads threads plus carry; returns this
 // thread's inclusive sum, *total the sum with the carry.
-__device__ __forceinline__ int32_t block_scan_1024(int32_t x, int32_t carry, int32_t *warp_incl, int32_t *total) {
+template <int kThreads>
+__device__ __forceinline__ int32_t block_scan(int32_t x, int32_t carry, int32_t *warp_incl, int32_t *total) {
+    constexpr int kWarps = kThreads / 32;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -101,18 +116,15 @@ __device__ __forceinline__ int32_t block_scan_1024(int32_t x, int32_t carry, int
     __syncthreads();  // the previous scan's reads of warp_incl
     if (lane == 31) warp_incl[w] = x;
     __syncthreads();
-    if (w == 0) {
-        int32_t s = warp_incl[lane];
+    int32_t s = lane < kWarps ? warp_incl[lane] : 0;  // every warp scans the warps' sums
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int32_t y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
-        }
-        warp_incl[lane] = s;
+    for (int o = 1; o < kWarps; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
     }
-    __syncthreads();
-    *total = carry + warp_incl[31];
-    return carry + x + (w > 0 ? warp_incl[w - 1] : 0);
+    *total = carry + __shfl_sync(0xffffffffu, s, kWarps - 1);
+    const int32_t before = __shfl_sync(0xffffffffu, s, w > 0 ? w - 1 : 0);
+    return carry + x + (w > 0 ? before : 0);
 }
 
 // Largest i in [0, n) with cu[i] <= x (cu not decreasing, cu[0] <= x).
@@ -132,72 +144,75 @@ __device__ __forceinline__ int32_t last_at_most(const int32_t *cu, int32_t n, in
 // the tile in which each CTA's range starts.  Row offsets that are not
 // increasing within [0, T] void the whole call (no tile: out stays as it
 // was), a length outside the table's reach counts as 0; both are recorded.
-static __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillArgs a) {
+// kThreads: 1024, or 512 for small batches, whose barriers are cheaper.
+template <int kThreads>
+static __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const __grid_constant__ PrefillArgs a) {
     grid_dependency_wait();
     grid_launch_dependents();
-    constexpr int32_t kSmemCu = 8192, kSmemSeqs = 2048;
+    constexpr int32_t kSmemCu = kThreads == 1024 ? 8192 : 1024, kSmemSeqs = kThreads == 1024 ? 2048 : 512,
+                      kSmemTiles = 256;
     __shared__ int32_t warp_incl[32];
     __shared__ int32_t cu_s[kSmemCu], tile0_s[kSmemSeqs];
+    __shared__ PrefillTile tiles_s[kSmemTiles];
     const int tid = threadIdx.x;
     const int64_t max_len = (int64_t)a.max_blocks * a.B;
     const int32_t tq = a.tq1 * a.nrt;
-    bool ok = true;
-    if (a.cu_q) {
-        for (int32_t i = tid; i <= a.N; i += 1024) {
-            const int32_t x = a.cu_q[i];
-            ok = ok && x >= 0 && x <= a.T && (i == 0 || a.cu_q[i - 1] <= x);
-        }
-    }
-    ok = __syncthreads_and(ok) != 0;
-    if (!ok) {
-        if (tid == 0) {
-            atomicOr(a.err, kErrBounds);
-            a.ctl[1] = a.ctl[2] = 0;
-            a.cu[0] = 0;
-        }
-        for (int32_t c = tid; c < a.C; c += 1024) a.starts[c] = WalkStart{};  // no work
-        return;
-    }
     int32_t *tile0 = a.N <= kSmemSeqs ? tile0_s : a.seq_tile0;  // first tile of each sequence
-    int32_t tiles = 0;
-    for (int32_t base = 0; base < a.N; base += 1024) {
-        const int32_t i = base + tid;
-        int32_t nt = 0;
-        if (i < a.N) {
-            const int32_t n = a.cu_q ? a.cu_q[i + 1] - a.cu_q[i] : 1;
-            nt = (int32_t)(((int64_t)n + tq - 1) / tq);
-            const int32_t L = a.seq_lens[i];
-            if (L < 0 || L > max_len) atomicOr(a.err, kErrLength);
+    int32_t tiles = a.N;
+    if (a.cu_q) {
+        bool ok = true;
+        tiles = 0;
+        for (int32_t base = 0; base < a.N; base += kThreads) {
+            const int32_t i = base + tid;
+            int32_t nt = 0;
+            if (i < a.N) {
+                const int32_t x = a.cu_q[i], y = a.cu_q[i + 1];
+                ok = ok && x >= 0 && y <= a.T && x <= y;
+                nt = ok ? (int32_t)(((int64_t)(y - x) + tq - 1) / tq) : 0;
+            }
+            int32_t total;
+            const int32_t incl = block_scan<kThreads>(nt, tiles, warp_incl, &total);
+            if (i < a.N) tile0[i] = incl - nt;
+            tiles = total;
         }
-        int32_t total;
-        const int32_t incl = block_scan_1024(nt, tiles, warp_incl, &total);
-        if (i < a.N) tile0[i] = incl - nt;
-        tiles = total;
+        ok = __syncthreads_and(ok) != 0;  // tile0 is read by this CTA's other threads
+        if (!ok) {
+            if (tid == 0) {
+                atomicOr(a.err, kErrBounds);
+                a.ctl[1] = a.ctl[2] = 0;
+                a.cu[0] = 0;
+            }
+            for (int32_t c = tid; c < a.C; c += kThreads) a.starts[c] = WalkStart{};  // no work
+            return;
+        }
     }
-    __syncthreads();  // tile0 is read by this CTA's other threads
     const bool in_smem = tiles + 1 <= kSmemCu;
     int32_t units = 0;
-    for (int32_t base = 0; base < tiles; base += 1024) {
+    for (int32_t base = 0; base < tiles; base += kThreads) {
         const int32_t k = base + tid;
         int32_t u = 0;
         if (k < tiles) {
             // the last sequence that starts at or before tile k (it has tiles);
             // single queries: a tile each
             const int32_t lo = a.cu_q ? last_at_most(tile0, a.N, k) : k;
-            const int32_t r0 = a.cu_q ? a.cu_q[lo] : lo, n = a.cu_q ? a.cu_q[lo + 1] - r0 : 1;
-            const int32_t t0 = (k - tile0[lo]) * tq;
             int32_t L = a.seq_lens[lo];
-            if (L < 0 || L > max_len) L = 0;
+            const int32_t r0 = a.cu_q ? a.cu_q[lo] : lo, n = a.cu_q ? a.cu_q[lo + 1] - r0 : 1;
+            const int32_t t0 = a.cu_q ? (k - tile0[lo]) * tq : 0;
+            if (L < 0 || L > max_len) {
+                atomicOr(a.err, kErrLength);
+                L = 0;
+            }
             PrefillTile t;
             t.seq = lo;
             t.row0 = r0 + t0;
             t.ntok = min(tq, n - t0);
             t.p0 = a.step ? L - n + t0 : L - 1;
             a.tiles[k] = t;
+            if (k < kSmemTiles) tiles_s[k] = t;
             u = prefill_units(t, a.kt, a.step) + a.extra;
         }
         int32_t total;
-        const int32_t incl = block_scan_1024(u, units, warp_incl, &total);
+        const int32_t incl = block_scan<kThreads>(u, units, warp_incl, &total);
         if (k < tiles) {
             a.cu[k] = incl - u;
             if (in_smem) cu_s[k] = incl - u;
@@ -210,9 +225,10 @@ static __global__ void __launch_bounds__(1024) prefill_plan_kernel(const Prefill
     }
     __syncthreads();
     const int32_t *cu = in_smem ? cu_s : a.cu;
+    auto tile_at = [&](int32_t k) { return k < kSmemTiles ? tiles_s[k] : a.tiles[k]; };
     const int64_t W = (int64_t)a.Hk * units;
-    const int32_t Ce = (int32_t)min(W, (int64_t)a.C);
-    for (int32_t c = tid; c < a.C; c += 1024) {
+    const int32_t Ce = active_ctas(a, W);
+    for (int32_t c = tid; c < a.C; c += kThreads) {
         WalkStart w{};
         if (c < Ce) {
             const int64_t lo = split_begin(c, W, Ce);
@@ -223,8 +239,8 @@ static __global__ void __launch_bounds__(1024) prefill_plan_kernel(const Prefill
             w.tiles = tiles;
             const int32_t begin = cu[w.k], next = w.k + 1 == tiles ? 0 : w.k + 1;
             auto end_of = [&](int32_t k) { return k + 1 == tiles ? units : cu[k + 1]; };
-            w.t = a.tiles[w.k];
-            w.t_next = a.tiles[next];
+            w.t = tile_at(w.k);
+            w.t_next = tile_at(next);
             w.x = lo - (r - begin);
             w.nu = end_of(w.k) - begin - a.extra;
             w.w_next = end_of(next) - cu[next];
@@ -303,7 +319,7 @@ __device__ __forceinline__ void note_cut(const PrefillArgs &a, int32_t c, bool w
     MergeEntry me{};
     if (work && cur.j0 > 0) {
         const int64_t W = (int64_t)a.Hk * a.cu[cur.tiles];
-        const int32_t Ce = (int32_t)min(W, (int64_t)a.C);
+        const int32_t Ce = active_ctas(a, W);
         const int32_t c0 = split_owner(cur.x + a.extra, W, Ce);
         if (c0 == c - 1) {
             me.row0 = cur.t.row0;
