@@ -33,10 +33,18 @@ bool f8_shape(const pa_cache_desc_t *c, int G, F8Args *f, size_t *smem) {
     return *smem <= 112 * 1024;
 }
 
-const void *f8_kernel(const pa_cache_desc_t *c) {
-    if (c->dtype == PA_FP8_E4M3_BLOCK)
-        return c->head_dim == 128 ? (const void *)decode_fp8_kernel<128, true> : (const void *)decode_fp8_kernel<64, true>;
-    return c->head_dim == 128 ? (const void *)decode_fp8_kernel<128, false> : (const void *)decode_fp8_kernel<64, false>;
+template <int D>
+const void *f8_kernel_for(F8Scales how) {
+    return how == kTokenScales    ? (const void *)decode_fp8_kernel<D, kTokenScales>
+           : how == kBlockScales8 ? (const void *)decode_fp8_kernel<D, kBlockScales8>
+                                  : (const void *)decode_fp8_kernel<D, kBlockScalesAny>;
+}
+// ks, vs: the call's scale arrays (nullptr: as if aligned).
+const void *f8_kernel(const pa_cache_desc_t *c, const F8Args &f, const uint8_t *ks, const uint8_t *vs) {
+    const F8Scales how = c->dtype != PA_FP8_E4M3_BLOCK                              ? kTokenScales
+                         : f.NH == 8 && (((uintptr_t)ks | (uintptr_t)vs) & 7) == 0 ? kBlockScales8
+                                                                                   : kBlockScalesAny;
+    return c->head_dim == 128 ? f8_kernel_for<128>(how) : f8_kernel_for<64>(how);
 }
 
 struct F8Plan {
@@ -69,7 +77,7 @@ pa_status_t decode_fp8_plan(const pa_cache_desc_t *c, int32_t N, int32_t H, cons
     p.threads = kF8Threads;
     p.max_tiles = N;
     p.smem = smem;
-    p.C = splits > 0 ? splits : default_ctas(f8_kernel(c), kF8Threads, smem);
+    p.C = splits > 0 ? splits : default_ctas(f8_kernel(c, pl->f, nullptr, nullptr), kF8Threads, smem);
     if (p.C <= 0) return PA_ERR_CUDA;
     prefill_workspace(&p, N, c->head_dim);
     return PA_OK;
@@ -156,7 +164,7 @@ extern "C" pa_status_t pa_decode_fp8(void *out, const void *q, const void *k_cac
     if ((st = prefill_bind(p, &a, workspace)) != PA_OK) return st;
     CUtensorMap tmk, tmv;
     if (!encode_codes_map(&tmk, k_cache, cache, f) || !encode_codes_map(&tmv, v_cache, cache, f)) return PA_ERR_CUDA;
-    const void *fn = f8_kernel(cache);
+    const void *fn = f8_kernel(cache, f, k_scale, v_scale);
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem) != cudaSuccess)
         return PA_ERR_CUDA;
     cudaGetLastError();
