@@ -846,7 +846,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
             m = mn;
         }
         const bool whole = cur.whole(), out32 = ((uintptr_t)a.out & 31) == 0;
-        const int64_t row = cur.slot(c) * (2 * kTcRows) + i * kTcRows + r;
+        const int64_t row = cur.slot(c) * (2 * kTcRows) + (sg.pair ? 0 : i) * kTcRows + r;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const bool odd_tile = any && odd.segment[sg.pair ? 0 : i] == (int32_t)segs;
         __nv_bfloat16 *op =

@@ -72,6 +72,16 @@ def test_any_split_count(kernel, splits):
     c.check(c.run(num_splits=splits, kernel=kernel), p_eps(BF, kernel))
 
 
+@pytest.mark.parametrize("splits", [1, 2, 3, 5, 7, 13, 29])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_short_tiles_per_cta(D, splits):
+    """Tiles of a few rows, several to a CTA, cut at either end of its range."""
+    c = Cross([3, 1, 8, 5, 2, 0, 7] * 3, [1000 - 41 * i for i in range(21)], 4, 2, D, 16, BF, seed=70 + splits)
+    out = c.run(num_splits=splits, kernel="mma")
+    assert error() == 0
+    c.check(out, p_eps(BF, "mma"))
+
+
 @pytest.mark.parametrize("n", [1, 63, 64, 65, 127, 128, 129, 255, 256, 257, 384])
 def test_encoder_lengths_around_unit_edges(n):
     c = Cross([3, 300], [n, n], 8, 2, 128, 16, BF, seed=60 + n)

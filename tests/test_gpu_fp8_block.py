@@ -292,6 +292,22 @@ def test_chunks_any_split_count(D, splits):
     assert error() == 0
 
 
+@pytest.mark.parametrize("splits", [1, 2, 3, 5, 7, 13, 29])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_short_chunks_per_cta(D, splits):
+    """Tiles of a few rows, several to a CTA, cut at either end of its range; blocks of very different size."""
+    b = Block8([3, 1, 8, 5, 2, 0, 7] * 3, [1000 - 41 * i for i in range(21)], 4, 2, D, 16, seed=80 + splits, spread=12)
+    out = pa.pa_prefill_fp8(**b.dev, num_splits=splits, kernel="mma")
+    assert error() == 0
+    b.check(out, P_MMA)
+
+
+@pytest.mark.parametrize("kernel", ["mma", "simt"])
+def test_chunks_over_blocks_of_very_different_size(kernel):
+    b = Block8([33, 3, 150], [700, 300, 2000], 16, 4, 128, 16, seed=41, spread=40)
+    b.check(pa.pa_prefill_fp8(**b.dev, kernel=kernel), P_MMA if kernel == "mma" else P_SIMT)
+
+
 @pytest.mark.parametrize("n", [1, 31, 32, 33, 63, 64, 65, 127, 128, 129, 256, 257])
 def test_chunk_lengths_around_tile_edges(n):
     b = Block8([n, 2], [n, 2 + n], 8, 2, 128, 16, seed=51 + n)
