@@ -64,7 +64,8 @@ pa_status_t prefill_layout(bool tc, const pa_cache_desc_t *c, int32_t N, int32_t
                            PrefillPlan *p) {
     const int32_t G = H / c->num_kv_heads;
     int threads = kSimtThreads;
-    const void *fn = tc ? prefill_tc_ptr(c->head_dim, c->dtype == PA_FP8_E4M3_BLOCK, &p->smem, &threads)
+    p->conv = c->dtype != PA_FP8_E4M3_BLOCK ? 0 : (int64_t)T <= (int64_t)N * (kTcRows / G) ? 8 : 4;
+    const void *fn = tc ? prefill_tc_ptr(c->head_dim, p->conv, &p->smem, &threads)
                         : prefill_simt_ptr(c->dtype, c->head_dim, c->layout, &p->smem);
     if (!fn) return PA_ERR_UNSUPPORTED;
     p->tc = tc;
@@ -174,7 +175,7 @@ pa_status_t prefill_launch(const PrefillPlan &p, const pa_cache_desc_t *c, Prefi
     void *args[] = {&a};
     size_t smem;
     int threads;
-    const void *fn = p.tc ? prefill_tc_ptr(c->head_dim, c->dtype == PA_FP8_E4M3_BLOCK, &smem, &threads)
+    const void *fn = p.tc ? prefill_tc_ptr(c->head_dim, p.conv, &smem, &threads)
                           : prefill_simt_ptr(c->dtype, c->head_dim, c->layout, &smem);
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)

@@ -48,27 +48,38 @@ constexpr unsigned long long kTcUnitNs = 4096;
 // each (a row's 128 scores stay in registers), the third one keeps 88:
 // 256 x 208 + 128 x 88 = 384 x 168.
 constexpr int kTcSoftmaxRegs = 208, kTcOtherRegs = 88;
-// The 8-bit form has a fourth warpgroup, the converters: 512 threads x 128 at
-// launch, 256 x kTcSoftmaxRegs8 + 128 x (kTcOtherRegs8 + kTcConvertRegs) = 512 x 128.
-constexpr int kTcThreads8 = 512, kTcSoftmaxRegs8 = 192, kTcOtherRegs8 = 64, kTcConvertRegs = 64;
 
-// kFp8: codes arrive in a ring of their own (raw) and are turned into the bf16
-// units of the ring that the MMAs read.
-template <int D, bool kFp8>
+// kConv: the warps that turn an 8-bit cache's codes, which arrive in a ring of their
+// own (raw), into the bf16 units of the ring that the MMAs read; 0 for a bf16 cache.
+// Both forms over an 8-bit cache are right for every call; which one is faster:
+//   4  512 threads x 128 registers at launch, 256 x 192 + 128 x 64 + 128 x 64.
+//      A row's scores stay in registers.  A unit takes the converters about 1.8 us,
+//      two row tiles' softmax and products longer.
+//   8  640 x 96, 256 x 112 + 128 x 88 + 256 x 80 and some left.  A unit takes the
+//      converters half of that; the softmax, short of registers, reads its scores twice,
+//      and shares tiles of one row tile (TcSegment), which leaves it time for that.
+// Chunks of 8 tokens on 16 contexts up to 32768, 32 / 8 heads, head_dim 128: 191 and 161 us.
+// A batch of longer chunks: 181 and 204 us.  Eight warps where the call's chunks
+// have no more tokens than a row tile on average (prefill_layout).
+template <int D, int kConv>
 struct TcPrefill {
+    static constexpr bool kFp8 = kConv > 0, kMayPair = kConv != 4;
+    static constexpr int kSoftmaxRegs = kConv == 8 ? 112 : kConv == 4 ? 192 : kTcSoftmaxRegs;
+    static constexpr int kOtherRegs = kConv == 4 ? 64 : kTcOtherRegs, kConvertRegs = kConv == 8 ? 80 : 64;
     static constexpr int kPanels = D / 64;
     static constexpr uint32_t kPanel = 128 * 128;            // 128 rows of 64 bf16
     static constexpr uint32_t kTile = kPanels * kPanel;      // Q row tile, K or V unit
     static constexpr int kStages = kFp8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);  // ring of K and V units
     static constexpr int kRaw = kFp8 ? (D == 128 ? 4 : 8) : 0;  // units of codes on their way (64 KiB)
     static constexpr uint32_t kRawTile = 128 * D;
-    static constexpr int kThreads = kFp8 ? kTcThreads8 : kTcThreads;
+    static constexpr int kThreads = kTcThreads + 32 * kConv;
     static constexpr uint32_t kRing = 2 * kTile;             // after the two Q row tiles
     static constexpr uint32_t kRawRing = kRing + kStages * kTile;
     static constexpr uint32_t kBars = kRawRing + kRaw * kRawTile;
-    static constexpr uint32_t kRawBars = kBars + 288 + 3 * D * 4;  // barriers; columns with odd values
+    static constexpr uint32_t kBarBytes = (120 + 16 * kStages + 12 + 31) & ~31;  // barriers, OddColumns::segment, the tensor memory's address
+    static constexpr uint32_t kRawBars = kBars + kBarBytes + 3 * D * 4;  // barriers; columns with odd values
     static constexpr uint32_t kMl = kRawBars + 16 * kRaw;  // (m, l) of the second warpgroup's rows
-    static constexpr uint32_t kMeta = kMl + (kFp8 ? 0 : 1024), kMetaBytes = 80;  // per raw unit: scales of its (up to 16) boxes, their number
+    static constexpr uint32_t kMeta = kMl + 1024, kMetaBytes = 40;  // per raw unit: scales of its (up to 16) boxes as bf16, then the number of boxes
     static constexpr uint32_t kBytes = kMeta + kMetaBytes * kRaw;
     static_assert(kBytes <= 227 * 1024, "a CTA's shared memory");
     static constexpr size_t kSmem = kBytes;
@@ -113,9 +124,8 @@ __device__ __forceinline__ void tc_wait(uint32_t bar, uint32_t parity, bool &abo
 // for its own softmax between two products: with a.pair the two warpgroups hold
 // the same rows and take the units in turn, and the one that had the first unit
 // joins the two results at the segment's end.  That one changes from such a
-// segment to the next (`first`, counted alike by every role).  (Not over the 8-bit
-// cache, where the converters are what bounds a unit.)
-template <bool kFp8>
+// segment to the next (`first`, counted alike by every role).
+template <bool kMayPair>
 struct TcSegment {
     PrefillTile t;
     int32_t keys;   // keys the tile sees
@@ -136,7 +146,7 @@ struct TcSegment {
             je[i] = min(cur.j1, (int32_t)(((uint32_t)ki + kTcKeys - 1) / kTcKeys));  // the sum may pass 2^31
         }
         jend = max(je[0], je[1]);
-        pair = !kFp8 && a.pair && t.ntok <= a.tq1;
+        pair = kMayPair && a.pair && t.ntok <= a.tq1;
     }
 };
 
@@ -145,10 +155,18 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
-__device__ __forceinline__ float lds_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+__device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
+}
+__device__ __forceinline__ float lds_bf16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+    return __uint_as_float((uint32_t)v << 16);
+}
+__device__ __forceinline__ void sts_u16(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
 }
 __device__ __forceinline__ void sts_u32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
@@ -208,7 +226,7 @@ template <int D, bool kIsV>
 __device__ __forceinline__ void tc_producer(const PrefillArgs &a, uint8_t *smem, const TcBars &bar,
                                             const CUtensorMap *tmq, const CUtensorMap *tm, int32_t gran,
                                             int32_t c, int lane) {
-    using L = TcPrefill<D, false>;
+    using L = TcPrefill<D, 0>;
     if (lane == 0) {
         if (!kIsV) prefetch_tmap(tmq);
         prefetch_tmap(tm);
@@ -224,7 +242,7 @@ __device__ __forceinline__ void tc_producer(const PrefillArgs &a, uint8_t *smem,
     PrefillCursor cur;
     if (!cur.init(a, c)) return;
     do {
-        const TcSegment<false> sg(a, cur);
+        const TcSegment<L::kMayPair> sg(a, cur);
         if (sg.jend <= cur.j0) continue;
         const int32_t *row = a.tables + (int64_t)sg.t.seq * a.max_blocks;
         auto has_key = [&](int32_t j) { return has_box && (int64_t)j * kTcKeys + bi * gran < sg.keys; };
@@ -274,11 +292,25 @@ __device__ __forceinline__ void tc_producer(const PrefillArgs &a, uint8_t *smem,
 // ring with an entry of kRawEnd boxes, at which the converters stop.
 constexpr int32_t kRawEnd = -1;
 
-template <int D, bool kIsV>
+// Ring entry of unit u's K and V, of n units that a segment begins with at entry 0.
+// Over the 8-bit cache, whose rings are short, a pair's entries come in the order
+// of their use, K0 K1 V0 K2 V1 .. (the next but one S follows an O): with K and V
+// in turn, K would wait for the slot of a V that has just been used.  Everything
+// else takes K and V in turn.
+template <bool kFp8>
+__device__ __forceinline__ uint32_t k_entry(bool pair, int32_t u) {
+    return kFp8 && pair && u > 0 ? 2u * (uint32_t)u - 1u : 2u * (uint32_t)u;
+}
+template <bool kFp8>
+__device__ __forceinline__ uint32_t v_entry(bool pair, int32_t u, int32_t n) {
+    return kFp8 && pair && u + 1 < n ? 2u * (uint32_t)u + 2u : 2u * (uint32_t)u + 1u;
+}
+
+template <int D, int kConv, bool kIsV>
 __device__ __forceinline__ void tc_producer8(const PrefillArgs &a, uint8_t *smem, const TcBars &bar,
                                              const CUtensorMap *tmq, const CUtensorMap *tm, int32_t gran,
                                              int32_t c, int lane) {
-    using L = TcPrefill<D, true>;
+    using L = TcPrefill<D, kConv>;
     if (lane == 0) {
         if (!kIsV) prefetch_tmap(tmq);
         prefetch_tmap(tm);
@@ -287,13 +319,13 @@ __device__ __forceinline__ void tc_producer8(const PrefillArgs &a, uint8_t *smem
     const int32_t nbm = kTcKeys / gran;  // boxes of a unit (at most 16), one per lane
     const uint8_t *scales = kIsV ? a.v_scale : a.k_scale;
     const uint64_t policy = l2_policy_evict_first();
-    uint32_t n = kIsV ? 1 : 0;  // next entry
+    uint32_t base = 0;  // entries of the segments before
     QSlots q;
     bool abort = false;
     PrefillWalk<false> cur;
     if (cur.init(a, c)) {
         do {
-            const TcSegment<true> sg(a, cur);
+            const TcSegment<L::kMayPair> sg(a, cur);
             if (sg.jend <= cur.j0) continue;
             const int32_t *row = a.tables + (int64_t)sg.t.seq * a.max_blocks;
             auto has_key = [&](int32_t j) { return lane < nbm && (int64_t)j * kTcKeys + lane * gran < sg.keys; };
@@ -307,7 +339,9 @@ __device__ __forceinline__ void tc_producer8(const PrefillArgs &a, uint8_t *smem
                 if (__any_sync(0xffffffffu, abort)) break;
             }
             uint32_t sc = scale_at(phys);
-            for (int32_t j = cur.j0; j < sg.jend; ++j, n += 2) {
+            const int32_t nu = sg.jend - cur.j0;
+            for (int32_t j = cur.j0; j < sg.jend; ++j) {
+                const uint32_t n = base + (kIsV ? v_entry<true>(sg.pair, j - cur.j0, nu) : k_entry<true>(sg.pair, j - cur.j0));
                 const bool box = has_key(j);
                 int32_t at = a.NB * a.B;  // a bad entry reads zeros: the box lies past the pool
                 if (phys >= 0 && phys < a.NB)
@@ -322,8 +356,8 @@ __device__ __forceinline__ void tc_producer8(const PrefillArgs &a, uint8_t *smem
                 const uint32_t st = n % L::kRaw;
                 if (n >= L::kRaw) tc_wait(bar.raw_free + 8 * st, (n / L::kRaw + 1) & 1, abort, a.err);
                 if (__any_sync(0xffffffffu, abort)) break;
-                if (box) sts_u32(meta + st * L::kMetaBytes + (uint32_t)lane * 4, __float_as_uint(scale_of(sc_now)));
-                if (lane == 0) sts_u32(meta + st * L::kMetaBytes + 64, boxes);
+                if (box) sts_u16(meta + st * L::kMetaBytes + (uint32_t)lane * 2, __float_as_uint(scale_of(sc_now)) >> 16);
+                if (lane == 0) sts_u32(meta + st * L::kMetaBytes + 32, boxes);
                 __syncwarp();  // in place before lane 0 publishes the entry
                 if (lane == 0) mbar_arrive_expect_tx(bar.raw_full + 8 * st, boxes * (uint32_t)gran * D);
                 __syncwarp();
@@ -331,35 +365,35 @@ __device__ __forceinline__ void tc_producer8(const PrefillArgs &a, uint8_t *smem
                     tma_load_3d_hint(raw + st * L::kRawTile + (uint32_t)(lane * gran) * D, tm, bar.raw_full + 8 * st, 0, at,
                                      cur.kvh, policy);
             }
+            base += 2 * (uint32_t)nu;
             if (__any_sync(0xffffffffu, abort)) break;
         } while (cur.next(a));
     }
-    // This warp's copies in flight, and the issuer's last arrivals on the free
-    // barriers, land before the CTA may exit (the copies before the end entry
-    // takes its barrier a phase on).
-    static_assert(L::kRaw % 2 == 0, "K's entries and V's have slots of their own");
+    // Every copy lands before the converters, which wait for each entry, come to the
+    // end entry.  After a wait that ran out, look at the last ones here.
     bool late = false;
-    const uint32_t mine = kIsV ? 1u : 0u, total = n - mine;
-    for (uint32_t k = (total > (uint32_t)L::kRaw ? total - L::kRaw : 0) + mine; k < total; k += 2)
-        tc_wait(bar.raw_full + 8 * (k % L::kRaw), (k / L::kRaw) & 1, late, a.err);
+    if (abort)
+        for (uint32_t k = base > (uint32_t)L::kRaw ? base - L::kRaw : 0; k < base; ++k)
+            tc_wait(bar.raw_full + 8 * (k % L::kRaw), (k / L::kRaw) & 1, late, a.err);
     if (!kIsV) {
-        const uint32_t st = n % L::kRaw;
-        if (n >= L::kRaw) tc_wait(bar.raw_free + 8 * st, (n / L::kRaw + 1) & 1, abort, a.err);
+        const uint32_t st = base % L::kRaw;
+        if (base >= L::kRaw) tc_wait(bar.raw_free + 8 * st, (base / L::kRaw + 1) & 1, abort, a.err);
         if (lane == 0 && !abort) {
-            sts_u32(meta + st * L::kMetaBytes + 64, (uint32_t)kRawEnd);
+            sts_u32(meta + st * L::kMetaBytes + 32, (uint32_t)kRawEnd);
             mbar_arrive(bar.raw_full + 8 * st);
         }
+        // the issuer's last arrivals on the free barriers land before the CTA may exit
+        for (uint32_t k = base > (uint32_t)L::kStages ? base - L::kStages : 0; k < base; ++k)
+            tc_wait(bar.kv_free + 8 * (k % L::kStages), (k / L::kStages) & 1, late, a.err);
     }
-    for (uint32_t k = total > (uint32_t)L::kStages ? total - L::kStages : 0; k < total; ++k)
-        if ((k & 1u) == mine) tc_wait(bar.kv_free + 8 * (k % L::kStages), (k / L::kStages) & 1, late, a.err);
     if (!kIsV) drain_q(bar, q, late, a.err);
 }
 
 // ------------------------------------------------------- 8-bit: converters
-// Four warps turn entry n of the raw ring into entry n of the bf16 ring: code * 2^(byte - 127), in fp32 and then bf16 (one
-// rounding, of values that bf16 holds exactly unless they leave its range).  Per
-// two codes: a conversion to fp16, two to fp32, a packed product, a packed
-// conversion.  (Shifting codes into place as bf16 and one packed bf16 product
+// kConv warps turn entry n of the raw ring into entry n of the bf16 ring: code *
+// 2^(byte - 127), in fp32 and then bf16 (one rounding, of values that bf16 holds
+// exactly unless they leave its range).  Per two codes: a conversion to fp16, two
+// to fp32, a packed product, a packed conversion.  (Shifting codes into place as bf16 and one packed bf16 product
 // took as many instructions with the look for NaN codes, and longer.)
 // A thread takes 16 codes at a time (a 16-byte load) and stores them as two
 // 16-byte chunks of a swizzled 128-byte line.  Eight lanes' loads and stores fall
@@ -377,18 +411,18 @@ __device__ __forceinline__ void codes_bf16(uint32_t w, uint64_t s2, uint32_t &lo
     hi = pack_bf16x2(u, v);
 }
 
-template <int D>
+template <int D, int kConv>
 __device__ __forceinline__ void tc_converter(const PrefillArgs &a, uint8_t *smem, const TcBars &bar, int32_t gran, int tid) {
-    using L = TcPrefill<D, true>;
-    constexpr int kRowsPass = D == 128 ? 16 : 32;  // rows of the four warps at once
+    using L = TcPrefill<D, kConv>;
+    constexpr int kRowsPass = (D == 128 ? 4 : 8) * kConv;  // rows of the warps at once
     constexpr int kPasses = 128 / kRowsPass, kBatch = 2;  // loads of a thread in flight
     const uint32_t raw = smem_u32(smem) + L::kRawRing, ring = smem_u32(smem) + L::kRing;
     const uint32_t meta = smem_u32(smem) + L::kMeta;
     const int lane = tid & 31;
     const int shift = __ffs(gran) - 1;  // gran = gcd(block size, 128)
-    // D 128: the first two warps take the first panel, the others the second
-    const int r0 = D == 128 ? ((tid >> 2) & 8) | (((tid >> 3) & 3) ^ (tid & 4 ? 5 : 0)) : tid >> 2;
-    const uint32_t panel = D == 128 ? (uint32_t)tid >> 6 : 0u, ch = (uint32_t)tid & 3u;
+    // D 128: half of the warps take the first panel, the others the second
+    const int r0 = D == 128 ? ((tid >> 2) & (kRowsPass - 8)) | (((tid >> 3) & 3) ^ (tid & 4 ? 5 : 0)) : tid >> 2;
+    const uint32_t panel = D == 128 ? (uint32_t)tid / (16u * kConv) : 0u, ch = (uint32_t)tid & 3u;
     const uint32_t src = D == 128 ? (uint32_t)r0 * 128u + (((panel * 4u + ch) ^ (uint32_t)(r0 & 7)) << 4) : (uint32_t)tid * 16u;
     // rows of a thread are a multiple of 8 apart: their swizzle is the same
     const uint32_t dst = panel * L::kPanel + (uint32_t)r0 * 128u + (((ch * 2u) ^ (uint32_t)(r0 & 7)) << 4);
@@ -396,13 +430,13 @@ __device__ __forceinline__ void tc_converter(const PrefillArgs &a, uint8_t *smem
     for (uint32_t n = 0;; ++n) {
         const uint32_t rs = n % L::kRaw, st = n % L::kStages;
         tc_wait(bar.raw_full + 8 * rs, (n / L::kRaw) & 1, abort, a.err, a.wait_ns);
-        const int32_t boxes = __float_as_int(lds_f32(meta + rs * L::kMetaBytes + 64));
+        const int32_t boxes = (int32_t)lds_u32(meta + rs * L::kMetaBytes + 32);
         if (__any_sync(0xffffffffu, abort || boxes == kRawEnd)) break;
         if (n >= L::kStages) tc_wait(bar.kv_free + 8 * st, (n / L::kStages + 1) & 1, abort, a.err, a.wait_ns);
         if (__any_sync(0xffffffffu, abort)) break;
         const int32_t rows = boxes * gran;
         const uint32_t from = raw + rs * L::kRawTile + src, to = ring + st * L::kTile + dst, scales = meta + rs * L::kMetaBytes;
-        auto scale = [&](int p) { return lds_f32(scales + (uint32_t)(((p * kRowsPass + r0) >> shift) * 4)); };
+        auto scale = [&](int p) { return lds_bf16(scales + (uint32_t)(((p * kRowsPass + r0) >> shift) * 2)); };
         uint4 w[kBatch];
         float s[kBatch];
 #pragma unroll
@@ -460,19 +494,19 @@ template <int D>
 __device__ __forceinline__ uint32_t v_chunk(uint32_t vbase, int e) {  // address of 16-byte chunk e % (D / 8) of row e / (D / 8)
     constexpr int kChunks = D / 8;
     const int r = e / kChunks, ch = e % kChunks;
-    return vbase + (uint32_t)(ch >> 3) * TcPrefill<D, false>::kPanel + (uint32_t)r * 128u +
+    return vbase + (uint32_t)(ch >> 3) * TcPrefill<D, 0>::kPanel + (uint32_t)r * 128u +
            (uint32_t)(((ch & 7) ^ (r & 7)) << 4);
 }
 // Sign bits of the halves whose exponent is all ones (bf16 infinities and NaN).
 __device__ __forceinline__ uint32_t odd_bits(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
-template <int D, bool kFp8>
+template <int D, int kConv>
 __device__ __forceinline__ void tc_guard(const PrefillArgs &a, uint8_t *smem, const TcBars &bar, const OddColumns &odd,
                                          int32_t c, int lane) {
-    using L = TcPrefill<D, kFp8>;
+    using L = TcPrefill<D, kConv>;
     constexpr int kChunks = D / 8;
     const uint32_t ring = smem_u32(smem) + L::kRing;
-    uint32_t n = 1, segs = 0, units = 0;  // ring entry of V, segments, guarded units
+    uint32_t n = 0, segs = 0, units = 0;  // ring entries of the segments before, segments, guarded units
     uint32_t no[2] = {0, 0};              // earlier segments with units per row tile
     uint32_t held = 0;                    // the segment that the columns belong to
     int first = 0;                        // (TcSegment)
@@ -482,7 +516,7 @@ __device__ __forceinline__ void tc_guard(const PrefillArgs &a, uint8_t *smem, co
     if (lane == 0) note_cut(a, c, work, cur);
     if (!work) return;
     do {
-        const TcSegment<kFp8> sg(a, cur);
+        const TcSegment<L::kMayPair> sg(a, cur);
         if (sg.jend <= cur.j0) continue;
         ++segs;
         for (int32_t j = max(cur.j0, guard_from(sg)); j < sg.jend; ++j, ++units) {
@@ -490,7 +524,8 @@ __device__ __forceinline__ void tc_guard(const PrefillArgs &a, uint8_t *smem, co
             // may last while the other roles work through most of the CTA's
             // range, so their limit grows with the range.
             tc_wait(bar.v_go, units & 1, abort, a.err, a.wait_ns);
-            const uint32_t vbase = ring + ((n + 2 * (uint32_t)(j - cur.j0)) % L::kStages) * L::kTile;
+            const uint32_t vbase =
+                ring + (n + v_entry<L::kFp8>(sg.pair, j - cur.j0, sg.jend - cur.j0)) % L::kStages * L::kTile;
             const int32_t pos0 = j * kTcKeys;
             const int nk = min(kTcKeys, sg.keys - pos0), nk16 = (nk + 15) & ~15;
             const int r0 = min(nk, max(0, sg.t.p0 + 1 - pos0));
@@ -562,10 +597,10 @@ __device__ __forceinline__ int32_t uniform(int32_t x) { return __shfl_sync(0xfff
 // One warp; one elected lane issues.  MMAs of one thread complete in order, so S of a
 // unit may be computed over the P of the one before (its O += P V was issued
 // earlier), and a row tile's S being complete says that its earlier O is too.
-template <int D, bool kFp8>
+template <int D, int kConv>
 __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, const TcBars &bar, uint32_t tmem,
                                           int32_t c, int lane) {
-    using L = TcPrefill<D, kFp8>;
+    using L = TcPrefill<D, kConv>;
     constexpr uint32_t IDESC_S = tc_idesc_bf16(128, kTcKeys, false, false);
     constexpr uint32_t IDESC_O = tc_idesc_bf16(128, D, false, true);
     const uint32_t ring = smem_u32(smem) + L::kRing;
@@ -583,7 +618,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
     PrefillCursor cur;
     if (!cur.init(a, c)) return;
     do {
-        const TcSegment<kFp8> sg(a, cur);
+        const TcSegment<L::kMayPair> sg(a, cur);
         const int32_t j0 = uniform(cur.j0), jend = uniform(sg.jend), jg = uniform(guard_from(sg)),
                       keys = uniform(sg.keys);
         const int32_t je[2] = {uniform(sg.je[0]), uniform(sg.je[1])};
@@ -616,7 +651,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
             const uint32_t base = n;
             n += 2 * (uint32_t)(jend - j0);
             auto s_of = [&](int i, int32_t j) {
-                const uint32_t ek = base + 2 * (uint32_t)(j - j0), sk = ek % L::kStages;
+                const uint32_t ek = base + k_entry<L::kFp8>(true, j - j0), sk = ek % L::kStages;
                 tc_wait(bar.kv_full + 8 * sk, (ek / L::kStages) & 1, abort, a.err);
                 tc_fence_after();
                 issue_s(i, sk, q0);
@@ -629,7 +664,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
             first ^= 1;
 #pragma unroll 1
             for (int32_t j = j0; j < jend; ++j, i ^= 1) {
-                const uint32_t ev = base + 2 * (uint32_t)(j - j0) + 1, sv = ev % L::kStages;
+                const uint32_t ev = base + v_entry<L::kFp8>(true, j - j0, jend - j0), sv = ev % L::kStages;
                 tc_wait(bar.kv_full + 8 * sv, (ev / L::kStages) & 1, abort, a.err);
                 const bool guarded = j >= jg;
                 int ksteps = kTcKeys / 16;
@@ -723,13 +758,78 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
     // this warp is in flight once they have (see the kernel's end).
 }
 
+// A row's O out of tensor memory, with the other warpgroup's where there is one
+// (tO_other; w0 and w1 their weights), and with the values that are not finite that
+// the row sees (odd): to out, or to the segment's piece
+// with (m, l).
+template <int D, class Walk, class Segment>
+__device__ __forceinline__ void write_rows(const PrefillArgs &a, const Walk &cur, int32_t c, const Segment &sg, int i, int r,
+                                           int32_t tok, int g, bool valid, int32_t last, bool any, const int32_t *odd,
+                                           uint32_t tO, float w0, uint32_t tO_other, float w1, float m, float l) {
+    const bool whole = cur.whole(), out32 = ((uintptr_t)a.out & 31) == 0;
+    const int64_t row = cur.slot(c) * (2 * kTcRows) + (sg.pair ? 0 : i) * kTcRows + r;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __nv_bfloat16 *op = (__nv_bfloat16 *)a.out + ((int64_t)(sg.t.row0 + tok) * a.H + (int64_t)cur.kvh * a.G + g) * D;
+    // 16 columns at a time in a short loop: this code runs once per segment, and
+    // unrolled over a row most of its time was its own fetching
+    // (68 sequences of 1 to 130 tokens over 1 to 1664 states: 120 and 115 us).
+#pragma unroll 1
+    for (int d0 = 0; d0 < D; d0 += 16) {
+        float o[16];
+        if (any) {
+            tmem_ld16(tO + (uint32_t)d0, o);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = 0.f;
+        }
+        if (tO_other) {
+            float y[16];
+            tmem_ld16(tO_other + (uint32_t)d0, y);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = fmaf(w1, y[k], w0 * o[k]);
+        }
+        if (odd) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const int32_t *first = odd + d0 + k;
+                if (last >= first[0]) o[k] += INFINITY;
+                if (last >= first[D]) o[k] -= INFINITY;
+                if (last >= first[2 * D]) o[k] += __uint_as_float(0x7fffffffu);
+            }
+        }
+        if (!valid) continue;
+        // A thread writes a row, so a store's lanes are rows apart: whole sectors
+        // where out's alignment allows.
+        if (whole) {
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+            if (out32) {
+                store32(op + d0, w);
+            } else {
+                *reinterpret_cast<uint4 *>(op + d0) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4 *>(op + d0 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; k += 8) {
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[k + e]);
+                store32(a.acc + row * D + d0 + k, w);
+            }
+        }
+    }
+    if (valid && !whole) a.ml[row] = make_float2(m, l);
+}
+
 // ----------------------------------------------------------------- softmax
 // Four warps per row tile; a thread owns one query row (tensor-memory lane).
-template <int D, bool kFp8>
+template <int D, int kConv>
 __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &bar, uint32_t tmem,
                                            const OddColumns &odd, float2 *ml, int32_t c,
                                            int i, int warp, int lane) {
-    using L = TcPrefill<D, kFp8>;
+    using L = TcPrefill<D, kConv>;
     const int r = warp * 32 + lane;  // row of the row tile
     const uint32_t t_lane = (uint32_t)(warp * 32) << 16;
     const uint32_t tS = tmem + L::kS + i * 128 + t_lane, tO = tmem + L::kO + i * D + t_lane, tO_other = tmem + L::kO + (1 - i) * D + t_lane;
@@ -742,7 +842,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
     PrefillWalk<false> cur;
     if (!cur.init(a, c)) return;
     do {
-        const TcSegment<kFp8> sg(a, cur);
+        const TcSegment<L::kMayPair> sg(a, cur);
         const int32_t tok = (sg.pair ? 0 : i * a.tq1) + tok_r;
         const bool valid = tok_r < a.tq1 && tok < sg.t.ntok;
         const bool warp_rows = __any_sync(0xffffffffu, valid);
@@ -758,21 +858,36 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
             ++ns;
             tc_fence_after();
             if (warp_rows) {
-                float x[128];
-                tmem_ld_cols(tS, x);
                 const int32_t nvis = last - j * kTcKeys + 1;
-                if (__any_sync(0xffffffffu, valid && nvis < kTcKeys)) {
+                const bool masked = __any_sync(0xffffffffu, valid && nvis < kTcKeys);
+                // A row's scores in registers, all 128 or (beside eight converter warps,
+                // for want of registers) 32 at a time, read twice.
+                constexpr int kCols = kConv == 8 ? 32 : 128;
+                float x[kCols];
+                auto read = [&](int h) {
+                    if constexpr (kCols == 32)
+                        tmem_ld32(tS + kCols * h, x);
+                    else
+                        tmem_ld_cols(tS + kCols * h, x);
+                    if (masked) {
 #pragma unroll
-                    for (int k = 0; k < 128; ++k) x[k] = k < nvis ? x[k] : -INFINITY;
+                        for (int k = 0; k < kCols; ++k) x[k] = kCols * h + k < nvis ? x[k] : -INFINITY;
+                    }
+                };
+                float top = -INFINITY;
+#pragma unroll 1
+                for (int h = 0; h < 128 / kCols; ++h) {
+                    read(h);
+                    float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                    for (int k = 4; k < kCols; k += 8) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            mx[q] = k + q + 4 < kCols ? fmaxf(fmaxf(mx[q], x[k + q]), x[k + q + 4]) : fmaxf(mx[q], x[k + q]);
+                    }
+                    top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
                 }
-                float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                for (int k = 4; k < 128; k += 8) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        mx[q] = k + q + 4 < 128 ? fmaxf(fmaxf(mx[q], x[k + q]), x[k + q + 4]) : fmaxf(mx[q], x[k + q]);
-                }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+                top *= sl;
                 // Lazy running maximum: moved (with l and O rescaled) only when
                 // a score passes it by more than kLazyMaxSlack.
                 const bool grow = valid && top > m + kLazyMaxSlack;
@@ -795,18 +910,27 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
                 const float mref = m == -INFINITY ? 0.f : m;  // a row without keys so far: zeros
                 const uint64_t sl2 = f32x2(sl, sl), mm2 = f32x2(-mref, -mref);
                 uint64_t sum[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
+                auto weigh = [&](int h, int at) {  // columns 32 h .., in x from `at` on
                     uint32_t w[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         float y0, y1;
-                        f32x2_get(fma_f32x2(f32x2(x[32 * h + 2 * k], x[32 * h + 2 * k + 1]), sl2, mm2), y0, y1);
+                        f32x2_get(fma_f32x2(f32x2(x[at + 2 * k], x[at + 2 * k + 1]), sl2, mm2), y0, y1);
                         const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
                         sum[k & 1] = add_f32x2(sum[k & 1], f32x2(p0, p1));
                         w[k] = pack_bf16x2(p0, p1);
                     }
-                    tmem_st16_async(tS + 16 * h, w);
+                    tmem_st16_async(tS + 16 * h, w);  // over columns that have been read
+                };
+                if constexpr (kCols == 32) {
+#pragma unroll 1
+                    for (int h = 0; h < 4; ++h) {
+                        read(h);
+                        weigh(h, 0);
+                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) weigh(h, 32 * h);
                 }
                 float s0, s1;
                 f32x2_get(add_f32x2(sum[0], sum[1]), s0, s1);
@@ -845,69 +969,10 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
             l = w0 * l + w1 * y.y;
             m = mn;
         }
-        const bool whole = cur.whole(), out32 = ((uintptr_t)a.out & 31) == 0;
-        const int64_t row = cur.slot(c) * (2 * kTcRows) + (sg.pair ? 0 : i) * kTcRows + r;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
         const bool odd_tile = any && odd.segment[sg.pair ? 0 : i] == (int32_t)segs;
-        __nv_bfloat16 *op =
-            (__nv_bfloat16 *)a.out + ((int64_t)(sg.t.row0 + tok) * a.H + (int64_t)cur.kvh * a.G + g) * D;
-        if (warp_rows) {
-#pragma unroll 1
-            for (int d0 = 0; d0 < D; d0 += 64) {
-                float o[64];
-                if (any) {
-                    tmem_ld_cols(tO + (uint32_t)d0, o);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 64; ++k) o[k] = 0.f;
-                }
-                if (join) {
-#pragma unroll
-                    for (int h = 0; h < 64; h += 32) {
-                        float y[32];
-                        tmem_ld32(tO_other + (uint32_t)(d0 + h), y);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[h + k] = fmaf(w1, y[k], w0 * o[h + k]);
-                    }
-                }
-                if (odd_tile) {
-#pragma unroll
-                    for (int k = 0; k < 64; ++k) {
-                        const int32_t *first = odd.first + d0 + k;
-                        if (last >= first[0]) o[k] += INFINITY;
-                        if (last >= first[D]) o[k] -= INFINITY;
-                        if (last >= first[2 * D]) o[k] += __uint_as_float(0x7fffffffu);
-                    }
-                }
-                if (valid) {
-                    // A thread writes a row, so a store's lanes are rows
-                    // apart: whole sectors where out's alignment allows.
-                    if (whole) {
-#pragma unroll
-                        for (int k = 0; k < 64; k += 16) {
-                            uint32_t w[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[k + 2 * e] * inv, o[k + 2 * e + 1] * inv);
-                            if (out32) {
-                                store32(op + d0 + k, w);
-                            } else {
-                                *reinterpret_cast<uint4 *>(op + d0 + k) = make_uint4(w[0], w[1], w[2], w[3]);
-                                *reinterpret_cast<uint4 *>(op + d0 + k + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 64; k += 8) {
-                            uint32_t w[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[k + e]);
-                            store32(a.acc + row * D + d0 + k, w);
-                        }
-                    }
-                }
-            }
-            if (valid && !whole) a.ml[row] = make_float2(m, l);
-        }
+        if (warp_rows)
+            write_rows<D>(a, cur, c, sg, i, r, tok, g, valid, last, any, odd_tile ? odd.first : nullptr, tO, w0,
+                          join ? tO_other : 0u, w1, m, l);
         if (any) {  // O (and the odd columns) have been read
             tc_fence_before();
             __syncwarp();
@@ -917,12 +982,12 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
     } while (cur.next(a));
 }
 
-template <int D, bool kFp8>
-__global__ void __launch_bounds__(TcPrefill<D, kFp8>::kThreads, 1)
+template <int D, int kConv>
+__global__ void __launch_bounds__(TcPrefill<D, kConv>::kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const __grid_constant__ PrefillArgs a,
                       const int32_t gran) {
-    using L = TcPrefill<D, kFp8>;
+    using L = TcPrefill<D, kConv>;
     extern __shared__ __align__(1024) uint8_t smem_tc[];
     uint8_t *smem = smem_tc;
     if ((smem_u32(smem) & 1023) != 0) {  // no room to align it here (the layout fills the CTA's limit)
@@ -930,9 +995,9 @@ __global__ void __launch_bounds__(TcPrefill<D, kFp8>::kThreads, 1)
         return;
     }
     const TcBars bar(smem_u32(smem + L::kBars), L::kStages, smem_u32(smem + L::kRawBars), L::kRaw);
-    uint32_t *tmem_slot = (uint32_t *)(smem + L::kBars + 264);
-    const OddColumns odd{(int32_t *)(smem + L::kBars + 288), (int32_t *)(smem + L::kBars + 256)};
-    static_assert(120 + 16 * L::kStages <= 256, "the barriers fit");
+    uint32_t *tmem_slot = (uint32_t *)(smem + L::kBars + 128 + 16 * L::kStages);
+    const OddColumns odd{(int32_t *)(smem + L::kBars + L::kBarBytes), (int32_t *)(smem + L::kBars + 120 + 16 * L::kStages)};
+
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         mbar_init(bar.v_go, 1);
@@ -947,12 +1012,12 @@ __global__ void __launch_bounds__(TcPrefill<D, kFp8>::kThreads, 1)
             mbar_init(bar.o_free + 8 * i, 4);
         }
         for (int s = 0; s < L::kStages; ++s) {
-            mbar_init(bar.kv_full + 8 * s, kFp8 ? 4 : 1);
+            mbar_init(bar.kv_full + 8 * s, L::kFp8 ? kConv : 1);
             mbar_init(bar.kv_free + 8 * s, 1);
         }
         for (int s = 0; s < L::kRaw; ++s) {
             mbar_init(bar.raw_full + 8 * s, 1);
-            mbar_init(bar.raw_free + 8 * s, 4);
+            mbar_init(bar.raw_free + 8 * s, kConv);
         }
         odd.segment[0] = odd.segment[1] = 0;
         fence_mbarrier_init();
@@ -967,28 +1032,28 @@ __global__ void __launch_bounds__(TcPrefill<D, kFp8>::kThreads, 1)
     grid_launch_dependents();
     const int32_t c = blockIdx.x;
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFp8 ? kTcSoftmaxRegs8 : kTcSoftmaxRegs));
-        tc_softmax<D, kFp8>(a, bar, tmem, odd, (float2 *)(smem + L::kMl), c, warp >> 2, warp & 3, lane);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kSoftmaxRegs));
+        tc_softmax<D, kConv>(a, bar, tmem, odd, (float2 *)(smem + L::kMl), c, warp >> 2, warp & 3, lane);
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFp8 ? kTcOtherRegs8 : kTcOtherRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kOtherRegs));
         if (warp == 8) {
-            tc_issuer<D, kFp8>(a, smem, bar, tmem, c, lane);
+            tc_issuer<D, kConv>(a, smem, bar, tmem, c, lane);
         } else if (warp == 9) {
-            if constexpr (kFp8)
-                tc_producer8<D, false>(a, smem, bar, &tmq, &tmk, gran, c, lane);
+            if constexpr (L::kFp8)
+                tc_producer8<D, kConv, false>(a, smem, bar, &tmq, &tmk, gran, c, lane);
             else
                 tc_producer<D, false>(a, smem, bar, &tmq, &tmk, gran, c, lane);
         } else if (warp == 10) {
-            if constexpr (kFp8)
-                tc_producer8<D, true>(a, smem, bar, &tmq, &tmv, gran, c, lane);
+            if constexpr (L::kFp8)
+                tc_producer8<D, kConv, true>(a, smem, bar, &tmq, &tmv, gran, c, lane);
             else
                 tc_producer<D, true>(a, smem, bar, &tmq, &tmv, gran, c, lane);
         } else {
-            tc_guard<D, kFp8>(a, smem, bar, odd, c, lane);
+            tc_guard<D, kConv>(a, smem, bar, odd, c, lane);
         }
-    } else if constexpr (kFp8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcConvertRegs));
-        tc_converter<D>(a, smem, bar, gran, tid - 384);
+    } else if constexpr (L::kFp8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kConvertRegs));
+        tc_converter<D, kConv>(a, smem, bar, gran, tid - 384);
     }
     // The softmax warps have waited for the last o_full, which every MMA
     // precedes: nothing uses the tensor memory any more.

@@ -314,6 +314,31 @@ def test_chunk_lengths_around_tile_edges(n):
     b.check(pa.pa_prefill_fp8(**b.dev), P_MMA)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("splits", [0, 1, 5, 60])
+def test_chunks_of_a_padded_batch(D, splits):
+    """Sequences without tokens bring the mean chunk below a row tile: long chunks beside short ones in that form."""
+    q, lens = [200, 260, 3, 0, 40, 129], [900, 300, 2000, 7, 40, 1300]
+    b = Block8(q + [0] * 40, lens + [0, 17] * 20, 16, 4, D, 16, seed=90, spread=12)
+    out = pa.pa_prefill_fp8(**b.dev, num_splits=splits, kernel="mma")
+    assert error() == 0
+    b.check(out, P_MMA)
+
+
+@pytest.mark.parametrize("pad", [0, 40])
+def test_nan_codes_in_long_chunks_of_a_padded_batch(pad):
+    b = Block8([300, 5] + [0] * pad, [700, 300] + [0] * pad, 8, 2, 128, 16, seed=91)
+    clean = pa.pa_prefill_fp8(**b.dev, kernel="mma")
+    for i, p in enumerate([500, 297]):  # rows 0..99 and 0..1 do not see these
+        row = int(slots_of(b.tables[i], b.seq_lens[i], 16)[p])
+        b.dev["v_cache"].view(torch.uint8)[row // 16, row % 16, 1, 5] = 0x7f
+    out = pa.pa_prefill_fp8(**b.dev, kernel="mma")
+    assert error() == 0
+    assert torch.equal(out[:100], clean[:100]) and torch.equal(out[300:302], clean[300:302])
+    assert torch.isnan(out[100:300, 4:, 5]).all() and torch.isnan(out[302:, 4:, 5]).all()
+    assert torch.equal(out[100:, :4], clean[100:, :4])
+
+
 def test_chunk_of_long_context():
     b = Block8([4, 1, 2], [20000, 9001, 127], 32, 8, 128, 16, seed=52)
     b.check(pa.pa_prefill_fp8(**b.dev), P_MMA)
