@@ -121,6 +121,8 @@ pa_status_t prefill_bind(const PrefillPlan &p, PrefillArgs *a, void *workspace) 
     a->tiles = (PrefillTile *)(ws + p.off_tiles);
     a->starts = (WalkStart *)(ws + p.off_start);
     a->merges = (MergeEntry *)(ws + p.off_merges);
+    a->cols = a->spread ? std::max(p.C / a->Hk, 1) : 1;
+    a->head_step = a->spread ? gcd(p.C, a->Hk) : a->Hk;
     a->few = (int64_t)p.max_tiles * a->Hk * 4 <= p.C ? 1 : 0;
     a->ml = (float2 *)(ws + p.off_ml);
     a->acc = (float *)(ws + p.off_acc);
@@ -274,12 +276,13 @@ pa_status_t chunk_call(const ChunkKind &kind, void *out, const void *q, const vo
     a.H = num_heads;
     a.step = kind.step;
     a.pair = kind.pair;
+    a.spread = kind.pair;
     a.min_w = 1;
     a.scale_log2 = scale * 1.4426950408889634f;
     return prefill_launch(p, cache, a, workspace, (cudaStream_t)stream);
 }
 
-// pa_prefill keeps its order of summation: no shared tiles.
+// pa_prefill keeps its order of summation: no shared tiles, its list as it was.
 constexpr ChunkKind kPrefill{false, 1, 0}, kCross{false, 0, 1}, kPrefillFp8{true, 1, 1};
 
 }  // namespace

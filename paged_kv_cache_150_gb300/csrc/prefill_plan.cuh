@@ -67,6 +67,9 @@ struct PrefillArgs {
     float scale_log2;
     int32_t step;         // positions that each token sees more than the one before it: 1, or 0 where all see all (pa_cross)
     int32_t pair;         // 1: both softmax warpgroups of the tcgen05 kernel share a tile of one row tile (TcSegment)
+    int32_t spread;       // 1: the order of heads (and tiles) that suits the memory; 0: by head, sequence and position
+    int32_t cols;         // columns of the order of tiles (tile_order)
+    int32_t head_step;    // heads that the CTAs walk through side by side (list_head)
     int32_t few;          // 1: few tiles in many pieces, merged by prefill_merge_few_kernel
     int32_t *ctl;         // ctl[1]: cut tiles listed, ctl[2]: most query rows of one
     MergeEntry *merges;   // [C] the cut tiles (note_cut)
@@ -140,6 +143,34 @@ __device__ __forceinline__ int32_t last_at_most(const int32_t *cu, int32_t n, in
     return lo;
 }
 
+// Tile of a KV head's list, of n by sequence and position, that stands at place k of
+// the order in `cols` columns: tiles 0, cols, 2 cols .., then 1, cols + 1 .. .  With a
+// column for each CTA that the head has, the tiles of one sequence, which read
+// the same keys and values, lie about a CTA's range apart, so that CTAs at work
+// side by side read them at the same time; one behind the other in one range,
+// a long context has left the L2 cache before its next tile comes.  32 / 8 heads of
+// 128: 32 x 400 tokens over 8000 states 1172 -> 1093 us, 32 x 1024 over 4000
+// 1418 -> 1288; nothing at head_dim 64 or with one tile per sequence.
+__device__ __forceinline__ int32_t tile_order(int32_t k, int32_t n, int32_t cols) {
+    if (cols <= 1) return k;
+    const int32_t full = n / cols, more = n - full * cols;  // the first `more` columns have full + 1 tiles
+    const int32_t c = k < more * (full + 1) ? k / (full + 1) : more + (k - more * (full + 1)) / full;
+    return (k - c * full - min(c, more)) * cols + c;
+}
+
+// KV head at a place of the list.  Heads lie side by side in the cache, D elements
+// each, so CTAs that read the same tokens for neighbouring heads at the same time
+// share the memory's pages.  Every head's list is the same, and C CTAs cut Hk of
+// them evenly: places whose distance is a multiple of Hk / gcd(C, Hk) are walked
+// in step.  Those places hold neighbouring heads.  On 152 CTAs, 4 tokens of many
+// sequences over 1000 to 6000 states, head_dim 64, whose rows are 128 bytes: 16, 20
+// or 32 heads 4.5 to 4.7 -> 6.3 TB/s (8 heads, in step as they are, 6.2); at
+// head_dim 128 6.7 either way.
+__device__ __forceinline__ int32_t list_head(const PrefillArgs &a, int32_t place) {
+    const int32_t phases = a.Hk / a.head_step;
+    return place % phases * a.head_step + place / phases;
+}
+
 // One CTA: the tiles of every sequence, the prefix sums of their units, and
 // the tile in which each CTA's range starts.  Row offsets that are not
 // increasing within [0, T] void the whole call (no tile: out stays as it
@@ -192,12 +223,13 @@ static __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const __g
         const int32_t k = base + tid;
         int32_t u = 0;
         if (k < tiles) {
-            // the last sequence that starts at or before tile k (it has tiles);
+            const int32_t at = tile_order(k, tiles, a.cols);
+            // the last sequence that starts at or before that tile (it has tiles);
             // single queries: a tile each
-            const int32_t lo = a.cu_q ? last_at_most(tile0, a.N, k) : k;
+            const int32_t lo = a.cu_q ? last_at_most(tile0, a.N, at) : at;
             int32_t L = a.seq_lens[lo];
             const int32_t r0 = a.cu_q ? a.cu_q[lo] : lo, n = a.cu_q ? a.cu_q[lo + 1] - r0 : 1;
-            const int32_t t0 = a.cu_q ? (k - tile0[lo]) * tq : 0;
+            const int32_t t0 = a.cu_q ? (at - tile0[lo]) * tq : 0;
             if (L < 0 || L > max_len) {
                 atomicOr(a.err, kErrLength);
                 L = 0;
@@ -233,8 +265,9 @@ static __global__ void __launch_bounds__(kThreads) prefill_plan_kernel(const __g
         if (c < Ce) {
             const int64_t lo = split_begin(c, W, Ce);
             w.hi = split_begin((int64_t)c + 1, W, Ce);
-            w.kvh = (int32_t)(lo / units);
-            const int32_t r = (int32_t)(lo - (int64_t)w.kvh * units);
+            const int32_t place = (int32_t)(lo / units);
+            const int32_t r = (int32_t)(lo - (int64_t)place * units);
+            w.kvh = list_head(a, place);
             w.k = last_at_most(cu, tiles, r);
             w.tiles = tiles;
             const int32_t begin = cu[w.k], next = w.k + 1 == tiles ? 0 : w.k + 1;
@@ -289,7 +322,8 @@ struct PrefillWalk {
         first = false;
         if (++k == tiles) {
             k = 0;
-            ++kvh;
+            kvh += a.head_step;  // list_head of the next place
+            if (kvh >= a.Hk) kvh += 1 - a.Hk;
         }
         if constexpr (kAhead) {
             t = t_next;
