@@ -131,9 +131,12 @@ struct TcSegment {
     int32_t keys;   // keys the tile sees
     int32_t je[2], jend;
     bool pair;
+    // End of row tile i's units.  (An index known only at run time would put the
+    // array, and with it every use of it, into memory.)
+    __device__ __forceinline__ int32_t end(int i) const { return i ? je[1] : je[0]; }
     // Whether warpgroup i has units of the segment.
     __device__ __forceinline__ bool has(int i, int32_t j0, int first) const {
-        return pair ? j0 + (i ^ first) < jend : j0 < je[i];
+        return pair ? j0 + (i ^ first) < jend : j0 < end(i);
     }
     template <class Walk>
     __device__ __forceinline__ TcSegment(const PrefillArgs &a, const Walk &cur) {
@@ -622,7 +625,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
         const int32_t j0 = uniform(cur.j0), jend = uniform(sg.jend), jg = uniform(guard_from(sg)),
                       keys = uniform(sg.keys);
         const int32_t je[2] = {uniform(sg.je[0]), uniform(sg.je[1])};
-        const bool pair = uniform(sg.pair) != 0;
+        const bool pair = L::kMayPair && uniform(sg.pair) != 0;
         if (jend <= j0) continue;
         const bool two = uniform(sg.t.ntok > a.tq1) != 0;
         const int q0 = uniform(two ? 0 : qs.next);  // Q's slot of the first row tile
@@ -848,7 +851,7 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
         const bool warp_rows = __any_sync(0xffffffffu, valid);
         const int32_t last = sg.t.p0 + a.step * tok;  // last key that this row sees
         // This warpgroup's units: every one of its row tile's, or every other one.
-        const int32_t je = sg.pair ? sg.jend : sg.je[i], jf = cur.j0 + (sg.pair ? i ^ first : 0), dj = sg.pair ? 2 : 1;
+        const int32_t je = sg.pair ? sg.jend : sg.end(i), jf = cur.j0 + (sg.pair ? i ^ first : 0), dj = sg.pair ? 2 : 1;
         const bool second = sg.pair && i != first;
         if (sg.pair && sg.jend > cur.j0) first ^= 1;
         if (sg.jend > cur.j0) ++segs;
