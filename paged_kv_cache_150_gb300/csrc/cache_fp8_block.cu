@@ -18,7 +18,7 @@
 // Bound by HBM traffic (x once, codes once) on prompts and by latency on a
 // decode step.
 #include "fp8_rows.cuh"
-#include "prefill_plan.cuh"  // last_at_most
+#include "pa_internal.h"
 
 namespace pa {
 

@@ -1,6 +1,6 @@
-// Chunk attention on the CUDA cores (pa_prefill for fp32, head_dim 256, the
-// split layout and block sizes the tensor-core kernel does not take; and the
-// single queries of pa_decode_fp8 in the same cases).
+// Chunk attention on the CUDA cores (pa_prefill and pa_cross for fp32, head_dim
+// 256, the split layout and block sizes the tensor-core kernel does not take;
+// pa_prefill_fp8 and the single queries of pa_decode_fp8 in the same cases).
 //
 // One CTA of 256 threads holds a tile of 64 query rows (64 / G tokens x the G
 // heads of one KV head) and walks its units of 64 keys: S = Q K^T with 4 x 4
