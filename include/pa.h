@@ -561,6 +561,8 @@ pa_status_t pa_prefill_fp8(void *out, const void *q, const void *k_cache, const 
  *     before they are pushed, one outside the pool is recorded.
  * workspace  device scratch of pa_tables_workspace_bytes(num_reqs, num_rows)
  *     bytes, 256-byte aligned; calls that share it must be ordered on one stream.
+ * PA_ERR_UNSUPPORTED: num_rows, max_blocks_per_row, batch_width or max_tokens
+ *     above 2^30.
  * One kernel per call, or two for larger batches.
  * ---------------------------------------------------------------------- */
 typedef struct pa_tables {

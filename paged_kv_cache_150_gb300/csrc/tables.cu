@@ -364,6 +364,8 @@ __global__ void __launch_bounds__(256) release_fill_kernel(const __grid_constant
 
 namespace {
 
+constexpr int32_t kMostEntries = 1 << 30;  // of a loop: its index and a stride stay within 32 bits
+
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 size_t tables_workspace(int32_t N, int32_t R) {
@@ -380,6 +382,7 @@ pa_status_t tables_args(const pa_tables_t *s, const int32_t *rows, int32_t N, vo
         (int64_t)s->num_blocks * s->block_size >= ((int64_t)1 << 31))
         return PA_ERR_INVALID_ARG;
     if (N > s->num_rows) return PA_ERR_INVALID_ARG;  // the rows of a call are distinct
+    if (s->num_rows > kMostEntries || s->max_blocks_per_row > kMostEntries) return PA_ERR_UNSUPPORTED;
     if (!s->tables || !s->lens || !s->free_list || !s->free_count || !workspace) return PA_ERR_INVALID_ARG;
     if (((uintptr_t)workspace & 255) != 0) return PA_ERR_INVALID_ARG;
     if (workspace_bytes < tables_workspace(N, s->num_rows)) return PA_ERR_WORKSPACE;
@@ -399,11 +402,12 @@ pa_status_t tables_args(const pa_tables_t *s, const int32_t *rows, int32_t N, vo
     a->ctl = (int32_t *)ws;
     a->reqs = (TableReq *)(ws + 256);
     a->claims = (int32_t *)(ws + 256 + align256(sizeof(TableReq) * (size_t)std::max(N, 1)));
-    a->err = device_error_word();
-    return a->err ? PA_OK : PA_ERR_CUDA;
+    return PA_OK;
 }
 
 pa_status_t launch_tables(const void *plan, const void *fill, dim3 grid, TablesArgs &a, cudaStream_t s) {
+    a.err = device_error_word();
+    if (!a.err) return PA_ERR_CUDA;
     cudaGetLastError();
     void *args[] = {&a};
     if (launch_pdl(plan, dim3(1), dim3(1024), args, 0, s) != cudaSuccess) return PA_ERR_CUDA;
@@ -429,6 +433,7 @@ extern "C" pa_status_t pa_extend_tables(const pa_tables_t *state, const int32_t 
     if (st != PA_OK) return st;
     if (max_tokens < 0 || (batch_tables && batch_width <= 0)) return PA_ERR_INVALID_ARG;
     if (batch_tables && (int64_t)num_reqs * batch_width >= ((int64_t)1 << 31)) return PA_ERR_INVALID_ARG;
+    if (max_tokens > kMostEntries || (batch_tables && batch_width > kMostEntries)) return PA_ERR_UNSUPPORTED;
     if (!cu_q_lens || (max_tokens > 0 && !slot_mapping) || (num_reqs > 0 && (!new_lens || !seq_lens))) return PA_ERR_INVALID_ARG;
     a.new_lens = new_lens;
     a.batch_tables = num_reqs > 0 ? batch_tables : nullptr;

@@ -136,5 +136,10 @@ def test_tables_refusals(lib):
             assert call(state(p=None), p=P) == BAD
             assert call(state(), p=P, ws=16) == _lib.PA_ERR_WORKSPACE
     if _no_gpu():
+        for call in (extend, release):
+            for kw in (dict(num_rows=(1 << 30) + 1, max_blocks_per_row=1), dict(num_rows=1, max_blocks_per_row=(1 << 30) + 1)):
+                assert call(state(block_size=1, **kw), n=1, p=P, ws=1 << 40) == UNSUP, kw
+        assert extend(state(), p=P, t=(1 << 30) + 1) == UNSUP
+        assert extend(state(), n=1, p=P, bt=P, bw=(1 << 30) + 1) == UNSUP
         assert extend(state(), p=P, wsp=ctypes.c_void_p(0x1010)) == BAD
         assert lib.pa_extend_tables(ctypes.byref(state()), None, P, 4, P, 0, P, P, P, 4, P, 1 << 20, None) in (BAD, _lib.PA_ERR_CUDA)
