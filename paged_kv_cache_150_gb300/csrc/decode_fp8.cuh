@@ -2,9 +2,10 @@
 // 128, block sizes that are multiples of 8).
 //
 // What is computed: pa_decode's attention over K = 2^ek k8, V = 2^ev v8 with
-// one exponent per token and KV head, or per block and KV head.  The codes are multiplied as fp16, which
-// holds every e4m3 value exactly, on mma.sync (single queries: 8 heads or less
-// per KV head, a contraction too thin for tcgen05's 128 rows):
+// one exponent per token and KV head, or per block and KV head.  The codes are
+// multiplied as fp16, which holds every e4m3 value exactly, on mma.sync (single
+// queries: 8 heads or less per KV head, a contraction too thin for tcgen05's 128
+// rows):
 //   S^T (16 tokens x 8 heads) = k8 Q^T, Q in fp16 scaled per row by a power of
 //     two so that its largest element lies in [2^14, 2^15): exact for every
 //     element within 2^28 of it;
@@ -24,9 +25,10 @@
 // 128) take 169 to 174 us (6.2 to 6.4 TB/s) with the work list and the merge. The
 // same bytes with 4 / 2 / 1 KV heads 174 / 181 / 221 us; head_dim 64 reaches 4.2 to
 // 4.7 TB/s with 8 KV heads and 2.7 with one.  With a scale per block 168 us, and
-// 325 us on 256 sequences of 16 to 8192 tokens (2203 MB, 6.8 TB/s).  A CTA is 8 consumer warps and a TMA producer,
-// two CTAs per SM; a stage is 8 slices of 16 tokens of one KV head (K and V,
-// 32 KiB at head_dim 128): NH heads (the largest of 8, 4, 2, 1 that divides Hk)
+// 325 us on 256 sequences of 16 to 8192 tokens (2203 MB, 6.8 TB/s).
+// A CTA is 8 consumer warps and a TMA producer, two CTAs per SM; a stage is 8
+// slices of 16 tokens of one KV head (K and V, 32 KiB at head_dim 128): NH heads
+// (the largest of 8, 4, 2, 1 that divides Hk)
 // x 128 / NH tokens, so that a stage is one contiguous piece of every block it
 // touches.  Warp w takes head w % NH, tokens 16 (w / NH) ...; with NH < 8 the
 // warps of a head join their parts in shared memory at a segment's end.
@@ -110,14 +112,15 @@ __device__ __forceinline__ int32_t f8_units_end(const PrefillCursor &cur, int32_
 enum F8Scales { kTokenScales, kBlockScales8, kBlockScalesAny };
 
 // The block scales of NH heads, and their way to a stage.  p need not be aligned.
+// Read from L2: the kernel may have begun while the write before it ran.
 __device__ __forceinline__ uint64_t load_scales(const uint8_t *p, int32_t NH) {
     if (((uintptr_t)p & (uintptr_t)(NH - 1)) == 0) {
-        if (NH == 8) return __ldg(reinterpret_cast<const unsigned long long *>(p));
-        if (NH == 4) return __ldg(reinterpret_cast<const uint32_t *>(p));
-        if (NH == 2) return __ldg(reinterpret_cast<const uint16_t *>(p));
+        if (NH == 8) return __ldcg(reinterpret_cast<const unsigned long long *>(p));
+        if (NH == 4) return __ldcg(reinterpret_cast<const uint32_t *>(p));
+        if (NH == 2) return __ldcg(reinterpret_cast<const uint16_t *>(p));
     }
     uint64_t v = 0;
-    for (int32_t i = 0; i < NH; ++i) v |= (uint64_t)__ldg(p + i) << (8 * i);
+    for (int32_t i = 0; i < NH; ++i) v |= (uint64_t)__ldcg(p + i) << (8 * i);
     return v;
 }
 __device__ __forceinline__ void store_scales(uint32_t dst, uint64_t v, int32_t NH) {
@@ -161,8 +164,8 @@ __device__ __forceinline__ void f8_producer(const PrefillArgs &a, const F8Args &
         if (lane < nbox && p >= 0 && p < a.NB) {
             const int64_t at = (int64_t)p * f.Hk + cur.kvh * f.NH;
             if (kScales == kBlockScales8) {
-                k = __ldg(reinterpret_cast<const unsigned long long *>(a.k_scale + at));
-                v = __ldg(reinterpret_cast<const unsigned long long *>(a.v_scale + at));
+                k = __ldcg(reinterpret_cast<const unsigned long long *>(a.k_scale + at));
+                v = __ldcg(reinterpret_cast<const unsigned long long *>(a.v_scale + at));
             } else {
                 k = load_scales(a.k_scale + at, f.NH);
                 v = load_scales(a.v_scale + at, f.NH);

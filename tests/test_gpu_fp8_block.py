@@ -385,6 +385,18 @@ def test_the_nan_byte_makes_its_block_nan(kernel, which):
     assert torch.isnan(one[0, 4:]).all() and torch.isfinite(one[:, :4]).all() and torch.isfinite(one[1]).all()
 
 
+@pytest.mark.parametrize("which", ["k_scale", "v_scale"])
+def test_the_nan_byte_in_long_chunks(which):
+    """As above for more rows than a row tile has: rows before the block's first position do not see it."""
+    b = Block8([100], [170], 8, 2, 128, 16, seed=92)
+    clean = pa.pa_prefill_fp8(**b.dev, kernel="mma")
+    b.dev[which][int(b.tables[0, 9]), 1] = 255  # positions 144 .. 159, tokens from 74 on
+    out = pa.pa_prefill_fp8(**b.dev, kernel="mma")
+    assert error() == 0
+    assert torch.isnan(out[74:, 4:]).all()
+    assert torch.equal(out[:, :4], clean[:, :4]) and torch.equal(out[:74], clean[:74])
+
+
 @pytest.mark.parametrize("kernel", ["mma", "simt"])
 def test_blocks_of_the_smallest_and_largest_bytes(kernel):
     """V of bytes 14 and 240 in one head each (K ordinary): the ends of what bf16 holds exactly."""
