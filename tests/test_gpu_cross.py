@@ -82,6 +82,17 @@ def test_many_short_tiles_per_cta(D, splits):
     c.check(out, p_eps(BF, "mma"))
 
 
+@pytest.mark.parametrize("splits", [0, 1, 4, 6, 30])
+@pytest.mark.parametrize("kernel", ["mma", "simt"])
+@pytest.mark.parametrize("Hk", [1, 3, 10, 12, 20])
+def test_numbers_of_heads_and_ctas(Hk, kernel, splits):
+    """The order of heads and tiles depends on the CTAs that a head has: none, some, with and without a common divisor."""
+    c = Cross([5, 300, 1, 0, 140, 33], [200, 500, 129, 64, 0, 1000], Hk, Hk, 64, 16, BF, seed=90 + Hk)
+    out = c.run(num_splits=splits, kernel=kernel)
+    assert error() == 0
+    c.check(out, p_eps(BF, kernel))
+
+
 @pytest.mark.parametrize("n", [1, 63, 64, 65, 127, 128, 129, 255, 256, 257, 384])
 def test_encoder_lengths_around_unit_edges(n):
     c = Cross([3, 300], [n, n], 8, 2, 128, 16, BF, seed=60 + n)

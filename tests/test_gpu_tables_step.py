@@ -127,3 +127,92 @@ def test_a_captured_decode_step():
         if i in (0, 1, 16, 19):
             s.check(list(range(R)), out[0], out[1], out[2], q, own, cross, 2.0 ** -11, 2.0 ** -25)
     assert pa.pa_get_device_error(raise_on_error=False) == 0
+
+
+FIRST_CALLS = """
+import torch
+import paged_kv_cache_150_gb300 as pa
+
+g = torch.Generator(device="cuda").manual_seed(19)
+bf = torch.bfloat16
+i32 = dict(dtype=torch.int32, device="cuda")
+nb, b, hk, d, h, width = 40, 16, 8, 128, 32, 10
+tables, lens, count = torch.full((4, width), -1, **i32), torch.tensor([17, 0, 3, 0], **i32), torch.tensor([nb - 3], **i32)
+tables[0, :2], tables[2, 0] = torch.tensor([39, 38], **i32), 37
+free, rows, done, new = torch.arange(nb, **i32), torch.tensor([3, 0], **i32), torch.tensor([2], **i32), torch.tensor([100, 5], **i32)
+kept = [x.clone() for x in (tables, lens, count, free)]
+k, v = (torch.randn(105, hk, d, generator=g, device="cuda").to(bf) for _ in range(2))
+q, one = torch.randn(105, h, d, generator=g, device="cuda").to(bf), torch.randn(2, h, d, generator=g, device="cuda").to(bf)
+codes = [torch.zeros(nb, b, hk, d, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2)]
+scales = [torch.full((nb, hk), 120, dtype=torch.uint8, device="cuda") for _ in range(2)]
+enc = [torch.randn(nb, b, hk, d, generator=g, device="cuda").to(bf) for _ in range(2)]
+enc_tables, seen = torch.randperm(nb, generator=g, **i32).view(2, 20).contiguous(), torch.tensor([300, 77], **i32)
+few, cu_few = torch.randn(7, h, d, generator=g, device="cuda").to(bf), torch.tensor([0, 3, 7], **i32)
+batch = (torch.zeros(2, width, **i32), torch.zeros(2, **i32), torch.zeros(3, **i32), torch.zeros(128, **i32))
+outs = [torch.zeros_like(q) for _ in range(4)] + [torch.zeros_like(one), torch.zeros_like(few), torch.zeros_like(few)]
+
+
+def step():
+    pa.pa_release_tables(tables, lens, free, count, done, b)
+    bt, sl, cu, _ = pa.pa_extend_tables(tables, lens, free, count, new, b, 128, rows=rows, out=batch)
+    pa.pa_write_blocks_fp8(k, v, bt, sl, cu, *codes, *scales)
+    pa.pa_prefill_fp8(q, *codes, *scales, bt, sl, cu, 0.1, out=outs[0], kernel="mma")
+    pa.pa_prefill_fp8(q, *codes, *scales, bt, sl, cu, 0.1, out=outs[1], kernel="simt")
+    pa.pa_cross(q, *enc, enc_tables, seen, cu, 0.1, out=outs[2])
+    pa.pa_cross(q, *enc, enc_tables, seen, cu, 0.1, out=outs[3], kernel="simt")
+    pa.pa_decode_fp8(one, *codes, *scales, bt, sl, 0.1, out=outs[4])
+    pa.pa_prefill_fp8(few, *codes, *scales, bt, sl, cu_few, 0.1, out=outs[5])
+    pa.pa_cross(few, *enc, enc_tables, seen, cu_few, 0.1, out=outs[6])
+
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+state = (tables, lens, count, free)
+results = (*batch, *outs, *state, *[c.view(torch.uint8) for c in codes], *scales)
+graph.replay()
+torch.cuda.synchronize()
+got = [x.clone() for x in results]
+for x, y in zip(state, kept):
+    x.copy_(y)
+for x in outs:
+    x.zero_()
+step()
+assert pa.pa_get_device_error(raise_on_error=False) == 0
+for x, y in zip(got, results):
+    assert torch.equal(x, y) and torch.count_nonzero(x)
+print("captured first")
+"""
+
+
+def test_the_first_calls_of_a_process_can_be_captured():
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "captured first" in done.stdout, done.stderr[-2000:]
+
+
+def test_calls_on_two_streams_at_once():
+    """Chunks over the 8-bit cache, cross attention and tables of two batches, each on a stream of its own."""
+    a, b = Loop(81), Loop(82)
+    new = {a: [30, 1, 64, 5, 47, 100], b: [7, 90, 2, 33, 1, 12]}
+    rows, data = i32(list(range(R))), {}
+    for s in (a, b):
+        T = sum(new[s])
+        data[s] = (i32(new[s]), s.rand(T, H, D), s.rand(T, HK, D), s.rand(T, HK, D), T)
+    torch.cuda.synchronize()
+    got = {}
+    for s in (a, b):
+        s.stream = torch.cuda.Stream()
+    for s in (a, b):
+        with torch.cuda.stream(s.stream):
+            got[s] = s.step(rows, *data[s])
+    torch.cuda.synchronize()
+    assert pa.pa_get_device_error(raise_on_error=False) == 0
+    for s in (a, b):
+        bt, sl, cu, _, own, cross = got[s]
+        assert sl.tolist() == new[s]
+        s.check(list(range(R)), bt, sl, cu, data[s][1], own, cross)
