@@ -99,6 +99,10 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
 // Units of T tokens that the current segment takes: [j0, j1), none without keys.
 __device__ __forceinline__ int32_t f8_units_end(const PrefillCursor &cur, int32_t T) {
     const int32_t keys = cur.t.p0 + 1;

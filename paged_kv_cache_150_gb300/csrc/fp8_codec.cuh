@@ -52,10 +52,6 @@ __device__ __forceinline__ float4 decode4(uint32_t w) {
     return make_float4(a.x, a.y, b.x, b.y);
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
 // The codes of a word's low and high half to fp16 (exact).
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
     asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
