@@ -35,9 +35,8 @@
 //
 // Encoder states (pa_cross): 64 to 448 tokens of 32 sequences over 1000 to 4096
 // states (32 / 8 heads, head_dim 128, 258 GFLOP) 223 to 235 us; 1 to 8 tokens of 128
-// sequences over 100 to 1500 (16 heads, head_dim 64, 433 MB) 112 to 115 us, bound
-// by a unit's chain (S, its softmax, O += P V, the next S) and a tile's end, every
-// seventh unit or so.
+// sequences over 100 to 1500 (16 heads, head_dim 64, 433 MB) 112 to 115 us, held by
+// a tile's end every seventh unit or so (over long contexts 6.3 TB/s).
 #pragma once
 
 #include <cuda.h>  // CUtensorMap
