@@ -58,15 +58,16 @@ constexpr int kTcSoftmaxRegs = 208, kTcOtherRegs = 88;
 // kConv: the warps that turn an 8-bit cache's codes, which arrive in a ring of their
 // own (raw), into the bf16 units of the ring that the MMAs read; 0 for a bf16 cache.
 // Both forms over an 8-bit cache are right for every call; which one is faster:
-//   4  512 threads x 128 registers at launch, 256 x 192 + 128 x 64 + 128 x 64.
+//   4  512 threads x 128 registers at launch, 256 x 192 + 128 x 64 + 128 x 64 of them.
 //      A row's scores stay in registers.  A unit takes the converters about 1.8 us,
 //      two row tiles' softmax and products longer.
 //   8  640 x 96, 256 x 112 + 128 x 88 + 256 x 80 and some left.  A unit takes the
 //      converters half of that; the softmax, short of registers, reads its scores twice,
 //      and shares tiles of one row tile (TcSegment), which leaves it time for that.
-// Chunks of 8 tokens on 16 contexts up to 32768, 32 / 8 heads, head_dim 128: 191 and 161 us.
-// A batch of longer chunks: 181 and 204 us.  Eight warps where the call's chunks
-// have no more tokens than a row tile on average (prefill_layout).
+// 32 / 8 heads, head_dim 128: 3 to 8 tokens of 64 sequences over 500 to 8192, 517 MB,
+// 191 and 161 us; 17 to 700 tokens of 16 sequences over up to 6000, 167 GFLOP, 181
+// and 204 us.  Eight warps where the call's chunks have no more tokens than a row
+// tile on average (prefill_layout).
 template <int D, int kConv>
 struct TcPrefill {
     static constexpr bool kFp8 = kConv > 0, kMayPair = kConv != 4;
