@@ -67,8 +67,12 @@ __device__ __forceinline__ WriteUnit find_unit(const WriteBlocksArgs &a, const i
         if (u == (uint32_t)base) atomicOr(a.err, kErrLength);
         return w;
     }
-    const int32_t start = L - n, blk = start / a.B + (int32_t)(u - (uint32_t)base);
-    if (blk > (L - 1) / a.B) return w;
+    // The spare numbers (and those of a padded batch's rows) are told by their
+    // distance: the block itself may lie past 32 bits.
+    const int32_t start = L - n, first = start / a.B;
+    const uint32_t at = u - (uint32_t)base;
+    if (at > (uint32_t)((L - 1) / a.B - first)) return w;
+    const int32_t blk = first + (int32_t)at;
     const int32_t p0 = max(start, blk * a.B);  // first new position of the block
     w.off = p0 - blk * a.B;
     w.held = w.off;

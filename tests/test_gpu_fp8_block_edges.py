@@ -1,0 +1,40 @@
+"""pa_write_blocks_fp8 at the ends of its ranges and next to other calls."""
+import pytest
+import torch
+
+import paged_kv_cache_150_gb300 as pa
+from _block8 import BF, E4M3, code_values, write_rule
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+def error():
+    return pa.pa_get_device_error(raise_on_error=False)
+
+
+def values(codes):
+    return code_values()[codes.view(torch.uint8).cpu().long()]
+
+
+@pytest.mark.parametrize("pad", [0, 5])
+def test_write_at_the_longest_reach(pad):
+    """The last three of 2^31 - 1 positions in blocks of one token, with rows of a
+    padded batch behind them: the numbers past the sequence's blocks name none."""
+    L, Hk, D = 2 ** 31 - 1, 2, 64
+    table = torch.zeros(1, L, dtype=torch.int32, device="cuda")
+    table[0, -3:] = i32([3, 1, 4])
+    g = torch.Generator().manual_seed(30 + pad)
+    k, v = (torch.randn(3 + pad, Hk, D, generator=g).to(BF) for _ in range(2))
+    old = [torch.randint(0, 120, (5, 1, Hk, D), generator=g, dtype=torch.int32).to(torch.uint8) for _ in range(2)]
+    bytes_ = [torch.randint(100, 140, (5, Hk), generator=g, dtype=torch.int32).to(torch.uint8) for _ in range(2)]
+    codes, scales = [x.cuda().view(E4M3) for x in old], [x.cuda() for x in bytes_]
+    pa.pa_write_blocks_fp8(k.cuda(), v.cuda(), table, i32([L]), i32([0, 3]), *codes, *scales)
+    assert error() == 0
+    for x, c, s, c0, s0 in zip((k, v), codes, scales, old, bytes_):
+        # the same three blocks of a sequence of three positions
+        want, byte = write_rule(x[:3], code_values()[c0.long()], s0, [[3, 1, 4]], [3], [0, 3], 1, 5)
+        assert torch.equal(values(c), want) and torch.equal(s.cpu(), byte)
