@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(256) write_fp8_any_kernel(const T *__restrict_
         }
         const int64_t dst = (int64_t)s * Hk + (r - t * Hk);
         uint32_t ka = 0, va = 0;
-        for (int32_t d = lane; d < D; d += 32) {
+        for (uint32_t d = lane; d < (uint32_t)D; d += 32) {
             ka = max(ka, finite_bits(to_f32(k[r * D + d])));
             va = max(va, finite_bits(to_f32(v[r * D + d])));
         }
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(256) write_fp8_any_kernel(const T *__restrict_
         va = __reduce_max_sync(0xffffffffu, va);
         const int32_t ke = row_exponent(ka), ve = row_exponent(va);
         const float ki = inv_scale(ke), vi = inv_scale(ve);
-        for (int32_t d = lane; d < D; d += 32) {
+        for (uint32_t d = lane; d < (uint32_t)D; d += 32) {
             kc[dst * D + d] = (uint8_t)__nv_cvt_float_to_fp8(to_f32(k[r * D + d]) * ki, __NV_SATFINITE, __NV_E4M3);
             vc[dst * D + d] = (uint8_t)__nv_cvt_float_to_fp8(to_f32(v[r * D + d]) * vi, __NV_SATFINITE, __NV_E4M3);
         }

@@ -235,11 +235,12 @@ __global__ void __launch_bounds__(256) write_blocks_any_kernel(const __grid_cons
     if (!load_offsets(a, cu_s)) return;
     const int32_t *cu = a.N < kCuSmem ? cu_s : a.cu;
     const int lane = threadIdx.x & 31;
-    const uint64_t items = (uint64_t)a.units * 2 * a.Hk;
+    const uint32_t Hk = (uint32_t)a.Hk, D = (uint32_t)a.D;  // 2 Hk and D + 31 may pass 2^31
+    const uint64_t items = (uint64_t)a.units * (2 * Hk);
     for (uint64_t item = ((uint64_t)blockIdx.x * 256 + threadIdx.x) >> 5; item < items; item += (uint64_t)gridDim.x * 8) {
-        const uint32_t u = (uint32_t)(item / (2 * a.Hk)), hs = (uint32_t)(item - (uint64_t)u * 2 * a.Hk);
-        const bool is_v = hs >= (uint32_t)a.Hk;
-        const uint32_t h = is_v ? hs - a.Hk : hs;
+        const uint32_t u = (uint32_t)(item / (2 * Hk)), hs = (uint32_t)(item - (uint64_t)u * (2 * Hk));
+        const bool is_v = hs >= Hk;
+        const uint32_t h = is_v ? hs - Hk : hs;
         const WriteUnit w = find_unit(a, cu, u);
         if (w.phys < 0) continue;
         const T *x = (const T *)(is_v ? a.v : a.k) + ((int64_t)w.row0 * a.Hk + h) * a.D;
@@ -249,18 +250,18 @@ __global__ void __launch_bounds__(256) write_blocks_any_kernel(const __grid_cons
         const uint32_t old = w.held > 0 ? *scale : 0u;
         uint32_t top = 0;
         for (int32_t t = 0; t < w.ntok; ++t)
-            for (int32_t d = lane; d < a.D; d += 32) top = max(top, finite_bits(to_f32(x[t * stride + d])));
+            for (uint32_t d = lane; d < D; d += 32) top = max(top, finite_bits(to_f32(x[t * stride + d])));
         top = __reduce_max_sync(0xffffffffu, top);
         uint32_t byte;
         const int32_t e = block_exponent(top, w.held, old, &byte);
         const float inv = inv_scale(e), f = recode_factor(e, old);
         for (int32_t t = 0; t < w.ntok; ++t)
-            for (int32_t d = lane; d < a.D; d += 32)
+            for (uint32_t d = lane; d < D; d += 32)
                 codes[(w.off + t) * stride + d] =
                     (uint8_t)__nv_cvt_float_to_fp8(to_f32(x[t * stride + d]) * inv, __NV_SATFINITE, __NV_E4M3);
         if (w.held > 0 && f != 1.f)
             for (int32_t t = 0; t < w.held; ++t)
-                for (int32_t d = lane; d < a.D; d += 32) {
+                for (uint32_t d = lane; d < D; d += 32) {
                     uint8_t *p = codes + t * stride + d;
                     *p = (uint8_t)__nv_cvt_float_to_fp8(decode4(*p).x * f, __NV_SATFINITE, __NV_E4M3);
                 }

@@ -38,3 +38,23 @@ def test_write_at_the_longest_reach(pad):
         # the same three blocks of a sequence of three positions
         want, byte = write_rule(x[:3], code_values()[c0.long()], s0, [[3, 1, 4]], [3], [0, 3], 1, 5)
         assert torch.equal(values(c), want) and torch.equal(s.cpu(), byte)
+
+
+def test_write_of_more_than_2_to_the_30_heads():
+    """One position of 2^30 KV heads of one element: twice the heads pass 31 bits."""
+    Hk, period = 2 ** 30, 2 ** 12
+    g = torch.Generator().manual_seed(31)
+    x = [(torch.randn(1, period, 1, generator=g) * torch.exp2(torch.randint(-40, 40, (1, period, 1), generator=g).float())).to(BF)
+         for _ in range(2)]
+    k, v = (y.cuda().repeat(1, Hk // period, 1) for y in x)
+    codes = [torch.zeros(2, 1, Hk, 1, dtype=torch.uint8, device="cuda").view(E4M3) for _ in range(2)]
+    scales = [torch.full((2, Hk), 9, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    pa.pa_write_blocks_fp8(k, v, i32([[1]]), i32([1]), i32([0, 1]), *codes, *scales)
+    assert error() == 0
+    for y, c, s in zip(x, codes, scales):
+        want, byte = write_rule(y, torch.zeros(1, 1, period, 1, dtype=torch.float64), torch.zeros(1, period, dtype=torch.uint8),
+                                [[0]], [1], [0, 1], 1, 1)
+        first = c.view(torch.uint8)[1, 0, :period, 0]
+        assert torch.equal(values(first), want[0, 0, :, 0])
+        assert bool((c.view(torch.uint8)[1].view(-1, period) == first).all()) and torch.count_nonzero(c.view(torch.uint8)[0]) == 0
+        assert bool((s[1].view(-1, period) == byte[0].cuda()).all()) and bool((s[0] == 9).all())
