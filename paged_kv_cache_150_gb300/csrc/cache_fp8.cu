@@ -17,8 +17,8 @@ constexpr int kWriteRows = 4, kWriteCtas = 4, kReadRows = 2, kReadCtas = 6;
 // t * Hk + h; L lanes (a power of two) hold a row, one vector each, a warp
 // takes 32 / L rows at a time, kWriteRows passes at once, K and V together.
 template <typename T, int L>
-__global__ void __launch_bounds__(256, kWriteCtas) write_fp8_kernel(const T *__restrict__ k, const T *__restrict__ v,
-                                                        const int32_t *__restrict__ slots, uint32_t rows, uint32_t Hk,
+__global__ void __launch_bounds__(256, kWriteCtas) write_fp8_kernel(const T *k, const T *v, const int32_t *slots,
+                                                        uint32_t rows, uint32_t Hk,
                                                         int32_t vecs, uint8_t *__restrict__ kc,
                                                         uint8_t *__restrict__ vc, uint8_t *__restrict__ ks,
                                                         uint8_t *__restrict__ vs, int64_t num_slots,
@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(256, kWriteCtas) write_fp8_kernel(const T *__r
             ku[u] = vu[u] = make_uint4(0u, 0u, 0u, 0u);
             if (r < rows) {
                 const uint32_t t = r / Hk;
-                const int32_t s = __ldg(slots + t);
+                const int32_t s = slots[t];
                 if (s >= num_slots) {
                     if (li == 0) atomicOr(err, kErrBounds);
                 } else if (s >= 0) {
@@ -78,8 +78,7 @@ __global__ void __launch_bounds__(256, kWriteCtas) write_fp8_kernel(const T *__r
 // Write, any row length and alignment: one warp per row, two passes over it
 // (the second finds it in L1 or L2), one element per lane at a time.
 template <typename T>
-__global__ void __launch_bounds__(256) write_fp8_any_kernel(const T *__restrict__ k, const T *__restrict__ v,
-                                                            const int32_t *__restrict__ slots, int64_t rows,
+__global__ void __launch_bounds__(256) write_fp8_any_kernel(const T *k, const T *v, const int32_t *slots, int64_t rows,
                                                             int32_t Hk, int32_t D, uint8_t *__restrict__ kc,
                                                             uint8_t *__restrict__ vc, uint8_t *__restrict__ ks,
                                                             uint8_t *__restrict__ vs, int64_t num_slots,
@@ -90,7 +89,7 @@ __global__ void __launch_bounds__(256) write_fp8_any_kernel(const T *__restrict_
     const int64_t nw = ((int64_t)gridDim.x * blockDim.x) >> 5;
     for (int64_t r = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; r < rows; r += nw) {
         const int64_t t = r / Hk;
-        const int32_t s = __ldg(slots + t);
+        const int32_t s = slots[t];
         if (s < 0) continue;
         if (s >= num_slots) {
             if (lane == 0) atomicOr(err, kErrBounds);
@@ -129,10 +128,9 @@ __device__ __forceinline__ int64_t scale_row(int32_t s, uint32_t h, uint32_t Hk,
 // K and V in flight.
 template <typename T, bool kBlock>
 __global__ void __launch_bounds__(256, kReadCtas) read_fp8_kernel(T *__restrict__ k, T *__restrict__ v,
-                                                       const int32_t *__restrict__ slots, uint32_t total, uint32_t Hk,
-                                                       uint32_t vecs, const uint8_t *__restrict__ kc,
-                                                       const uint8_t *__restrict__ vc, const uint8_t *__restrict__ ks,
-                                                       const uint8_t *__restrict__ vs, uint32_t B, int64_t num_slots,
+                                                       const int32_t *slots, uint32_t total, uint32_t Hk,
+                                                       uint32_t vecs, const uint8_t *kc, const uint8_t *vc,
+                                                       const uint8_t *ks, const uint8_t *vs, uint32_t B, int64_t num_slots,
                                                        unsigned int *__restrict__ err) {
     grid_dependency_wait();
     grid_launch_dependents();
@@ -149,7 +147,7 @@ __global__ void __launch_bounds__(256, kReadCtas) read_fp8_kernel(T *__restrict_
             kb[u] = vb[u] = kScaleBias;
             if (i < total) {
                 const uint32_t r = i / vecs, t = r / Hk, c = i - r * vecs;
-                const int32_t s = __ldg(slots + t);
+                const int32_t s = slots[t];
                 if (s >= num_slots) {
                     if (c == 0) atomicOr(err, kErrBounds);
                 } else if (s >= 0) {
@@ -157,8 +155,8 @@ __global__ void __launch_bounds__(256, kReadCtas) read_fp8_kernel(T *__restrict_
                     kq[u] = __ldcs(reinterpret_cast<const Code *>(kc) + src * vecs + c);
                     vq[u] = __ldcs(reinterpret_cast<const Code *>(vc) + src * vecs + c);
                     const int64_t sr = scale_row<kBlock>(s, r - t * Hk, Hk, B);
-                    kb[u] = __ldg(ks + sr);
-                    vb[u] = __ldg(vs + sr);
+                    kb[u] = ks[sr];
+                    vb[u] = vs[sr];
                 }
             }
         }
@@ -188,19 +186,17 @@ __global__ void __launch_bounds__(256, kReadCtas) read_fp8_kernel(T *__restrict_
 // Read-back, any row length and alignment: one element per thread.
 template <typename T, bool kBlock>
 __global__ void __launch_bounds__(256) read_fp8_any_kernel(T *__restrict__ k, T *__restrict__ v,
-                                                           const int32_t *__restrict__ slots, int64_t total,
-                                                           int32_t Hk, int32_t D, const uint8_t *__restrict__ kc,
-                                                           const uint8_t *__restrict__ vc,
-                                                           const uint8_t *__restrict__ ks,
-                                                           const uint8_t *__restrict__ vs, uint32_t B,
-                                                           int64_t num_slots, unsigned int *__restrict__ err) {
+                                                           const int32_t *slots, int64_t total, int32_t Hk, int32_t D,
+                                                           const uint8_t *kc, const uint8_t *vc, const uint8_t *ks,
+                                                           const uint8_t *vs, uint32_t B, int64_t num_slots,
+                                                           unsigned int *__restrict__ err) {
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t stride = (int64_t)gridDim.x * blockDim.x;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += stride) {
         const int64_t r = i / D, t = r / Hk;
         const int32_t d = (int32_t)(i - r * D);
-        const int32_t s = __ldg(slots + t);
+        const int32_t s = slots[t];
         float kx = 0.f, vx = 0.f;
         if (s >= num_slots) {
             if (d == 0) atomicOr(err, kErrBounds);

@@ -19,8 +19,8 @@ namespace pa {
 constexpr int kUnroll = 4;
 
 template <typename V>
-__device__ __forceinline__ void warp_copy_rows(V *__restrict__ kd, V *__restrict__ vd, const V *__restrict__ ks,
-                                               const V *__restrict__ vs, int64_t n, int lane, bool streaming) {
+__device__ __forceinline__ void warp_copy_rows(V *__restrict__ kd, V *__restrict__ vd, const V *ks, const V *vs,
+                                               int64_t n, int lane, bool streaming) {
     for (int64_t j0 = 0; j0 < n; j0 += 32 * kUnroll) {
         V kx[kUnroll], vx[kUnroll];
 #pragma unroll
@@ -49,9 +49,8 @@ __device__ __forceinline__ void warp_copy_rows(V *__restrict__ kd, V *__restrict
 // dropped by a ballot without touching their rows.
 template <typename V>
 __global__ void __launch_bounds__(256, 4) reshape_and_cache_kernel(
-    const V *__restrict__ k, const V *__restrict__ v, const int32_t *__restrict__ slots,
-    int32_t num_tokens, V *__restrict__ k_cache, V *__restrict__ v_cache, int64_t num_slots,
-    int32_t row_vecs, unsigned int *__restrict__ err) {
+    const V *k, const V *v, const int32_t *slots, int32_t num_tokens, V *__restrict__ k_cache,
+    V *__restrict__ v_cache, int64_t num_slots, int32_t row_vecs, unsigned int *__restrict__ err) {
     grid_dependency_wait();    // launched programmatically: the previous grid's writes first
     grid_launch_dependents();  // a programmatically launched successor may get resident early
     constexpr int kChunk = 32 * kUnroll;
@@ -65,7 +64,7 @@ __global__ void __launch_bounds__(256, 4) reshape_and_cache_kernel(
     const int64_t n = min((int64_t)kChunk, (int64_t)row_vecs - j0);
     for (int64_t t0 = wt; t0 < num_tokens; t0 += 32 * NWt) {
         const int64_t tl = t0 + (int64_t)lane * NWt;
-        const int32_t sl = tl < num_tokens ? __ldg(slots + tl) : -1;
+        const int32_t sl = tl < num_tokens ? slots[tl] : -1;
         const bool bad = (int64_t)sl >= num_slots;
         if (__any_sync(0xffffffffu, bad) && lane == 0 && j0 == 0) atomicOr(err, kErrBounds);
         unsigned int todo = __ballot_sync(0xffffffffu, sl >= 0 && !bad);
@@ -85,7 +84,7 @@ __global__ void __launch_bounds__(256, 4) reshape_and_cache_kernel(
 // per (head, d) at stride B.
 template <typename T>
 __global__ void __launch_bounds__(256) reshape_and_cache_split_kernel(
-    const T *__restrict__ k, const T *__restrict__ v, const int32_t *__restrict__ slots, int32_t num_tokens,
+    const T *k, const T *v, const int32_t *slots, int32_t num_tokens,
     T *__restrict__ k_cache, T *__restrict__ v_cache, int64_t num_slots, int32_t B, int32_t Hk, int32_t D,
     unsigned int *__restrict__ err) {
     grid_dependency_wait();
@@ -98,7 +97,7 @@ __global__ void __launch_bounds__(256) reshape_and_cache_split_kernel(
         const int32_t t = (int32_t)(i / per_tok);
         const int32_t r = (int32_t)(i - (int64_t)t * per_tok);
         const int32_t h = r / D, d = r - h * D;
-        const int32_t s = __ldg(slots + t);
+        const int32_t s = slots[t];
         if (s < 0) continue;
         if ((int64_t)s >= num_slots) {
             if (r == 0) atomicOr(err, kErrBounds);
@@ -116,8 +115,7 @@ __global__ void __launch_bounds__(256) reshape_and_cache_split_kernel(
 
 template <typename V>
 __global__ void __launch_bounds__(256) copy_blocks_kernel(V *__restrict__ k_cache, V *__restrict__ v_cache,
-                                                          const int32_t *__restrict__ pairs,
-                                                          int32_t num_pairs, int32_t num_blocks,
+                                                          const int32_t *pairs, int32_t num_pairs, int32_t num_blocks,
                                                           int64_t block_vecs, int32_t chunks_per_pair,
                                                           unsigned int *__restrict__ err) {
     grid_dependency_wait();    // launched programmatically: the previous grid's writes first
@@ -125,8 +123,8 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(V *__restrict__ k_cach
     const int32_t p = blockIdx.x / chunks_per_pair;
     const int32_t chunk = blockIdx.x - p * chunks_per_pair;
     if (p >= num_pairs) return;
-    const int32_t src = __ldg(pairs + 2 * p);
-    const int32_t dst = __ldg(pairs + 2 * p + 1);
+    const int32_t src = pairs[2 * p];
+    const int32_t dst = pairs[2 * p + 1];
     if (src < 0 || src >= num_blocks || dst < 0 || dst >= num_blocks) {
         if (chunk == 0 && threadIdx.x == 0) atomicOr(err, kErrBounds);
         return;

@@ -124,10 +124,10 @@ constexpr int fma_min_ctas() { return (GMAX == 8 || GMAX * D >= 1024) ? 2 : 3; }
 template <typename T, int D, int GMAX>
 __global__ void __launch_bounds__(160, fma_min_ctas<D, GMAX>()) decode_fma_kernel(
     const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const T *__restrict__ q,
-    T *__restrict__ out, const int32_t *__restrict__ tables, int32_t max_blocks, const int32_t *__restrict__ lens,
-    const int32_t *__restrict__ cu, int32_t N, int32_t H, int32_t Hk, int32_t G, int32_t B, int32_t NB, int32_t NH,
+    T *__restrict__ out, const int32_t *__restrict__ tables, int32_t max_blocks, const int32_t *lens,
+    const int32_t *cu, int32_t N, int32_t H, int32_t Hk, int32_t G, int32_t B, int32_t NB, int32_t NH,
     int32_t S, float scale_log2, int32_t C, float2 *__restrict__ ml_ws, float *__restrict__ acc_ws,
-    unsigned int *__restrict__ counters, const int32_t *__restrict__ start_seq, unsigned int *__restrict__ err) {
+    unsigned int *__restrict__ counters, const int32_t *start_seq, unsigned int *__restrict__ err) {
     constexpr int E = FmaElt<T>::kLine, EC = FmaElt<T>::kChunk;
     constexpr int DL = D / E;     // 128-byte lines per token row
     constexpr int EPL = D / 32;   // output elements per lane in the P V phase

@@ -136,7 +136,7 @@ __device__ __forceinline__ void merge_pieces(T *__restrict__ out_base, const Pie
 // Pieces of the sequence's own blocks: its range of the flattened (head
 // group g, sequence, own block) list of W blocks cut over Ce CTAs; warp w of
 // the group holds KV head g * NH + w.
-__device__ __forceinline__ PieceRange own_range(const float2 *ml, const float *acc, const int32_t *__restrict__ cu,
+__device__ __forceinline__ PieceRange own_range(const float2 *ml, const float *acc, const int32_t *cu,
                                                 int32_t N, int32_t seq, int32_t g, int32_t w, int32_t G,
                                                 int32_t HPG, int64_t W, int32_t Ce) {
     const int64_t x0 = (int64_t)g * cu[N] + cu[seq];
@@ -380,8 +380,8 @@ __device__ __forceinline__ bool pair_is_long(const int32_t *cu, int32_t Wg, int6
 // same list), and their merges dealt out over the grid.
 template <int D>
 __global__ void __launch_bounds__(256) long_merge_kernel(
-    __nv_bfloat16 *__restrict__ out, const int32_t *__restrict__ cu, int32_t N, int32_t H, int32_t Hk, int32_t G,
-    int32_t NH, int32_t C, const float2 *__restrict__ ml_ws, const float *__restrict__ acc_ws, int32_t min_pieces) {
+    __nv_bfloat16 *__restrict__ out, const int32_t *cu, int32_t N, int32_t H, int32_t Hk, int32_t G,
+    int32_t NH, int32_t C, const float2 *ml_ws, const float *acc_ws, int32_t min_pieces) {
     constexpr int kSmemCu = 4096, kChunk = 256;
     __shared__ int32_t cu_s[kSmemCu];
     __shared__ int32_t longs[kChunk];
@@ -439,8 +439,8 @@ __global__ void __launch_bounds__(256) long_merge_kernel(
 // attention launch, since work after it on the stream may rely on both.
 template <int D>
 __global__ void __launch_bounds__(256, 2) shared_merge_kernel(
-    __nv_bfloat16 *__restrict__ out, const int32_t *__restrict__ cu, int32_t N, int32_t H, int32_t Hk, int32_t G,
-    int32_t NH, int32_t C, const float2 *__restrict__ ml_ws, const float *__restrict__ acc_ws, const SharedArgs sh) {
+    __nv_bfloat16 *__restrict__ out, const int32_t *cu, int32_t N, int32_t H, int32_t Hk, int32_t G,
+    int32_t NH, int32_t C, const float2 *ml_ws, const float *acc_ws, const SharedArgs sh) {
     const int32_t Cs = sh.ctl[0];
     const int64_t wid = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;

@@ -480,9 +480,9 @@ template <int D, int B, int LAYOUT, bool kShared>
 __device__ __forceinline__ void own_block_cta(
     uint8_t *smem, const CUtensorMap *tmk, const CUtensorMap *tmv, const __nv_bfloat16 *__restrict__ q,
     __nv_bfloat16 *__restrict__ out, const int32_t *__restrict__ tables, int32_t max_blocks,
-    const int32_t *__restrict__ lens, const int32_t *cu, int32_t N, int32_t H, int32_t G, int32_t NB,
+    const int32_t *lens, const int32_t *cu, int32_t N, int32_t H, int32_t G, int32_t NB,
     int32_t NH, float scale_log2, float2 *__restrict__ ml_ws, float *__restrict__ acc_ws,
-    unsigned int *__restrict__ counters, const int32_t *__restrict__ start_seq, int32_t Hk, int32_t C,
+    unsigned int *__restrict__ counters, const int32_t *start_seq, int32_t Hk, int32_t C,
     int32_t Cs, const SharedArgs &sh, unsigned int *__restrict__ err, int32_t min_pieces, int32_t cta, int tid,
     uint32_t bar) {
     using Tile = MmaTile<D, B>;
@@ -766,7 +766,7 @@ __device__ __forceinline__ void own_block_cta(
 // cu_l[0..N] in shared memory by the whole CTA: the plan kernel's cu[] (the
 // same clamping of bad lengths to 0), without waiting for that kernel.  Each
 // thread scans a contiguous chunk; one block-wide scan joins the chunks.
-__device__ __forceinline__ void local_prefix_sums(const int32_t *__restrict__ seq_lens, int32_t N, int32_t B,
+__device__ __forceinline__ void local_prefix_sums(const int32_t *seq_lens, int32_t N, int32_t B,
                                                   int32_t max_len, int32_t *cu_l) {
     __shared__ int32_t warp_sum[32];
     const int32_t t = threadIdx.x, nt = blockDim.x;
@@ -832,11 +832,11 @@ __global__ void __launch_bounds__(32 * (kMmaMaxHeads + 1) * (kShared ? shared_ha
     const __grid_constant__ CUtensorMap tmk1, const __grid_constant__ CUtensorMap tmv1,
     const __grid_constant__ CUtensorMap tmkp, const __grid_constant__ CUtensorMap tmvp,
     const __nv_bfloat16 *__restrict__ q, __nv_bfloat16 *__restrict__ out,
-    const int32_t *__restrict__ tables, int32_t max_blocks, const int32_t *__restrict__ lens,
-    const int32_t *__restrict__ cu, int32_t N, int32_t H, int32_t Hk, int32_t G, int32_t NB,
+    const int32_t *__restrict__ tables, int32_t max_blocks, const int32_t *lens,
+    const int32_t *cu, int32_t N, int32_t H, int32_t Hk, int32_t G, int32_t NB,
     int32_t NH, float scale_log2, int32_t C, float2 *__restrict__ ml_ws, float *__restrict__ acc_ws,
-    unsigned int *__restrict__ counters, const int32_t *__restrict__ start_seq, unsigned int *__restrict__ err,
-    const SharedArgs sh, const int32_t *__restrict__ seq_lens, int32_t local_cu, int32_t min_pieces) {
+    unsigned int *__restrict__ counters, const int32_t *start_seq, unsigned int *__restrict__ err,
+    const SharedArgs sh, const int32_t *seq_lens, int32_t local_cu, int32_t min_pieces) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
 

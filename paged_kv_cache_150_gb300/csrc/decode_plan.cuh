@@ -14,7 +14,7 @@ namespace pa {
 // head, block size, rows per pass, and every index it holds), so that a bad
 // plan can only switch sharing off, never send a kernel out of bounds.
 // Block-wide; every thread returns the verdict.
-__device__ bool plan_valid(const int32_t *__restrict__ w, int32_t N, int32_t G, int32_t B, int32_t Hk,
+__device__ bool plan_valid(const int32_t *w, int32_t N, int32_t G, int32_t B, int32_t Hk,
                            int32_t max_blocks, int *s_flag, int *s_count) {
     if (threadIdx.x == 0) {
         const int32_t groups = w[4], M = w[5], V = w[6];
@@ -69,7 +69,7 @@ __device__ bool plan_valid(const int32_t *__restrict__ w, int32_t N, int32_t G, 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(1024) decode_plan_kernel(const int32_t *__restrict__ seq_lens, int32_t N,
+__global__ void __launch_bounds__(1024) decode_plan_kernel(const int32_t *seq_lens, int32_t N,
                                                            int32_t B, int32_t max_len, int32_t HD,
                                                            int32_t *__restrict__ lens_ws,
                                                            int32_t *__restrict__ cu,
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(1024) decode_plan_kernel(const int32_t *__rest
                                                            int32_t NG, int32_t C,
                                                            int32_t *__restrict__ start_seq,
                                                            unsigned int *__restrict__ err,
-                                                           const int32_t *__restrict__ plan, int32_t G,
+                                                           const int32_t *plan, int32_t G,
                                                            int32_t Hk, int32_t NH, int32_t *__restrict__ skip,
                                                            int32_t *__restrict__ ctl,
                                                            int32_t *__restrict__ start_s,

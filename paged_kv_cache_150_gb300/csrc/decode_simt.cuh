@@ -28,10 +28,10 @@ template <typename T, int D, int GMAX, int LAYOUT>
 __global__ void __launch_bounds__(256) decode_simt_kernel(
     const T *__restrict__ q, T *__restrict__ out, const T *__restrict__ k_cache,
     const T *__restrict__ v_cache, const int32_t *__restrict__ tables, int32_t max_blocks,
-    const int32_t *__restrict__ lens, const int32_t *__restrict__ cu, int32_t N, int32_t H,
+    const int32_t *lens, const int32_t *cu, int32_t N, int32_t H,
     int32_t Hk, int32_t G, int32_t B, int32_t NB, int32_t NH, float scale_log2, int32_t C,
     float2 *__restrict__ ml_ws, float *__restrict__ acc_ws, unsigned int *__restrict__ counters,
-    const int32_t *__restrict__ start_seq, unsigned int *__restrict__ err) {
+    const int32_t *start_seq, unsigned int *__restrict__ err) {
     constexpr int VPL = D / 32;
     grid_dependency_wait();  // the plan kernel's cu[] / lens (programmatic launch)
     const int32_t NG = Hk / NH;

@@ -182,6 +182,10 @@ __device__ __forceinline__ void grid_dependency_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 // Allow the next grid on the stream (if launched programmatically) to start.
+// It may be resident while this one writes, so kernels read what the grid
+// before them may write with plain or L2 loads: non-coherent ones (__ldg, and
+// what the compiler makes of const __restrict__ parameters) hold only for
+// memory that nothing writes during a kernel's life.
 __device__ __forceinline__ void grid_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -316,8 +320,7 @@ struct BlockCursor {
     int32_t nb;  // blocks of the current sequence
     int32_t b0;  // blocks of the current sequence before the list's first (skip[seq]; 0 without skip)
 
-    __device__ __forceinline__ void init(int64_t x, const int32_t *__restrict__ cu, int32_t N,
-                                         const int32_t *__restrict__ skip = nullptr) {
+    __device__ __forceinline__ void init(int64_t x, const int32_t *cu, int32_t N, const int32_t *skip = nullptr) {
         const int32_t Wg = cu[N];
         g = (int32_t)(x / Wg);
         const int32_t r = (int32_t)(x - (int64_t)g * Wg);
@@ -338,8 +341,8 @@ struct BlockCursor {
 
     // Position at flattened block x when the sequence holding it is known
     // (from the plan kernel's per-CTA start table): no search.
-    __device__ __forceinline__ void init_at(int64_t x, int32_t s, const int32_t *__restrict__ cu, int32_t N,
-                                            const int32_t *__restrict__ skip = nullptr) {
+    __device__ __forceinline__ void init_at(int64_t x, int32_t s, const int32_t *cu, int32_t N,
+                                            const int32_t *skip = nullptr) {
         const int32_t Wg = cu[N];
         g = (int32_t)(x / Wg);
         seq = s;
@@ -348,8 +351,7 @@ struct BlockCursor {
         b0 = skip ? skip[s] : 0;
     }
 
-    __device__ __forceinline__ void advance(const int32_t *__restrict__ cu, int32_t N,
-                                            const int32_t *__restrict__ skip = nullptr) {
+    __device__ __forceinline__ void advance(const int32_t *cu, int32_t N, const int32_t *skip = nullptr) {
         if (++blk < nb) return;
         blk = 0;
         do {

@@ -72,8 +72,8 @@ __device__ __forceinline__ float4 cache4(const PrefillArgs &a, int64_t slot, int
     if constexpr (std::is_same<CT, CacheE4m3>::value || std::is_same<CT, CacheE4m3Block>::value) {
         const int64_t row = slot * a.Hk + kvh;
         const int64_t at = std::is_same<CT, CacheE4m3>::value ? row : slot / a.B * a.Hk + kvh;
-        const float s = scale_of(__ldg((IS_V ? a.v_scale : a.k_scale) + at));
-        const float4 x = decode4(__ldg(reinterpret_cast<const uint32_t *>((const uint8_t *)base + row * D + d)));
+        const float s = scale_of((IS_V ? a.v_scale : a.k_scale)[at]);
+        const float4 x = decode4(*reinterpret_cast<const uint32_t *>((const uint8_t *)base + row * D + d));
         return make_float4(x.x * s, x.y * s, x.z * s, x.w * s);
     } else if constexpr (LAYOUT == PA_LAYOUT_ROW) {
         return load4((const CT *)base + (slot * a.Hk + kvh) * D + d);

@@ -58,3 +58,70 @@ def test_write_of_more_than_2_to_the_30_heads():
         assert torch.equal(values(first), want[0, 0, :, 0])
         assert bool((c.view(torch.uint8)[1].view(-1, period) == first).all()) and torch.count_nonzero(c.view(torch.uint8)[0]) == 0
         assert bool((s[1].view(-1, period) == byte[0].cuda()).all()) and bool((s[0] == 9).all())
+
+
+def growing_step(i, n, Hk, D, g):
+    """A token for each of n requests, larger from step to step: exponents of partly filled blocks grow."""
+    return [(torch.randn(n, Hk, D, generator=g, device="cuda") * 2.0 ** (i - 10)).to(BF) for _ in range(2)]
+
+
+class Steps:
+    """Requests of a token per step: tables, the 8-bit pool with block scales, an
+    8-bit pool with a scale per token and a bf16 pool at the same slots, read back."""
+
+    def __init__(self, n=300, Hk=3, D=64, B=16, steps=20):
+        self.n, self.B = n, B
+        W = -(-steps // B) + 1
+        NB = n * W
+        self.tables = torch.full((n, W), -1, dtype=torch.int32, device="cuda")
+        self.lens, self.count = torch.zeros(n, dtype=torch.int32, device="cuda"), i32([NB])
+        self.free = torch.arange(NB - 1, -1, -1, dtype=torch.int32, device="cuda")  # neighbours to neighbouring requests
+        self.new = torch.ones(n, dtype=torch.int32, device="cuda")
+        self.block = [torch.zeros(NB, B, Hk, D, dtype=torch.uint8, device="cuda").view(E4M3) for _ in range(2)] + \
+                     [torch.zeros(NB, Hk, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        self.token = [torch.zeros(NB, B, Hk, D, dtype=torch.uint8, device="cuda").view(E4M3) for _ in range(2)] + \
+                     [torch.zeros(NB, B, Hk, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        self.bf = [torch.zeros(NB, B, Hk, D, dtype=BF, device="cuda") for _ in range(2)]
+        self.ws = torch.empty(pa.pa_tables_workspace_bytes(n, n), dtype=torch.uint8, device="cuda")
+        self.q = torch.randn(n, Hk, D, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(BF)
+
+    def step(self, k, v, sync):
+        """The step's calls, with nothing between them or one wait behind each; what they give."""
+        bt, sl, cu, slots = pa.pa_extend_tables(self.tables, self.lens, self.free, self.count, self.new, self.B, self.n,
+                                                workspace=self.ws)
+        sync()
+        pa.pa_write_blocks_fp8(k, v, bt, sl, cu, *self.block)
+        sync()
+        back = pa.pa_gather_cache_fp8(*self.block, slots)
+        sync()
+        slow = pa.pa_decode_fp8(self.q, *self.block, bt, sl, 0.125, kernel="simt")
+        sync()
+        pa.pa_reshape_and_cache_fp8(k, v, slots, *self.token)
+        sync()
+        back_t = pa.pa_gather_cache_fp8(*self.token, slots)
+        sync()
+        pa.pa_reshape_and_cache(*back_t, slots, *self.bf)
+        sync()
+        out = pa.pa_decode(self.q, *self.bf, bt, sl, 0.125)
+        return (bt, sl, slots, slow, out) + back + back_t
+
+    def state(self):
+        return [x.view(torch.uint8) for x in self.block + self.token] + self.bf + [self.tables, self.lens, self.free]
+
+
+def test_calls_behind_their_writers():
+    """Each call reads what the one before it has just written, bit for bit as with a wait between them."""
+    steps = 20
+    a, b = Steps(steps=steps), Steps(steps=steps)
+    g = torch.Generator(device="cuda").manual_seed(32)
+    rows = [growing_step(i, a.n, 3, 64, g) for i in range(steps)]
+    torch.cuda.synchronize()
+    got = [a.step(*r, lambda: None) for r in rows]
+    torch.cuda.synchronize()
+    want = [b.step(*r, torch.cuda.synchronize) for r in rows]
+    assert error() == 0
+    for i, (x, y) in enumerate(zip(got, want)):
+        for u, w in zip(x, y):
+            assert torch.equal(u, w), "step %d" % i
+    for u, w in zip(a.state(), b.state()):
+        assert torch.equal(u, w)
