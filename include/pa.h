@@ -553,8 +553,9 @@ pa_status_t pa_prefill_fp8(void *out, const void *q, const void *k_cache, const 
  *     length below 0 or past its row, more than max_tokens tokens, more blocks
  *     than batch_width or a count outside [0, num_blocks] records
  *     PA_ERR_DEVICE_BOUNDS.  Such a call changes no state and receives no new
- *     token: lengths as before (0 where there is none), cu_q_lens all 0, slots
- *     all -1.  A block id outside the pool gives slots of -1 and is recorded.
+ *     token: lengths as before (0 where there is none, and for all requests but
+ *     the first that name one row), cu_q_lens all 0, slots all -1.  A block id
+ *     outside the pool gives slots of -1 and is recorded.
  * pa_release_tables  the requests' blocks go onto the stack, request by request,
  *     each from its first block to its last, and their lengths become 0.  The
  *     same refusals (also more blocks than the pool has); ids are not checked

@@ -43,7 +43,7 @@ struct TablesArgs {
     int32_t *seq_lens, *cu_q, *slots;
     int32_t max_tokens;
     TableReq *reqs;   // [N]
-    int32_t *claims;  // [R] the request that names each row
+    int32_t *claims;  // [R] the first request that names each row
     int32_t *ctl;     // [0] the stack's count when the call began
     unsigned int *err;
 };
@@ -63,7 +63,7 @@ struct TableLook {
     int32_t row, old, len, blocks;  // blocks taken or given back
     unsigned int bad;
 };
-// claims: of the requests that name one row one is the row's, the others refuse the call.
+// claims: of the requests that name one row the first is the row's, the others refuse the call.
 template <bool kRelease>
 __device__ __forceinline__ TableLook look_at(const TablesArgs &a, int32_t i, int32_t row, int32_t claim) {
     TableLook q{row, 0, 0, 0, 0u};
@@ -190,6 +190,16 @@ __global__ void __launch_bounds__(1024) tables_plan_kernel(const __grid_constant
         scan_1024(&scan, blocks, tokens, bad, &b, &t);
         all_blocks += b;  // N rows of at most 2^31 entries in all
         all_tokens += t;
+    }
+    if (bad) {
+        // A row named twice stays the first request's, whichever store came last
+        // (here, where the call is refused already: 0.4 us in front of every scan).
+        for (int32_t i = tid; i < a.N; i += 1024) {
+            const int32_t row = i == tid ? row0 : row_of(a, i);
+            if (row >= 0 && *(volatile int32_t *)(claims + row) != i) atomicMin(claims + row, i);
+        }
+        __syncthreads();
+        if (tid < a.N && a.N <= 1024) mine = look(tid);
     }
     if (kRelease) {
         if (!bad && (int64_t)count + all_blocks > a.NB) bad = kErrBounds;  // more blocks than the pool has
