@@ -780,6 +780,7 @@ __device__ __forceinline__ void write_rows(const PrefillArgs &a, const Walk &cur
     const int64_t row = cur.slot(c) * (2 * kTcRows) + (sg.pair ? 0 : i) * kTcRows + r;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     __nv_bfloat16 *op = (__nv_bfloat16 *)a.out + ((int64_t)(sg.t.row0 + tok) * a.H + (int64_t)cur.kvh * a.G + g) * D;
+    __syncwarp();  // converged, as the tensor memory's loads want it
     // 16 columns at a time in a short loop: this code runs once per segment, and
     // unrolled over a row most of its time was its own fetching
     // (68 sequences of 1 to 130 tokens over 1 to 1664 states: 120 and 115 us).
@@ -807,18 +808,18 @@ __device__ __forceinline__ void write_rows(const PrefillArgs &a, const Walk &cur
                 if (last >= first[2 * D]) o[k] += __uint_as_float(0x7fffffffu);
             }
         }
-        if (!valid) continue;
         // A thread writes a row, so a store's lanes are rows apart: whole sectors
-        // where out's alignment allows.
+        // where out's alignment allows.  Predicated, so that the warp stays
+        // converged for the next load.
         if (whole) {
             uint32_t w[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
             if (out32) {
-                store32(op + d0, w);
+                store32_if(valid, op + d0, w);
             } else {
-                *reinterpret_cast<uint4 *>(op + d0) = make_uint4(w[0], w[1], w[2], w[3]);
-                *reinterpret_cast<uint4 *>(op + d0 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                store16_if(valid, op + d0, make_uint4(w[0], w[1], w[2], w[3]));
+                store16_if(valid, op + d0 + 8, make_uint4(w[4], w[5], w[6], w[7]));
             }
         } else {
 #pragma unroll
@@ -826,7 +827,7 @@ __device__ __forceinline__ void write_rows(const PrefillArgs &a, const Walk &cur
                 uint32_t w[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[k + e]);
-                store32(a.acc + row * D + d0 + k, w);
+                store32_if(valid, a.acc + row * D + d0 + k, w);
             }
         }
     }

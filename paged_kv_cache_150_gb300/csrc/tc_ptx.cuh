@@ -204,10 +204,17 @@ __device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 32 bytes, 32-byte aligned, in one store (a whole sector of its line).
-__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+// 32 bytes, 32-byte aligned, in one store (a whole sector of its line), and 16, in
+// the lanes that have `on`: no branch, so the warp stays converged.
+__device__ __forceinline__ void store32_if(bool on, void *p, const uint32_t (&w)[8]) {
+    asm volatile(
+        "{ .reg .pred q; setp.ne.b32 q, %9, 0; @q st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8}; }" ::"l"(p),
+        "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"((uint32_t)on)
+        : "memory");
+}
+__device__ __forceinline__ void store16_if(bool on, void *p, const uint4 &w) {
+    asm volatile("{ .reg .pred q; setp.ne.b32 q, %5, 0; @q st.global.v4.b32 [%0], {%1, %2, %3, %4}; }" ::"l"(p),
+                 "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w), "r"((uint32_t)on)
                  : "memory");
 }
 
