@@ -378,7 +378,8 @@ int32_t pa_split_owner(int64_t total_blocks, int32_t num_splits, int64_t x);
  *               > 0 and 16-byte aligned q and out; CUDA cores take the rest.
  * ---------------------------------------------------------------------- */
 typedef struct pa_prefill_opts {
-    int32_t num_splits; /* persistent CTAs sharing the work; 0 = one wave on this device */
+    int32_t num_splits; /* persistent CTAs sharing the work; 0 = one wave on this device (pa_decode_fp8
+                           over block scales: fewer where the contexts are short) */
     int32_t kernel;     /* pa_kernel_t; PA_KERNEL_MMA: the tcgen05 kernel or PA_ERR_UNSUPPORTED */
 } pa_prefill_opts_t;
 

@@ -151,7 +151,8 @@ extern "C" pa_status_t pa_decode_fp8(void *out, const void *q, const void *k_cac
     a.N = num_seqs;
     a.T = num_seqs;
     a.step = 1;
-    a.min_w = cache->dtype == PA_FP8_E4M3_BLOCK ? kMinWeight : 1;
+    // a number of CTAs that the caller gives is taken as it is
+    a.min_w = cache->dtype == PA_FP8_E4M3_BLOCK && !(opts && opts->num_splits > 0) ? kMinWeight : 1;
     a.H = num_heads;
     a.scale_log2 = scale * 1.4426950408889634f;
     cudaStream_t s = (cudaStream_t)stream;

@@ -62,7 +62,7 @@ struct PrefillArgs {
     int32_t kt;           // keys per unit
     int32_t extra;        // weight of a tile beside its units
     int32_t C;            // persistent CTAs
-    int32_t min_w;        // weight that a CTA's range should have (active_ctas); 1: any
+    int32_t min_w;        // weight that a CTA's range should have (active_ctas); 1: any (a split count that the caller gives)
     int32_t max_tiles;    // capacity of tiles[] and cu[]
     float scale_log2;
     int32_t step;         // positions that each token sees more than the one before it: 1, or 0 where all see all (pa_cross)

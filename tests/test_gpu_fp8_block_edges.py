@@ -125,3 +125,18 @@ def test_calls_behind_their_writers():
             assert torch.equal(u, w), "step %d" % i
     for u, w in zip(a.state(), b.state()):
         assert torch.equal(u, w)
+
+
+def test_decode_takes_the_split_count_that_it_is_given():
+    """One context of 100 units: 96 CTAs cut it into more pieces than 48 do, which
+    shows in the last bits; left to itself the call takes 48 of a wave."""
+    g = torch.Generator().manual_seed(33)
+    codes = [torch.randint(0, 120, (100, 16, 8, 128), generator=g, dtype=torch.int32).to(torch.uint8).cuda().view(E4M3)
+             for _ in range(2)]
+    scales = [torch.randint(117, 121, (100, 8), generator=g, dtype=torch.int32).to(torch.uint8).cuda() for _ in range(2)]
+    q = torch.randn(1, 32, 128, generator=g).to(BF).cuda()
+    table = torch.randperm(100, generator=g).to(torch.int32).view(1, -1).cuda()
+    out = {n: pa.pa_decode_fp8(q, *codes, *scales, table, i32([1600]), 0.05, kernel="mma", num_splits=n) for n in (0, 48, 96)}
+    assert error() == 0
+    assert not torch.equal(out[96], out[48])
+    assert torch.equal(out[0], out[48])
