@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(256, kWriteBlocksCtas) write_blocks_kernel(con
                 old[s] = byte;
             }
             team_sync<W>(team);  // the old bytes and tops have been read
-            if (ti < 2) *scale[ti] = (uint8_t)old[ti];
+            if (ti < 2) *(ti ? scale[1] : scale[0]) = (uint8_t)(ti ? old[1] : old[0]);  // (an index would put both in memory)
             src[0] += vecs, src[1] += vecs;
             dst[0] += a.D, dst[1] += a.D;
         }
