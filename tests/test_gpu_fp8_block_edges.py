@@ -140,3 +140,46 @@ def test_decode_takes_the_split_count_that_it_is_given():
     assert error() == 0
     assert not torch.equal(out[96], out[48])
     assert torch.equal(out[0], out[48])
+
+
+def test_writes_on_two_streams_that_recode_what_their_blocks_hold():
+    """A decode loop per stream, with a workspace that it keeps: each step's rows are
+    larger, so the exponent of a partly filled block grows and its codes are rounded
+    anew; codes, bytes and outputs bit for bit as one loop after the other gives them."""
+    def loop(seed, n, Hk, D, B, steps=24):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        W = -(-steps // B)
+        pool = [torch.zeros(n * W, B, Hk, D, dtype=torch.uint8, device="cuda").view(E4M3) for _ in range(2)] + \
+               [torch.zeros(n * W, Hk, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        tables = torch.arange(n * W, dtype=torch.int32, device="cuda").view(W, n).t().contiguous()
+        cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+        lens = [torch.full((n,), i + 1, dtype=torch.int32, device="cuda") for i in range(steps)]
+        rows = [growing_step(i, n, Hk, D, g) for i in range(steps)]
+        q = torch.randn(n, 4 * Hk, D, generator=g, device="cuda").to(BF)
+        ws = torch.empty(pa.pa_prefill_fp8_workspace_bytes(pool[0], n, n, 4 * Hk), dtype=torch.uint8, device="cuda")
+        outs = [torch.zeros_like(q) for _ in range(steps)]
+
+        def step(i):
+            pa.pa_write_blocks_fp8(*rows[i], tables, lens[i], cu, *pool)
+            pa.pa_prefill_fp8(q, *pool, tables, lens[i], cu, 0.125, out=outs[i], workspace=ws)
+        return step, pool, outs
+
+    shapes = [(34, 200, 8, 128, 16), (35, 150, 3, 64, 8)]
+    runs = []
+    for together in (False, True):
+        loops = [loop(*s) for s in shapes]
+        streams = [torch.cuda.Stream() for _ in loops]
+        torch.cuda.synchronize()
+        for i in range(24):
+            for (step, _, _), s in zip(loops, streams):
+                with torch.cuda.stream(s):
+                    step(i)
+                if not together:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert error() == 0
+        runs.append([[x.view(torch.uint8) for x in pool] + outs for _, pool, outs in loops])
+    for x, y in zip(*runs):
+        for u, w in zip(x, y):
+            assert torch.equal(u, w)
+        assert int(x[2].min()) > 0 and torch.isfinite(x[-1]).all()
