@@ -30,3 +30,9 @@ def test_every_recorded_workload_was_taken_on_the_same_sources():
     assert len({e["source_sha"] for e in record.values()}) == 1
     for e in record.values():
         assert e["dram_bytes_per_launch"] > 0 and os.path.exists(os.path.join(bench.ROOT, e["report"]))
+
+
+def test_the_record_was_taken_on_the_present_sources():
+    """The benchmark reports no DRAM traffic from a record of other sources."""
+    record = json.load(open(os.path.join(bench.ROOT, "profiles", "decode_traffic.json")))
+    assert {e["source_sha"] for e in record.values()} == {bench.source_sha()}
