@@ -66,7 +66,7 @@ pa_status_t decode_fp8_plan(const pa_cache_desc_t *c, int32_t N, int32_t H, cons
     const int32_t splits = opts ? opts->num_splits : 0;
     size_t smem = 0;
     pl->mma = want != PA_KERNEL_SIMT && aligned && f8_shape(c, G, &pl->f, &smem);
-    if (!pl->mma) return want == PA_KERNEL_MMA ? PA_ERR_UNSUPPORTED : prefill_layout(false, c, N, N, H, splits, &pl->p);
+    if (!pl->mma) return want == PA_KERNEL_MMA ? PA_ERR_UNSUPPORTED : prefill_layout(false, false, c, N, N, H, splits, &pl->p);
     PrefillPlan &p = pl->p;
     p.tc = false;
     p.rows = kF8SlotRows;

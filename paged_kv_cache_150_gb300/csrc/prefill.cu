@@ -60,12 +60,13 @@ bool encode_tc_maps(CUtensorMap *q, CUtensorMap *k, CUtensorMap *v, const Prefil
 
 }  // namespace
 
-pa_status_t prefill_layout(bool tc, const pa_cache_desc_t *c, int32_t N, int32_t T, int32_t H, int32_t num_splits,
-                           PrefillPlan *p) {
+pa_status_t prefill_layout(bool tc, bool pair, const pa_cache_desc_t *c, int32_t N, int32_t T, int32_t H,
+                           int32_t num_splits, PrefillPlan *p) {
     const int32_t G = H / c->num_kv_heads;
     int threads = kSimtThreads;
     p->conv = c->dtype != PA_FP8_E4M3_BLOCK ? 0 : (int64_t)T <= (int64_t)N * (kTcRows / G) ? 8 : 4;
-    const void *fn = tc ? prefill_tc_ptr(c->head_dim, p->conv, &p->smem, &threads)
+    p->pair = pair;
+    const void *fn = tc ? prefill_tc_ptr(c->head_dim, p->conv, pair, &p->smem, &threads)
                         : prefill_simt_ptr(c->dtype, c->head_dim, c->layout, &p->smem);
     if (!fn) return PA_ERR_UNSUPPORTED;
     p->tc = tc;
@@ -177,7 +178,7 @@ pa_status_t prefill_launch(const PrefillPlan &p, const pa_cache_desc_t *c, Prefi
     void *args[] = {&a};
     size_t smem;
     int threads;
-    const void *fn = p.tc ? prefill_tc_ptr(c->head_dim, p.conv, &smem, &threads)
+    const void *fn = p.tc ? prefill_tc_ptr(c->head_dim, p.conv, p.pair, &smem, &threads)
                           : prefill_simt_ptr(c->dtype, c->head_dim, c->layout, &smem);
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
@@ -204,7 +205,8 @@ namespace {
 // Which call: its caches' kind and what a token sees.
 struct ChunkKind {
     bool fp8;      // pa_prefill_fp8: an 8-bit cache with block scales, q and out bf16
-    int32_t step, pair;  // PrefillArgs
+    int32_t step;  // PrefillArgs
+    bool pair;     // PrefillPlan; and the list's order (PrefillArgs::spread)
 };
 
 // The call's plan; fits: its scale and alignment suit the tcgen05 kernel.
@@ -221,7 +223,7 @@ pa_status_t prefill_plan_of(const ChunkKind &kind, const pa_cache_desc_t *c, int
     if (G > 64) return PA_ERR_UNSUPPORTED;
     const bool tc = want != PA_KERNEL_SIMT && fits && tc_supported(c, G);
     if (want == PA_KERNEL_MMA && !tc) return PA_ERR_UNSUPPORTED;
-    return prefill_layout(tc, c, N, T, H, opts ? opts->num_splits : 0, p);
+    return prefill_layout(tc, kind.pair, c, N, T, H, opts ? opts->num_splits : 0, p);
 }
 
 size_t chunk_workspace_bytes(const ChunkKind &kind, const pa_cache_desc_t *cache, int32_t num_seqs, int32_t num_tokens,
@@ -275,15 +277,14 @@ pa_status_t chunk_call(const ChunkKind &kind, void *out, const void *q, const vo
     a.T = num_tokens;
     a.H = num_heads;
     a.step = kind.step;
-    a.pair = kind.pair;
-    a.spread = kind.pair;
+    a.spread = kind.pair ? 1 : 0;
     a.min_w = 1;
     a.scale_log2 = scale * 1.4426950408889634f;
     return prefill_launch(p, cache, a, workspace, (cudaStream_t)stream);
 }
 
 // pa_prefill keeps its order of summation: no shared tiles, its list as it was.
-constexpr ChunkKind kPrefill{false, 1, 0}, kCross{false, 0, 1}, kPrefillFp8{true, 1, 1};
+constexpr ChunkKind kPrefill{false, 1, false}, kCross{false, 0, true}, kPrefillFp8{true, 1, true};
 
 }  // namespace
 }  // namespace pa

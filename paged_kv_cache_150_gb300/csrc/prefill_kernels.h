@@ -18,6 +18,7 @@ struct PrefillPlan {
     int32_t extra;     // weight of a tile beside its units
     int32_t threads;   // of an attention CTA
     int32_t conv;      // tcgen05 kernel over an 8-bit cache: its converter warps
+    bool pair;         // tcgen05 kernel: may share tiles of one row tile (TcSegment)
     int32_t C, max_tiles;
     size_t smem;
     size_t off_ctl, off_tile0, off_cu, off_tiles, off_start, off_merges, off_ml, off_acc, total;
@@ -28,12 +29,13 @@ struct PrefillPlan {
 const void *prefill_simt_ptr(int cache_dtype, int D, int layout, size_t *smem);
 
 // prefill_tc_kernel for head_dim 64 or 128, over a bf16 cache (conv 0) or, with 4 or 8
-// converter warps, an 8-bit one with block scales.
-const void *prefill_tc_ptr(int D, int conv, size_t *smem, int *threads);
+// converter warps, an 8-bit one with block scales; pair: the form that shares tiles of
+// one row tile (8 converters always do, 4 never).
+const void *prefill_tc_ptr(int D, int conv, bool pair, size_t *smem, int *threads);
 
 // Lays out a call of the CUDA-core kernel (tc false) or the tcgen05 one.
-pa_status_t prefill_layout(bool tc, const pa_cache_desc_t *c, int32_t N, int32_t T, int32_t H, int32_t num_splits,
-                           PrefillPlan *p);
+pa_status_t prefill_layout(bool tc, bool pair, const pa_cache_desc_t *c, int32_t N, int32_t T, int32_t H,
+                           int32_t num_splits, PrefillPlan *p);
 
 // The workspace behind p's shape (tiles, units, CTAs set) and head_dim.
 void prefill_workspace(PrefillPlan *p, int32_t N, int32_t head_dim);

@@ -66,7 +66,6 @@ struct PrefillArgs {
     int32_t max_tiles;    // capacity of tiles[] and cu[]
     float scale_log2;
     int32_t step;         // positions that each token sees more than the one before it: 1, or 0 where all see all (pa_cross)
-    int32_t pair;         // 1: both softmax warpgroups of the tcgen05 kernel share a tile of one row tile (TcSegment)
     int32_t spread;       // 1: the order of heads (and tiles) that suits the memory; 0: by head, sequence and position
     int32_t cols;         // columns of the order of tiles (tile_order)
     int32_t head_step;    // heads that the CTAs walk through side by side (list_head)

@@ -55,6 +55,10 @@ constexpr unsigned long long kTcUnitNs = 4096;
 // 256 x 208 + 128 x 88 = 384 x 168.
 constexpr int kTcSoftmaxRegs = 208, kTcOtherRegs = 88;
 
+// kPair: the form that shares tiles of one row tile (TcSegment), for pa_cross and short
+// 8-bit chunks.  pa_prefill, which does not, has a form without that code: with it as a
+// run-time choice the same calls took 69.7, 58.5 and 87.5 us (QSlots).
+//
 // kConv: the warps that turn an 8-bit cache's codes, which arrive in a ring of their
 // own (raw), into the bf16 units of the ring that the MMAs read; 0 for a bf16 cache.
 // Both forms over an 8-bit cache are right for every call; which one is faster:
@@ -68,9 +72,10 @@ constexpr int kTcSoftmaxRegs = 208, kTcOtherRegs = 88;
 // 191 and 161 us; 17 to 700 tokens of 16 sequences over up to 6000, 167 GFLOP, 181
 // and 204 us.  Eight warps where the call's chunks have no more tokens than a row
 // tile on average (prefill_layout).
-template <int D, int kConv>
+template <int D, int kConv, bool kPair>
 struct TcPrefill {
-    static constexpr bool kFp8 = kConv > 0, kMayPair = kConv != 4;
+    static constexpr bool kFp8 = kConv > 0, kMayPair = kPair;
+    static constexpr bool kOneSlot = !kFp8 && !kPair;  // pa_prefill (QSlots)
     static constexpr int kSoftmaxRegs = kConv == 8 ? 112 : kConv == 4 ? 192 : kTcSoftmaxRegs;
     static constexpr int kOtherRegs = kConv == 4 ? 64 : kTcOtherRegs, kConvertRegs = kConv == 8 ? 80 : 64;
     static constexpr int kPanels = D / 64;
@@ -128,7 +133,7 @@ __device__ __forceinline__ void tc_wait(uint32_t bar, uint32_t parity, bool &abo
 
 // Units of a segment that each row tile takes: [j0, je[i]).  A tile of one row
 // tile would leave the second softmax warpgroup idle and wait, unit after unit,
-// for its own softmax between two products: with a.pair the two warpgroups hold
+// for its own softmax between two products: with kMayPair the two warpgroups hold
 // the same rows and take the units in turn, and the one that had the first unit
 // joins the two results at the segment's end.  That one changes from such a
 // segment to the next (`first`, counted alike by every role).
@@ -156,7 +161,7 @@ struct TcSegment {
             je[i] = min(cur.j1, (int32_t)(((uint32_t)ki + kTcKeys - 1) / kTcKeys));  // the sum may pass 2^31
         }
         jend = max(je[0], je[1]);
-        pair = kMayPair && a.pair && t.ntok <= a.tq1;
+        pair = kMayPair && t.ntok <= a.tq1;
     }
 };
 
@@ -188,8 +193,11 @@ __device__ __forceinline__ void sts128(uint32_t addr, const uint4 &v) {
 // ------------------------------------------------------------------ Q slots
 // Q's two row tiles in shared memory, each with barriers of its own.  A tile of
 // two row tiles takes both; one of a single row tile takes them in turn, so that
-// its rows, and the K behind them, are fetched while the tile before is at work.
-// The K producer and the issuer count alike.
+// its rows, and the K behind them, are fetched while the tile before is at work
+// (long 8-bit chunks 191 -> 184 us).  pa_prefill's form takes both as one slot: a second
+// pair of barriers for each of its tiles cost it 4 to 9% on short contexts (16 x 400
+// tokens, 32 / 8 heads: 62.2 and 65.7 us at head_dim 128, 51.0 and 53.0 at 64; 64 x 40
+// over 1000 79.6 and 86.3).  The K producer and the issuer count alike.
 struct QSlots {
     uint32_t n0 = 0, n1 = 0;  // tiles that each slot has held
     int next = 0;             // the slot of the next tile of a single row tile
@@ -200,20 +208,34 @@ template <class L>
 __device__ __forceinline__ void load_q(const PrefillArgs &a, const PrefillTile &t, int32_t kvh, uint32_t q_dst,
                                        const TcBars &bar, const CUtensorMap *tmq, QSlots &q, bool &abort, int lane) {
     const bool two = t.ntok > a.tq1;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        if (!two && s != q.next) continue;
+    auto wait = [&](int s) {
         if (q.n(s) > 0) tc_wait(bar.q_free + 8 * s, (q.n(s) - 1) & 1, abort, a.err);
         ++q.n(s);
-        if (__any_sync(0xffffffffu, abort)) return;
+        return !__any_sync(0xffffffffu, abort);
+    };
+    auto load = [&](int slot, uint32_t full, int32_t row) {
+        for (int32_t p = 0; p < L::kPanels; ++p)
+            tma_load_4d(q_dst + slot * L::kTile + p * L::kPanel, tmq, full, 0, p, kvh * a.G, row);
+    };
+    const uint32_t bytes = (uint32_t)(L::kPanels * a.tq1 * a.G) * 128u;  // of a row tile
+    if constexpr (L::kOneSlot) {
+        if (!wait(0)) return;
         if (lane == 0) {
-            mbar_arrive_expect_tx(bar.q_full + 8 * s, (uint32_t)(L::kPanels * a.tq1 * a.G) * 128u);
-            for (int32_t p = 0; p < L::kPanels; ++p)
-                tma_load_4d(q_dst + s * L::kTile + p * L::kPanel, tmq, bar.q_full + 8 * s, 0, p, kvh * a.G,
-                            t.row0 + (two ? s * a.tq1 : 0));
+            mbar_arrive_expect_tx(bar.q_full, two ? 2 * bytes : bytes);
+            for (int32_t i = 0; i < (two ? 2 : 1); ++i) load(i, bar.q_full, t.row0 + i * a.tq1);
         }
+    } else {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (!two && s != q.next) continue;
+            if (!wait(s)) return;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar.q_full + 8 * s, bytes);
+                load(s, bar.q_full + 8 * s, t.row0 + (two ? s * a.tq1 : 0));
+            }
+        }
+        if (!two) q.next ^= 1;
     }
-    if (!two) q.next ^= 1;
 }
 // The last fetches and the issuer's last arrivals on the free barriers.
 __device__ __forceinline__ void drain_q(const TcBars &bar, QSlots &q, bool &late, unsigned int *err) {
@@ -232,11 +254,11 @@ __device__ __forceinline__ void drain_q(const TcBars &bar, QSlots &q, bool &late
 // lane's next box is read a unit ahead and looked at when its unit comes, so
 // no load is waited for.  Q: one box of tq1 tokens x G heads per row tile and
 // 64-element panel.
-template <int D, bool kIsV>
+template <int D, bool kPair, bool kIsV>
 __device__ __forceinline__ void tc_producer(const PrefillArgs &a, uint8_t *smem, const TcBars &bar,
                                             const CUtensorMap *tmq, const CUtensorMap *tm, int32_t gran,
                                             int32_t c, int lane) {
-    using L = TcPrefill<D, 0>;
+    using L = TcPrefill<D, 0, kPair>;
     if (lane == 0) {
         if (!kIsV) prefetch_tmap(tmq);
         prefetch_tmap(tm);
@@ -316,11 +338,11 @@ __device__ __forceinline__ uint32_t v_entry(bool pair, int32_t u, int32_t n) {
     return kFp8 && pair && u + 1 < n ? 2u * (uint32_t)u + 2u : 2u * (uint32_t)u + 1u;
 }
 
-template <int D, int kConv, bool kIsV>
+template <int D, int kConv, bool kPair, bool kIsV>
 __device__ __forceinline__ void tc_producer8(const PrefillArgs &a, uint8_t *smem, const TcBars &bar,
                                              const CUtensorMap *tmq, const CUtensorMap *tm, int32_t gran,
                                              int32_t c, int lane) {
-    using L = TcPrefill<D, kConv>;
+    using L = TcPrefill<D, kConv, kPair>;
     if (lane == 0) {
         if (!kIsV) prefetch_tmap(tmq);
         prefetch_tmap(tm);
@@ -421,9 +443,9 @@ __device__ __forceinline__ void codes_bf16(uint32_t w, uint64_t s2, uint32_t &lo
     hi = pack_bf16x2(u, v);
 }
 
-template <int D, int kConv>
+template <int D, int kConv, bool kPair>
 __device__ __forceinline__ void tc_converter(const PrefillArgs &a, uint8_t *smem, const TcBars &bar, int32_t gran, int tid) {
-    using L = TcPrefill<D, kConv>;
+    using L = TcPrefill<D, kConv, kPair>;
     constexpr int kRowsPass = (D == 128 ? 4 : 8) * kConv;  // rows of the warps at once
     constexpr int kPasses = 128 / kRowsPass, kBatch = 2;  // loads of a thread in flight
     const uint32_t raw = smem_u32(smem) + L::kRawRing, ring = smem_u32(smem) + L::kRing;
@@ -504,16 +526,16 @@ template <int D>
 __device__ __forceinline__ uint32_t v_chunk(uint32_t vbase, int e) {  // address of 16-byte chunk e % (D / 8) of row e / (D / 8)
     constexpr int kChunks = D / 8;
     const int r = e / kChunks, ch = e % kChunks;
-    return vbase + (uint32_t)(ch >> 3) * TcPrefill<D, 0>::kPanel + (uint32_t)r * 128u +
+    return vbase + (uint32_t)(ch >> 3) * TcPrefill<D, 0, false>::kPanel + (uint32_t)r * 128u +
            (uint32_t)(((ch & 7) ^ (r & 7)) << 4);
 }
 // Sign bits of the halves whose exponent is all ones (bf16 infinities and NaN).
 __device__ __forceinline__ uint32_t odd_bits(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
-template <int D, int kConv>
+template <int D, int kConv, bool kPair>
 __device__ __forceinline__ void tc_guard(const PrefillArgs &a, uint8_t *smem, const TcBars &bar, const OddColumns &odd,
                                          int32_t c, int lane) {
-    using L = TcPrefill<D, kConv>;
+    using L = TcPrefill<D, kConv, kPair>;
     constexpr int kChunks = D / 8;
     const uint32_t ring = smem_u32(smem) + L::kRing;
     uint32_t n = 0, segs = 0, units = 0;  // ring entries of the segments before, segments, guarded units
@@ -607,10 +629,10 @@ __device__ __forceinline__ int32_t uniform(int32_t x) { return __shfl_sync(0xfff
 // One warp; one elected lane issues.  MMAs of one thread complete in order, so S of a
 // unit may be computed over the P of the one before (its O += P V was issued
 // earlier), and a row tile's S being complete says that its earlier O is too.
-template <int D, int kConv>
+template <int D, int kConv, bool kPair>
 __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, const TcBars &bar, uint32_t tmem,
                                           int32_t c, int lane) {
-    using L = TcPrefill<D, kConv>;
+    using L = TcPrefill<D, kConv, kPair>;
     constexpr uint32_t IDESC_S = tc_idesc_bf16(128, kTcKeys, false, false);
     constexpr uint32_t IDESC_O = tc_idesc_bf16(128, D, false, true);
     const uint32_t ring = smem_u32(smem) + L::kRing;
@@ -634,10 +656,10 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
         const int32_t je[2] = {uniform(sg.je[0]), uniform(sg.je[1])};
         const bool pair = L::kMayPair && uniform(sg.pair) != 0;
         if (jend <= j0) continue;
-        const bool two = uniform(sg.t.ntok > a.tq1) != 0;
-        const int q0 = uniform(two ? 0 : qs.next);  // Q's slot of the first row tile
+        const bool two = L::kOneSlot || uniform(sg.t.ntok > a.tq1) != 0;
+        const int q0 = L::kOneSlot ? 0 : uniform(two ? 0 : qs.next);  // Q's slot of the first row tile
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int s = 0; s < (L::kOneSlot ? 1 : 2); ++s)
             if (two || s == q0) {
                 tc_wait(bar.q_full + 8 * s, qs.n(s) & 1, abort, a.err);
                 ++qs.n(s);
@@ -645,7 +667,7 @@ __device__ __forceinline__ void tc_issuer(const PrefillArgs &a, uint8_t *smem, c
         if (!two) qs.next ^= 1;
         auto free_q = [&]() {
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+            for (int s = 0; s < (L::kOneSlot ? 1 : 2); ++s)
                 if (two || s == q0) tc_commit_if(one, bar.q_free + 8 * s);
         };
         auto issue_s = [&](int i, uint32_t slot, int q) {  // slot q of Q
@@ -836,11 +858,11 @@ __device__ __forceinline__ void write_rows(const PrefillArgs &a, const Walk &cur
 
 // ----------------------------------------------------------------- softmax
 // Four warps per row tile; a thread owns one query row (tensor-memory lane).
-template <int D, int kConv>
+template <int D, int kConv, bool kPair>
 __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &bar, uint32_t tmem,
                                            const OddColumns &odd, float2 *ml, int32_t c,
                                            int i, int warp, int lane) {
-    using L = TcPrefill<D, kConv>;
+    using L = TcPrefill<D, kConv, kPair>;
     const int r = warp * 32 + lane;  // row of the row tile
     const uint32_t t_lane = (uint32_t)(warp * 32) << 16;
     const uint32_t tS = tmem + L::kS + i * 128 + t_lane, tO = tmem + L::kO + i * D + t_lane, tO_other = tmem + L::kO + (1 - i) * D + t_lane;
@@ -993,12 +1015,12 @@ __device__ __forceinline__ void tc_softmax(const PrefillArgs &a, const TcBars &b
     } while (cur.next(a));
 }
 
-template <int D, int kConv>
-__global__ void __launch_bounds__(TcPrefill<D, kConv>::kThreads, 1)
+template <int D, int kConv, bool kPair>
+__global__ void __launch_bounds__(TcPrefill<D, kConv, kPair>::kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const __grid_constant__ PrefillArgs a,
                       const int32_t gran) {
-    using L = TcPrefill<D, kConv>;
+    using L = TcPrefill<D, kConv, kPair>;
     extern __shared__ __align__(1024) uint8_t smem_tc[];
     uint8_t *smem = smem_tc;
     if ((smem_u32(smem) & 1023) != 0) {  // no room to align it here (the layout fills the CTA's limit)
@@ -1044,27 +1066,27 @@ __global__ void __launch_bounds__(TcPrefill<D, kConv>::kThreads, 1)
     const int32_t c = blockIdx.x;
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kSoftmaxRegs));
-        tc_softmax<D, kConv>(a, bar, tmem, odd, (float2 *)(smem + L::kMl), c, warp >> 2, warp & 3, lane);
+        tc_softmax<D, kConv, kPair>(a, bar, tmem, odd, (float2 *)(smem + L::kMl), c, warp >> 2, warp & 3, lane);
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kOtherRegs));
         if (warp == 8) {
-            tc_issuer<D, kConv>(a, smem, bar, tmem, c, lane);
+            tc_issuer<D, kConv, kPair>(a, smem, bar, tmem, c, lane);
         } else if (warp == 9) {
             if constexpr (L::kFp8)
-                tc_producer8<D, kConv, false>(a, smem, bar, &tmq, &tmk, gran, c, lane);
+                tc_producer8<D, kConv, kPair, false>(a, smem, bar, &tmq, &tmk, gran, c, lane);
             else
-                tc_producer<D, false>(a, smem, bar, &tmq, &tmk, gran, c, lane);
+                tc_producer<D, kPair, false>(a, smem, bar, &tmq, &tmk, gran, c, lane);
         } else if (warp == 10) {
             if constexpr (L::kFp8)
-                tc_producer8<D, kConv, true>(a, smem, bar, &tmq, &tmv, gran, c, lane);
+                tc_producer8<D, kConv, kPair, true>(a, smem, bar, &tmq, &tmv, gran, c, lane);
             else
-                tc_producer<D, true>(a, smem, bar, &tmq, &tmv, gran, c, lane);
+                tc_producer<D, kPair, true>(a, smem, bar, &tmq, &tmv, gran, c, lane);
         } else {
-            tc_guard<D, kConv>(a, smem, bar, odd, c, lane);
+            tc_guard<D, kConv, kPair>(a, smem, bar, odd, c, lane);
         }
     } else if constexpr (L::kFp8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kConvertRegs));
-        tc_converter<D, kConv>(a, smem, bar, gran, tid - 384);
+        tc_converter<D, kConv, kPair>(a, smem, bar, gran, tid - 384);
     }
     // The softmax warps have waited for the last o_full, which every MMA
     // precedes: nothing uses the tensor memory any more.
