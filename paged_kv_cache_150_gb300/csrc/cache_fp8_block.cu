@@ -144,11 +144,12 @@ __device__ __forceinline__ void recode_rows(uint8_t *codes, int32_t held, int32_
 // many per block as its registers hold: a team of W of the CTA's 8 warps takes a
 // unit and `heads` of its KV heads, one after the other, K and V together.  A
 // thread's vectors are the same column of rows a step apart.
-// 48 prompts of 700 to 4500 tokens (8 heads, head_dim 128, bf16; 591 MB): 107 us,
-// 5.5 TB/s, 0.82 of the copy bandwidth.  With a search per head and a division per
-// vector it took 152 instructions per vector of 8 values and 161 us; with half the
-// vectors per thread and 3 or 4 CTAs 109 and 113 us.  One token of 64 sequences:
-// 4.5 us.
+// 48 prompts of 700 to 4500 tokens (8 heads, head_dim 128, bf16; 591 MB): 109 us, 5.4
+// TB/s, 0.80 of the copy bandwidth (104 in a graph); fp32 (985 MB) 214 us, 4.6 TB/s;
+// head_dim 64 75 and 109 us.  With a search per head and a division per vector it
+// took 152 instructions per vector of 8 values and 161 us, when this form took 107; with
+// half the vectors per thread and 3 or 4 CTAs 109 and 113 us.  One token of 64
+// sequences: 4.3 to 4.4 us.
 template <typename T, int W>
 __global__ void __launch_bounds__(256, kWriteBlocksCtas) write_blocks_kernel(const __grid_constant__ WriteBlocksArgs a, const int32_t heads) {
     grid_dependency_wait();

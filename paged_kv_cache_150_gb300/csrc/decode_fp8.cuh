@@ -24,8 +24,10 @@
 // Bound by the K and V bytes: 16 sequences of 32768 tokens (64 / 8 heads, head_dim
 // 128) take 169 to 174 us (6.2 to 6.4 TB/s) with the work list and the merge. The
 // same bytes with 4 / 2 / 1 KV heads 174 / 181 / 221 us; head_dim 64 reaches 4.2 to
-// 4.7 TB/s with 8 KV heads and 2.7 with one.  With a scale per block 168 us, and
-// 325 us on 256 sequences of 16 to 8192 tokens (2203 MB, 6.8 TB/s).
+// 4.7 TB/s with 8 KV heads and 2.7 with one.  With a scale per block 169 to 172 us, and
+// 332 to 337 us on 256 sequences of 16 to 8192 tokens (2203 MB, 6.5 to 6.6 TB/s); the same
+// bytes with 4 / 2 / 1 KV heads 177 / 185 / 282 us, head_dim 64 4.7 TB/s with 8 KV heads
+// and 2.2 with one.
 // A CTA is 8 consumer warps and a TMA producer, two CTAs per SM; a stage is 8
 // slices of 16 tokens of one KV head (K and V, 32 KiB at head_dim 128): NH heads
 // (the largest of 8, 4, 2, 1 that divides Hk)
@@ -116,7 +118,8 @@ __device__ __forceinline__ int32_t f8_units_end(const PrefillCursor &cur, int32_
 enum F8Scales { kTokenScales, kBlockScales8, kBlockScalesAny };
 
 // The block scales of NH heads, and their way to a stage.  p need not be aligned.
-// Read from L2: the kernel may have begun while the write before it ran.
+// (The work list's kernel has waited for the write before a call, so this one begins
+// behind it.  A byte is read once per unit: no use of L1.)
 __device__ __forceinline__ uint64_t load_scales(const uint8_t *p, int32_t NH) {
     if (((uintptr_t)p & (uintptr_t)(NH - 1)) == 0) {
         if (NH == 8) return __ldcg(reinterpret_cast<const unsigned long long *>(p));

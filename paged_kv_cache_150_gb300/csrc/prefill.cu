@@ -64,6 +64,8 @@ pa_status_t prefill_layout(bool tc, bool pair, const pa_cache_desc_t *c, int32_t
                            int32_t num_splits, PrefillPlan *p) {
     const int32_t G = H / c->num_kv_heads;
     int threads = kSimtThreads;
+    // T counts the rows of q, those behind the last sequence too, as the lengths are on
+    // the GPU: few tokens in a long padded buffer take the form of long chunks.
     p->conv = c->dtype != PA_FP8_E4M3_BLOCK ? 0 : (int64_t)T <= (int64_t)N * (kTcRows / G) ? 8 : 4;
     p->pair = pair;
     const void *fn = tc ? prefill_tc_ptr(c->head_dim, p->conv, pair, &p->smem, &threads)

@@ -34,9 +34,10 @@
 // 365 us on that prompt, no difference on long contexts.
 //
 // Encoder states (pa_cross): 64 to 448 tokens of 32 sequences over 1000 to 4096
-// states (32 / 8 heads, head_dim 128, 258 GFLOP) 223 to 235 us; 1 to 8 tokens of 128
-// sequences over 100 to 1500 (16 heads, head_dim 64, 433 MB) 112 to 115 us, held by
-// a tile's end every seventh unit or so (over long contexts 6.3 TB/s).
+// states (32 / 8 heads, head_dim 128, 258 GFLOP) 226 to 251 us (between boxes, and with the
+// power cap); 1 to 8 tokens of 128 sequences over 100 to 1500 (16 heads, head_dim 64, 433
+// MB) 114 to 115 us, held by a tile's end every seventh unit or so (over long contexts
+// 6.3 TB/s).
 #pragma once
 
 #include <cuda.h>  // CUtensorMap
@@ -68,10 +69,16 @@ constexpr int kTcSoftmaxRegs = 208, kTcOtherRegs = 88;
 //   8  640 x 96, 256 x 112 + 128 x 88 + 256 x 80 and some left.  A unit takes the
 //      converters half of that; the softmax, short of registers, reads its scores twice,
 //      and shares tiles of one row tile (TcSegment), which leaves it time for that.
-// 32 / 8 heads, head_dim 128: 3 to 8 tokens of 64 sequences over 500 to 8192, 517 MB,
-// 191 and 161 us; 17 to 700 tokens of 16 sequences over up to 6000, 167 GFLOP, 181
-// and 204 us.  Eight warps where the call's chunks have no more tokens than a row
-// tile on average (prefill_layout).
+// Eight warps where the call's chunks have no more tokens than a row tile on average
+// (prefill_layout).  Sequences of 4096 tokens, chunks of 1/8, 1, 1.5 and 4 row tiles, eight
+// and four warps in us:
+//   64 x, 32 / 8 heads of 128     162 186   169 194   251 230   484 448
+//   64 x, 32 / 8 heads of 64      134 158   138 164   221 191   421 361
+//   64 x, 16 / 16 heads of 128    309 357   321 374   488 460   926 892
+//   64 x, 8 / 1 heads of 128       35  39    38  42    52  49    88  80
+//   16 x, 32 / 8 heads of 128      54  61    60  67    85  79   144 133
+// 256 sequences of 600, 32 / 8 heads of 128: 163 224, 167 230, 228 261, 433 506: over short
+// contexts eight would stay the faster there (heads of 64: 202 206 and 344 312).
 template <int D, int kConv, bool kPair>
 struct TcPrefill {
     static constexpr bool kFp8 = kConv > 0, kMayPair = kPair;
